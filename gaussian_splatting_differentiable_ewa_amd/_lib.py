@@ -38,7 +38,13 @@ EXPORTS = (
     "gs_rasterize_fwd_bwd_l1_noalloc", "gs_rasterize_fwd_bwd_l1_noalloc_max_bytes",
     "gs_window_gaussians", "gs_window_gaussians_workspace_bytes", "gs_adam_step_visible",
     "gs_seen_gaussians", "gs_seen_gaussians_workspace_bytes", "gs_preprocess_bwd_compact", "gs_adam_step_compact",
+    "gs_rope_axes", "gs_norm_gate_fwd", "gs_norm_gate_bwd", "gs_norm_gate_bwd_workspace_bytes",
+    "gs_block_summary", "gs_block_select", "gs_block_attn_fwd", "gs_block_attn_fwd_workspace_bytes",
+    "gs_block_attn_bwd", "gs_block_attn_bwd_workspace_bytes",
 )
+GS_F32, GS_F16, GS_BF16 = range(3)
+GS_QUERY_GROUP, GS_KEY_BLOCK = 128, 64
+GS_MAX_SELECT_TOKENS = 2097152
 
 
 class GsError(RuntimeError):
@@ -53,6 +59,11 @@ class GsCamera(ctypes.Structure):
         ("R", ctypes.c_float * 9), ("t", ctypes.c_float * 3),
         ("near_plane", ctypes.c_float), ("far_plane", ctypes.c_float),
     ]
+
+
+class GsTokens(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64)]
 
 
 _P = ctypes.c_void_p
@@ -116,6 +127,21 @@ def lib():
             "gs_rasterize_fwd_bwd_l1_noalloc_max_bytes": ([], _SZ),
             "gs_raster_exp": ([_P, _P, _I64, _P], ctypes.c_int),
             "gs_stream_copy": ([_P, _P, _U64, _P], ctypes.c_int),
+            "gs_rope_axes": ([_P, _P, _P, _P, _I64, _I64, _I32, _I32, _I32, _I32, _P, _I64, _P, _P, _I32, _I32, _P],
+                             ctypes.c_int),
+            "gs_norm_gate_fwd": ([_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I64, _F32, _F32, _I32, _P], ctypes.c_int),
+            "gs_norm_gate_bwd_workspace_bytes": ([_I64, _I32, _I64], _SZ),
+            "gs_norm_gate_bwd": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I64, _F32, _I32, _P,
+                                  _SZ, _P], ctypes.c_int),
+            "gs_block_summary": ([_P, _I64, _I64, _I32, _I32, _I32, _P, _I64, _I64, _P, _P, _P], ctypes.c_int),
+            "gs_block_select": ([_P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _P, _I32, _I32, _P, _P],
+                                ctypes.c_int),
+            "gs_block_attn_fwd_workspace_bytes": ([_I64, _I64, _I32, _I32, _I32], _SZ),
+            "gs_block_attn_fwd": ([_P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _P, _I32, _I32, _F32, _P,
+                                   _P, _P, _SZ, _P], ctypes.c_int),
+            "gs_block_attn_bwd_workspace_bytes": ([_I64, _I64, _I64, _I32, _I32, _I32], _SZ),
+            "gs_block_attn_bwd": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _P, _I32, _I32,
+                                   _F32, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -410,3 +436,107 @@ def gs_stream_copy(dst, src, nbytes=None, stream=None):
     """Plain device copy of nbytes (default: all of src) from src to dst."""
     nb = src.numel() * src.element_size() if nbytes is None else int(nbytes)
     _check(lib().gs_stream_copy(_ptr(dst), _ptr(src), nb, _stream(stream)), "gs_stream_copy")
+
+
+# ---- token operators -----------------------------------------------------------
+# Token tensors are [batch][tokens][heads][dim] (any strides, dim contiguous).
+def dtype_of(t) -> int:
+    """gs_dtype of a tensor (raises for other types)."""
+    import torch
+    try:
+        return {torch.float32: GS_F32, torch.float16: GS_F16, torch.bfloat16: GS_BF16}[t.dtype]
+    except KeyError:
+        raise GsError(f"unsupported element type {t.dtype}") from None
+
+
+def _tok(t):
+    if t is None:
+        return None
+    sb, st, sh, sd = t.stride()
+    if sd != 1 and t.shape[3] > 1:
+        raise GsError("the last dimension of a token tensor must be contiguous")
+    return ctypes.byref(GsTokens(t.data_ptr(), sb, st, sh))
+
+
+def _blk(t):
+    """A summary [batch][heads][blocks](dim) as a token tensor of blocks."""
+    if t.dim() == 4 and t.stride(3) != 1 and t.shape[3] > 1:
+        raise GsError("the last dimension of a summary must be contiguous")
+    return ctypes.byref(GsTokens(t.data_ptr(), t.stride(0), t.stride(2), t.stride(1)))
+
+
+def _ws(ws):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def gs_rope_axes(q, k, q_out, k_out, pos, freq, pairs, interleaved=False, inverse=False, stream=None):
+    """pos int32 [batch or 1][tokens][3] contiguous; k and k_out may be None."""
+    b, n, hq, d = q.shape
+    _check(lib().gs_rope_axes(_tok(q), _tok(k), _tok(q_out), _tok(k_out), b, n, hq, 0 if k is None else k.shape[2], d,
+                              dtype_of(q), _ptr(pos), 0 if pos.shape[0] == 1 else pos.stride(0), _ptr(freq),
+                              (ctypes.c_int32 * 3)(*pairs), int(bool(interleaved)), int(bool(inverse)),
+                              _stream(stream)), "gs_rope_axes")
+
+
+def gs_norm_gate_fwd(x, f, gate, w_post, w_pre, y, h, stats, rows_per_gate, scale=1.0, eps=1e-6, stream=None):
+    """x, f, y, h [rows][channels] contiguous; f, gate, w_post, w_pre may be None."""
+    rows, c = x.shape
+    _check(lib().gs_norm_gate_fwd(_ptr(x), _ptr(f), _ptr(gate), _ptr(w_post), _ptr(w_pre), _ptr(y), _ptr(h), _ptr(stats),
+                                  rows, c, rows_per_gate, scale, eps, dtype_of(x), _stream(stream)), "gs_norm_gate_fwd")
+
+
+def norm_gate_bwd_workspace_bytes(rows: int, channels: int, rows_per_gate: int) -> int:
+    return lib().gs_norm_gate_bwd_workspace_bytes(rows, channels, rows_per_gate)
+
+
+def gs_norm_gate_bwd(gy, gh, x, f, gate, w_post, w_pre, stats, gx, gf, ggate, gw_post, gw_pre, rows_per_gate, ws,
+                     scale=1.0, stream=None):
+    """gy, f, gate, w_post, w_pre and the fp32 outputs may be None."""
+    rows, c = x.shape
+    _check(lib().gs_norm_gate_bwd(_ptr(gy), _ptr(gh), _ptr(x), _ptr(f), _ptr(gate), _ptr(w_post), _ptr(w_pre),
+                                  _ptr(stats), _ptr(gx), _ptr(gf), _ptr(ggate), _ptr(gw_post), _ptr(gw_pre), rows, c,
+                                  rows_per_gate, scale, dtype_of(x), *_ws(ws), _stream(stream)), "gs_norm_gate_bwd")
+
+
+def gs_block_summary(k, sum8, scale, kv_len=None, block0=0, blocks=None, stream=None):
+    """sum8 int8 [batch][heads][ceil(tokens / 64)][dim], scale fp32 without dim;
+    any strides, dim contiguous."""
+    b, n, h, d = k.shape
+    every = (n + GS_KEY_BLOCK - 1) // GS_KEY_BLOCK
+    _check(lib().gs_block_summary(_tok(k), b, n, h, d, dtype_of(k), _ptr(kv_len), block0,
+                                  every - block0 if blocks is None else blocks, _blk(sum8), _blk(scale),
+                                  _stream(stream)), "gs_block_summary")
+
+
+def gs_block_select(q, sum8, scale, tokens_k, heads_k, lists, kv_len=None, causal=False, stream=None):
+    """lists int32 [batch][heads_q][ceil(tokens_q / 128)][top]."""
+    b, n, h, d = q.shape
+    _check(lib().gs_block_select(_tok(q), _blk(sum8), _blk(scale), b, n, tokens_k, h, heads_k, d, dtype_of(q),
+                                 _ptr(kv_len), int(bool(causal)), lists.shape[3], _ptr(lists), _stream(stream)),
+           "gs_block_select")
+
+
+def block_attn_fwd_workspace_bytes(batch: int, tokens_q: int, heads_q: int, dim: int, top: int) -> int:
+    return lib().gs_block_attn_fwd_workspace_bytes(batch, tokens_q, heads_q, dim, top)
+
+
+def gs_block_attn_fwd(q, k, v, lists, out, lse, ws=None, kv_len=None, causal=False, sm_scale=None, stream=None):
+    """sm_scale: dim ** -0.5 by default."""
+    b, n, h, d = q.shape
+    _check(lib().gs_block_attn_fwd(_tok(q), _tok(k), _tok(v), _ptr(lists), b, n, k.shape[1], h, k.shape[2], d,
+                                   dtype_of(q), _ptr(kv_len), int(bool(causal)), lists.shape[3],
+                                   d ** -0.5 if sm_scale is None else sm_scale, _tok(out), _ptr(lse), *_ws(ws),
+                                   _stream(stream)), "gs_block_attn_fwd")
+
+
+def block_attn_bwd_workspace_bytes(batch: int, tokens_q: int, tokens_k: int, heads_q: int, heads_k: int, dim: int) -> int:
+    return lib().gs_block_attn_bwd_workspace_bytes(batch, tokens_q, tokens_k, heads_q, heads_k, dim)
+
+
+def gs_block_attn_bwd(gout, q, k, v, out, lse, lists, gq, gk, gv, ws, kv_len=None, causal=False, sm_scale=None,
+                      stream=None):
+    b, n, h, d = q.shape
+    _check(lib().gs_block_attn_bwd(_tok(gout), _tok(q), _tok(k), _tok(v), _tok(out), _ptr(lse), _ptr(lists), b, n,
+                                   k.shape[1], h, k.shape[2], d, dtype_of(q), _ptr(kv_len), int(bool(causal)),
+                                   lists.shape[3], d ** -0.5 if sm_scale is None else sm_scale, _tok(gq), _tok(gk),
+                                   _tok(gv), *_ws(ws), _stream(stream)), "gs_block_attn_bwd")

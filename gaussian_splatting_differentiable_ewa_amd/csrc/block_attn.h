@@ -1,0 +1,191 @@
+// Shared by the attention kernels (block_attn.hip, block_attn_bwd.hip): the
+// matrix instruction, the LDS tiles and their reads.
+//
+// Matrix tile: v_mfma 32x32x16. Lane l holds of A: row l & 31, of B: column
+// l & 31, eight consecutive k from 8 (l >> 5); of C: column l & 31, rows
+// 8 (i >> 2) + 4 (l >> 5) + (i & 3) for registers i = 0..15.
+//
+// Scores are formed transposed where queries are the columns (S^T = K Q^T): a
+// lane then holds 16 keys of one query, so softmax needs one exchange between
+// the two lane halves and the rescaling of the output is one factor per lane.
+// And C's rows of registers 8g..8g+7 are, as a set, the 16 k of one B operand:
+// slot s of half hi stands for row 16 g + 8 (s >> 2) + 4 hi + (s & 3). The
+// order of k inside a product is free as long as A uses the same one, so
+// probabilities go from C to B without crossing lanes, and A (the transposed
+// values) is read from LDS in that order by two 4-row transposing reads.
+#pragma once
+
+#include "tokens.h"
+
+namespace gs {
+
+constexpr int QG = GS_QUERY_GROUP, KB = GS_KEY_BLOCK;
+constexpr int ATT_THREADS = 256;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+typedef float acc16 __attribute__((ext_vector_type(16)));
+typedef short short4v __attribute__((ext_vector_type(4)));
+typedef float float4v __attribute__((ext_vector_type(4)));
+
+template <typename T>
+struct Mma;
+template <>
+struct Mma<bf16> {
+    typedef bf16 v8 __attribute__((ext_vector_type(8)));
+    typedef bf16 v4 __attribute__((ext_vector_type(4)));
+    static __device__ __forceinline__ acc16 mma(v8 a, v8 b, acc16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+};
+template <>
+struct Mma<f16> {
+    typedef f16 v8 __attribute__((ext_vector_type(8)));
+    typedef f16 v4 __attribute__((ext_vector_type(4)));
+    static __device__ __forceinline__ acc16 mma(v8 a, v8 b, acc16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+};
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// A tile of 64 rows of D elements in LDS, in 16-byte chunks; chunk c of a row
+// sits at c ^ swizzle(row). The swizzle serves both reads without bank
+// conflicts (64 banks of 4 bytes): 16 lanes reading the same chunk of 16
+// consecutive rows fall on 16 different 16-byte bank groups, and the four
+// rows of a transposing read (rows 4m..4m+3, 64 bytes of each) on four
+// different 64-byte ones.
+template <int D>
+struct Tile {
+    static constexpr int CHUNKS = D / 8;
+    static constexpr int ELEMS = KB * D;
+    static __device__ __forceinline__ int swizzle(int row)
+    {
+        if constexpr (D == 128) return ((row & 3) << 2) | ((row >> 2) & 3);
+        else return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+    }
+    // element offset of chunk c of a row
+    static __device__ __forceinline__ int at(int row, int c) { return (row * CHUNKS + (c ^ swizzle(row))) * 8; }
+};
+
+// This wave's share of loading 64 rows into a tile, straight to LDS (16 bytes
+// a lane; the LDS side of such a load is linear in the lane, so the swizzle
+// is applied to the global side). Row r comes from token min(t0 + r, last).
+template <typename T, int D, int WAVES>
+__device__ __forceinline__ void load_tile(T* tile, const T* base, int64_t stride, int64_t t0, int64_t last, int wave)
+{
+    constexpr int CH = Tile<D>::CHUNKS, PER = CH / WAVES;
+    const int lane = lane_id();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int first = (wave * PER + i) * 64, n = first + lane;
+        const int row = n / CH, c = (n % CH) ^ Tile<D>::swizzle(row);
+        int64_t t = t0 + row;
+        t = t < last ? t : last;
+        const T* src = base + t * stride + c * 8;
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                         (__attribute__((address_space(3))) void*)(tile + first * 8), 16, 0, 0);
+    }
+}
+
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// A operand, rows of the tile: row r0 + (l & 31), k = 16 step + 8 (l >> 5) ...
+template <typename T, int D>
+__device__ __forceinline__ typename Mma<T>::v8 read_rows(const T* tile, int r0, int step)
+{
+    const int l = lane_id();
+    return *(const typename Mma<T>::v8*)(tile + Tile<D>::at(r0 + (l & 31), step * 2 + (l >> 5)));
+}
+
+// A operand, columns of the tile as rows: row = column c0 + (l & 31), k = the
+// tile's rows r0 + 8 (s >> 2) + 4 (l >> 5) + (s & 3) for slots s = 0..7.
+// In each 16 lanes a transposing read takes 4 rows x 16 columns, 8 bytes a
+// lane (lane i: row i / 4, columns 4 (i % 4) ...), and hands lane i column i.
+template <typename T, int D>
+__device__ __forceinline__ typename Mma<T>::v8 read_cols(const T* tile, int r0, int c0)
+{
+    const int l = lane_id(), hi = l >> 5, row = 4 * hi + ((l & 15) >> 2), col = c0 + (l & 16) + 4 * (l & 3);
+    union {
+        short4v h[2];
+        typename Mma<T>::v8 v;
+    } u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const T* p = tile + Tile<D>::at(r0 + 8 * i + row, col >> 3) + (col & 7);
+        u.h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4v*)p);
+    }
+    return u.v;
+}
+
+// B operand kept in registers: column = token, k = 16 step + 8 (l >> 5) ...
+template <typename T, int D>
+__device__ __forceinline__ void load_cols(const T* row, typename Mma<T>::v8 (&out)[D / 16])
+{
+    const int hi = lane_id() >> 5;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) out[s] = *(const typename Mma<T>::v8*)(row + s * 16 + hi * 8);
+}
+
+// Registers 8g..8g+7 of C as a B operand, rounded to nearest even.
+template <typename T>
+__device__ __forceinline__ typename Mma<T>::v8 as_operand(const acc16& c, int g)
+{
+    typename Mma<T>::v8 v;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) v[s] = (T)c[8 * g + s];
+    return v;
+}
+
+__device__ __forceinline__ acc16 zero16()
+{
+    acc16 z;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = 0.f;
+    return z;
+}
+
+// Row of C that register i of this lane holds.
+__device__ __forceinline__ int c_row(int i, int hi) { return 8 * (i >> 2) + 4 * hi + (i & 3); }
+
+struct AttnArgs {
+    int64_t tokens_q, tokens_k, groups, blocks;
+    int32_t heads_q, heads_k, causal, top, splits;
+    float scale;  // of the scores
+};
+
+// Valid keys of a sequence.
+__device__ __forceinline__ int64_t seq_len(const int32_t* kv_len, int64_t b, int64_t tokens)
+{
+    const int64_t n = kv_len ? kv_len[b] : tokens;
+    return n < 0 ? 0 : (n > tokens ? tokens : n);
+}
+
+// Whether entry j of a list counts: ascending, inside the visible blocks.
+__device__ __forceinline__ bool entry_ok(const int32_t* list, int j, int64_t visible)
+{
+    const int id = list[j], before = j > 0 ? list[j - 1] : -1;
+    return id > before && id < visible;
+}
+
+// 4 consecutive elements, 8 bytes.
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float a, float b, float c, float d)
+{
+    typename Mma<T>::v4 v;
+    v[0] = (T)a, v[1] = (T)b, v[2] = (T)c, v[3] = (T)d;
+    *(typename Mma<T>::v4*)p = v;
+}
+
+// Host: the checks both directions share. GS_OK with `empty` when there is
+// nothing to do for the queries.
+gs_status attn_check(int64_t batch, int64_t tokens_q, int64_t tokens_k, int32_t heads_q, int32_t heads_k, int32_t dim,
+                     int32_t dtype, int32_t top, float sm_scale);
+
+inline bool attn_view_ok(const gs_tokens* t, int64_t batch, int64_t tokens, int64_t heads)
+{
+    return rows_aligned(t, batch, tokens, heads, 2, 16);
+}
+
+}  // namespace gs

@@ -1,0 +1,357 @@
+// gs_block_attn_fwd: softmax attention of query groups over their listed key
+// blocks.
+#include "block_attn.h"
+
+namespace gs {
+
+// Softmax state of a wave's 32 queries (one per lane column).
+template <int D>
+struct Online {
+    float m, l;  // running maximum (scaled to base 2) and this lane half's sum
+    acc16 o[D / 32];
+    __device__ __forceinline__ void init()
+    {
+        m = -INFINITY;
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) o[i] = zero16();
+    }
+};
+
+// One block of 64 keys: limit is the number of keys, counted from the block's
+// first, that this lane's query sees (>= 64: all of them).
+template <typename T, int D>
+__device__ __forceinline__ void attend_block(const T* kt, const T* vt, const typename Mma<T>::v8 (&q)[D / 16],
+                                             Online<D>& st, float c, int limit, bool masked)
+{
+    const int hi = lane_id() >> 5;
+    acc16 s[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        s[t] = zero16();
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) s[t] = Mma<T>::mma(read_rows<T, D>(kt, t * 32, k), q[k], s[t]);
+    }
+    if (masked) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[t][i] = t * 32 + c_row(i, hi) < limit ? s[t][i] : -INFINITY;
+    }
+    float mx = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[t][i]);
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    const float m = fmaxf(st.m, mx * c);
+    const float ms = m == -INFINITY ? 0.f : m;  // nothing seen so far: every p is 0
+    if (__any(m > st.m)) {
+        const float f = exp2_fast(st.m - ms);
+        st.l *= f;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) st.o[i][j] *= f;
+    }
+    st.m = m;
+    typename Mma<T>::v8 p[4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            s[t][i] = exp2_fast(fmaf(s[t][i], c, -ms));
+            st.l += s[t][i];
+        }
+        p[2 * t] = as_operand<T>(s[t], 0);
+        p[2 * t + 1] = as_operand<T>(s[t], 1);
+    }
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) st.o[i] = Mma<T>::mma(read_cols<T, D>(vt, k * 16, i * 32), p[k], st.o[i]);
+}
+
+// Many queries: a workgroup per (batch, head, group), four waves of 32
+// queries, the listed blocks one after the other through two LDS stages.
+template <typename T, int D>
+__global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_fwd(View<const T> q, View<const T> k, View<const T> v,
+                                                             const int32_t* __restrict__ lists,
+                                                             const int32_t* __restrict__ kv_len, View<T> out,
+                                                             float* __restrict__ lse, const AttnArgs a)
+{
+    __shared__ alignas(16) T s_tile[2][2][Tile<D>::ELEMS];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), hi = lane >> 5;
+    const int64_t id = xcd_contiguous(blockIdx.x, gridDim.x);
+    const int64_t bh = id / a.groups, g = id - bh * a.groups;
+    const int64_t b = bh / a.heads_q, h = bh - b * a.heads_q, hk = h / (a.heads_q / a.heads_k);
+    const int32_t* list = lists + id * a.top;
+    const int64_t len = seq_len(kv_len, b, a.tokens_k);
+    const int64_t i0 = g * QG, i = i0 + wave * 32 + (lane & 31);
+    // keys the lane's query and the group's last and first query see
+    const int64_t past = len - a.tokens_q;
+    const int64_t end = i0 + QG < a.tokens_q ? i0 + QG : a.tokens_q;
+    const int64_t mine = a.causal && past + i + 1 < len ? past + i + 1 : len;
+    const int64_t most = a.causal && past + end < len ? past + end : len;
+    const int64_t least = a.causal && past + i0 + 1 < len ? past + i0 + 1 : len;
+    const int64_t visible = most > 0 ? (most + KB - 1) / KB : 0;
+    const float c = a.scale * LOG2E;
+
+    typename Mma<T>::v8 qf[D / 16];
+    load_cols<T, D>(q.at(b, i < a.tokens_q ? i : a.tokens_q - 1, h), qf);
+    Online<D> st;
+    st.init();
+    const T* kb = k.at(b, 0, hk);
+    const T* vb = v.at(b, 0, hk);
+    int j = 0;
+    while (j < a.top && !entry_ok(list, j, visible)) ++j;
+    if (j < a.top) {
+        load_tile<T, D, 4>(s_tile[0][0], kb, k.st, (int64_t)list[j] * KB, len - 1, wave);
+        load_tile<T, D, 4>(s_tile[0][1], vb, v.st, (int64_t)list[j] * KB, len - 1, wave);
+    }
+    for (int stage = 0; j < a.top; stage ^= 1) {
+        int next = j + 1;
+        while (next < a.top && !entry_ok(list, next, visible)) ++next;
+        wait_loads();
+        __syncthreads();  // the stage is whole, and the other one is read out
+        if (next < a.top) {
+            load_tile<T, D, 4>(s_tile[stage ^ 1][0], kb, k.st, (int64_t)list[next] * KB, len - 1, wave);
+            load_tile<T, D, 4>(s_tile[stage ^ 1][1], vb, v.st, (int64_t)list[next] * KB, len - 1, wave);
+        }
+        const int64_t k0 = (int64_t)list[j] * KB, rest = mine - k0;
+        const int limit = (int)(rest < 0 ? 0 : (rest < KB ? rest : KB));
+        attend_block<T, D>(s_tile[stage][0], s_tile[stage][1], qf, st, c, limit, k0 + KB > least);
+        j = next;
+    }
+    if (i >= a.tokens_q) return;
+    const float l = st.l + __shfl_xor(st.l, 32);
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    T* o = out.at(b, i, h);
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            store4<T>(o + t * 32 + r * 8 + hi * 4, st.o[t][4 * r] * inv, st.o[t][4 * r + 1] * inv,
+                      st.o[t][4 * r + 2] * inv, st.o[t][4 * r + 3] * inv);
+    if (hi == 0) lse[bh * a.tokens_q + i] = l > 0.f ? (st.m + log2f(l)) * LN2 : -INFINITY;
+}
+
+// Few queries: a workgroup per 32 queries and split of their list; its four
+// waves take the split's entries in turn, each with its own tiles, and join
+// at the end (the softmax states of disjoint key sets add after rescaling to
+// the common maximum). With more than one split the joined states go to the
+// workspace and k_attn_join ends the work.
+template <typename T, int D>
+__global__ __launch_bounds__(ATT_THREADS, 1) void k_attn_few(View<const T> q, View<const T> k, View<const T> v,
+                                                             const int32_t* __restrict__ lists,
+                                                             const int32_t* __restrict__ kv_len, View<T> out,
+                                                             float* __restrict__ lse, float* __restrict__ part,
+                                                             const AttnArgs a)
+{
+    __shared__ alignas(16) T s_tile[4][2][Tile<D>::ELEMS];
+    __shared__ float s_m[4][32], s_l[4][32];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), hi = lane >> 5;
+    const int64_t tiles = (a.tokens_q + 31) / 32;
+    const int64_t unit = blockIdx.x / a.splits;
+    const int split = (int)(blockIdx.x - unit * a.splits);
+    const int64_t bh = unit / tiles, tile = unit - bh * tiles;
+    const int64_t b = bh / a.heads_q, h = bh - b * a.heads_q, hk = h / (a.heads_q / a.heads_k);
+    const int64_t i0 = tile * 32, i = i0 + (lane & 31);
+    const int32_t* list = lists + (bh * a.groups + i0 / QG) * a.top;
+    const int64_t len = seq_len(kv_len, b, a.tokens_k), past = len - a.tokens_q;
+    const int64_t end = i0 + 32 < a.tokens_q ? i0 + 32 : a.tokens_q;
+    const int64_t mine = a.causal && past + i + 1 < len ? past + i + 1 : len;
+    const int64_t most = a.causal && past + end < len ? past + end : len;
+    const int64_t least = a.causal && past + i0 + 1 < len ? past + i0 + 1 : len;
+    const int64_t visible = most > 0 ? (most + KB - 1) / KB : 0;
+    const float c = a.scale * LOG2E;
+
+    typename Mma<T>::v8 qf[D / 16];
+    load_cols<T, D>(q.at(b, i < a.tokens_q ? i : a.tokens_q - 1, h), qf);
+    Online<D> st;
+    st.init();
+    const T* kb = k.at(b, 0, hk);
+    const T* vb = v.at(b, 0, hk);
+    for (int j = split * 4 + wave; j < a.top; j += 4 * a.splits) {
+        if (!entry_ok(list, j, visible)) continue;
+        const int64_t k0 = (int64_t)list[j] * KB, rest = mine - k0;
+        // the wave's own reads of the tile's last contents are done: their
+        // results were used
+        load_tile<T, D, 1>(s_tile[wave][0], kb, k.st, k0, len - 1, 0);
+        load_tile<T, D, 1>(s_tile[wave][1], vb, v.st, k0, len - 1, 0);
+        wait_loads();
+        const int limit = (int)(rest < 0 ? 0 : (rest < KB ? rest : KB));
+        attend_block<T, D>(s_tile[wave][0], s_tile[wave][1], qf, st, c, limit, k0 + KB > least);
+    }
+    const float l = st.l + __shfl_xor(st.l, 32);
+    if (hi == 0) s_m[wave][lane] = st.m, s_l[wave][lane] = l;
+    __syncthreads();  // also: every wave is done with its tiles
+    // the waves' outputs side by side in the tiles' memory: [wave][D][32]
+    float* s_o = (float*)&s_tile[0][0][0];
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s_o[(wave * D + t * 32 + c_row(r, hi)) * 32 + (lane & 31)] = st.o[t][r];
+    __syncthreads();
+    const int col = threadIdx.x & 31;
+    float m = -INFINITY, f[4], total = 0.f;
+    for (int w = 0; w < 4; ++w) m = fmaxf(m, s_m[w][col]);
+    for (int w = 0; w < 4; ++w) {
+        f[w] = m == -INFINITY ? 0.f : exp2_fast(s_m[w][col] - m);
+        total += f[w] * s_l[w][col];
+    }
+    const int64_t at = i0 + col;
+    if (at >= a.tokens_q) return;
+    const float inv = total > 0.f ? 1.f / total : 0.f;
+    constexpr int PER = D / 8;  // dimensions of one thread
+    const int d0 = (threadIdx.x >> 5) * PER;
+    float x[PER];
+#pragma unroll
+    for (int d = 0; d < PER; ++d) {
+        x[d] = 0.f;
+        for (int w = 0; w < 4; ++w) x[d] += f[w] * s_o[(w * D + d0 + d) * 32 + col];
+    }
+    if (a.splits == 1) {
+        T* o = out.at(b, at, h) + d0;
+#pragma unroll
+        for (int d = 0; d < PER; d += 4) store4<T>(o + d, x[d] * inv, x[d + 1] * inv, x[d + 2] * inv, x[d + 3] * inv);
+        if (d0 == 0) lse[bh * a.tokens_q + at] = total > 0.f ? (m + log2f(total)) * LN2 : -INFINITY;
+    } else {
+        float* p = part + ((bh * a.tokens_q + at) * a.splits + split) * (D + 4);
+#pragma unroll
+        for (int d = 0; d < PER; d += 4) *(float4*)(p + 4 + d0 + d) = make_float4(x[d], x[d + 1], x[d + 2], x[d + 3]);
+        if (d0 == 0) p[0] = m, p[1] = total;
+    }
+}
+
+// Joins the splits of one query: D / 4 threads a query.
+template <typename T, int D>
+__global__ __launch_bounds__(ATT_THREADS) void k_attn_join(const float* __restrict__ part, int64_t queries, View<T> out,
+                                                           float* __restrict__ lse, const AttnArgs a)
+{
+    constexpr int TH = D / 4;
+    const int64_t row = (int64_t)blockIdx.x * (ATT_THREADS / TH) + threadIdx.x / TH;
+    if (row >= queries) return;
+    const int d0 = threadIdx.x % TH * 4;
+    const float* p = part + row * a.splits * (D + 4);
+    float m = -INFINITY, total = 0.f;
+    for (int s = 0; s < a.splits; ++s) m = fmaxf(m, p[s * (D + 4)]);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < a.splits; ++s) {
+        const float* ps = p + s * (D + 4);
+        const float f = m == -INFINITY ? 0.f : exp2_fast(ps[0] - m);
+        const float4 y = *(const float4*)(ps + 4 + d0);
+        total += f * ps[1];
+        x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
+    }
+    const float inv = total > 0.f ? 1.f / total : 0.f;
+    const int64_t bh = row / a.tokens_q, i = row - bh * a.tokens_q, b = bh / a.heads_q, h = bh - b * a.heads_q;
+    store4<T>(out.at(b, i, h) + d0, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    if (d0 == 0) lse[row] = total > 0.f ? (m + log2f(total)) * LN2 : -INFINITY;
+}
+
+gs_status attn_check(int64_t batch, int64_t tokens_q, int64_t tokens_k, int32_t heads_q, int32_t heads_k, int32_t dim,
+                     int32_t dtype, int32_t top, float sm_scale)
+{
+    const int64_t most = (int64_t)1 << 40;
+    if (batch < 0 || tokens_q < 0 || tokens_k < 0 || tokens_q > most || tokens_k > ((int64_t)1 << 36) || heads_q < 1 ||
+        heads_k < 1 || heads_q % heads_k != 0 || dim < 1 || !dtype_ok(dtype) || top < 1 || !(sm_scale > 0.f) ||
+        !(sm_scale < INFINITY))
+        return GS_ERR_INVALID_ARGUMENT;
+    if ((dim != 64 && dim != 128) || dtype == GS_F32) return GS_ERR_UNSUPPORTED;
+    // one workgroup of 256 threads per unit of 32 queries (or 64 keys): below 2^32 threads in all
+    const int64_t units = (int64_t)1 << 23;
+    const int64_t per = std::max((tokens_q + 31) / 32, (tokens_k + KB - 1) / KB);
+    if (batch > units || (batch > 0 && heads_q > units / batch) ||
+        (batch > 0 && per > units / (batch * heads_q)))
+        return GS_ERR_UNSUPPORTED;
+    return GS_OK;
+}
+
+// The split of few queries: while a group's workgroups do not fill the CUs.
+struct Plan {
+    bool few;
+    int splits;
+};
+
+static Plan attn_plan(int64_t batch, int64_t tokens_q, int32_t heads_q, int32_t top)
+{
+    const int64_t groups = (tokens_q + QG - 1) / QG, tiles = (tokens_q + 31) / 32, bh = batch * heads_q;
+    Plan p{};
+    p.few = bh * groups < 512;
+    p.splits = 1;
+    if (p.few) {
+        const int64_t want = (256 + bh * tiles - 1) / (bh * tiles), most = (top + 3) / 4;
+        p.splits = (int)std::max<int64_t>(1, std::min(want, most));
+    }
+    return p;
+}
+
+template <typename T, int D>
+static gs_status attn_fwd_launch(const gs_tokens* q, const gs_tokens* k, const gs_tokens* v, const int32_t* list,
+                                 const int32_t* kv_len, const gs_tokens* out, float* lse, float* part, int64_t batch,
+                                 AttnArgs a, const Plan& plan, hipStream_t s)
+{
+    const int64_t bh = batch * a.heads_q;
+    if (!plan.few) {
+        hipLaunchKernelGGL((k_attn_fwd<T, D>), dim3((unsigned)(bh * a.groups)), dim3(ATT_THREADS), 0, s,
+                           view_of<const T>(q), view_of<const T>(k), view_of<const T>(v), list, kv_len, view_of<T>(out),
+                           lse, a);
+        GS_CHECK_LAUNCH();
+        return GS_OK;
+    }
+    const int64_t tiles = (a.tokens_q + 31) / 32;
+    hipLaunchKernelGGL((k_attn_few<T, D>), dim3((unsigned)(bh * tiles * a.splits)), dim3(ATT_THREADS), 0, s,
+                       view_of<const T>(q), view_of<const T>(k), view_of<const T>(v), list, kv_len, view_of<T>(out), lse,
+                       part, a);
+    GS_CHECK_LAUNCH();
+    if (a.splits > 1) {
+        hipLaunchKernelGGL((k_attn_join<T, D>), dim3(grid_for((uint64_t)(bh * a.tokens_q), ATT_THREADS / (D / 4))),
+                           dim3(ATT_THREADS), 0, s, part, bh * a.tokens_q, view_of<T>(out), lse, a);
+        GS_CHECK_LAUNCH();
+    }
+    return GS_OK;
+}
+
+}  // namespace gs
+
+extern "C" {
+
+size_t gs_block_attn_fwd_workspace_bytes(int64_t batch, int64_t tokens_q, int32_t heads_q, int32_t dim, int32_t top)
+{
+    using namespace gs;
+    if (attn_check(batch, tokens_q, 0, heads_q, 1, dim, GS_BF16, top, 1.f) != GS_OK) return 0;
+    if (batch == 0 || tokens_q == 0) return 0;
+    const Plan p = attn_plan(batch, tokens_q, heads_q, top);
+    return p.splits > 1 ? (size_t)(batch * heads_q * tokens_q) * p.splits * (dim + 4) * 4 : 0;
+}
+
+gs_status gs_block_attn_fwd(const gs_tokens* q, const gs_tokens* k, const gs_tokens* v, const int32_t* list,
+                            int64_t batch, int64_t tokens_q, int64_t tokens_k, int32_t heads_q, int32_t heads_k,
+                            int32_t dim, int32_t dtype, const int32_t* kv_len, int32_t causal, int32_t top,
+                            float sm_scale, const gs_tokens* out, float* lse, void* ws, size_t ws_bytes, void* stream)
+{
+    using namespace gs;
+    if (!q || !k || !v || !out) return GS_ERR_INVALID_ARGUMENT;
+    const gs_status st = attn_check(batch, tokens_q, tokens_k, heads_q, heads_k, dim, dtype, top, sm_scale);
+    if (st != GS_OK) return st;
+    if (batch == 0 || tokens_q == 0) return GS_OK;
+    if (!q->data || !out->data || !lse || !list || (tokens_k > 0 && (!k->data || !v->data)))
+        return GS_ERR_INVALID_ARGUMENT;
+    if (!attn_view_ok(q, batch, tokens_q, heads_q) || !attn_view_ok(out, batch, tokens_q, heads_q) ||
+        (tokens_k > 0 && (!attn_view_ok(k, batch, tokens_k, heads_k) || !attn_view_ok(v, batch, tokens_k, heads_k))))
+        return GS_ERR_UNSUPPORTED;
+    const size_t need = gs_block_attn_fwd_workspace_bytes(batch, tokens_q, heads_q, dim, top);
+    if (need > 0 && (!ws || ((uintptr_t)ws & 15) || ws_bytes < need)) return GS_ERR_INVALID_ARGUMENT;
+    const Plan plan = attn_plan(batch, tokens_q, heads_q, top);
+    const AttnArgs a{tokens_q, tokens_k, (tokens_q + QG - 1) / QG, (tokens_k + KB - 1) / KB, heads_q, heads_k,
+                     causal != 0, top, plan.splits, sm_scale};
+    const hipStream_t s = (hipStream_t)stream;
+    if (dtype == GS_BF16)
+        return dim == 128 ? attn_fwd_launch<bf16, 128>(q, k, v, list, kv_len, out, lse, (float*)ws, batch, a, plan, s)
+                          : attn_fwd_launch<bf16, 64>(q, k, v, list, kv_len, out, lse, (float*)ws, batch, a, plan, s);
+    return dim == 128 ? attn_fwd_launch<f16, 128>(q, k, v, list, kv_len, out, lse, (float*)ws, batch, a, plan, s)
+                      : attn_fwd_launch<f16, 64>(q, k, v, list, kv_len, out, lse, (float*)ws, batch, a, plan, s);
+}
+
+}  // extern "C"

@@ -1,0 +1,396 @@
+// gs_block_attn_bwd: gradients of the attention over listed key blocks.
+//
+// Two passes without atomics, so the bits repeat: one over the query groups
+// (gq, and D = sum gout out), one over the key blocks (gk, gv), which walks
+// the groups that list its block. Those come from a bit matrix
+// [batch][head][block][groups / 32], set from the lists (an OR: any order).
+// Both passes form S and P again from lse: 7 products in all where the
+// formula's 5 would need fp32 atomics on gq.
+#include "block_attn.h"
+
+namespace gs {
+
+__global__ __launch_bounds__(ATT_THREADS) void k_zero_words(uint32_t* __restrict__ p, int64_t n)
+{
+    for (int64_t i = (int64_t)blockIdx.x * ATT_THREADS + threadIdx.x; i < n; i += (int64_t)gridDim.x * ATT_THREADS) p[i] = 0;
+}
+
+__device__ __forceinline__ void set_bit(const int32_t* __restrict__ lists, const int32_t* __restrict__ kv_len,
+                                        uint32_t* __restrict__ bits, int64_t e, const AttnArgs& a)
+{
+    const int64_t id = e / a.top, bh = id / a.groups, g = id - bh * a.groups;
+    const int64_t len = seq_len(kv_len, bh / a.heads_q, a.tokens_k), past = len - a.tokens_q;
+    const int64_t end = g * QG + QG < a.tokens_q ? g * QG + QG : a.tokens_q;
+    const int64_t most = a.causal && past + end < len ? past + end : len;
+    const int64_t visible = most > 0 ? (most + KB - 1) / KB : 0;
+    const int j = (int)(e - id * a.top);
+    if (!entry_ok(lists + id * a.top, j, visible)) return;
+    const int64_t words = (a.groups + 31) / 32;
+    atomicOr(&bits[(bh * a.blocks + lists[e]) * words + g / 32], 1u << (g & 31));
+}
+
+// A thread per list entry.
+__global__ __launch_bounds__(ATT_THREADS) void k_list_bits(const int32_t* __restrict__ lists,
+                                                           const int32_t* __restrict__ kv_len,
+                                                           uint32_t* __restrict__ bits, int64_t entries,
+                                                           const AttnArgs a)
+{
+    for (int64_t e = (int64_t)blockIdx.x * ATT_THREADS + threadIdx.x; e < entries; e += (int64_t)gridDim.x * ATT_THREADS)
+        set_bit(lists, kv_len, bits, e, a);
+}
+
+// gq of a group: four waves of 32 queries, the listed blocks in turn.
+//   dS^T = P^T (V gout^T - D),  gq^T += K^T dS^T
+template <typename T, int D>
+__global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_gq(View<const T> go, View<const T> q, View<const T> k,
+                                                            View<const T> v, View<const T> out,
+                                                            const float* __restrict__ lse,
+                                                            const int32_t* __restrict__ lists,
+                                                            const int32_t* __restrict__ kv_len, View<T> gq,
+                                                            float* __restrict__ delta, const AttnArgs a)
+{
+    __shared__ alignas(16) T s_tile[2][2][Tile<D>::ELEMS];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), hi = lane >> 5;
+    const int64_t id = xcd_contiguous(blockIdx.x, gridDim.x);
+    const int64_t bh = id / a.groups, g = id - bh * a.groups;
+    const int64_t b = bh / a.heads_q, h = bh - b * a.heads_q, hk = h / (a.heads_q / a.heads_k);
+    const int32_t* list = lists + id * a.top;
+    const int64_t len = seq_len(kv_len, b, a.tokens_k);
+    const int64_t i0 = g * QG, i = i0 + wave * 32 + (lane & 31), ic = i < a.tokens_q ? i : a.tokens_q - 1;
+    const int64_t past = len - a.tokens_q;
+    const int64_t end = i0 + QG < a.tokens_q ? i0 + QG : a.tokens_q;
+    const int64_t mine = a.causal && past + i + 1 < len ? past + i + 1 : len;
+    const int64_t most = a.causal && past + end < len ? past + end : len;
+    const int64_t least = a.causal && past + i0 + 1 < len ? past + i0 + 1 : len;
+    const int64_t visible = most > 0 ? (most + KB - 1) / KB : 0;
+    const float c = a.scale * LOG2E;
+    const T* kb = k.at(b, 0, hk);
+    const T* vb = v.at(b, 0, hk);
+    int j = 0;
+    while (j < a.top && !entry_ok(list, j, visible)) ++j;
+    if (j < a.top) {
+        load_tile<T, D, 4>(s_tile[0][0], kb, k.st, (int64_t)list[j] * KB, len - 1, wave);
+        load_tile<T, D, 4>(s_tile[0][1], vb, v.st, (int64_t)list[j] * KB, len - 1, wave);
+    }
+    typename Mma<T>::v8 qf[D / 16], gf[D / 16];
+    load_cols<T, D>(q.at(b, ic, h), qf);
+    load_cols<T, D>(go.at(b, ic, h), gf);
+    float dl = 0.f;
+    {
+        typename Mma<T>::v8 of[D / 16];
+        load_cols<T, D>(out.at(b, ic, h), of);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dl = fmaf((float)gf[s][e], (float)of[s][e], dl);
+        dl += __shfl_xor(dl, 32);
+    }
+    if (i < a.tokens_q && hi == 0) delta[bh * a.tokens_q + i] = dl;
+    // a query that saw nothing has lse = -inf: P = exp2(S - inf) = 0
+    const float ls = lse[bh * a.tokens_q + ic], nl = ls == -INFINITY ? -INFINITY : -ls * LOG2E;
+    acc16 acc[D / 32];
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t) acc[t] = zero16();
+    for (int stage = 0; j < a.top; stage ^= 1) {
+        int next = j + 1;
+        while (next < a.top && !entry_ok(list, next, visible)) ++next;
+        wait_loads();
+        __syncthreads();
+        if (next < a.top) {
+            load_tile<T, D, 4>(s_tile[stage ^ 1][0], kb, k.st, (int64_t)list[next] * KB, len - 1, wave);
+            load_tile<T, D, 4>(s_tile[stage ^ 1][1], vb, v.st, (int64_t)list[next] * KB, len - 1, wave);
+        }
+        const T *kt = s_tile[stage][0], *vt = s_tile[stage][1];
+        const int64_t k0 = (int64_t)list[j] * KB, rest = mine - k0;
+        const int limit = (int)(rest < 0 ? 0 : (rest < KB ? rest : KB));
+        const bool masked = k0 + KB > least;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            acc16 s = zero16(), p = zero16();
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) s = Mma<T>::mma(read_rows<T, D>(kt, t * 32, x), qf[x], s);
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) p = Mma<T>::mma(read_rows<T, D>(vt, t * 32, x), gf[x], p);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[r] = exp2_fast(fmaf(s[r], c, nl));
+            if (masked) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[r] = t * 32 + c_row(r, hi) < limit ? s[r] : 0.f;
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[r] *= p[r] - dl;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const typename Mma<T>::v8 ds = as_operand<T>(s, x);
+#pragma unroll
+                for (int y = 0; y < D / 32; ++y)
+                    acc[y] = Mma<T>::mma(read_cols<T, D>(kt, t * 32 + x * 16, y * 32), ds, acc[y]);
+            }
+        }
+        j = next;
+    }
+    if (i >= a.tokens_q) return;
+    T* o = gq.at(b, i, h);
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            store4<T>(o + t * 32 + r * 8 + hi * 4, acc[t][4 * r] * a.scale, acc[t][4 * r + 1] * a.scale,
+                      acc[t][4 * r + 2] * a.scale, acc[t][4 * r + 3] * a.scale);
+}
+
+// Walks the (head of the key head, half group of 64 queries) pairs that list
+// a block; every thread steps the same way.
+struct Walk {
+    const uint32_t* bits;  // of the first head, this block
+    int64_t head_stride, words, tokens_q;
+    int heads;
+    // state
+    int h;
+    int64_t word, q0;
+    uint32_t left;
+    int half;
+    __device__ __forceinline__ void start()
+    {
+        h = words > 0 ? 0 : heads;
+        word = -1;
+        left = 0;
+        half = 1;
+        q0 = 0;
+    }
+    __device__ __forceinline__ bool next()
+    {
+        if (half == 0 && (q0 + 64) < tokens_q) {
+            half = 1;
+            q0 += 64;
+            return true;
+        }
+        if (h >= heads) return false;
+        while (left == 0) {
+            if (++word == words) {
+                word = 0;
+                if (++h == heads) return false;
+            }
+            left = __builtin_amdgcn_readfirstlane(bits[h * head_stride + word]);
+        }
+        const int bit = __builtin_ctz(left);
+        left &= left - 1;
+        q0 = (word * 32 + bit) * QG;
+        half = 0;
+        return true;
+    }
+};
+
+// gk and gv of a block of 64 keys. Wave w: keys 32 (w & 1) .. + 32 of it, and
+// of every 64 queries 32 (w >> 1) .. + 32; the two query halves join at the
+// end. S and dP are formed with queries as rows, so that a lane holds one key:
+//   gv^T += gout^T P,  gk^T += q^T dS
+template <typename T, int D>
+__global__ __launch_bounds__(ATT_THREADS, 1) void k_attn_gkv(View<const T> go, View<const T> q, View<const T> k,
+                                                             View<const T> v, const float* __restrict__ lse,
+                                                             const float* __restrict__ delta,
+                                                             const uint32_t* __restrict__ bits,
+                                                             const int32_t* __restrict__ kv_len, View<T> gk, View<T> gv,
+                                                             const AttnArgs a)
+{
+    __shared__ alignas(16) T s_tile[2][2][Tile<D>::ELEMS];
+    __shared__ float s_row[2][2][64];  // per query: -lse in base 2, D
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), hi = lane >> 5;
+    const int kh = wave & 1, qh = wave >> 1;
+    const int64_t id = xcd_contiguous(blockIdx.x, gridDim.x);
+    const int64_t bh = id / a.blocks, blk = id - bh * a.blocks;
+    const int64_t b = bh / a.heads_k, hk = bh - b * a.heads_k;
+    const int per = a.heads_q / a.heads_k;
+    const int64_t len = seq_len(kv_len, b, a.tokens_k), past = len - a.tokens_q;
+    const int64_t key = blk * KB + kh * 32 + (lane & 31);
+    // keys past the end hold anything: take a valid one, its P is masked
+    const int64_t last = len > 0 ? len - 1 : 0, kc = key < last ? key : last;
+    const float c = a.scale * LOG2E;
+    typename Mma<T>::v8 kf[D / 16], vf[D / 16];
+    load_cols<T, D>(k.at(b, kc, hk), kf);
+    load_cols<T, D>(v.at(b, kc, hk), vf);
+    acc16 ak[D / 32], av[D / 32];
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t) ak[t] = zero16(), av[t] = zero16();
+
+    Walk w;
+    w.words = (a.groups + 31) / 32;
+    w.head_stride = a.blocks * w.words;
+    w.bits = bits + ((b * a.heads_q + hk * per) * a.blocks + blk) * w.words;
+    w.tokens_q = a.tokens_q;
+    w.heads = per;
+    w.start();
+    auto load = [&](int stage) {
+        const int64_t h = hk * per + w.h;
+        load_tile<T, D, 4>(s_tile[stage][0], q.at(b, 0, h), q.st, w.q0, a.tokens_q - 1, wave);
+        load_tile<T, D, 4>(s_tile[stage][1], go.at(b, 0, h), go.st, w.q0, a.tokens_q - 1, wave);
+        if (threadIdx.x < 64) {
+            const int64_t i = w.q0 + threadIdx.x;
+            const bool on = i < a.tokens_q;
+            const int64_t at = (b * a.heads_q + h) * a.tokens_q + (on ? i : a.tokens_q - 1);
+            const float ls = lse[at], dl = delta[at];
+            // queries past the end and queries that saw nothing: P = 0
+            s_row[stage][0][threadIdx.x] = on && ls > -INFINITY ? -ls * LOG2E : -INFINITY;
+            s_row[stage][1][threadIdx.x] = dl;
+        }
+    };
+    bool more = w.next();
+    int64_t q0 = w.q0;
+    if (more) load(0);
+    for (int stage = 0; more; stage ^= 1) {
+        wait_loads();
+        __syncthreads();
+        const int64_t now = q0;
+        more = w.next();
+        q0 = w.q0;
+        if (more) load(stage ^ 1);
+        const T *qt = s_tile[stage][0], *gt = s_tile[stage][1];
+        acc16 s = zero16(), p = zero16();
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) s = Mma<T>::mma(read_rows<T, D>(qt, qh * 32, x), kf[x], s);
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) p = Mma<T>::mma(read_rows<T, D>(gt, qh * 32, x), vf[x], p);
+        const bool masked = (int64_t)(blk + 1) * KB > (a.causal && past + now + 1 < len ? past + now + 1 : len);
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+            const int row = qh * 32 + 8 * r4 + 4 * hi;
+            const float4v nl = *(const float4v*)&s_row[stage][0][row], dl = *(const float4v*)&s_row[stage][1][row];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = 4 * r4 + e;
+                float x = exp2_fast(fmaf(s[r], c, nl[e]));
+                if (masked) {
+                    const int64_t sees = a.causal && past + now + row + e + 1 < len ? past + now + row + e + 1 : len;
+                    x = key < sees ? x : 0.f;
+                }
+                s[r] = x;
+                p[r] = x * (p[r] - dl[e]);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const typename Mma<T>::v8 pp = as_operand<T>(s, x), ds = as_operand<T>(p, x);
+#pragma unroll
+            for (int y = 0; y < D / 32; ++y) {
+                av[y] = Mma<T>::mma(read_cols<T, D>(gt, qh * 32 + x * 16, y * 32), pp, av[y]);
+                ak[y] = Mma<T>::mma(read_cols<T, D>(qt, qh * 32 + x * 16, y * 32), ds, ak[y]);
+            }
+        }
+    }
+    // join the query halves: the second one's sums through LDS
+    __syncthreads();
+    float* s_acc = (float*)&s_tile[0][0][0];  // [2 key halves][D / 32 x 16][64 lanes], gk then gv
+    constexpr int REGS = D / 32 * 16;
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+        acc16(&acc)[D / 32] = pass == 0 ? ak : av;
+        if (qh == 1) {
+#pragma unroll
+            for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s_acc[(kh * REGS + t * 16 + r) * 64 + lane] = acc[t][r];
+        }
+        __syncthreads();
+        if (qh == 0 && key < a.tokens_k) {
+            const float f = pass == 0 ? a.scale : 1.f;
+            T* o = pass == 0 ? gk.at(b, key, hk) : gv.at(b, key, hk);
+#pragma unroll
+            for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float x[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[e] = (acc[t][4 * r + e] + s_acc[(kh * REGS + t * 16 + 4 * r + e) * 64 + lane]) * f;
+                    store4<T>(o + t * 32 + r * 8 + hi * 4, x[0], x[1], x[2], x[3]);
+                }
+        }
+        __syncthreads();
+    }
+}
+
+template <typename T, int D>
+static gs_status attn_bwd_launch(const gs_tokens* go, const gs_tokens* q, const gs_tokens* k, const gs_tokens* v,
+                                 const gs_tokens* out, const float* lse, const int32_t* list, const int32_t* kv_len,
+                                 const gs_tokens* gq, const gs_tokens* gk, const gs_tokens* gv, float* delta,
+                                 uint32_t* bits, int64_t batch, const AttnArgs& a, hipStream_t s)
+{
+    const int64_t lists = batch * a.heads_q * a.groups, blocks = batch * a.heads_k * a.blocks;
+    const int64_t words = batch * a.heads_q * a.blocks * ((a.groups + 31) / 32);
+    if (lists > 0) {
+        hipLaunchKernelGGL((k_attn_gq<T, D>), dim3((unsigned)lists), dim3(ATT_THREADS), 0, s, view_of<const T>(go),
+                           view_of<const T>(q), view_of<const T>(k), view_of<const T>(v), view_of<const T>(out), lse, list,
+                           kv_len, view_of<T>(gq), delta, a);
+        GS_CHECK_LAUNCH();
+    }
+    if (blocks > 0) {
+        if (words > 0) {
+            hipLaunchKernelGGL(k_zero_words, dim3(std::min(grid_for((uint64_t)words, ATT_THREADS), 65536u)), dim3(ATT_THREADS), 0, s, bits,
+                               words);
+            GS_CHECK_LAUNCH();
+            hipLaunchKernelGGL(k_list_bits, dim3((unsigned)std::min<int64_t>((lists * a.top + ATT_THREADS - 1) / ATT_THREADS, 65536)), dim3(ATT_THREADS), 0, s,
+                               list, kv_len, bits, lists * a.top, a);
+            GS_CHECK_LAUNCH();
+        }
+        hipLaunchKernelGGL((k_attn_gkv<T, D>), dim3((unsigned)blocks), dim3(ATT_THREADS), 0, s, view_of<const T>(go),
+                           view_of<const T>(q), view_of<const T>(k), view_of<const T>(v), lse, delta, bits, kv_len,
+                           view_of<T>(gk), view_of<T>(gv), a);
+        GS_CHECK_LAUNCH();
+    }
+    return GS_OK;
+}
+
+static size_t delta_bytes(int64_t batch, int64_t tokens_q, int32_t heads_q)
+{
+    return (size_t)((batch * heads_q * tokens_q * 4 + 15) / 16 * 16);
+}
+
+}  // namespace gs
+
+extern "C" {
+
+size_t gs_block_attn_bwd_workspace_bytes(int64_t batch, int64_t tokens_q, int64_t tokens_k, int32_t heads_q,
+                                         int32_t heads_k, int32_t dim)
+{
+    using namespace gs;
+    if (attn_check(batch, tokens_q, tokens_k, heads_q, heads_k, dim, GS_BF16, 1, 1.f) != GS_OK) return 0;
+    const int64_t groups = (tokens_q + QG - 1) / QG, blocks = (tokens_k + KB - 1) / KB;
+    return delta_bytes(batch, tokens_q, heads_q) + (size_t)(batch * heads_q * blocks * ((groups + 31) / 32)) * 4 + 16;
+}
+
+gs_status gs_block_attn_bwd(const gs_tokens* gout, const gs_tokens* q, const gs_tokens* k, const gs_tokens* v,
+                            const gs_tokens* out, const float* lse, const int32_t* list, int64_t batch,
+                            int64_t tokens_q, int64_t tokens_k, int32_t heads_q, int32_t heads_k, int32_t dim,
+                            int32_t dtype, const int32_t* kv_len, int32_t causal, int32_t top, float sm_scale,
+                            const gs_tokens* gq, const gs_tokens* gk, const gs_tokens* gv, void* ws, size_t ws_bytes,
+                            void* stream)
+{
+    using namespace gs;
+    if (!gout || !q || !k || !v || !out || !gq || !gk || !gv) return GS_ERR_INVALID_ARGUMENT;
+    const gs_status st = attn_check(batch, tokens_q, tokens_k, heads_q, heads_k, dim, dtype, top, sm_scale);
+    if (st != GS_OK) return st;
+    const bool queries = batch > 0 && tokens_q > 0, keys = batch > 0 && tokens_k > 0;
+    if (!queries && !keys) return GS_OK;
+    const size_t need = gs_block_attn_bwd_workspace_bytes(batch, tokens_q, tokens_k, heads_q, heads_k, dim);
+    if (!ws || ((uintptr_t)ws & 15) || ws_bytes < need) return GS_ERR_INVALID_ARGUMENT;
+    if (queries && (!gout->data || !q->data || !out->data || !gq->data || !lse || !list)) return GS_ERR_INVALID_ARGUMENT;
+    if (keys && (!k->data || !v->data || !gk->data || !gv->data)) return GS_ERR_INVALID_ARGUMENT;
+    if (queries)
+        for (const gs_tokens* t : {gout, q, out, gq})
+            if (!attn_view_ok(t, batch, tokens_q, heads_q)) return GS_ERR_UNSUPPORTED;
+    if (keys)
+        for (const gs_tokens* t : {k, v, gk, gv})
+            if (!attn_view_ok(t, batch, tokens_k, heads_k)) return GS_ERR_UNSUPPORTED;
+    const AttnArgs a{tokens_q, tokens_k, (tokens_q + QG - 1) / QG, (tokens_k + KB - 1) / KB, heads_q, heads_k,
+                     causal != 0, top, 1, sm_scale};
+    float* delta = (float*)ws;
+    uint32_t* bits = (uint32_t*)((char*)ws + delta_bytes(batch, tokens_q, heads_q));
+    const hipStream_t s = (hipStream_t)stream;
+    if (dtype == GS_BF16)
+        return dim == 128 ? attn_bwd_launch<bf16, 128>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, delta, bits, batch, a, s)
+                          : attn_bwd_launch<bf16, 64>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, delta, bits, batch, a, s);
+    return dim == 128 ? attn_bwd_launch<f16, 128>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, delta, bits, batch, a, s)
+                      : attn_bwd_launch<f16, 64>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, delta, bits, batch, a, s);
+}
+
+}  // extern "C"

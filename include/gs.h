@@ -669,6 +669,213 @@ gs_status gs_raster_exp(const float* x, float* y, int64_t n, void* stream);
  */
 gs_status gs_stream_copy(void* dst, const void* src, uint64_t bytes, void* stream);
 
+/* ==========================================================================
+ * Token operators: the layers of a network that predicts Gaussians from posed
+ * views and is trained through the rasterizer above. A token stands for one
+ * GS_TILE x GS_TILE tile of a view; its features are the network's.
+ *
+ *   gs_rope_axes            rotary positions over up to three axes
+ *   gs_norm_gate_fwd/_bwd   norms after and before a block, gate, residual
+ *   gs_block_summary        8-bit means of blocks of keys
+ *   gs_block_select         the key blocks each group of queries attends to
+ *   gs_block_attn_fwd/_bwd  attention over those blocks
+ *
+ * Memory, streams and errors as for every entry point above (caller-owned
+ * device memory, enqueue only, host checks first). The formulas are written
+ * out at each call.
+ * ======================================================================== */
+
+typedef enum gs_dtype { GS_F32 = 0, GS_F16 = 1, GS_BF16 = 2 } gs_dtype;
+
+#define GS_QUERY_GROUP 128 /* consecutive queries that share one list of key blocks */
+#define GS_KEY_BLOCK 64    /* consecutive keys of one block */
+#define GS_MAX_SELECT_TOKENS 2097152 /* most keys gs_block_select ranks */
+
+/* A token tensor [batch][tokens][heads][dim] (host struct): device data and
+ * the strides of the first three dimensions in elements; dim is contiguous.
+ * So packed projections and transposed head layouts need no copy. */
+typedef struct gs_tokens {
+    void* data;
+    int64_t stride_b, stride_t, stride_h;
+} gs_tokens;
+
+/*
+ * gs_rope_axes -- rotary positions with several axes (view or time, row,
+ * column) on queries and keys in one pass. Pair j of a head's dim / 2 pairs
+ * belongs to axis a(j) (the first pairs[0] pairs to axis 0, the next pairs[1]
+ * to axis 1, then pairs[2] to axis 2; the rest are copied unrotated) and is
+ * turned by the angle t = pos[b][l][a(j)] * freq[j]:
+ *   (x0, x1) -> (x0 cos t - x1 sin t, x0 sin t + x1 cos t)
+ * With `inverse` the angle is -t: the inverse rotation, which is also the
+ * gradient's way back (the rotation is orthogonal). The angle's product is
+ * not rounded before the sine (its rounding error is carried).
+ *   q, k         inputs (k may be NULL); q_out, k_out outputs, which may be
+ *                the inputs themselves
+ *   heads_q/_k   heads of each (heads_k 0 without k)
+ *   dim          even, 2..512
+ *   pos          device int32 [batch or 1][tokens][3]: stride_pos_b elements
+ *                from one batch entry to the next (0: shared)
+ *   freq         device fp32 [dim / 2], radians per position
+ *   pairs        host int32[3], >= 0, sum <= dim / 2
+ *   interleaved  non-zero: pair j is elements (2j, 2j + 1); else (j, j + dim / 2)
+ * Errors: null pointers, negative sizes, odd or too large dim, bad pairs or
+ * dtype; GS_ERR_UNSUPPORTED past 2^31 work items (16 bytes of four heads each).
+ */
+gs_status gs_rope_axes(const gs_tokens* q, const gs_tokens* k, const gs_tokens* q_out, const gs_tokens* k_out,
+                       int64_t batch, int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t dim, int32_t dtype,
+                       const int32_t* pos, int64_t stride_pos_b, const float* freq, const int32_t* pairs,
+                       int32_t interleaved, int32_t inverse, void* stream);
+
+/*
+ * gs_norm_gate_fwd -- the end of one block of a network and the start of the
+ * next in one pass over [rows][channels]:
+ *   r_post = 1 / sqrt(mean f^2 + eps),  y = x + scale * gate[s] * w_post * f * r_post
+ *   r_pre  = 1 / sqrt(mean y^2 + eps),  h = y * r_pre * w_pre
+ * (root-mean-square norms of the block's output f and of the new residual
+ * stream y; gate row s = row / rows_per_gate, e.g. one gate per view.)
+ *   x      residual stream; f the block's output, or NULL (y = x: the norm
+ *          before the first block; gate, w_post and y are then not used)
+ *   gate   fp32 [ceil(rows / rows_per_gate)][channels], or NULL (ones)
+ *   w_post, w_pre  fp32 [channels], or NULL (ones)
+ *   y, h   out, the type of x (y may alias x or f, h may alias f)
+ *   stats  out fp32 [2][rows]: r_post, r_pre (for the backward pass)
+ * h comes from y before y is rounded to its type.
+ * Errors: null pointers, rows < 0, channels outside 1..16384, rows_per_gate
+ * < 1, a bad dtype, eps < 0.
+ */
+gs_status gs_norm_gate_fwd(const void* x, const void* f, const float* gate, const float* w_post, const float* w_pre,
+                           void* y, void* h, float* stats, int64_t rows, int32_t channels, int64_t rows_per_gate,
+                           float scale, float eps, int32_t dtype, void* stream);
+
+/* Workspace of gs_norm_gate_bwd (bytes); 0 on invalid sizes. */
+size_t gs_norm_gate_bwd_workspace_bytes(int64_t rows, int32_t channels, int64_t rows_per_gate);
+
+/*
+ * gs_norm_gate_bwd -- gradients of gs_norm_gate_fwd from those of y and h.
+ * With yh = y r_pre, fh = f r_post:
+ *   d1 = gh w_pre,  t = gy + r_pre (d1 - yh mean(d1 yh)),       gx = t
+ *   d2 = scale t gate w_post,  gf = r_post (d2 - fh mean(d2 fh))
+ *   A[s] = sum over the rows of gate s of scale t fh
+ *   ggate[s] = w_post A[s],  gw_post = sum_s gate[s] A[s],  gw_pre = sum gh yh
+ *   gy           gradient of y, or NULL (zero)
+ *   x, f, gate, w_post, w_pre, scale, stats   as of the forward call; y is
+ *                formed again from x and f
+ *   gx           out, the type of x; gf out (not with f NULL)
+ *   ggate, gw_post, gw_pre   out fp32, each may be NULL (not wanted)
+ * The sums over rows are taken in a fixed order: the same bits on every call.
+ * gx may alias gy or x, gf may alias f or gh.
+ *   ws  workspace of gs_norm_gate_bwd_workspace_bytes(...)
+ * Errors: as gs_norm_gate_fwd, plus a small workspace or one off 16 bytes;
+ * GS_ERR_UNSUPPORTED when gates x ceil(channels / 64) passes 2^21.
+ */
+gs_status gs_norm_gate_bwd(const void* gy, const void* gh, const void* x, const void* f, const float* gate,
+                           const float* w_post, const float* w_pre, const float* stats, void* gx, void* gf,
+                           float* ggate, float* gw_post, float* gw_pre, int64_t rows, int32_t channels,
+                           int64_t rows_per_gate, float scale, int32_t dtype, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * gs_block_summary -- an 8-bit mean of every block of GS_KEY_BLOCK keys, the
+ * cheap stand-in that gs_block_select scores. Whole-number arithmetic, so the
+ * result does not depend on any order:
+ *   fixed(x) = round_to_even(256 x) clamped to +-32768, NaN -> 0
+ *   S = sum of fixed over the block's valid keys, per dimension
+ *   e = max(0, bits(max |S|) - 7)       (bits(0) = 0)
+ *   sum8 = min(127, (S + (e ? 2^(e-1) : 0)) >> e),  scale = 2^e * fl(1 / valid keys)
+ * (a block without valid keys has zeros and scale 1).
+ *   k              keys, GS_F16, GS_BF16 or GS_F32
+ *   kv_len         device int32 [batch]: keys at or past it are not read into
+ *                  the sums; or NULL (all `tokens` are valid)
+ *   block0, blocks the blocks to write, [block0, block0 + blocks): a growing
+ *                  cache renews only its last ones (values past the end of
+ *                  `tokens` are an error)
+ *   sum8           out int8, a token tensor of ceil(tokens / 64) blocks
+ *   scale          out fp32, the same without dim (strides in elements)
+ * Errors: null pointers, bad sizes or dtype, dim not a multiple of 8 or
+ * outside 8..256; GS_ERR_UNSUPPORTED when rows of k are not 16-byte aligned.
+ */
+gs_status gs_block_summary(const gs_tokens* k, int64_t batch, int64_t tokens, int32_t heads, int32_t dim,
+                           int32_t dtype, const int32_t* kv_len, int64_t block0, int64_t blocks,
+                           const gs_tokens* sum8, const gs_tokens* scale, void* stream);
+
+/*
+ * gs_block_select -- for every group of GS_QUERY_GROUP consecutive queries of
+ * every query head (the last group may be shorter: a single new token is a
+ * group of one), the `top` key blocks that matter most by a cheap score:
+ *   score = fl(dot(q8, sum8) * scale)
+ * with q8 the group's 8-bit mean (formed as in gs_block_summary over its
+ * queries) and sum8, scale of the key head h / (heads_q / heads_k). The dot
+ * product is a whole number, so scores are exact and ties go to the lowest
+ * block.
+ *   Visible blocks: those that start before the sequence's end (kv_len, or
+ *   tokens_k) and, when `causal`, not after the group's last query (query i
+ *   stands at position kv_len - tokens_q + i). Blocks that hold positions of
+ *   the group itself come before every score when `causal`.
+ *   list  out int32 [batch][heads_q][ceil(tokens_q / 128)][top]: the chosen
+ *         blocks in ascending order, -1 after the last
+ * Errors: null pointers, bad sizes, heads_q not a multiple of heads_k, top
+ * outside 1..32768, dim not a multiple of 8 or outside 8..256, tokens_k over
+ * GS_MAX_SELECT_TOKENS; GS_ERR_UNSUPPORTED when rows of q are not 16-byte
+ * aligned or rows of sum8 not 8-byte aligned.
+ */
+gs_status gs_block_select(const gs_tokens* q, const gs_tokens* sum8, const gs_tokens* scale, int64_t batch,
+                          int64_t tokens_q, int64_t tokens_k, int32_t heads_q, int32_t heads_k, int32_t dim,
+                          int32_t dtype, const int32_t* kv_len, int32_t causal, int32_t top, int32_t* list,
+                          void* stream);
+
+/* Workspace of gs_block_attn_fwd (bytes); may be 0. */
+size_t gs_block_attn_fwd_workspace_bytes(int64_t batch, int64_t tokens_q, int32_t heads_q, int32_t dim, int32_t top);
+
+/*
+ * gs_block_attn_fwd -- softmax attention of each query over the keys of its
+ * group's listed blocks:
+ *   out = sum_j p_j v_j,  p = softmax_j(sm_scale q . k_j),
+ *   lse = log sum_j exp(sm_scale q . k_j)
+ * over keys j of the listed blocks with j < kv_len (or tokens_k) and, when
+ * `causal`, j <= kv_len - tokens_q + i for query i. A query that sees no key
+ * has out = 0 and lse = -infinity. Keys and values at or past kv_len are not
+ * used, whatever they hold.
+ *   list  int32 [batch][heads_q][ceil(tokens_q / 128)][top], ascending with
+ *         -1 after the last (gs_block_select's). An entry that does not
+ *         exceed the one before it or lies outside the visible blocks is
+ *         skipped, so no list leads out of k and v
+ *   sm_scale  > 0
+ *   q, k, v, out  GS_F16 or GS_BF16, dim 64 or 128; key head of query head h:
+ *         h / (heads_q / heads_k)
+ *   lse   out fp32 [batch][heads_q][tokens_q]
+ * Scores, softmax statistics and sums are fp32; the probabilities are rounded
+ * to the inputs' type for their product with v.
+ * Errors: null pointers, bad sizes, heads_q not a multiple of heads_k, top <
+ * 1, a small workspace; GS_ERR_UNSUPPORTED for another dtype or dim, or rows
+ * that are not 16-byte aligned.
+ */
+gs_status gs_block_attn_fwd(const gs_tokens* q, const gs_tokens* k, const gs_tokens* v, const int32_t* list,
+                            int64_t batch, int64_t tokens_q, int64_t tokens_k, int32_t heads_q, int32_t heads_k,
+                            int32_t dim, int32_t dtype, const int32_t* kv_len, int32_t causal, int32_t top,
+                            float sm_scale, const gs_tokens* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace of gs_block_attn_bwd (bytes). */
+size_t gs_block_attn_bwd_workspace_bytes(int64_t batch, int64_t tokens_q, int64_t tokens_k, int32_t heads_q,
+                                         int32_t heads_k, int32_t dim);
+
+/*
+ * gs_block_attn_bwd -- gradients of gs_block_attn_fwd (the lists are taken as
+ * given). With D = sum_d gout out per query and P = exp(sm_scale q.k - lse):
+ *   dS = P (gout . v - D),  gq = sm_scale sum_j dS k_j,
+ *   gk = sm_scale sum_i dS q_i,  gv = sum_i P gout_i
+ * summed over the query heads that share a key head. Keys that no group lists
+ * get zeros, those past kv_len too. Every element of gq, gk and gv is
+ * written; the sums have a fixed order, so the bits repeat.
+ * P and dS are rounded to the inputs' type for the products.
+ *   ws  device workspace of gs_block_attn_bwd_workspace_bytes(...)
+ * Errors: as gs_block_attn_fwd.
+ */
+gs_status gs_block_attn_bwd(const gs_tokens* gout, const gs_tokens* q, const gs_tokens* k, const gs_tokens* v,
+                            const gs_tokens* out, const float* lse, const int32_t* list, int64_t batch,
+                            int64_t tokens_q, int64_t tokens_k, int32_t heads_q, int32_t heads_k, int32_t dim,
+                            int32_t dtype, const int32_t* kv_len, int32_t causal, int32_t top, float sm_scale,
+                            const gs_tokens* gq, const gs_tokens* gk, const gs_tokens* gv, void* ws, size_t ws_bytes,
+                            void* stream);
+
 #ifdef __cplusplus
 }
 #endif
