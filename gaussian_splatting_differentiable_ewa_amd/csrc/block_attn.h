@@ -166,7 +166,7 @@ __device__ __forceinline__ int64_t seq_len(const int32_t* kv_len, int64_t b, int
 __device__ __forceinline__ bool entry_ok(const int32_t* list, int j, int64_t visible)
 {
     const int id = list[j], before = j > 0 ? list[j - 1] : -1;
-    return id > before && id < visible;
+    return id >= 0 && id > before && id < visible;
 }
 
 // 4 consecutive elements, 8 bytes.

@@ -451,11 +451,11 @@ gs_status gs_norm_gate_bwd(const void* gy, const void* gh, const void* x, const 
     a.part_w = (float*)ws;
     a.part_a = a.part_w + (runs * channels + 3) / 4 * 4;
     float* a_of_gate = a.part_a + ((runs + gates) * channels + 3) / 4 * 4;
-    if (rows > 0 && norm_dispatch(a, dtype, true, s) != hipSuccess) return GS_ERR_HIP;
     const unsigned columns = grid_for((uint64_t)channels, 64);
     // with f absent only gw_pre is summed (gates taken as 0)
     const int64_t g = f ? gates : 0;
     if ((g + 1) * columns > ((int64_t)1 << 21)) return GS_ERR_UNSUPPORTED;  // 1024 threads each, below 2^32 in all
+    if (rows > 0 && norm_dispatch(a, dtype, true, s) != hipSuccess) return GS_ERR_HIP;
     hipLaunchKernelGGL(k_norm_sums, dim3((unsigned)(columns * (g + 1))), dim3(64 * SUMS_SLICES), 0, s, a.part_a, a.part_w,
                        a.w_post, a_of_gate, ggate, gw_pre, rows, rows_per_gate, g, a.run, runs, channels, scale);
     GS_CHECK_LAUNCH();
