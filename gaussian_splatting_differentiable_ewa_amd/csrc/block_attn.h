@@ -15,6 +15,8 @@
 // values) is read from LDS in that order by two 4-row transposing reads.
 #pragma once
 
+#include <type_traits>
+
 #include "tokens.h"
 
 namespace gs {
@@ -69,34 +71,79 @@ struct Tile {
     static __device__ __forceinline__ int at(int row, int c) { return (row * CHUNKS + (c ^ swizzle(row))) * 8; }
 };
 
-// This wave's share of loading 64 rows into a tile, straight to LDS (16 bytes
-// a lane; the LDS side of such a load is linear in the lane, so the swizzle
-// is applied to the global side). Row r comes from token min(t0 + r, last).
+// Loads of 64 rows into a tile, straight to LDS (16 bytes a lane; the LDS side
+// of such a load is linear in the lane, so the swizzle is applied to the
+// global side). Each of WAVES waves issues CHUNKS / WAVES instructions; one
+// covers 1024 bytes, ROWS rows. The lane's part of the address is a 32-bit
+// offset formed once (its chunk differs between instructions by an XOR), the
+// rest is uniform: one vector instruction per load.
 template <typename T, int D, int WAVES>
-__device__ __forceinline__ void load_tile(T* tile, const T* base, int64_t stride, int64_t t0, int64_t last, int wave)
-{
-    constexpr int CH = Tile<D>::CHUNKS, PER = CH / WAVES;
-    const int lane = lane_id();
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int first = (wave * PER + i) * 64, n = first + lane;
-        const int row = n / CH, c = (n % CH) ^ Tile<D>::swizzle(row);
-        int64_t t = t0 + row;
-        t = t < last ? t : last;
-        const T* src = base + t * stride + c * 8;
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                         (__attribute__((address_space(3))) void*)(tile + first * 8), 16, 0, 0);
+struct TileLoad {
+    static constexpr int CH = Tile<D>::CHUNKS, PER = CH / WAVES, ROWS = 64 / CH;
+    uint32_t row, chunk;  // bytes
+    int64_t stride;       // elements
+    __device__ __forceinline__ explicit TileLoad(int64_t st) : stride(st)
+    {
+        const uint32_t r = lane_id() / CH, c = (lane_id() % CH) ^ Tile<D>::swizzle(r);
+        row = r * (uint32_t)st * (uint32_t)sizeof(T);
+        chunk = c * 16;
     }
+    static __device__ __forceinline__ void one(T* tile, const void* src)
+    {
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                         (__attribute__((address_space(3))) void*)tile, 16, 0, 0);
+    }
+    // Rows t0 .. t0 + 63; past `last`, row `last` again (masked by the reader,
+    // but never a row that may hold anything).
+    __device__ __forceinline__ void operator()(T* tile, const T* base, int64_t t0, int64_t last, int wave) const
+    {
+        const T* first = base + (t0 + wave * PER * ROWS) * stride;
+        T* to = tile + wave * PER * 512;
+        if (t0 + 63 <= last) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const uint32_t x = D == 128 ? (i & 3) * 16 : (i & 1) * 32;
+                one(to + i * 512, (const char*)(first + i * ROWS * stride) + ((chunk ^ x) + row));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const uint32_t x = D == 128 ? (i & 3) * 16 : (i & 1) * 32;
+                const int64_t t = t0 + (wave * PER + i) * ROWS + lane_id() / CH;
+                one(to + i * 512, (const char*)(base + (t < last ? t : last) * stride) + (chunk ^ x));
+            }
+        }
+    }
+};
+
+// Order of the instructions around: AHEAD + N LDS reads and MFMAS matrix
+// instructions, the reads AHEAD of their use, PER reads after each matrix
+// instruction. (The compiler by itself reads one operand and waits for it.)
+template <int READS, int MFMAS, int AHEAD>
+__device__ __forceinline__ void interleave()
+{
+    constexpr int PER = READS / MFMAS;
+    static_assert(READS % MFMAS == 0 && AHEAD % PER == 0, "whole operands");
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+    for (int i = 0; i < MFMAS - AHEAD / PER; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, AHEAD / PER, 0);
 }
 
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// In both reads r0 is a multiple of 16, which the swizzle does not see: it goes
+// into the instruction's offset, and the lane's address serves all of them.
 
 // A operand, rows of the tile: row r0 + (l & 31), k = 16 step + 8 (l >> 5) ...
 template <typename T, int D>
 __device__ __forceinline__ typename Mma<T>::v8 read_rows(const T* tile, int r0, int step)
 {
     const int l = lane_id();
-    return *(const typename Mma<T>::v8*)(tile + Tile<D>::at(r0 + (l & 31), step * 2 + (l >> 5)));
+    return *(const typename Mma<T>::v8*)(tile + r0 * D + Tile<D>::at(l & 31, step * 2 + (l >> 5)));
 }
 
 // A operand, columns of the tile as rows: row = column c0 + (l & 31), k = the
@@ -113,7 +160,7 @@ __device__ __forceinline__ typename Mma<T>::v8 read_cols(const T* tile, int r0, 
     } u;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const T* p = tile + Tile<D>::at(r0 + 8 * i + row, col >> 3) + (col & 7);
+        const T* p = tile + r0 * D + Tile<D>::at(8 * i + row, col >> 3) + (col & 7);
         u.h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4v*)p);
     }
     return u.v;
@@ -169,6 +216,24 @@ __device__ __forceinline__ bool entry_ok(const int32_t* list, int j, int64_t vis
     return id >= 0 && id > before && id < visible;
 }
 
+// The entries of an ascending list: blocks that every query of the group sees
+// whole come first, those that a sequence's end or the causal limit cuts come
+// last. So the first loop has no masks (and, one step per stage, constant LDS
+// addresses); the second has.
+template <typename Step, typename More, typename Cut>
+__device__ __forceinline__ void walk_blocks(Step&& step, More&& more, Cut&& cut)
+{
+    int stage = 0;
+    while (more() && !cut()) {
+        step(0, std::false_type{});
+        stage = 1;
+        if (!more() || cut()) break;
+        step(1, std::false_type{});
+        stage = 0;
+    }
+    for (; more(); stage ^= 1) step(stage, std::true_type{});
+}
+
 // 4 consecutive elements, 8 bytes.
 template <typename T>
 __device__ __forceinline__ void store4(T* p, float a, float b, float c, float d)
@@ -183,9 +248,10 @@ __device__ __forceinline__ void store4(T* p, float a, float b, float c, float d)
 gs_status attn_check(int64_t batch, int64_t tokens_q, int64_t tokens_k, int32_t heads_q, int32_t heads_k, int32_t dim,
                      int32_t dtype, int32_t top, float sm_scale);
 
+// Rows on 16 bytes, and eight of them within the loads' 32-bit offsets.
 inline bool attn_view_ok(const gs_tokens* t, int64_t batch, int64_t tokens, int64_t heads)
 {
-    return rows_aligned(t, batch, tokens, heads, 2, 16);
+    return rows_aligned(t, batch, tokens, heads, 2, 16) && (tokens <= 1 || (t->stride_t >= 0 && t->stride_t < (1 << 27)));
 }
 
 }  // namespace gs

@@ -18,11 +18,18 @@ struct Online {
     }
 };
 
+// The running maximum is renewed, and sums and outputs rescaled, only when a
+// score exceeds it by more than 2^8: until then probabilities are at most 256
+// instead of 1, which neither their type nor the fp32 sums notice. With the
+// maximum renewed at every rise some of the 32 queries rose at nearly every
+// block, at 64 multiplications a lane.
+constexpr float RISE = 8.f;
+
 // One block of 64 keys: limit is the number of keys, counted from the block's
 // first, that this lane's query sees (>= 64: all of them).
-template <typename T, int D>
+template <typename T, int D, bool MASKED>
 __device__ __forceinline__ void attend_block(const T* kt, const T* vt, const typename Mma<T>::v8 (&q)[D / 16],
-                                             Online<D>& st, float c, int limit, bool masked)
+                                             Online<D>& st, float c, int limit)
 {
     const int hi = lane_id() >> 5;
     acc16 s[2];
@@ -32,29 +39,31 @@ __device__ __forceinline__ void attend_block(const T* kt, const T* vt, const typ
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) s[t] = Mma<T>::mma(read_rows<T, D>(kt, t * 32, k), q[k], s[t]);
     }
-    if (masked) {
+    interleave<D / 8, D / 8, 4>();
+    if constexpr (MASKED) {
+        const int rows = limit - 4 * hi;  // against constants: no registers for the rows
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[t][i] = t * 32 + c_row(i, hi) < limit ? s[t][i] : -INFINITY;
+            for (int i = 0; i < 16; ++i) s[t][i] = t * 32 + c_row(i, 0) < rows ? s[t][i] : -INFINITY;
     }
     float mx = -INFINITY;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[t][i]);
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
-    const float m = fmaxf(st.m, mx * c);
-    const float ms = m == -INFINITY ? 0.f : m;  // nothing seen so far: every p is 0
-    if (__any(m > st.m)) {
-        const float f = exp2_fast(st.m - ms);
+    mx = fmaxf(mx, __shfl_xor(mx, 32)) * c;
+    if (__any(mx > st.m + RISE)) {
+        const float m = fmaxf(st.m, mx);
+        const float f = m == -INFINITY ? 1.f : exp2_fast(st.m - m);
+        st.m = m;
         st.l *= f;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
             for (int j = 0; j < 16; ++j) st.o[i][j] *= f;
     }
-    st.m = m;
+    const float ms = st.m == -INFINITY ? 0.f : st.m;  // nothing seen so far: every p is 0
     typename Mma<T>::v8 p[4];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -70,12 +79,13 @@ __device__ __forceinline__ void attend_block(const T* kt, const T* vt, const typ
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) st.o[i] = Mma<T>::mma(read_cols<T, D>(vt, k * 16, i * 32), p[k], st.o[i]);
+    interleave<D / 4, D / 8, 8>();
 }
 
 // Many queries: a workgroup per (batch, head, group), four waves of 32
 // queries, the listed blocks one after the other through two LDS stages.
 template <typename T, int D>
-__global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_fwd(View<const T> q, View<const T> k, View<const T> v,
+__global__ __launch_bounds__(ATT_THREADS, D == 64 ? 4 : 2) void k_attn_fwd(View<const T> q, View<const T> k, View<const T> v,
                                                              const int32_t* __restrict__ lists,
                                                              const int32_t* __restrict__ kv_len, View<T> out,
                                                              float* __restrict__ lse, const AttnArgs a)
@@ -103,26 +113,28 @@ __global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_fwd(View<const T> q, Vi
     st.init();
     const T* kb = k.at(b, 0, hk);
     const T* vb = v.at(b, 0, hk);
+    const TileLoad<T, D, 4> load_k(k.st), load_v(v.st);
     int j = 0;
     while (j < a.top && !entry_ok(list, j, visible)) ++j;
     if (j < a.top) {
-        load_tile<T, D, 4>(s_tile[0][0], kb, k.st, (int64_t)list[j] * KB, len - 1, wave);
-        load_tile<T, D, 4>(s_tile[0][1], vb, v.st, (int64_t)list[j] * KB, len - 1, wave);
+        load_k(s_tile[0][0], kb, (int64_t)list[j] * KB, len - 1, wave);
+        load_v(s_tile[0][1], vb, (int64_t)list[j] * KB, len - 1, wave);
     }
-    for (int stage = 0; j < a.top; stage ^= 1) {
+    auto step = [&](int S, auto masked) __attribute__((always_inline)) {
         int next = j + 1;
         while (next < a.top && !entry_ok(list, next, visible)) ++next;
         wait_loads();
         __syncthreads();  // the stage is whole, and the other one is read out
         if (next < a.top) {
-            load_tile<T, D, 4>(s_tile[stage ^ 1][0], kb, k.st, (int64_t)list[next] * KB, len - 1, wave);
-            load_tile<T, D, 4>(s_tile[stage ^ 1][1], vb, v.st, (int64_t)list[next] * KB, len - 1, wave);
+            load_k(s_tile[S ^ 1][0], kb, (int64_t)list[next] * KB, len - 1, wave);
+            load_v(s_tile[S ^ 1][1], vb, (int64_t)list[next] * KB, len - 1, wave);
         }
         const int64_t k0 = (int64_t)list[j] * KB, rest = mine - k0;
         const int limit = (int)(rest < 0 ? 0 : (rest < KB ? rest : KB));
-        attend_block<T, D>(s_tile[stage][0], s_tile[stage][1], qf, st, c, limit, k0 + KB > least);
+        attend_block<T, D, decltype(masked)::value>(s_tile[S][0], s_tile[S][1], qf, st, c, limit);
         j = next;
-    }
+    };
+    walk_blocks(step, [&] { return j < a.top; }, [&] { return (int64_t)list[j] * KB + KB > least; });
     if (i >= a.tokens_q) return;
     const float l = st.l + __shfl_xor(st.l, 32);
     const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -172,16 +184,18 @@ __global__ __launch_bounds__(ATT_THREADS, 1) void k_attn_few(View<const T> q, Vi
     st.init();
     const T* kb = k.at(b, 0, hk);
     const T* vb = v.at(b, 0, hk);
+    const TileLoad<T, D, 1> load_k(k.st), load_v(v.st);
     for (int j = split * 4 + wave; j < a.top; j += 4 * a.splits) {
         if (!entry_ok(list, j, visible)) continue;
         const int64_t k0 = (int64_t)list[j] * KB, rest = mine - k0;
         // the wave's own reads of the tile's last contents are done: their
         // results were used
-        load_tile<T, D, 1>(s_tile[wave][0], kb, k.st, k0, len - 1, 0);
-        load_tile<T, D, 1>(s_tile[wave][1], vb, v.st, k0, len - 1, 0);
+        load_k(s_tile[wave][0], kb, k0, len - 1, 0);
+        load_v(s_tile[wave][1], vb, k0, len - 1, 0);
         wait_loads();
         const int limit = (int)(rest < 0 ? 0 : (rest < KB ? rest : KB));
-        attend_block<T, D>(s_tile[wave][0], s_tile[wave][1], qf, st, c, limit, k0 + KB > least);
+        // one form for both kinds of block: a wave has few
+        attend_block<T, D, true>(s_tile[wave][0], s_tile[wave][1], qf, st, c, limit);
     }
     const float l = st.l + __shfl_xor(st.l, 32);
     if (hi == 0) s_m[wave][lane] = st.m, s_l[wave][lane] = l;

@@ -66,11 +66,12 @@ __global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_gq(View<const T> go, Vi
     const float c = a.scale * LOG2E;
     const T* kb = k.at(b, 0, hk);
     const T* vb = v.at(b, 0, hk);
+    const TileLoad<T, D, 4> load_k(k.st), load_v(v.st);
     int j = 0;
     while (j < a.top && !entry_ok(list, j, visible)) ++j;
     if (j < a.top) {
-        load_tile<T, D, 4>(s_tile[0][0], kb, k.st, (int64_t)list[j] * KB, len - 1, wave);
-        load_tile<T, D, 4>(s_tile[0][1], vb, v.st, (int64_t)list[j] * KB, len - 1, wave);
+        load_k(s_tile[0][0], kb, (int64_t)list[j] * KB, len - 1, wave);
+        load_v(s_tile[0][1], vb, (int64_t)list[j] * KB, len - 1, wave);
     }
     typename Mma<T>::v8 qf[D / 16], gf[D / 16];
     load_cols<T, D>(q.at(b, ic, h), qf);
@@ -91,19 +92,7 @@ __global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_gq(View<const T> go, Vi
     acc16 acc[D / 32];
 #pragma unroll
     for (int t = 0; t < D / 32; ++t) acc[t] = zero16();
-    for (int stage = 0; j < a.top; stage ^= 1) {
-        int next = j + 1;
-        while (next < a.top && !entry_ok(list, next, visible)) ++next;
-        wait_loads();
-        __syncthreads();
-        if (next < a.top) {
-            load_tile<T, D, 4>(s_tile[stage ^ 1][0], kb, k.st, (int64_t)list[next] * KB, len - 1, wave);
-            load_tile<T, D, 4>(s_tile[stage ^ 1][1], vb, v.st, (int64_t)list[next] * KB, len - 1, wave);
-        }
-        const T *kt = s_tile[stage][0], *vt = s_tile[stage][1];
-        const int64_t k0 = (int64_t)list[j] * KB, rest = mine - k0;
-        const int limit = (int)(rest < 0 ? 0 : (rest < KB ? rest : KB));
-        const bool masked = k0 + KB > least;
+    auto block = [&](const T* kt, const T* vt, auto masked, int limit) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             acc16 s = zero16(), p = zero16();
@@ -111,11 +100,13 @@ __global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_gq(View<const T> go, Vi
             for (int x = 0; x < D / 16; ++x) s = Mma<T>::mma(read_rows<T, D>(kt, t * 32, x), qf[x], s);
 #pragma unroll
             for (int x = 0; x < D / 16; ++x) p = Mma<T>::mma(read_rows<T, D>(vt, t * 32, x), gf[x], p);
+            interleave<D / 8, D / 8, 4>();
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = exp2_fast(fmaf(s[r], c, nl));
-            if (masked) {
+            if constexpr (decltype(masked)::value) {
+                const int rows = limit - 4 * hi;  // against constants: no registers for the rows
 #pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = t * 32 + c_row(r, hi) < limit ? s[r] : 0.f;
+                for (int r = 0; r < 16; ++r) s[r] = t * 32 + c_row(r, 0) < rows ? s[r] : 0.f;
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] *= p[r] - dl;
@@ -126,9 +117,24 @@ __global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_gq(View<const T> go, Vi
                 for (int y = 0; y < D / 32; ++y)
                     acc[y] = Mma<T>::mma(read_cols<T, D>(kt, t * 32 + x * 16, y * 32), ds, acc[y]);
             }
+            interleave<D / 8, D / 16, 4>();
+            __builtin_amdgcn_sched_barrier(0);  // keeps the halves' registers apart
         }
+    };
+    auto step = [&](int S, auto masked) __attribute__((always_inline)) {
+        int next = j + 1;
+        while (next < a.top && !entry_ok(list, next, visible)) ++next;
+        wait_loads();
+        __syncthreads();
+        if (next < a.top) {
+            load_k(s_tile[S ^ 1][0], kb, (int64_t)list[next] * KB, len - 1, wave);
+            load_v(s_tile[S ^ 1][1], vb, (int64_t)list[next] * KB, len - 1, wave);
+        }
+        const int64_t k0 = (int64_t)list[j] * KB, rest = mine - k0;
+        block(s_tile[S][0], s_tile[S][1], masked, (int)(rest < 0 ? 0 : (rest < KB ? rest : KB)));
         j = next;
-    }
+    };
+    walk_blocks(step, [&] { return j < a.top; }, [&] { return (int64_t)list[j] * KB + KB > least; });
     if (i >= a.tokens_q) return;
     T* o = gq.at(b, i, h);
 #pragma unroll
@@ -220,10 +226,11 @@ __global__ __launch_bounds__(ATT_THREADS, 1) void k_attn_gkv(View<const T> go, V
     w.tokens_q = a.tokens_q;
     w.heads = per;
     w.start();
-    auto load = [&](int stage) {
+    const TileLoad<T, D, 4> load_q(q.st), load_g(go.st);
+    auto load = [&](int stage) __attribute__((always_inline)) {
         const int64_t h = hk * per + w.h;
-        load_tile<T, D, 4>(s_tile[stage][0], q.at(b, 0, h), q.st, w.q0, a.tokens_q - 1, wave);
-        load_tile<T, D, 4>(s_tile[stage][1], go.at(b, 0, h), go.st, w.q0, a.tokens_q - 1, wave);
+        load_q(s_tile[stage][0], q.at(b, 0, h), w.q0, a.tokens_q - 1, wave);
+        load_g(s_tile[stage][1], go.at(b, 0, h), w.q0, a.tokens_q - 1, wave);
         if (threadIdx.x < 64) {
             const int64_t i = w.q0 + threadIdx.x;
             const bool on = i < a.tokens_q;
