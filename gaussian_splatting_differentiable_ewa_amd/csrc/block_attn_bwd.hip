@@ -6,6 +6,8 @@
 // [batch][head][block][groups / 32], set from the lists (an OR: any order).
 // Both passes form S and P again from lse: 7 products in all where the
 // formula's 5 would need fp32 atomics on gq.
+#include <algorithm>
+
 #include "block_attn.h"
 
 namespace gs {
@@ -145,32 +147,25 @@ __global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_gq(View<const T> go, Vi
                       acc[t][4 * r + 2] * a.scale, acc[t][4 * r + 3] * a.scale);
 }
 
-// Walks the (head of the key head, half group of 64 queries) pairs that list
-// a block; every thread steps the same way.
+// Walks the (head of the key head, group of queries) pairs that list a block;
+// every thread steps the same way.
 struct Walk {
     const uint32_t* bits;  // of the first head, this block
-    int64_t head_stride, words, tokens_q;
+    int64_t head_stride, words;
     int heads;
     // state
     int h;
     int64_t word, q0;
     uint32_t left;
-    int half;
     __device__ __forceinline__ void start()
     {
         h = words > 0 ? 0 : heads;
         word = -1;
         left = 0;
-        half = 1;
         q0 = 0;
     }
     __device__ __forceinline__ bool next()
     {
-        if (half == 0 && (q0 + 64) < tokens_q) {
-            half = 1;
-            q0 += 64;
-            return true;
-        }
         if (h >= heads) return false;
         while (left == 0) {
             if (++word == words) {
@@ -182,63 +177,110 @@ struct Walk {
         const int bit = __builtin_ctz(left);
         left &= left - 1;
         q0 = (word * 32 + bit) * QG;
-        half = 0;
         return true;
     }
 };
 
-// gk and gv of a block of 64 keys. Wave w: keys 32 (w & 1) .. + 32 of it, and
-// of every 64 queries 32 (w >> 1) .. + 32; the two query halves join at the
-// end. S and dP are formed with queries as rows, so that a lane holds one key:
-//   gv^T += gout^T P,  gk^T += q^T dS
-template <typename T, int D>
-__global__ __launch_bounds__(ATT_THREADS, 1) void k_attn_gkv(View<const T> go, View<const T> q, View<const T> k,
-                                                             View<const T> v, const float* __restrict__ lse,
-                                                             const float* __restrict__ delta,
-                                                             const uint32_t* __restrict__ bits,
-                                                             const int32_t* __restrict__ kv_len, View<T> gk, View<T> gv,
-                                                             const AttnArgs a)
+// Blocks of one key head by the number of groups that list them, most first:
+// the grid takes them in this order, so that the launch does not end on a
+// block that many groups list. A counting sort on min(groups, ORDER_CLASSES - 1).
+// Ties may fall in any order: a block's result does not depend on its place.
+constexpr int ORDER_CLASSES = 1024;
+
+__global__ __launch_bounds__(ATT_THREADS) void k_block_order(const uint32_t* __restrict__ bits,
+                                                             uint32_t* __restrict__ order, const AttnArgs a)
 {
-    __shared__ alignas(16) T s_tile[2][2][Tile<D>::ELEMS];
-    __shared__ float s_row[2][2][64];  // per query: -lse in base 2, D
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), hi = lane >> 5;
-    const int kh = wave & 1, qh = wave >> 1;
-    const int64_t id = xcd_contiguous(blockIdx.x, gridDim.x);
-    const int64_t bh = id / a.blocks, blk = id - bh * a.blocks;
-    const int64_t b = bh / a.heads_k, hk = bh - b * a.heads_k;
+    __shared__ uint32_t s_start[ORDER_CLASSES], s_part[ATT_THREADS];
+    const int64_t bh = blockIdx.x, words = (a.groups + 31) / 32;
     const int per = a.heads_q / a.heads_k;
-    const int64_t len = seq_len(kv_len, b, a.tokens_k), past = len - a.tokens_q;
+    const int64_t first = bh / a.heads_k * a.heads_q + bh % a.heads_k * per;  // the first query head
+    for (int i = threadIdx.x; i < ORDER_CLASSES; i += ATT_THREADS) s_start[i] = 0;
+    __syncthreads();
+    auto cls = [&](int64_t blk) {
+        uint32_t n = 0;
+        for (int h = 0; h < per; ++h)
+            for (int64_t w = 0; w < words; ++w) n += __popc(bits[((first + h) * a.blocks + blk) * words + w]);
+        return ORDER_CLASSES - 1 - (n < ORDER_CLASSES - 1 ? n : ORDER_CLASSES - 1);
+    };
+    for (int64_t i = threadIdx.x; i < a.blocks; i += ATT_THREADS) atomicAdd(&s_start[cls(i)], 1u);
+    __syncthreads();
+    // exclusive sums: four classes a thread
+    constexpr int PER = ORDER_CLASSES / ATT_THREADS;
+    uint32_t v[PER], sum = 0;
+    for (int i = 0; i < PER; ++i) sum += v[i] = s_start[threadIdx.x * PER + i];
+    s_part[threadIdx.x] = sum;
+    __syncthreads();
+    uint32_t before = 0;
+    for (int i = 0; i < (int)threadIdx.x; ++i) before += s_part[i];
+    for (int i = 0; i < PER; ++i) {
+        s_start[threadIdx.x * PER + i] = before;
+        before += v[i];
+    }
+    __syncthreads();
+    for (int64_t i = threadIdx.x; i < a.blocks; i += ATT_THREADS) order[bh * a.blocks + atomicAdd(&s_start[cls(i)], 1u)] = (uint32_t)i;
+}
+
+// gk and gv of a block of 64 keys: eight waves, four for either. Wave w of the
+// four: keys 32 (w & 1) .. + 32, and of every 64 queries 32 (w >> 1) .. + 32;
+// the two query halves join at the end. S and dP are formed with queries as
+// rows, so that a lane holds one key:
+//   gv^T += gout^T P,  gk^T += q^T dS
+// Registers decide the shape. One wave with both sums (128 registers at dim
+// 128), k and v (64) and S, dP (32) needs 340 and leaves a SIMD with one wave,
+// which multiplies or computes exponentials but not both. Split by result,
+// either wave fits 256, each SIMD holds one of each kind, and the price is S
+// formed twice (5 products instead of 4). Stages are whole groups.
+constexpr int GKV_THREADS = 512;
+
+template <typename T, int D>
+struct GkvShared {
+    alignas(16) T tile[2][2][2][Tile<D>::ELEMS];  // stage; q, gout; half of the group
+    alignas(16) float row[2][2][QG];              // stage; -lse in base 2, D; query
+};
+
+// One kind of wave: FOR_V gv, else gk. Both kinds pass the same barriers.
+template <typename T, int D, bool FOR_V>
+__device__ __forceinline__ void gkv_wave(GkvShared<T, D>& sh, const View<const T>& go, const View<const T>& q,
+                                         const View<const T>& k, const View<const T>& v, const float* __restrict__ lse,
+                                         const float* __restrict__ delta, const uint32_t* __restrict__ bits, int64_t blk,
+                                         int64_t b, int64_t hk, int64_t len, const View<T>& result, const AttnArgs& a,
+                                         int wave)
+{
+    const int lane = lane_id(), hi = lane >> 5, kh = wave & 1, qh = (wave >> 1) & 1;
+    const int per = a.heads_q / a.heads_k;
+    const int64_t past = len - a.tokens_q;
     const int64_t key = blk * KB + kh * 32 + (lane & 31);
     // keys past the end hold anything: take a valid one, its P is masked
     const int64_t last = len > 0 ? len - 1 : 0, kc = key < last ? key : last;
     const float c = a.scale * LOG2E;
-    typename Mma<T>::v8 kf[D / 16], vf[D / 16];
+    typename Mma<T>::v8 kf[D / 16], vf[FOR_V ? 1 : D / 16];
     load_cols<T, D>(k.at(b, kc, hk), kf);
-    load_cols<T, D>(v.at(b, kc, hk), vf);
-    acc16 ak[D / 32], av[D / 32];
+    if constexpr (!FOR_V) load_cols<T, D>(v.at(b, kc, hk), vf);
+    acc16 acc[D / 32];
 #pragma unroll
-    for (int t = 0; t < D / 32; ++t) ak[t] = zero16(), av[t] = zero16();
+    for (int t = 0; t < D / 32; ++t) acc[t] = zero16();
 
     Walk w;
     w.words = (a.groups + 31) / 32;
     w.head_stride = a.blocks * w.words;
     w.bits = bits + ((b * a.heads_q + hk * per) * a.blocks + blk) * w.words;
-    w.tokens_q = a.tokens_q;
     w.heads = per;
     w.start();
     const TileLoad<T, D, 4> load_q(q.st), load_g(go.st);
     auto load = [&](int stage) __attribute__((always_inline)) {
         const int64_t h = hk * per + w.h;
-        load_q(s_tile[stage][0], q.at(b, 0, h), w.q0, a.tokens_q - 1, wave);
-        load_g(s_tile[stage][1], go.at(b, 0, h), w.q0, a.tokens_q - 1, wave);
-        if (threadIdx.x < 64) {
+        // the four waves of a kind load a half
+        constexpr int HALF = FOR_V ? 0 : 1;
+        load_q(sh.tile[stage][0][HALF], q.at(b, 0, h), w.q0 + HALF * 64, a.tokens_q - 1, wave & 3);
+        load_g(sh.tile[stage][1][HALF], go.at(b, 0, h), w.q0 + HALF * 64, a.tokens_q - 1, wave & 3);
+        if (FOR_V && threadIdx.x < QG) {
             const int64_t i = w.q0 + threadIdx.x;
             const bool on = i < a.tokens_q;
             const int64_t at = (b * a.heads_q + h) * a.tokens_q + (on ? i : a.tokens_q - 1);
             const float ls = lse[at], dl = delta[at];
             // queries past the end and queries that saw nothing: P = 0
-            s_row[stage][0][threadIdx.x] = on && ls > -INFINITY ? -ls * LOG2E : -INFINITY;
-            s_row[stage][1][threadIdx.x] = dl;
+            sh.row[stage][0][threadIdx.x] = on && ls > -INFINITY ? -ls * LOG2E : -INFINITY;
+            sh.row[stage][1][threadIdx.x] = dl;
         }
     };
     bool more = w.next();
@@ -251,76 +293,95 @@ __global__ __launch_bounds__(ATT_THREADS, 1) void k_attn_gkv(View<const T> go, V
         more = w.next();
         q0 = w.q0;
         if (more) load(stage ^ 1);
-        const T *qt = s_tile[stage][0], *gt = s_tile[stage][1];
-        acc16 s = zero16(), p = zero16();
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) s = Mma<T>::mma(read_rows<T, D>(qt, qh * 32, x), kf[x], s);
+        for (int half = 0; half < 2; ++half) {
+            // (a second half past the last query has P = 0 throughout)
+            const T *qt = sh.tile[stage][0][half], *gt = sh.tile[stage][1][half];
+            const int row = half * 64 + qh * 32;
+            const float* nl = &sh.row[stage][0][row + 4 * hi];
+            const float* dl = &sh.row[stage][1][row + 4 * hi];
+            acc16 s = zero16(), p = zero16();
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) p = Mma<T>::mma(read_rows<T, D>(gt, qh * 32, x), vf[x], p);
-        const bool masked = (int64_t)(blk + 1) * KB > (a.causal && past + now + 1 < len ? past + now + 1 : len);
+            for (int x = 0; x < D / 16; ++x) s = Mma<T>::mma(read_rows<T, D>(qt, qh * 32, x), kf[x], s);
+            if constexpr (!FOR_V) {
 #pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4) {
-            const int row = qh * 32 + 8 * r4 + 4 * hi;
-            const float4v nl = *(const float4v*)&s_row[stage][0][row], dl = *(const float4v*)&s_row[stage][1][row];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = 4 * r4 + e;
-                float x = exp2_fast(fmaf(s[r], c, nl[e]));
-                if (masked) {
-                    const int64_t sees = a.causal && past + now + row + e + 1 < len ? past + now + row + e + 1 : len;
-                    x = key < sees ? x : 0.f;
-                }
-                s[r] = x;
-                p[r] = x * (p[r] - dl[e]);
+                for (int x = 0; x < D / 16; ++x) p = Mma<T>::mma(read_rows<T, D>(gt, qh * 32, x), vf[x], p);
             }
-        }
+            interleave<(FOR_V ? 1 : 2) * D / 16, (FOR_V ? 1 : 2) * D / 16, 4>();
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const typename Mma<T>::v8 pp = as_operand<T>(s, x), ds = as_operand<T>(p, x);
+            for (int r = 0; r < 16; ++r) s[r] = exp2_fast(fmaf(s[r], c, nl[c_row(r, 0)]));
+            const int64_t first = now + row;
+            if ((blk + 1) * KB > (a.causal && past + first + 1 < len ? past + first + 1 : len)) {
+                asm volatile("");  // a branch, not selects in every step
+                // rows from `from` on see this lane's key
+                const int64_t d = a.causal ? key - past - first - 4 * hi : 0;
+                const int from = key >= len ? 64 : (int)(d > 64 ? 64 : (d < 0 ? 0 : d));
 #pragma unroll
-            for (int y = 0; y < D / 32; ++y) {
-                av[y] = Mma<T>::mma(read_cols<T, D>(gt, qh * 32 + x * 16, y * 32), pp, av[y]);
-                ak[y] = Mma<T>::mma(read_cols<T, D>(qt, qh * 32 + x * 16, y * 32), ds, ak[y]);
+                for (int r = 0; r < 16; ++r) s[r] = c_row(r, 0) >= from ? s[r] : 0.f;
             }
+            if constexpr (!FOR_V) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[r] *= p[r] - dl[c_row(r, 0)];
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const typename Mma<T>::v8 op = as_operand<T>(s, x);
+#pragma unroll
+                for (int y = 0; y < D / 32; ++y)
+                    acc[y] = Mma<T>::mma(read_cols<T, D>(FOR_V ? gt : qt, qh * 32 + x * 16, y * 32), op, acc[y]);
+            }
+            interleave<D / 8, D / 16, 4>();
+            __builtin_amdgcn_sched_barrier(0);  // keeps the halves' registers apart
         }
     }
     // join the query halves: the second one's sums through LDS
     __syncthreads();
-    float* s_acc = (float*)&s_tile[0][0][0];  // [2 key halves][D / 32 x 16][64 lanes], gk then gv
     constexpr int REGS = D / 32 * 16;
+    float* mine = (float*)&sh.tile[0][0][0][0] + ((FOR_V ? 2 : 0) + kh) * REGS * 64 + lane;
+    if (qh == 1) {
 #pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
-        acc16(&acc)[D / 32] = pass == 0 ? ak : av;
-        if (qh == 1) {
+        for (int t = 0; t < D / 32; ++t)
 #pragma unroll
-            for (int t = 0; t < D / 32; ++t)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s_acc[(kh * REGS + t * 16 + r) * 64 + lane] = acc[t][r];
-        }
-        __syncthreads();
-        if (qh == 0 && key < a.tokens_k) {
-            const float f = pass == 0 ? a.scale : 1.f;
-            T* o = pass == 0 ? gk.at(b, key, hk) : gv.at(b, key, hk);
-#pragma unroll
-            for (int t = 0; t < D / 32; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    float x[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        x[e] = (acc[t][4 * r + e] + s_acc[(kh * REGS + t * 16 + 4 * r + e) * 64 + lane]) * f;
-                    store4<T>(o + t * 32 + r * 8 + hi * 4, x[0], x[1], x[2], x[3]);
-                }
-        }
-        __syncthreads();
+            for (int r = 0; r < 16; ++r) mine[(t * 16 + r) * 64] = acc[t][r];
     }
+    __syncthreads();
+    if (qh == 1 || key >= a.tokens_k) return;
+    const float f = FOR_V ? 1.f : a.scale;
+    T* o = result.at(b, key, hk);
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = (acc[t][4 * r + e] + mine[(t * 16 + 4 * r + e) * 64]) * f;
+            store4<T>(o + t * 32 + r * 8 + hi * 4, x[0], x[1], x[2], x[3]);
+        }
+}
+
+template <typename T, int D>
+__global__ __launch_bounds__(GKV_THREADS, D == 64 ? 4 : 2) void k_attn_gkv(
+    View<const T> go, View<const T> q, View<const T> k, View<const T> v, const float* __restrict__ lse,
+    const float* __restrict__ delta, const uint32_t* __restrict__ bits, const uint32_t* __restrict__ order,
+    const int32_t* __restrict__ kv_len, View<T> gk, View<T> gv, const AttnArgs a)
+{
+    __shared__ GkvShared<T, D> sh;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t id = xcd_contiguous(blockIdx.x, gridDim.x);
+    const int64_t bh = id / a.blocks, blk = order[id];
+    const int64_t b = bh / a.heads_k, hk = bh - b * a.heads_k;
+    const int64_t len = seq_len(kv_len, b, a.tokens_k);
+    if (wave < 4)
+        gkv_wave<T, D, true>(sh, go, q, k, v, lse, delta, bits, blk, b, hk, len, gv, a, wave);
+    else
+        gkv_wave<T, D, false>(sh, go, q, k, v, lse, delta, bits, blk, b, hk, len, gk, a, wave);
 }
 
 template <typename T, int D>
 static gs_status attn_bwd_launch(const gs_tokens* go, const gs_tokens* q, const gs_tokens* k, const gs_tokens* v,
                                  const gs_tokens* out, const float* lse, const int32_t* list, const int32_t* kv_len,
                                  const gs_tokens* gq, const gs_tokens* gk, const gs_tokens* gv, float* delta,
-                                 uint32_t* bits, int64_t batch, const AttnArgs& a, hipStream_t s)
+                                 uint32_t* bits, uint32_t* order, int64_t batch, const AttnArgs& a, hipStream_t s)
 {
     const int64_t lists = batch * a.heads_q * a.groups, blocks = batch * a.heads_k * a.blocks;
     const int64_t words = batch * a.heads_q * a.blocks * ((a.groups + 31) / 32);
@@ -339,8 +400,10 @@ static gs_status attn_bwd_launch(const gs_tokens* go, const gs_tokens* q, const 
                                list, kv_len, bits, lists * a.top, a);
             GS_CHECK_LAUNCH();
         }
-        hipLaunchKernelGGL((k_attn_gkv<T, D>), dim3((unsigned)blocks), dim3(ATT_THREADS), 0, s, view_of<const T>(go),
-                           view_of<const T>(q), view_of<const T>(k), view_of<const T>(v), lse, delta, bits, kv_len,
+        hipLaunchKernelGGL(k_block_order, dim3((unsigned)(batch * a.heads_k)), dim3(ATT_THREADS), 0, s, bits, order, a);
+        GS_CHECK_LAUNCH();
+        hipLaunchKernelGGL((k_attn_gkv<T, D>), dim3((unsigned)blocks), dim3(GKV_THREADS), 0, s, view_of<const T>(go),
+                           view_of<const T>(q), view_of<const T>(k), view_of<const T>(v), lse, delta, bits, order, kv_len,
                            view_of<T>(gk), view_of<T>(gv), a);
         GS_CHECK_LAUNCH();
     }
@@ -350,6 +413,11 @@ static gs_status attn_bwd_launch(const gs_tokens* go, const gs_tokens* q, const 
 static size_t delta_bytes(int64_t batch, int64_t tokens_q, int32_t heads_q)
 {
     return (size_t)((batch * heads_q * tokens_q * 4 + 15) / 16 * 16);
+}
+
+static int64_t bits_words(int64_t batch, int64_t groups, int64_t blocks, int32_t heads_q)
+{
+    return batch * heads_q * blocks * ((groups + 31) / 32);
 }
 
 }  // namespace gs
@@ -362,7 +430,7 @@ size_t gs_block_attn_bwd_workspace_bytes(int64_t batch, int64_t tokens_q, int64_
     using namespace gs;
     if (attn_check(batch, tokens_q, tokens_k, heads_q, heads_k, dim, GS_BF16, 1, 1.f) != GS_OK) return 0;
     const int64_t groups = (tokens_q + QG - 1) / QG, blocks = (tokens_k + KB - 1) / KB;
-    return delta_bytes(batch, tokens_q, heads_q) + (size_t)(batch * heads_q * blocks * ((groups + 31) / 32)) * 4 + 16;
+    return delta_bytes(batch, tokens_q, heads_q) + (size_t)(bits_words(batch, groups, blocks, heads_q) + batch * heads_k * blocks) * 4 + 16;
 }
 
 gs_status gs_block_attn_bwd(const gs_tokens* gout, const gs_tokens* q, const gs_tokens* k, const gs_tokens* v,
@@ -392,12 +460,13 @@ gs_status gs_block_attn_bwd(const gs_tokens* gout, const gs_tokens* q, const gs_
                      causal != 0, top, 1, sm_scale};
     float* delta = (float*)ws;
     uint32_t* bits = (uint32_t*)((char*)ws + delta_bytes(batch, tokens_q, heads_q));
+    uint32_t* order = bits + bits_words(batch, a.groups, a.blocks, heads_q);
     const hipStream_t s = (hipStream_t)stream;
     if (dtype == GS_BF16)
-        return dim == 128 ? attn_bwd_launch<bf16, 128>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, delta, bits, batch, a, s)
-                          : attn_bwd_launch<bf16, 64>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, delta, bits, batch, a, s);
-    return dim == 128 ? attn_bwd_launch<f16, 128>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, delta, bits, batch, a, s)
-                      : attn_bwd_launch<f16, 64>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, delta, bits, batch, a, s);
+        return dim == 128 ? attn_bwd_launch<bf16, 128>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, delta, bits, order, batch, a, s)
+                          : attn_bwd_launch<bf16, 64>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, delta, bits, order, batch, a, s);
+    return dim == 128 ? attn_bwd_launch<f16, 128>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, delta, bits, order, batch, a, s)
+                      : attn_bwd_launch<f16, 64>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, delta, bits, order, batch, a, s);
 }
 
 }  // extern "C"
