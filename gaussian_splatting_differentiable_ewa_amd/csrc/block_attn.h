@@ -216,6 +216,35 @@ __device__ __forceinline__ bool entry_ok(const int32_t* list, int j, int64_t vis
     return id >= 0 && id > before && id < visible;
 }
 
+// Walks the entries of a list that count, 64 of them held by the wave's lanes:
+// a step costs a few scalar instructions instead of a dependent load.
+struct ListWalk {
+    const int32_t* list;
+    int64_t visible;
+    int top, base, ids;  // ids: lane l holds entry base + l
+    uint64_t left;
+    __device__ __forceinline__ ListWalk(const int32_t* l, int n, int64_t vis) : list(l), visible(vis), top(n), base(0) { fetch(); }
+    __device__ __forceinline__ void fetch()
+    {
+        const int j = base + (int)lane_id();
+        ids = j < top ? list[j] : -1;
+        const int before = j > 0 && j < top ? list[j - 1] : -1;
+        left = ballot(ids >= 0 && ids > before && ids < visible);
+    }
+    // The next block, or -1.
+    __device__ __forceinline__ int next()
+    {
+        while (left == 0) {
+            base += 64;
+            if (base >= top) return -1;
+            fetch();
+        }
+        const int j = __builtin_ctzll(left);
+        left &= left - 1;
+        return __builtin_amdgcn_readlane(ids, j);
+    }
+};
+
 // The entries of an ascending list: blocks that every query of the group sees
 // whole come first, those that a sequence's end or the causal limit cuts come
 // last. So the first loop has no masks (and, one step per stage, constant LDS

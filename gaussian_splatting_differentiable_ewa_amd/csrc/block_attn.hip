@@ -114,27 +114,26 @@ __global__ __launch_bounds__(ATT_THREADS, D == 64 ? 4 : 2) void k_attn_fwd(View<
     const T* kb = k.at(b, 0, hk);
     const T* vb = v.at(b, 0, hk);
     const TileLoad<T, D, 4> load_k(k.st), load_v(v.st);
-    int j = 0;
-    while (j < a.top && !entry_ok(list, j, visible)) ++j;
-    if (j < a.top) {
-        load_k(s_tile[0][0], kb, (int64_t)list[j] * KB, len - 1, wave);
-        load_v(s_tile[0][1], vb, (int64_t)list[j] * KB, len - 1, wave);
+    ListWalk walk(list, a.top, visible);
+    int blk = walk.next();
+    if (blk >= 0) {
+        load_k(s_tile[0][0], kb, (int64_t)blk * KB, len - 1, wave);
+        load_v(s_tile[0][1], vb, (int64_t)blk * KB, len - 1, wave);
     }
     auto step = [&](int S, auto masked) __attribute__((always_inline)) {
-        int next = j + 1;
-        while (next < a.top && !entry_ok(list, next, visible)) ++next;
+        const int next = walk.next();
         wait_loads();
         __syncthreads();  // the stage is whole, and the other one is read out
-        if (next < a.top) {
-            load_k(s_tile[S ^ 1][0], kb, (int64_t)list[next] * KB, len - 1, wave);
-            load_v(s_tile[S ^ 1][1], vb, (int64_t)list[next] * KB, len - 1, wave);
+        if (next >= 0) {
+            load_k(s_tile[S ^ 1][0], kb, (int64_t)next * KB, len - 1, wave);
+            load_v(s_tile[S ^ 1][1], vb, (int64_t)next * KB, len - 1, wave);
         }
-        const int64_t k0 = (int64_t)list[j] * KB, rest = mine - k0;
+        const int64_t k0 = (int64_t)blk * KB, rest = mine - k0;
         const int limit = (int)(rest < 0 ? 0 : (rest < KB ? rest : KB));
         attend_block<T, D, decltype(masked)::value>(s_tile[S][0], s_tile[S][1], qf, st, c, limit);
-        j = next;
+        blk = next;
     };
-    walk_blocks(step, [&] { return j < a.top; }, [&] { return (int64_t)list[j] * KB + KB > least; });
+    walk_blocks(step, [&] { return blk >= 0; }, [&] { return (int64_t)blk * KB + KB > least; });
     if (i >= a.tokens_q) return;
     const float l = st.l + __shfl_xor(st.l, 32);
     const float inv = l > 0.f ? 1.f / l : 0.f;

@@ -41,7 +41,8 @@ __global__ __launch_bounds__(ATT_THREADS) void k_list_bits(const int32_t* __rest
         set_bit(lists, kv_len, bits, e, a);
 }
 
-// gq of a group: four waves of 32 queries, the listed blocks in turn.
+// gq of a group (and, for the other pass, -lse in base 2 and D of its 128
+// queries, [list][2][128]): four waves of 32 queries, the listed blocks in turn.
 //   dS^T = P^T (V gout^T - D),  gq^T += K^T dS^T
 template <typename T, int D>
 __global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_gq(View<const T> go, View<const T> q, View<const T> k,
@@ -49,7 +50,7 @@ __global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_gq(View<const T> go, Vi
                                                             const float* __restrict__ lse,
                                                             const int32_t* __restrict__ lists,
                                                             const int32_t* __restrict__ kv_len, View<T> gq,
-                                                            float* __restrict__ delta, const AttnArgs a)
+                                                            float* __restrict__ rows, const AttnArgs a)
 {
     __shared__ alignas(16) T s_tile[2][2][Tile<D>::ELEMS];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), hi = lane >> 5;
@@ -69,11 +70,11 @@ __global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_gq(View<const T> go, Vi
     const T* kb = k.at(b, 0, hk);
     const T* vb = v.at(b, 0, hk);
     const TileLoad<T, D, 4> load_k(k.st), load_v(v.st);
-    int j = 0;
-    while (j < a.top && !entry_ok(list, j, visible)) ++j;
-    if (j < a.top) {
-        load_k(s_tile[0][0], kb, (int64_t)list[j] * KB, len - 1, wave);
-        load_v(s_tile[0][1], vb, (int64_t)list[j] * KB, len - 1, wave);
+    ListWalk walk(list, a.top, visible);
+    int blk = walk.next();
+    if (blk >= 0) {
+        load_k(s_tile[0][0], kb, (int64_t)blk * KB, len - 1, wave);
+        load_v(s_tile[0][1], vb, (int64_t)blk * KB, len - 1, wave);
     }
     typename Mma<T>::v8 qf[D / 16], gf[D / 16];
     load_cols<T, D>(q.at(b, ic, h), qf);
@@ -88,9 +89,14 @@ __global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_gq(View<const T> go, Vi
             for (int e = 0; e < 8; ++e) dl = fmaf((float)gf[s][e], (float)of[s][e], dl);
         dl += __shfl_xor(dl, 32);
     }
-    if (i < a.tokens_q && hi == 0) delta[bh * a.tokens_q + i] = dl;
-    // a query that saw nothing has lse = -inf: P = exp2(S - inf) = 0
-    const float ls = lse[bh * a.tokens_q + ic], nl = ls == -INFINITY ? -INFINITY : -ls * LOG2E;
+    // a query that saw nothing has lse = -inf: P = exp2(S - inf) = 0; so has
+    // one past the end, for the pass over the keys
+    const float ls = lse[bh * a.tokens_q + ic], nl = ls == -INFINITY || i >= a.tokens_q ? -INFINITY : -ls * LOG2E;
+    if (hi == 0) {
+        float* row = rows + id * 2 * QG + wave * 32 + lane;
+        row[0] = nl;
+        row[QG] = dl;
+    }
     acc16 acc[D / 32];
 #pragma unroll
     for (int t = 0; t < D / 32; ++t) acc[t] = zero16();
@@ -124,19 +130,18 @@ __global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_gq(View<const T> go, Vi
         }
     };
     auto step = [&](int S, auto masked) __attribute__((always_inline)) {
-        int next = j + 1;
-        while (next < a.top && !entry_ok(list, next, visible)) ++next;
+        const int next = walk.next();
         wait_loads();
         __syncthreads();
-        if (next < a.top) {
-            load_k(s_tile[S ^ 1][0], kb, (int64_t)list[next] * KB, len - 1, wave);
-            load_v(s_tile[S ^ 1][1], vb, (int64_t)list[next] * KB, len - 1, wave);
+        if (next >= 0) {
+            load_k(s_tile[S ^ 1][0], kb, (int64_t)next * KB, len - 1, wave);
+            load_v(s_tile[S ^ 1][1], vb, (int64_t)next * KB, len - 1, wave);
         }
-        const int64_t k0 = (int64_t)list[j] * KB, rest = mine - k0;
+        const int64_t k0 = (int64_t)blk * KB, rest = mine - k0;
         block(s_tile[S][0], s_tile[S][1], masked, (int)(rest < 0 ? 0 : (rest < KB ? rest : KB)));
-        j = next;
+        blk = next;
     };
-    walk_blocks(step, [&] { return j < a.top; }, [&] { return (int64_t)list[j] * KB + KB > least; });
+    walk_blocks(step, [&] { return blk >= 0; }, [&] { return (int64_t)blk * KB + KB > least; });
     if (i >= a.tokens_q) return;
     T* o = gq.at(b, i, h);
 #pragma unroll
@@ -148,35 +153,40 @@ __global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_gq(View<const T> go, Vi
 }
 
 // Walks the (head of the key head, group of queries) pairs that list a block;
-// every thread steps the same way.
+// every wave steps the same way. 64 words of the bit matrix are held by the
+// lanes: a step costs a few scalar instructions instead of a dependent load.
 struct Walk {
     const uint32_t* bits;  // of the first head, this block
-    int64_t head_stride, words;
-    int heads;
+    int64_t head_stride, total;
+    int words;
     // state
-    int h;
-    int64_t word, q0;
-    uint32_t left;
-    __device__ __forceinline__ void start()
+    int64_t base, q0;
+    uint64_t some;  // lanes with words left
+    uint32_t held, left;
+    int h, at;
+    __device__ __forceinline__ Walk(const uint32_t* p, int64_t stride, int n, int heads)
+        : bits(p), head_stride(stride), total((int64_t)n * heads), words(n), base(-64), q0(0), some(0), held(0), left(0), h(0), at(0)
     {
-        h = words > 0 ? 0 : heads;
-        word = -1;
-        left = 0;
-        q0 = 0;
     }
     __device__ __forceinline__ bool next()
     {
-        if (h >= heads) return false;
         while (left == 0) {
-            if (++word == words) {
-                word = 0;
-                if (++h == heads) return false;
+            while (some == 0) {
+                base += 64;
+                if (base >= total) return false;
+                const int64_t i = base + lane_id();
+                held = i < total ? bits[i / words * head_stride + i % words] : 0;
+                some = ballot(held != 0);
             }
-            left = __builtin_amdgcn_readfirstlane(bits[h * head_stride + word]);
+            at = __builtin_ctzll(some);
+            some &= some - 1;
+            left = __builtin_amdgcn_readlane(held, at);
         }
         const int bit = __builtin_ctz(left);
         left &= left - 1;
-        q0 = (word * 32 + bit) * QG;
+        const int64_t i = base + at;
+        h = (int)(i / words);
+        q0 = (i - (int64_t)h * words) * 32 * QG + bit * QG;
         return true;
     }
 };
@@ -241,9 +251,8 @@ struct GkvShared {
 // One kind of wave: FOR_V gv, else gk. Both kinds pass the same barriers.
 template <typename T, int D, bool FOR_V>
 __device__ __forceinline__ void gkv_wave(GkvShared<T, D>& sh, const View<const T>& go, const View<const T>& q,
-                                         const View<const T>& k, const View<const T>& v, const float* __restrict__ lse,
-                                         const float* __restrict__ delta, const uint32_t* __restrict__ bits, int64_t blk,
-                                         int64_t b, int64_t hk, int64_t len, const View<T>& result, const AttnArgs& a,
+                                         const View<const T>& k, const View<const T>& v, const float* __restrict__ rows,
+                                         const uint32_t* __restrict__ bits, int64_t blk, int64_t b, int64_t hk, int64_t len, const View<T>& result, const AttnArgs& a,
                                          int wave)
 {
     const int lane = lane_id(), hi = lane >> 5, kh = wave & 1, qh = (wave >> 1) & 1;
@@ -260,12 +269,8 @@ __device__ __forceinline__ void gkv_wave(GkvShared<T, D>& sh, const View<const T
 #pragma unroll
     for (int t = 0; t < D / 32; ++t) acc[t] = zero16();
 
-    Walk w;
-    w.words = (a.groups + 31) / 32;
-    w.head_stride = a.blocks * w.words;
-    w.bits = bits + ((b * a.heads_q + hk * per) * a.blocks + blk) * w.words;
-    w.heads = per;
-    w.start();
+    const int words = (int)((a.groups + 31) / 32);
+    Walk w(bits + ((b * a.heads_q + hk * per) * a.blocks + blk) * words, a.blocks * words, words, per);
     const TileLoad<T, D, 4> load_q(q.st), load_g(go.st);
     auto load = [&](int stage) __attribute__((always_inline)) {
         const int64_t h = hk * per + w.h;
@@ -273,14 +278,12 @@ __device__ __forceinline__ void gkv_wave(GkvShared<T, D>& sh, const View<const T
         constexpr int HALF = FOR_V ? 0 : 1;
         load_q(sh.tile[stage][0][HALF], q.at(b, 0, h), w.q0 + HALF * 64, a.tokens_q - 1, wave & 3);
         load_g(sh.tile[stage][1][HALF], go.at(b, 0, h), w.q0 + HALF * 64, a.tokens_q - 1, wave & 3);
-        if (FOR_V && threadIdx.x < QG) {
-            const int64_t i = w.q0 + threadIdx.x;
-            const bool on = i < a.tokens_q;
-            const int64_t at = (b * a.heads_q + h) * a.tokens_q + (on ? i : a.tokens_q - 1);
-            const float ls = lse[at], dl = delta[at];
-            // queries past the end and queries that saw nothing: P = 0
-            sh.row[stage][0][threadIdx.x] = on && ls > -INFINITY ? -ls * LOG2E : -INFINITY;
-            sh.row[stage][1][threadIdx.x] = dl;
+        // and the four gv waves the group's 2 x 128 row values, as they are
+        // (a load into registers would wait for all the loads before it)
+        if constexpr (FOR_V) {
+            const float* src = rows + (((b * a.heads_q + h) * a.groups + w.q0 / QG) * 4 + wave) * 64 + lane;
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                             (__attribute__((address_space(3))) void*)(&sh.row[stage][0][0] + wave * 64), 4, 0, 0);
         }
     };
     bool more = w.next();
@@ -361,8 +364,8 @@ __device__ __forceinline__ void gkv_wave(GkvShared<T, D>& sh, const View<const T
 
 template <typename T, int D>
 __global__ __launch_bounds__(GKV_THREADS, D == 64 ? 4 : 2) void k_attn_gkv(
-    View<const T> go, View<const T> q, View<const T> k, View<const T> v, const float* __restrict__ lse,
-    const float* __restrict__ delta, const uint32_t* __restrict__ bits, const uint32_t* __restrict__ order,
+    View<const T> go, View<const T> q, View<const T> k, View<const T> v, const float* __restrict__ rows,
+    const uint32_t* __restrict__ bits, const uint32_t* __restrict__ order,
     const int32_t* __restrict__ kv_len, View<T> gk, View<T> gv, const AttnArgs a)
 {
     __shared__ GkvShared<T, D> sh;
@@ -372,15 +375,15 @@ __global__ __launch_bounds__(GKV_THREADS, D == 64 ? 4 : 2) void k_attn_gkv(
     const int64_t b = bh / a.heads_k, hk = bh - b * a.heads_k;
     const int64_t len = seq_len(kv_len, b, a.tokens_k);
     if (wave < 4)
-        gkv_wave<T, D, true>(sh, go, q, k, v, lse, delta, bits, blk, b, hk, len, gv, a, wave);
+        gkv_wave<T, D, true>(sh, go, q, k, v, rows, bits, blk, b, hk, len, gv, a, wave);
     else
-        gkv_wave<T, D, false>(sh, go, q, k, v, lse, delta, bits, blk, b, hk, len, gk, a, wave);
+        gkv_wave<T, D, false>(sh, go, q, k, v, rows, bits, blk, b, hk, len, gk, a, wave);
 }
 
 template <typename T, int D>
 static gs_status attn_bwd_launch(const gs_tokens* go, const gs_tokens* q, const gs_tokens* k, const gs_tokens* v,
                                  const gs_tokens* out, const float* lse, const int32_t* list, const int32_t* kv_len,
-                                 const gs_tokens* gq, const gs_tokens* gk, const gs_tokens* gv, float* delta,
+                                 const gs_tokens* gq, const gs_tokens* gk, const gs_tokens* gv, float* rows,
                                  uint32_t* bits, uint32_t* order, int64_t batch, const AttnArgs& a, hipStream_t s)
 {
     const int64_t lists = batch * a.heads_q * a.groups, blocks = batch * a.heads_k * a.blocks;
@@ -388,7 +391,7 @@ static gs_status attn_bwd_launch(const gs_tokens* go, const gs_tokens* q, const 
     if (lists > 0) {
         hipLaunchKernelGGL((k_attn_gq<T, D>), dim3((unsigned)lists), dim3(ATT_THREADS), 0, s, view_of<const T>(go),
                            view_of<const T>(q), view_of<const T>(k), view_of<const T>(v), view_of<const T>(out), lse, list,
-                           kv_len, view_of<T>(gq), delta, a);
+                           kv_len, view_of<T>(gq), rows, a);
         GS_CHECK_LAUNCH();
     }
     if (blocks > 0) {
@@ -403,16 +406,16 @@ static gs_status attn_bwd_launch(const gs_tokens* go, const gs_tokens* q, const 
         hipLaunchKernelGGL(k_block_order, dim3((unsigned)(batch * a.heads_k)), dim3(ATT_THREADS), 0, s, bits, order, a);
         GS_CHECK_LAUNCH();
         hipLaunchKernelGGL((k_attn_gkv<T, D>), dim3((unsigned)blocks), dim3(GKV_THREADS), 0, s, view_of<const T>(go),
-                           view_of<const T>(q), view_of<const T>(k), view_of<const T>(v), lse, delta, bits, order, kv_len,
+                           view_of<const T>(q), view_of<const T>(k), view_of<const T>(v), rows, bits, order, kv_len,
                            view_of<T>(gk), view_of<T>(gv), a);
         GS_CHECK_LAUNCH();
     }
     return GS_OK;
 }
 
-static size_t delta_bytes(int64_t batch, int64_t tokens_q, int32_t heads_q)
+static size_t row_bytes(int64_t batch, int64_t tokens_q, int32_t heads_q)
 {
-    return (size_t)((batch * heads_q * tokens_q * 4 + 15) / 16 * 16);
+    return (size_t)(batch * heads_q * ((tokens_q + QG - 1) / QG)) * 2 * QG * 4;
 }
 
 static int64_t bits_words(int64_t batch, int64_t groups, int64_t blocks, int32_t heads_q)
@@ -430,7 +433,7 @@ size_t gs_block_attn_bwd_workspace_bytes(int64_t batch, int64_t tokens_q, int64_
     using namespace gs;
     if (attn_check(batch, tokens_q, tokens_k, heads_q, heads_k, dim, GS_BF16, 1, 1.f) != GS_OK) return 0;
     const int64_t groups = (tokens_q + QG - 1) / QG, blocks = (tokens_k + KB - 1) / KB;
-    return delta_bytes(batch, tokens_q, heads_q) + (size_t)(bits_words(batch, groups, blocks, heads_q) + batch * heads_k * blocks) * 4 + 16;
+    return row_bytes(batch, tokens_q, heads_q) + (size_t)(bits_words(batch, groups, blocks, heads_q) + batch * heads_k * blocks) * 4 + 16;
 }
 
 gs_status gs_block_attn_bwd(const gs_tokens* gout, const gs_tokens* q, const gs_tokens* k, const gs_tokens* v,
@@ -458,15 +461,15 @@ gs_status gs_block_attn_bwd(const gs_tokens* gout, const gs_tokens* q, const gs_
             if (!attn_view_ok(t, batch, tokens_k, heads_k)) return GS_ERR_UNSUPPORTED;
     const AttnArgs a{tokens_q, tokens_k, (tokens_q + QG - 1) / QG, (tokens_k + KB - 1) / KB, heads_q, heads_k,
                      causal != 0, top, 1, sm_scale};
-    float* delta = (float*)ws;
-    uint32_t* bits = (uint32_t*)((char*)ws + delta_bytes(batch, tokens_q, heads_q));
+    float* rows = (float*)ws;
+    uint32_t* bits = (uint32_t*)((char*)ws + row_bytes(batch, tokens_q, heads_q));
     uint32_t* order = bits + bits_words(batch, a.groups, a.blocks, heads_q);
     const hipStream_t s = (hipStream_t)stream;
     if (dtype == GS_BF16)
-        return dim == 128 ? attn_bwd_launch<bf16, 128>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, delta, bits, order, batch, a, s)
-                          : attn_bwd_launch<bf16, 64>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, delta, bits, order, batch, a, s);
-    return dim == 128 ? attn_bwd_launch<f16, 128>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, delta, bits, order, batch, a, s)
-                      : attn_bwd_launch<f16, 64>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, delta, bits, order, batch, a, s);
+        return dim == 128 ? attn_bwd_launch<bf16, 128>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, rows, bits, order, batch, a, s)
+                          : attn_bwd_launch<bf16, 64>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, rows, bits, order, batch, a, s);
+    return dim == 128 ? attn_bwd_launch<f16, 128>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, rows, bits, order, batch, a, s)
+                      : attn_bwd_launch<f16, 64>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, rows, bits, order, batch, a, s);
 }
 
 }  // extern "C"
