@@ -133,6 +133,11 @@ __device__ __forceinline__ void interleave()
     __builtin_amdgcn_sched_group_barrier(0x008, AHEAD / PER, 0);
 }
 
+// Loads to LDS are waited for here, before the barrier that hands the stage
+// over. The compiler must not wait for them by itself, at reads of the other
+// stage: it does so at the first transposing read unless the accesses carry
+// alias scopes, which they get where the body is an inlined function with
+// __restrict__ arguments. Hence each kernel below is one.
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // In both reads r0 is a multiple of 16, which the swizzle does not see: it goes
@@ -253,13 +258,7 @@ template <typename Step, typename More, typename Cut>
 __device__ __forceinline__ void walk_blocks(Step&& step, More&& more, Cut&& cut)
 {
     int stage = 0;
-    while (more() && !cut()) {
-        step(0, std::false_type{});
-        stage = 1;
-        if (!more() || cut()) break;
-        step(1, std::false_type{});
-        stage = 0;
-    }
+    for (; more() && !cut(); stage ^= 1) step(stage, std::false_type{});
     for (; more(); stage ^= 1) step(stage, std::true_type{});
 }
 

@@ -85,12 +85,11 @@ __device__ __forceinline__ void attend_block(const T* kt, const T* vt, const typ
 // Many queries: a workgroup per (batch, head, group), four waves of 32
 // queries, the listed blocks one after the other through two LDS stages.
 template <typename T, int D>
-__global__ __launch_bounds__(ATT_THREADS, D == 64 ? 4 : 2) void k_attn_fwd(View<const T> q, View<const T> k, View<const T> v,
-                                                             const int32_t* __restrict__ lists,
-                                                             const int32_t* __restrict__ kv_len, View<T> out,
-                                                             float* __restrict__ lse, const AttnArgs a)
+__device__ __forceinline__ void attn_fwd(T (&s_tile)[2][2][Tile<D>::ELEMS], const View<const T>& q, const View<const T>& k,
+                                         const View<const T>& v, const int32_t* __restrict__ lists,
+                                         const int32_t* __restrict__ kv_len, const View<T>& out,
+                                         float* __restrict__ lse, const AttnArgs& a)
 {
-    __shared__ alignas(16) T s_tile[2][2][Tile<D>::ELEMS];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), hi = lane >> 5;
     const int64_t id = xcd_contiguous(blockIdx.x, gridDim.x);
     const int64_t bh = id / a.groups, g = id - bh * a.groups;
@@ -145,6 +144,16 @@ __global__ __launch_bounds__(ATT_THREADS, D == 64 ? 4 : 2) void k_attn_fwd(View<
             store4<T>(o + t * 32 + r * 8 + hi * 4, st.o[t][4 * r] * inv, st.o[t][4 * r + 1] * inv,
                       st.o[t][4 * r + 2] * inv, st.o[t][4 * r + 3] * inv);
     if (hi == 0) lse[bh * a.tokens_q + i] = l > 0.f ? (st.m + log2f(l)) * LN2 : -INFINITY;
+}
+
+template <typename T, int D>
+__global__ __launch_bounds__(ATT_THREADS, D == 64 ? 4 : 2) void k_attn_fwd(View<const T> q, View<const T> k,
+                                                                          View<const T> v, const int32_t* lists,
+                                                                          const int32_t* kv_len, View<T> out, float* lse,
+                                                                          const AttnArgs a)
+{
+    __shared__ alignas(16) T s_tile[2][2][Tile<D>::ELEMS];
+    attn_fwd<T, D>(s_tile, q, k, v, lists, kv_len, out, lse, a);
 }
 
 // Few queries: a workgroup per 32 queries and split of their list; its four

@@ -45,14 +45,12 @@ __global__ __launch_bounds__(ATT_THREADS) void k_list_bits(const int32_t* __rest
 // queries, [list][2][128]): four waves of 32 queries, the listed blocks in turn.
 //   dS^T = P^T (V gout^T - D),  gq^T += K^T dS^T
 template <typename T, int D>
-__global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_gq(View<const T> go, View<const T> q, View<const T> k,
-                                                            View<const T> v, View<const T> out,
-                                                            const float* __restrict__ lse,
-                                                            const int32_t* __restrict__ lists,
-                                                            const int32_t* __restrict__ kv_len, View<T> gq,
-                                                            float* __restrict__ rows, const AttnArgs a)
+__device__ __forceinline__ void attn_gq(T (&s_tile)[2][2][Tile<D>::ELEMS], const View<const T>& go, const View<const T>& q,
+                                        const View<const T>& k, const View<const T>& v, const View<const T>& out,
+                                        const float* __restrict__ lse, const int32_t* __restrict__ lists,
+                                        const int32_t* __restrict__ kv_len, const View<T>& gq, float* __restrict__ rows,
+                                        const AttnArgs& a)
 {
-    __shared__ alignas(16) T s_tile[2][2][Tile<D>::ELEMS];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), hi = lane >> 5;
     const int64_t id = xcd_contiguous(blockIdx.x, gridDim.x);
     const int64_t bh = id / a.groups, g = id - bh * a.groups;
@@ -150,6 +148,16 @@ __global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_gq(View<const T> go, Vi
         for (int r = 0; r < 4; ++r)
             store4<T>(o + t * 32 + r * 8 + hi * 4, acc[t][4 * r] * a.scale, acc[t][4 * r + 1] * a.scale,
                       acc[t][4 * r + 2] * a.scale, acc[t][4 * r + 3] * a.scale);
+}
+
+template <typename T, int D>
+__global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_gq(View<const T> go, View<const T> q, View<const T> k,
+                                                            View<const T> v, View<const T> out, const float* lse,
+                                                            const int32_t* lists, const int32_t* kv_len, View<T> gq,
+                                                            float* rows, const AttnArgs a)
+{
+    __shared__ alignas(16) T s_tile[2][2][Tile<D>::ELEMS];
+    attn_gq<T, D>(s_tile, go, q, k, v, out, lse, lists, kv_len, gq, rows, a);
 }
 
 // Walks the (head of the key head, group of queries) pairs that list a block;
