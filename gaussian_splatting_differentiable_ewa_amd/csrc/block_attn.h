@@ -171,6 +171,50 @@ __device__ __forceinline__ typename Mma<T>::v8 read_cols(const T* tile, int r0, 
     return u.v;
 }
 
+// The same reads with the lane's LDS addresses held in registers, for a kernel
+// whose tiles lie at multiples of a power of two from LDS address 0: a stage
+// is then one bit of the address, flipped in place, and everything else (the
+// operand, the half, rows) an offset of the instruction.
+template <typename T, int D>
+struct LaneAddresses {
+    uint32_t row[D / 16], col[D / 32][2];
+    __device__ __forceinline__ LaneAddresses(uint32_t r0)
+    {
+        const int l = lane_id(), hi = l >> 5;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) row[x] = (r0 * D + Tile<D>::at(l & 31, x * 2 + hi)) * sizeof(T);
+#pragma unroll
+        for (int y = 0; y < D / 32; ++y)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int c = y * 32 + (l & 16) + 4 * (l & 3);
+                col[y][i] = (r0 * D + Tile<D>::at(8 * i + 4 * hi + ((l & 15) >> 2), c >> 3) + (c & 7)) * sizeof(T);
+            }
+    }
+    __device__ __forceinline__ void flip(uint32_t bit)
+    {
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) row[x] ^= bit;
+#pragma unroll
+        for (int y = 0; y < D / 32; ++y) col[y][0] ^= bit, col[y][1] ^= bit;
+    }
+    __device__ __forceinline__ typename Mma<T>::v8 rows(int x, uint32_t offset) const
+    {
+        return *(const __attribute__((address_space(3))) typename Mma<T>::v8*)(row[x] + offset);
+    }
+    __device__ __forceinline__ typename Mma<T>::v8 cols(int y, uint32_t offset) const
+    {
+        union {
+            short4v h[2];
+            typename Mma<T>::v8 v;
+        } u;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            u.h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4v*)(col[y][i] + offset));
+        return u.v;
+    }
+};
+
 // B operand kept in registers: column = token, k = 16 step + 8 (l >> 5) ...
 template <typename T, int D>
 __device__ __forceinline__ void load_cols(const T* row, typename Mma<T>::v8 (&out)[D / 16])

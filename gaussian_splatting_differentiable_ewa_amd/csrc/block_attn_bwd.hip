@@ -168,12 +168,12 @@ struct Walk {
     int64_t head_stride, total;
     int words;
     // state
-    int64_t base, q0;
+    int64_t base;
     uint64_t some;  // lanes with words left
     uint32_t held, left;
-    int h, at;
+    int h, at, q0;
     __device__ __forceinline__ Walk(const uint32_t* p, int64_t stride, int n, int heads)
-        : bits(p), head_stride(stride), total((int64_t)n * heads), words(n), base(-64), q0(0), some(0), held(0), left(0), h(0), at(0)
+        : bits(p), head_stride(stride), total((int64_t)n * heads), words(n), base(-64), some(0), held(0), left(0), h(0), at(0), q0(0)
     {
     }
     __device__ __forceinline__ bool next()
@@ -194,7 +194,7 @@ struct Walk {
         left &= left - 1;
         const int64_t i = base + at;
         h = (int)(i / words);
-        q0 = (i - (int64_t)h * words) * 32 * QG + bit * QG;
+        q0 = ((int)(i - (int64_t)h * words) * 32 + bit) * QG;
         return true;
     }
 };
@@ -250,83 +250,95 @@ __global__ __launch_bounds__(ATT_THREADS) void k_block_order(const uint32_t* __r
 // formed twice (5 products instead of 4). Stages are whole groups.
 constexpr int GKV_THREADS = 512;
 
+// LDS of the workgroup (dynamic, so that it begins at LDS address 0): stage,
+// then q and gout, then the halves of the group as tiles; behind them the
+// stages' row values (-lse in base 2, D).
 template <typename T, int D>
-struct GkvShared {
-    alignas(16) T tile[2][2][2][Tile<D>::ELEMS];  // stage; q, gout; half of the group
-    alignas(16) float row[2][2][QG];              // stage; -lse in base 2, D; query
+struct GkvLds {
+    static constexpr uint32_t TILE = Tile<D>::ELEMS * sizeof(T), OPERAND = 2 * TILE, STAGE = 2 * OPERAND;
+    static constexpr uint32_t ROWS = 2 * STAGE, ROW_STAGE = 2 * QG * 4, BYTES = ROWS + 2 * ROW_STAGE;
 };
 
 // One kind of wave: FOR_V gv, else gk. Both kinds pass the same barriers.
 template <typename T, int D, bool FOR_V>
-__device__ __forceinline__ void gkv_wave(GkvShared<T, D>& sh, const View<const T>& go, const View<const T>& q,
+__device__ __forceinline__ void gkv_wave(char* lds, const View<const T>& go, const View<const T>& q,
                                          const View<const T>& k, const View<const T>& v, const float* __restrict__ rows,
-                                         const uint32_t* __restrict__ bits, int64_t blk, int64_t b, int64_t hk, int64_t len, const View<T>& result, const AttnArgs& a,
-                                         int wave)
+                                         const uint32_t* __restrict__ bits, int blk, int b, int hk, int len,
+                                         const View<T>& result, const AttnArgs& a, int wave)
 {
+    using M = GkvLds<T, D>;
+    typedef typename Mma<T>::v8 v8;
     const int lane = lane_id(), hi = lane >> 5, kh = wave & 1, qh = (wave >> 1) & 1;
-    const int per = a.heads_q / a.heads_k;
-    const int64_t past = len - a.tokens_q;
-    const int64_t key = blk * KB + kh * 32 + (lane & 31);
-    // keys past the end hold anything: take a valid one, its P is masked
-    const int64_t last = len > 0 ? len - 1 : 0, kc = key < last ? key : last;
+    const int per = a.heads_q / a.heads_k, tokens_q = (int)a.tokens_q, past = len - tokens_q;
+    const int key = blk * KB + kh * 32 + (lane & 31);
     const float c = a.scale * LOG2E;
-    typename Mma<T>::v8 kf[D / 16], vf[FOR_V ? 1 : D / 16];
-    load_cols<T, D>(k.at(b, kc, hk), kf);
-    if constexpr (!FOR_V) load_cols<T, D>(v.at(b, kc, hk), vf);
+    v8 kf[D / 16], vf[FOR_V ? 1 : D / 16];
+    {
+        // keys past the end hold anything: take a valid one, its P is masked
+        const int last = len > 0 ? len - 1 : 0, kc = key < last ? key : last;
+        load_cols<T, D>(k.at(b, kc, hk), kf);
+        if constexpr (!FOR_V) load_cols<T, D>(v.at(b, kc, hk), vf);
+    }
     acc16 acc[D / 32];
 #pragma unroll
     for (int t = 0; t < D / 32; ++t) acc[t] = zero16();
 
     const int words = (int)((a.groups + 31) / 32);
-    Walk w(bits + ((b * a.heads_q + hk * per) * a.blocks + blk) * words, a.blocks * words, words, per);
+    Walk w(bits + (((int64_t)b * a.heads_q + hk * per) * a.blocks + blk) * words, a.blocks * words, words, per);
     const TileLoad<T, D, 4> load_q(q.st), load_g(go.st);
-    auto load = [&](int stage) __attribute__((always_inline)) {
-        const int64_t h = hk * per + w.h;
+    auto load = [&](uint32_t stage) __attribute__((always_inline)) {
+        const int h = hk * per + w.h;
         // the four waves of a kind load a half
         constexpr int HALF = FOR_V ? 0 : 1;
-        load_q(sh.tile[stage][0][HALF], q.at(b, 0, h), w.q0 + HALF * 64, a.tokens_q - 1, wave & 3);
-        load_g(sh.tile[stage][1][HALF], go.at(b, 0, h), w.q0 + HALF * 64, a.tokens_q - 1, wave & 3);
+        T* to = (T*)(lds + stage * M::STAGE + HALF * M::TILE);
+        load_q(to, q.at(b, 0, h), w.q0 + HALF * 64, tokens_q - 1, wave & 3);
+        load_g(to + 2 * Tile<D>::ELEMS, go.at(b, 0, h), w.q0 + HALF * 64, tokens_q - 1, wave & 3);
         // and the four gv waves the group's 2 x 128 row values, as they are
         // (a load into registers would wait for all the loads before it)
         if constexpr (FOR_V) {
-            const float* src = rows + (((b * a.heads_q + h) * a.groups + w.q0 / QG) * 4 + wave) * 64 + lane;
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                             (__attribute__((address_space(3))) void*)(&sh.row[stage][0][0] + wave * 64), 4, 0, 0);
+            const float* src = rows + ((((int64_t)b * a.heads_q + h) * a.groups + w.q0 / QG) * 4 + wave) * 64 + lane;
+            __builtin_amdgcn_global_load_lds(
+                (const __attribute__((address_space(1))) void*)src,
+                (__attribute__((address_space(3))) void*)(lds + M::ROWS + stage * M::ROW_STAGE + wave * 256), 4, 0, 0);
         }
     };
+    LaneAddresses<T, D> at(qh * 32);
+    uint32_t stage = 0;
     bool more = w.next();
-    int64_t q0 = w.q0;
+    int q0 = w.q0;
     if (more) load(0);
-    for (int stage = 0; more; stage ^= 1) {
+    while (more) {
         wait_loads();
         __syncthreads();
-        const int64_t now = q0;
+        const int now = q0;
         more = w.next();
         q0 = w.q0;
         if (more) load(stage ^ 1);
+        const float* row = (const float*)(lds + M::ROWS + stage * M::ROW_STAGE) + qh * 32 + 4 * hi;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             // (a second half past the last query has P = 0 throughout)
-            const T *qt = sh.tile[stage][0][half], *gt = sh.tile[stage][1][half];
-            const int row = half * 64 + qh * 32;
-            const float* nl = &sh.row[stage][0][row + 4 * hi];
-            const float* dl = &sh.row[stage][1][row + 4 * hi];
+            constexpr uint32_t Q = 0, G = M::OPERAND;
+            const uint32_t h0 = half * M::TILE;
             acc16 s = zero16(), p = zero16();
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int x = 0; x < D / 16; ++x) s = Mma<T>::mma(read_rows<T, D>(qt, qh * 32, x), kf[x], s);
+            for (int x = 0; x < D / 16; ++x) s = Mma<T>::mma(at.rows(x, Q + h0), kf[x], s);
             if constexpr (!FOR_V) {
 #pragma unroll
-                for (int x = 0; x < D / 16; ++x) p = Mma<T>::mma(read_rows<T, D>(gt, qh * 32, x), vf[x], p);
+                for (int x = 0; x < D / 16; ++x) p = Mma<T>::mma(at.rows(x, G + h0), vf[x], p);
             }
             interleave<(FOR_V ? 1 : 2) * D / 16, (FOR_V ? 1 : 2) * D / 16, 4>();
+            __builtin_amdgcn_sched_barrier(0);
+            const float* nl = row + half * 64;
+            const float* dl = nl + QG;
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = exp2_fast(fmaf(s[r], c, nl[c_row(r, 0)]));
-            const int64_t first = now + row;
+            const int first = now + half * 64 + qh * 32;
             if ((blk + 1) * KB > (a.causal && past + first + 1 < len ? past + first + 1 : len)) {
                 asm volatile("");  // a branch, not selects in every step
                 // rows from `from` on see this lane's key
-                const int64_t d = a.causal ? key - past - first - 4 * hi : 0;
-                const int from = key >= len ? 64 : (int)(d > 64 ? 64 : (d < 0 ? 0 : d));
+                const int from = key >= len ? 64 : (a.causal ? key - past - first - 4 * hi : 0);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] = c_row(r, 0) >= from ? s[r] : 0.f;
             }
@@ -334,21 +346,24 @@ __device__ __forceinline__ void gkv_wave(GkvShared<T, D>& sh, const View<const T
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] *= p[r] - dl[c_row(r, 0)];
             }
+            const v8 op0 = as_operand<T>(s, 0), op1 = as_operand<T>(s, 1);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const typename Mma<T>::v8 op = as_operand<T>(s, x);
 #pragma unroll
                 for (int y = 0; y < D / 32; ++y)
-                    acc[y] = Mma<T>::mma(read_cols<T, D>(FOR_V ? gt : qt, qh * 32 + x * 16, y * 32), op, acc[y]);
+                    acc[y] = Mma<T>::mma(at.cols(y, (FOR_V ? G : Q) + h0 + x * 16 * D * sizeof(T)), x ? op1 : op0, acc[y]);
             }
-            interleave<D / 8, D / 16, 4>();
-            __builtin_amdgcn_sched_barrier(0);  // keeps the halves' registers apart
+            interleave<D / 8, D / 16, 8>();
+            __builtin_amdgcn_sched_barrier(0);
         }
+        at.flip(M::STAGE);
+        stage ^= 1;
     }
     // join the query halves: the second one's sums through LDS
     __syncthreads();
     constexpr int REGS = D / 32 * 16;
-    float* mine = (float*)&sh.tile[0][0][0][0] + ((FOR_V ? 2 : 0) + kh) * REGS * 64 + lane;
+    float* mine = (float*)lds + ((FOR_V ? 2 : 0) + kh) * REGS * 64 + lane;
     if (qh == 1) {
 #pragma unroll
         for (int t = 0; t < D / 32; ++t)
@@ -371,21 +386,22 @@ __device__ __forceinline__ void gkv_wave(GkvShared<T, D>& sh, const View<const T
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__(GKV_THREADS, D == 64 ? 4 : 2) void k_attn_gkv(
-    View<const T> go, View<const T> q, View<const T> k, View<const T> v, const float* __restrict__ rows,
-    const uint32_t* __restrict__ bits, const uint32_t* __restrict__ order,
-    const int32_t* __restrict__ kv_len, View<T> gk, View<T> gv, const AttnArgs a)
+__global__ __launch_bounds__(GKV_THREADS, D == 64 ? 4 : 2) void k_attn_gkv(View<const T> go, View<const T> q,
+                                                                          View<const T> k, View<const T> v,
+                                                                          const float* rows, const uint32_t* bits,
+                                                                          const uint32_t* order, const int32_t* kv_len,
+                                                                          View<T> gk, View<T> gv, const AttnArgs a)
 {
-    __shared__ GkvShared<T, D> sh;
+    extern __shared__ __align__(16) char s_lds[];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t id = xcd_contiguous(blockIdx.x, gridDim.x);
-    const int64_t bh = id / a.blocks, blk = order[id];
-    const int64_t b = bh / a.heads_k, hk = bh - b * a.heads_k;
-    const int64_t len = seq_len(kv_len, b, a.tokens_k);
+    const int bh = (int)(id / a.blocks), blk = (int)order[id];
+    const int b = bh / a.heads_k, hk = bh - b * a.heads_k;
+    const int len = (int)seq_len(kv_len, b, a.tokens_k);
     if (wave < 4)
-        gkv_wave<T, D, true>(sh, go, q, k, v, rows, bits, blk, b, hk, len, gv, a, wave);
+        gkv_wave<T, D, true>(s_lds, go, q, k, v, rows, bits, blk, b, hk, len, gv, a, wave);
     else
-        gkv_wave<T, D, false>(sh, go, q, k, v, rows, bits, blk, b, hk, len, gk, a, wave);
+        gkv_wave<T, D, false>(s_lds, go, q, k, v, rows, bits, blk, b, hk, len, gk, a, wave);
 }
 
 template <typename T, int D>
@@ -413,7 +429,11 @@ static gs_status attn_bwd_launch(const gs_tokens* go, const gs_tokens* q, const 
         }
         hipLaunchKernelGGL(k_block_order, dim3((unsigned)(batch * a.heads_k)), dim3(ATT_THREADS), 0, s, bits, order, a);
         GS_CHECK_LAUNCH();
-        hipLaunchKernelGGL((k_attn_gkv<T, D>), dim3((unsigned)blocks), dim3(GKV_THREADS), 0, s, view_of<const T>(go),
+        constexpr uint32_t lds = GkvLds<T, D>::BYTES;
+        if (lds > 65536 && hipFuncSetAttribute((const void*)k_attn_gkv<T, D>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)lds) != hipSuccess)
+            return GS_ERR_HIP;
+        hipLaunchKernelGGL((k_attn_gkv<T, D>), dim3((unsigned)blocks), dim3(GKV_THREADS), lds, s, view_of<const T>(go),
                            view_of<const T>(q), view_of<const T>(k), view_of<const T>(v), rows, bits, order, kv_len,
                            view_of<T>(gk), view_of<T>(gv), a);
         GS_CHECK_LAUNCH();
