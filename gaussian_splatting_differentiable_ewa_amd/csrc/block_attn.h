@@ -102,13 +102,13 @@ struct TileLoad {
         if (t0 + 63 <= last) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const uint32_t x = D == 128 ? (i & 3) * 16 : (i & 1) * 32;
+                const uint32_t x = D == 128 ? ((wave * PER + i) & 3) * 16 : ((wave * PER + i) & 1) * 32;
                 one(to + i * 512, (const char*)(first + i * ROWS * stride) + ((chunk ^ x) + row));
             }
         } else {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const uint32_t x = D == 128 ? (i & 3) * 16 : (i & 1) * 32;
+                const uint32_t x = D == 128 ? ((wave * PER + i) & 3) * 16 : ((wave * PER + i) & 1) * 32;
                 const int64_t t = t0 + (wave * PER + i) * ROWS + lane_id() / CH;
                 one(to + i * 512, (const char*)(base + (t < last ? t : last) * stride) + (chunk ^ x));
             }
@@ -116,15 +116,15 @@ struct TileLoad {
     }
 };
 
-// Order of the instructions around: AHEAD + N LDS reads and MFMAS matrix
-// instructions, the reads AHEAD of their use, PER reads after each matrix
-// instruction. (The compiler by itself reads one operand and waits for it.)
-template <int READS, int MFMAS, int AHEAD>
+// Order of the instructions around: READS LDS reads (and FIRST more before
+// them) and MFMAS matrix instructions, the reads AHEAD of their use. (The
+// compiler by itself reads one operand and waits for it.)
+template <int READS, int MFMAS, int AHEAD, int FIRST = 0>
 __device__ __forceinline__ void interleave()
 {
     constexpr int PER = READS / MFMAS;
     static_assert(READS % MFMAS == 0 && AHEAD % PER == 0, "whole operands");
-    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, FIRST + AHEAD, 0);
 #pragma unroll
     for (int i = 0; i < MFMAS - AHEAD / PER; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
@@ -172,9 +172,8 @@ __device__ __forceinline__ typename Mma<T>::v8 read_cols(const T* tile, int r0, 
 }
 
 // The same reads with the lane's LDS addresses held in registers, for a kernel
-// whose tiles lie at multiples of a power of two from LDS address 0: a stage
-// is then one bit of the address, flipped in place, and everything else (the
-// operand, the half, rows) an offset of the instruction.
+// whose tiles begin at LDS address 0: moving to another stage is one addition
+// each, and the operand, the half and rows are offsets of the instruction.
 template <typename T, int D>
 struct LaneAddresses {
     uint32_t row[D / 16], col[D / 32][2];
@@ -191,12 +190,12 @@ struct LaneAddresses {
                 col[y][i] = (r0 * D + Tile<D>::at(8 * i + 4 * hi + ((l & 15) >> 2), c >> 3) + (c & 7)) * sizeof(T);
             }
     }
-    __device__ __forceinline__ void flip(uint32_t bit)
+    __device__ __forceinline__ void move(uint32_t by)
     {
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) row[x] ^= bit;
+        for (int x = 0; x < D / 16; ++x) row[x] += by;
 #pragma unroll
-        for (int y = 0; y < D / 32; ++y) col[y][0] ^= bit, col[y][1] ^= bit;
+        for (int y = 0; y < D / 32; ++y) col[y][0] += by, col[y][1] += by;
     }
     __device__ __forceinline__ typename Mma<T>::v8 rows(int x, uint32_t offset) const
     {

@@ -238,170 +238,227 @@ __global__ __launch_bounds__(ATT_THREADS) void k_block_order(const uint32_t* __r
     for (int64_t i = threadIdx.x; i < a.blocks; i += ATT_THREADS) order[bh * a.blocks + atomicAdd(&s_start[cls(i)], 1u)] = (uint32_t)i;
 }
 
-// gk and gv of a block of 64 keys: eight waves, four for either. Wave w of the
-// four: keys 32 (w & 1) .. + 32, and of every 64 queries 32 (w >> 1) .. + 32;
-// the two query halves join at the end. S and dP are formed with queries as
-// rows, so that a lane holds one key:
-//   gv^T += gout^T P,  gk^T += q^T dS
+// gk and gv of a block of 64 keys, 64 queries a step: eight waves, one of
+// either kind on each SIMD.
+//   Four form P and dS of a 32 x 32 tile each (keys 32 kh, queries 32 qh), with
+//   queries as rows, so that a lane holds one key, and leave them in LDS as the
+//   operands they are for: what lane l rounded, lane l reads.
+//   Four take the step before: gv^T += gout^T P or gk^T += q^T dS of 32 keys.
 // Registers decide the shape. One wave with both sums (128 registers at dim
 // 128), k and v (64) and S, dP (32) needs 340 and leaves a SIMD with one wave,
-// which multiplies or computes exponentials but not both. Split by result,
-// either wave fits 256, each SIMD holds one of each kind, and the price is S
-// formed twice (5 products instead of 4). Stages are whole groups.
+// which multiplies or computes exponentials but hardly both (measured: vector
+// instructions behind a matrix instruction of the same wave are not hidden, of
+// another wave they are). Split this way both kinds fit 256, and one
+// multiplies while the other computes. Three stages of queries: one
+// loading, one per kind.
 constexpr int GKV_THREADS = 512;
 
-// LDS of the workgroup (dynamic, so that it begins at LDS address 0): stage,
-// then q and gout, then the halves of the group as tiles; behind them the
-// stages' row values (-lse in base 2, D).
+// LDS of the workgroup, in bytes (dynamic, so that it begins at LDS address 0).
 template <typename T, int D>
 struct GkvLds {
-    static constexpr uint32_t TILE = Tile<D>::ELEMS * sizeof(T), OPERAND = 2 * TILE, STAGE = 2 * OPERAND;
-    static constexpr uint32_t ROWS = 2 * STAGE, ROW_STAGE = 2 * QG * 4, BYTES = ROWS + 2 * ROW_STAGE;
+    static constexpr uint32_t TILE = Tile<D>::ELEMS * sizeof(T);          // q or gout of 64 queries
+    static constexpr uint32_t STAGE = 2 * TILE;                            // q, gout
+    static constexpr uint32_t OPS = 3 * STAGE, OP = 1024;                  // an operand: 16 bytes a lane
+    static constexpr uint32_t ARRAY = 8 * OP, BUFFER = 2 * ARRAY;          // [2 kh][2 qh][2 steps]; P, dS
+    static constexpr uint32_t ROWS = OPS + 2 * BUFFER, ROW_STAGE = 2 * 64 * 4;  // -lse in base 2, D
+    static constexpr uint32_t BYTES = ROWS + 3 * ROW_STAGE;
 };
 
-// One kind of wave: FOR_V gv, else gk. Both kinds pass the same barriers.
-template <typename T, int D, bool FOR_V>
-__device__ __forceinline__ void gkv_wave(char* lds, const View<const T>& go, const View<const T>& q,
-                                         const View<const T>& k, const View<const T>& v, const float* __restrict__ rows,
-                                         const uint32_t* __restrict__ bits, int blk, int b, int hk, int len,
-                                         const View<T>& result, const AttnArgs& a, int wave)
-{
+// The steps of a block, the same for every wave, and this wave's loads.
+template <typename T, int D>
+struct GkvSteps {
     using M = GkvLds<T, D>;
-    typedef typename Mma<T>::v8 v8;
-    const int lane = lane_id(), hi = lane >> 5, kh = wave & 1, qh = (wave >> 1) & 1;
-    const int per = a.heads_q / a.heads_k, tokens_q = (int)a.tokens_q, past = len - tokens_q;
-    const int key = blk * KB + kh * 32 + (lane & 31);
-    const float c = a.scale * LOG2E;
-    v8 kf[D / 16], vf[FOR_V ? 1 : D / 16];
+    char* lds;
+    const View<const T>&q, &go;
+    const float* rows;
+    TileLoad<T, D, 8> load_q, load_g;
+    Walk w;
+    int64_t head0, groups;  // first query head of the batch entry; groups a head
+    int h0, b, tokens_q, wave, q0, half;
+    __device__ __forceinline__ GkvSteps(char* l, const View<const T>& q_, const View<const T>& go_, const float* r,
+                                        const Walk& walk, int b_, int h, const AttnArgs& a, int wave_)
+        : lds(l), q(q_), go(go_), rows(r), load_q(q_.st), load_g(go_.st), w(walk), head0((int64_t)b_ * a.heads_q),
+          groups(a.groups), h0(h), b(b_), tokens_q((int)a.tokens_q), wave(wave_), q0(0), half(1)
     {
-        // keys past the end hold anything: take a valid one, its P is masked
-        const int last = len > 0 ? len - 1 : 0, kc = key < last ? key : last;
-        load_cols<T, D>(k.at(b, kc, hk), kf);
-        if constexpr (!FOR_V) load_cols<T, D>(v.at(b, kc, hk), vf);
     }
-    acc16 acc[D / 32];
-#pragma unroll
-    for (int t = 0; t < D / 32; ++t) acc[t] = zero16();
-
-    const int words = (int)((a.groups + 31) / 32);
-    Walk w(bits + (((int64_t)b * a.heads_q + hk * per) * a.blocks + blk) * words, a.blocks * words, words, per);
-    const TileLoad<T, D, 4> load_q(q.st), load_g(go.st);
-    auto load = [&](uint32_t stage) __attribute__((always_inline)) {
-        const int h = hk * per + w.h;
-        // the four waves of a kind load a half
-        constexpr int HALF = FOR_V ? 0 : 1;
-        T* to = (T*)(lds + stage * M::STAGE + HALF * M::TILE);
-        load_q(to, q.at(b, 0, h), w.q0 + HALF * 64, tokens_q - 1, wave & 3);
-        load_g(to + 2 * Tile<D>::ELEMS, go.at(b, 0, h), w.q0 + HALF * 64, tokens_q - 1, wave & 3);
-        // and the four gv waves the group's 2 x 128 row values, as they are
-        // (a load into registers would wait for all the loads before it)
-        if constexpr (FOR_V) {
-            const float* src = rows + ((((int64_t)b * a.heads_q + h) * a.groups + w.q0 / QG) * 4 + wave) * 64 + lane;
+    __device__ __forceinline__ bool next()
+    {
+        if (half == 0 && q0 + 64 < tokens_q) {
+            half = 1;
+            q0 += 64;
+            return true;
+        }
+        if (!w.next()) return false;
+        half = 0;
+        q0 = w.q0;
+        return true;
+    }
+    __device__ __forceinline__ void load(uint32_t stage) const
+    {
+        const int h = h0 + w.h;
+        T* to = (T*)(lds + stage * M::STAGE);
+        load_q(to, q.at(b, 0, h), q0, tokens_q - 1, wave);
+        load_g(to + Tile<D>::ELEMS, go.at(b, 0, h), q0, tokens_q - 1, wave);
+        if (wave < 2) {  // the row values as they are: through registers they would wait for every load before them
+            const float* src = rows + (((head0 + h) * groups + q0 / QG) * 2 + wave) * QG + q0 % QG + lane_id();
             __builtin_amdgcn_global_load_lds(
                 (const __attribute__((address_space(1))) void*)src,
                 (__attribute__((address_space(3))) void*)(lds + M::ROWS + stage * M::ROW_STAGE + wave * 256), 4, 0, 0);
         }
-    };
+    }
+};
+
+// P and dS, tile by tile. LEAD waves run one step more than they compute.
+template <typename T, int D>
+__device__ __forceinline__ void gkv_scores(GkvSteps<T, D>& steps, const View<const T>& k, const View<const T>& v, int blk,
+                                           int hk, int len, const AttnArgs& a, int wave)
+{
+    using M = GkvLds<T, D>;
+    typedef typename Mma<T>::v8 v8;
+    const int lane = lane_id(), hi = lane >> 5, kh = wave & 1, qh = wave >> 1;
+    const int past = len - (int)a.tokens_q;
+    const int key = blk * KB + kh * 32 + (lane & 31);
+    const float c = a.scale * LOG2E;
+    v8 kf[D / 16], vf[D / 16];
+    {
+        // keys past the end hold anything: take a valid one, its P is masked
+        const int last = len > 0 ? len - 1 : 0, kc = key < last ? key : last;
+        load_cols<T, D>(k.at(steps.b, kc, hk), kf);
+        load_cols<T, D>(v.at(steps.b, kc, hk), vf);
+    }
     LaneAddresses<T, D> at(qh * 32);
-    uint32_t stage = 0;
-    bool more = w.next();
-    int q0 = w.q0;
-    if (more) load(0);
+    uint32_t stage = 0, buffer = 0;
+    bool more = steps.next();
+    if (more) steps.load(0);
     while (more) {
         wait_loads();
         __syncthreads();
-        const int now = q0;
-        more = w.next();
-        q0 = w.q0;
-        if (more) load(stage ^ 1);
-        const float* row = (const float*)(lds + M::ROWS + stage * M::ROW_STAGE) + qh * 32 + 4 * hi;
+        const int first = steps.q0 + qh * 32;
+        const uint32_t after = stage == 2 ? 0 : stage + 1;
+        more = steps.next();
+        if (more) steps.load(after);
+        const float* nl = (const float*)(steps.lds + M::ROWS + stage * M::ROW_STAGE) + qh * 32 + 4 * hi;
+        const float* dl = nl + 64;
+        acc16 s = zero16(), p = zero16();
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            // (a second half past the last query has P = 0 throughout)
-            constexpr uint32_t Q = 0, G = M::OPERAND;
-            const uint32_t h0 = half * M::TILE;
-            acc16 s = zero16(), p = zero16();
-            __builtin_amdgcn_sched_barrier(0);
+        for (int x = 0; x < D / 16; ++x) s = Mma<T>::mma(at.rows(x, 0), kf[x], s);
 #pragma unroll
-            for (int x = 0; x < D / 16; ++x) s = Mma<T>::mma(at.rows(x, Q + h0), kf[x], s);
-            if constexpr (!FOR_V) {
+        for (int x = 0; x < D / 16; ++x) p = Mma<T>::mma(at.rows(x, M::TILE), vf[x], p);
+        interleave<D / 8, D / 8, 4>();
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int x = 0; x < D / 16; ++x) p = Mma<T>::mma(at.rows(x, G + h0), vf[x], p);
-            }
-            interleave<(FOR_V ? 1 : 2) * D / 16, (FOR_V ? 1 : 2) * D / 16, 4>();
-            __builtin_amdgcn_sched_barrier(0);
-            const float* nl = row + half * 64;
-            const float* dl = nl + QG;
+        for (int r = 0; r < 16; ++r) s[r] = exp2_fast(fmaf(s[r], c, nl[c_row(r, 0)]));
+        if ((blk + 1) * KB > (a.causal && past + first + 1 < len ? past + first + 1 : len)) {
+            asm volatile("");  // a branch, not selects in every step
+            // rows from `from` on see this lane's key
+            const int from = key >= len ? 64 : (a.causal ? key - past - first - 4 * hi : 0);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[r] = exp2_fast(fmaf(s[r], c, nl[c_row(r, 0)]));
-            const int first = now + half * 64 + qh * 32;
-            if ((blk + 1) * KB > (a.causal && past + first + 1 < len ? past + first + 1 : len)) {
-                asm volatile("");  // a branch, not selects in every step
-                // rows from `from` on see this lane's key
-                const int from = key >= len ? 64 : (a.causal ? key - past - first - 4 * hi : 0);
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = c_row(r, 0) >= from ? s[r] : 0.f;
-            }
-            if constexpr (!FOR_V) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] *= p[r] - dl[c_row(r, 0)];
-            }
-            const v8 op0 = as_operand<T>(s, 0), op1 = as_operand<T>(s, 1);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-#pragma unroll
-                for (int y = 0; y < D / 32; ++y)
-                    acc[y] = Mma<T>::mma(at.cols(y, (FOR_V ? G : Q) + h0 + x * 16 * D * sizeof(T)), x ? op1 : op0, acc[y]);
-            }
-            interleave<D / 8, D / 16, 8>();
-            __builtin_amdgcn_sched_barrier(0);
+            for (int r = 0; r < 16; ++r) s[r] = c_row(r, 0) >= from ? s[r] : 0.f;
         }
-        at.flip(M::STAGE);
-        stage ^= 1;
-    }
-    // join the query halves: the second one's sums through LDS
-    __syncthreads();
-    constexpr int REGS = D / 32 * 16;
-    float* mine = (float*)lds + ((FOR_V ? 2 : 0) + kh) * REGS * 64 + lane;
-    if (qh == 1) {
+        v8* op = (v8*)(steps.lds + M::OPS + buffer * M::BUFFER + (kh * 2 + qh) * 2 * M::OP) + lane;
+        op[0] = as_operand<T>(s, 0);
+        op[M::OP / 16] = as_operand<T>(s, 1);
 #pragma unroll
-        for (int t = 0; t < D / 32; ++t)
+        for (int r = 0; r < 16; ++r) s[r] *= p[r] - dl[c_row(r, 0)];
+        op[M::ARRAY / 16] = as_operand<T>(s, 0);
+        op[(M::ARRAY + M::OP) / 16] = as_operand<T>(s, 1);
+        at.move(stage == 2 ? (uint32_t)-2 * M::STAGE : M::STAGE);
+        stage = after;
+        buffer ^= 1;
+    }
+    __syncthreads();  // hands over the last step
+}
+
+// gv (FOR_V) or gk of 32 keys: the step before that of the other waves.
+template <typename T, int D, bool FOR_V>
+__device__ __forceinline__ void gkv_sums(GkvSteps<T, D>& steps, const View<T>& result, int blk, int hk, const AttnArgs& a,
+                                         int kh)
+{
+    using M = GkvLds<T, D>;
+    typedef typename Mma<T>::v8 v8;
+    const int lane = lane_id(), hi = lane >> 5, key = blk * KB + kh * 32 + (lane & 31);
+    acc16 acc[D / 32];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) mine[(t * 16 + r) * 64] = acc[t][r];
+    for (int t = 0; t < D / 32; ++t) acc[t] = zero16();
+    LaneAddresses<T, D> at(0);
+    auto sum = [&](uint32_t buffer) __attribute__((always_inline)) {
+        const v8* op = (const v8*)(steps.lds + M::OPS + buffer * M::BUFFER + (FOR_V ? 0 : M::ARRAY) + kh * 4 * M::OP) + lane;
+        __builtin_amdgcn_sched_barrier(0);
+        v8 b[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) b[x] = op[x * (M::OP / 16)];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int y = 0; y < D / 32; ++y)
+                acc[y] = Mma<T>::mma(at.cols(y, (FOR_V ? M::TILE : 0) + x * 16 * D * sizeof(T)), b[x], acc[y]);
+        interleave<D / 4, D / 8, 8, 4>();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    uint32_t stage = 0, buffer = 1, done = 2;  // done: stage of the step before
+    bool more = steps.next();
+    if (more) steps.load(0);
+    bool some = false;
+    while (more) {
+        wait_loads();
+        __syncthreads();
+        const uint32_t after = stage == 2 ? 0 : stage + 1;
+        more = steps.next();
+        if (more) steps.load(after);
+        if (some) {
+            sum(buffer);
+            at.move(done == 2 ? (uint32_t)-2 * M::STAGE : M::STAGE);
+        }
+        some = true;
+        done = stage;
+        stage = after;
+        buffer ^= 1;
     }
     __syncthreads();
-    if (qh == 1 || key >= a.tokens_k) return;
+    if (some) sum(buffer);
+    if (key >= a.tokens_k) return;
     const float f = FOR_V ? 1.f : a.scale;
-    T* o = result.at(b, key, hk);
+    T* o = result.at(steps.b, key, hk);
 #pragma unroll
     for (int t = 0; t < D / 32; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            float x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = (acc[t][4 * r + e] + mine[(t * 16 + 4 * r + e) * 64]) * f;
-            store4<T>(o + t * 32 + r * 8 + hi * 4, x[0], x[1], x[2], x[3]);
-        }
+        for (int r = 0; r < 4; ++r)
+            store4<T>(o + t * 32 + r * 8 + hi * 4, acc[t][4 * r] * f, acc[t][4 * r + 1] * f, acc[t][4 * r + 2] * f,
+                      acc[t][4 * r + 3] * f);
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__(GKV_THREADS, D == 64 ? 4 : 2) void k_attn_gkv(View<const T> go, View<const T> q,
-                                                                          View<const T> k, View<const T> v,
-                                                                          const float* rows, const uint32_t* bits,
-                                                                          const uint32_t* order, const int32_t* kv_len,
-                                                                          View<T> gk, View<T> gv, const AttnArgs a)
+__device__ __forceinline__ void attn_gkv(char* lds, const View<const T>& go, const View<const T>& q, const View<const T>& k,
+                                         const View<const T>& v, const float* __restrict__ rows,
+                                         const uint32_t* __restrict__ bits, const uint32_t* __restrict__ order,
+                                         const int32_t* __restrict__ kv_len, const View<T>& gk, const View<T>& gv,
+                                         const AttnArgs& a)
 {
-    extern __shared__ __align__(16) char s_lds[];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t id = xcd_contiguous(blockIdx.x, gridDim.x);
     const int bh = (int)(id / a.blocks), blk = (int)order[id];
-    const int b = bh / a.heads_k, hk = bh - b * a.heads_k;
+    const int b = bh / a.heads_k, hk = bh - b * a.heads_k, per = a.heads_q / a.heads_k;
     const int len = (int)seq_len(kv_len, b, a.tokens_k);
+    const int words = (int)((a.groups + 31) / 32);
+    const Walk w(bits + (((int64_t)b * a.heads_q + hk * per) * a.blocks + blk) * words, a.blocks * words, words, per);
+    GkvSteps<T, D> steps(lds, q, go, rows, w, b, hk * per, a, wave);
     if (wave < 4)
-        gkv_wave<T, D, true>(s_lds, go, q, k, v, rows, bits, blk, b, hk, len, gv, a, wave);
+        gkv_scores<T, D>(steps, k, v, blk, hk, len, a, wave);
+    else if (wave < 6)
+        gkv_sums<T, D, true>(steps, gv, blk, hk, a, wave & 1);
     else
-        gkv_wave<T, D, false>(s_lds, go, q, k, v, rows, bits, blk, b, hk, len, gk, a, wave);
+        gkv_sums<T, D, false>(steps, gk, blk, hk, a, wave & 1);
+}
+
+template <typename T, int D>
+__global__ __launch_bounds__(GKV_THREADS, 2) void k_attn_gkv(View<const T> go, View<const T> q, View<const T> k,
+                                                             View<const T> v, const float* rows, const uint32_t* bits,
+                                                             const uint32_t* order, const int32_t* kv_len, View<T> gk,
+                                                             View<T> gv, const AttnArgs a)
+{
+    extern __shared__ __align__(16) char s_lds[];
+    attn_gkv<T, D>(s_lds, go, q, k, v, rows, bits, order, kv_len, gk, gv, a);
 }
 
 template <typename T, int D>
