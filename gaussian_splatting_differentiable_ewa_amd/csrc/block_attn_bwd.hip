@@ -249,8 +249,9 @@ __global__ __launch_bounds__(ATT_THREADS) void k_block_order(const uint32_t* __r
 // which multiplies or computes exponentials but hardly both (measured: vector
 // instructions behind a matrix instruction of the same wave are not hidden, of
 // another wave they are). Split this way both kinds fit 256, and one
-// multiplies while the other computes. Three stages of queries: one
-// loading, one per kind.
+// multiplies while the other computes. The first kind is the longer one, so
+// the other issues all loads. Three stages of queries: one loading, one per
+// kind.
 constexpr int GKV_THREADS = 512;
 
 // LDS of the workgroup, in bytes (dynamic, so that it begins at LDS address 0).
@@ -271,10 +272,10 @@ struct GkvSteps {
     char* lds;
     const View<const T>&q, &go;
     const float* rows;
-    TileLoad<T, D, 8> load_q, load_g;
+    TileLoad<T, D, 4> load_q, load_g;
     Walk w;
     int64_t head0, groups;  // first query head of the batch entry; groups a head
-    int h0, b, tokens_q, wave, q0, half;
+    int h0, b, tokens_q, wave, q0, half;  // wave: of the four that load
     __device__ __forceinline__ GkvSteps(char* l, const View<const T>& q_, const View<const T>& go_, const float* r,
                                         const Walk& walk, int b_, int h, const AttnArgs& a, int wave_)
         : lds(l), q(q_), go(go_), rows(r), load_q(q_.st), load_g(go_.st), w(walk), head0((int64_t)b_ * a.heads_q),
@@ -328,17 +329,14 @@ __device__ __forceinline__ void gkv_scores(GkvSteps<T, D>& steps, const View<con
     }
     LaneAddresses<T, D> at(qh * 32);
     uint32_t stage = 0, buffer = 0;
-    bool more = steps.next();
-    if (more) steps.load(0);
-    while (more) {
-        wait_loads();
+    while (steps.next()) {
         __syncthreads();
-        const int first = steps.q0 + qh * 32;
-        const uint32_t after = stage == 2 ? 0 : stage + 1;
-        more = steps.next();
-        if (more) steps.load(after);
-        const float* nl = (const float*)(steps.lds + M::ROWS + stage * M::ROW_STAGE) + qh * 32 + 4 * hi;
-        const float* dl = nl + 64;
+        float nl[16], dl[16];
+        const float* row = (const float*)(steps.lds + M::ROWS + stage * M::ROW_STAGE) + qh * 32 + 4 * hi;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) nl[r] = row[c_row(r, 0)];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) dl[r] = row[64 + c_row(r, 0)];
         acc16 s = zero16(), p = zero16();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -348,7 +346,8 @@ __device__ __forceinline__ void gkv_scores(GkvSteps<T, D>& steps, const View<con
         interleave<D / 8, D / 8, 4>();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = exp2_fast(fmaf(s[r], c, nl[c_row(r, 0)]));
+        for (int r = 0; r < 16; ++r) s[r] = exp2_fast(fmaf(s[r], c, nl[r]));
+        const int first = steps.q0 + qh * 32;
         if ((blk + 1) * KB > (a.causal && past + first + 1 < len ? past + first + 1 : len)) {
             asm volatile("");  // a branch, not selects in every step
             // rows from `from` on see this lane's key
@@ -360,11 +359,11 @@ __device__ __forceinline__ void gkv_scores(GkvSteps<T, D>& steps, const View<con
         op[0] = as_operand<T>(s, 0);
         op[M::OP / 16] = as_operand<T>(s, 1);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] *= p[r] - dl[c_row(r, 0)];
+        for (int r = 0; r < 16; ++r) s[r] *= p[r] - dl[r];
         op[M::ARRAY / 16] = as_operand<T>(s, 0);
         op[(M::ARRAY + M::OP) / 16] = as_operand<T>(s, 1);
         at.move(stage == 2 ? (uint32_t)-2 * M::STAGE : M::STAGE);
-        stage = after;
+        stage = stage == 2 ? 0 : stage + 1;
         buffer ^= 1;
     }
     __syncthreads();  // hands over the last step
@@ -396,10 +395,9 @@ __device__ __forceinline__ void gkv_sums(GkvSteps<T, D>& steps, const View<T>& r
         interleave<D / 4, D / 8, 8, 4>();
         __builtin_amdgcn_sched_barrier(0);
     };
-    uint32_t stage = 0, buffer = 1, done = 2;  // done: stage of the step before
-    bool more = steps.next();
+    uint32_t stage = 0, buffer = 1;
+    bool more = steps.next(), some = false;
     if (more) steps.load(0);
-    bool some = false;
     while (more) {
         wait_loads();
         __syncthreads();
@@ -408,10 +406,9 @@ __device__ __forceinline__ void gkv_sums(GkvSteps<T, D>& steps, const View<T>& r
         if (more) steps.load(after);
         if (some) {
             sum(buffer);
-            at.move(done == 2 ? (uint32_t)-2 * M::STAGE : M::STAGE);
+            at.move(stage == 0 ? (uint32_t)-2 * M::STAGE : M::STAGE);  // from stage - 1 to stage
         }
         some = true;
-        done = stage;
         stage = after;
         buffer ^= 1;
     }
@@ -442,7 +439,7 @@ __device__ __forceinline__ void attn_gkv(char* lds, const View<const T>& go, con
     const int len = (int)seq_len(kv_len, b, a.tokens_k);
     const int words = (int)((a.groups + 31) / 32);
     const Walk w(bits + (((int64_t)b * a.heads_q + hk * per) * a.blocks + blk) * words, a.blocks * words, words, per);
-    GkvSteps<T, D> steps(lds, q, go, rows, w, b, hk * per, a, wave);
+    GkvSteps<T, D> steps(lds, q, go, rows, w, b, hk * per, a, wave & 3);
     if (wave < 4)
         gkv_scores<T, D>(steps, k, v, blk, hk, len, a, wave);
     else if (wave < 6)
