@@ -138,7 +138,13 @@ __device__ __forceinline__ void interleave()
 // stage: it does so at the first transposing read unless the accesses carry
 // alias scopes, which they get where the body is an inlined function with
 // __restrict__ arguments. Hence each kernel below is one.
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void wait_loads()
+{
+    // vmcnt(0), the other counters as they are: a builtin, so that the compiler
+    // knows that nothing is outstanding behind it
+    __builtin_amdgcn_s_waitcnt(0x0f70);
+    asm volatile("" ::: "memory");
+}
 
 // In both reads r0 is a multiple of 16, which the swizzle does not see: it goes
 // into the instruction's offset, and the lane's address serves all of them.
@@ -231,6 +237,30 @@ __device__ __forceinline__ typename Mma<T>::v8 as_operand(const acc16& c, int g)
 #pragma unroll
     for (int s = 0; s < 8; ++s) v[s] = (T)c[8 * g + s];
     return v;
+}
+
+// sum += the eight elements, two at a time (products with one).
+__device__ __forceinline__ float add8(Mma<bf16>::v8 v, float sum)
+{
+    typedef bf16 v2 __attribute__((ext_vector_type(2)));
+    const v2 one = {(bf16)1.f, (bf16)1.f};
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const v2 x = {v[i], v[i + 1]};
+        sum = __builtin_amdgcn_fdot2_f32_bf16(x, one, sum, false);
+    }
+    return sum;
+}
+__device__ __forceinline__ float add8(Mma<f16>::v8 v, float sum)
+{
+    typedef f16 v2 __attribute__((ext_vector_type(2)));
+    const v2 one = {(f16)1.f, (f16)1.f};
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const v2 x = {v[i], v[i + 1]};
+        sum = __builtin_amdgcn_fdot2(x, one, sum, false);
+    }
+    return sum;
 }
 
 __device__ __forceinline__ acc16 zero16()

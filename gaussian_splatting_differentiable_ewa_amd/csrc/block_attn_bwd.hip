@@ -41,45 +41,94 @@ __global__ __launch_bounds__(ATT_THREADS) void k_list_bits(const int32_t* __rest
         set_bit(lists, kv_len, bits, e, a);
 }
 
+// Mean key of every block, fp32 [batch][head][block][D]; zero without valid
+// keys. One wave a block: D / 8 lanes across, the others along the keys.
+template <typename T, int D>
+__global__ __launch_bounds__(ATT_THREADS) void k_key_means(View<const T> k, const int32_t* __restrict__ kv_len,
+                                                           float* __restrict__ means, int64_t count, const AttnArgs a)
+{
+    constexpr int ACROSS = D / 8, ALONG = 64 / ACROSS;
+    const int64_t id = (int64_t)blockIdx.x * (ATT_THREADS / 64) + (threadIdx.x >> 6);
+    if (id >= count) return;
+    const int64_t bh = id / a.blocks, blk = id - bh * a.blocks, b = bh / a.heads_k, h = bh - b * a.heads_k;
+    const int64_t len = seq_len(kv_len, b, a.tokens_k), rest = len - blk * KB;
+    const int n = (int)(rest < 0 ? 0 : (rest < KB ? rest : KB));
+    const int c = lane_id() % ACROSS, first = lane_id() / ACROSS;
+    const T* base = k.at(b, blk * KB, h) + c * 8;
+    float sum[8] = {};
+#pragma unroll 4
+    for (int r = first; r < n; r += ALONG) {
+        float x[8];
+        load_f32<T, 8>(base + r * k.st, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += x[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        for (int off = ACROSS; off < 64; off <<= 1) sum[e] += __shfl_xor(sum[e], off);
+    if (first == 0) {
+        const float inv = n > 0 ? 1.f / (float)n : 0.f;
+        float* o = means + id * D + c * 8;
+        *(float4*)o = make_float4(sum[0] * inv, sum[1] * inv, sum[2] * inv, sum[3] * inv);
+        *(float4*)(o + 4) = make_float4(sum[4] * inv, sum[5] * inv, sum[6] * inv, sum[7] * inv);
+    }
+}
+
 // gq of a group (and, for the other pass, -lse in base 2 and D of its 128
 // queries, [list][2][128]): four waves of 32 queries, the listed blocks in turn.
 //   dS^T = P^T (V gout^T - D),  gq^T += K^T dS^T
+// D from the rounded `out` carries that rounding, an error e the same for all
+// keys of a query, so gq would be off by e sum_j P_j k_j: more than all the
+// other roundings together; and what the keys have in common, which cancels
+// in gq, does not cancel in the roundings of dS. But the exact dS of a query
+// add to zero, so with R the sum of the rounded ones gq - R c is gq's value
+// for any vector c, without either error's part along c. c is the mean key as
+// this wave's 32 queries weigh the blocks (from the first half of each; an
+// estimate is enough), and D + R goes to the other pass.
+// LDS of the workgroup, in bytes (dynamic, so that it begins at LDS address 0):
+// two stages of K and V, then c of the four waves.
 template <typename T, int D>
-__device__ __forceinline__ void attn_gq(T (&s_tile)[2][2][Tile<D>::ELEMS], const View<const T>& go, const View<const T>& q,
-                                        const View<const T>& k, const View<const T>& v, const View<const T>& out,
-                                        const float* __restrict__ lse, const int32_t* __restrict__ lists,
-                                        const int32_t* __restrict__ kv_len, const View<T>& gq, float* __restrict__ rows,
+struct GqLds {
+    static constexpr uint32_t TILE = Tile<D>::ELEMS * sizeof(T), STAGE = 2 * TILE, MEAN = 2 * STAGE;
+    static constexpr uint32_t BYTES = MEAN + 4 * D * 4;
+};
+
+template <typename T, int D>
+__device__ __forceinline__ void attn_gq(char* lds, const View<const T>& go, const View<const T>& q, const View<const T>& k,
+                                        const View<const T>& v, const View<const T>& out, const float* __restrict__ lse,
+                                        const int32_t* __restrict__ lists, const int32_t* __restrict__ kv_len,
+                                        const float* __restrict__ means, const View<T>& gq, float* __restrict__ rows,
                                         const AttnArgs& a)
 {
+    using M = GqLds<T, D>;
+    typedef typename Mma<T>::v8 v8;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), hi = lane >> 5;
     const int64_t id = xcd_contiguous(blockIdx.x, gridDim.x);
-    const int64_t bh = id / a.groups, g = id - bh * a.groups;
-    const int64_t b = bh / a.heads_q, h = bh - b * a.heads_q, hk = h / (a.heads_q / a.heads_k);
-    const int32_t* list = lists + id * a.top;
-    const int64_t len = seq_len(kv_len, b, a.tokens_k);
-    const int64_t i0 = g * QG, i = i0 + wave * 32 + (lane & 31), ic = i < a.tokens_q ? i : a.tokens_q - 1;
-    const int64_t past = len - a.tokens_q;
-    const int64_t end = i0 + QG < a.tokens_q ? i0 + QG : a.tokens_q;
-    const int64_t mine = a.causal && past + i + 1 < len ? past + i + 1 : len;
-    const int64_t most = a.causal && past + end < len ? past + end : len;
-    const int64_t least = a.causal && past + i0 + 1 < len ? past + i0 + 1 : len;
-    const int64_t visible = most > 0 ? (most + KB - 1) / KB : 0;
+    const int bh = (int)(id / a.groups), g = (int)(id - bh * a.groups);
+    const int b = bh / a.heads_q, h = bh - b * a.heads_q, hk = h / (a.heads_q / a.heads_k);
+    const int tokens_q = (int)a.tokens_q, len = (int)seq_len(kv_len, b, a.tokens_k), past = len - tokens_q;
+    const int i0 = g * QG, i = i0 + wave * 32 + (lane & 31), ic = i < tokens_q ? i : tokens_q - 1;
+    // keys the lane's query and the group's last and first query see
+    const int end = i0 + QG < tokens_q ? i0 + QG : tokens_q;
+    const int mine = a.causal && past + i + 1 < len ? past + i + 1 : len;
+    const int most = a.causal && past + end < len ? past + end : len;
+    const int least = a.causal && past + i0 + 1 < len ? past + i0 + 1 : len;
     const float c = a.scale * LOG2E;
     const T* kb = k.at(b, 0, hk);
     const T* vb = v.at(b, 0, hk);
     const TileLoad<T, D, 4> load_k(k.st), load_v(v.st);
-    ListWalk walk(list, a.top, visible);
+    ListWalk walk(lists + id * a.top, a.top, most > 0 ? (most + KB - 1) / KB : 0);
     int blk = walk.next();
     if (blk >= 0) {
-        load_k(s_tile[0][0], kb, (int64_t)blk * KB, len - 1, wave);
-        load_v(s_tile[0][1], vb, (int64_t)blk * KB, len - 1, wave);
+        load_k((T*)lds, kb, (int64_t)blk * KB, len - 1, wave);
+        load_v((T*)(lds + M::TILE), vb, (int64_t)blk * KB, len - 1, wave);
     }
-    typename Mma<T>::v8 qf[D / 16], gf[D / 16];
+    v8 qf[D / 16], gf[D / 16];
     load_cols<T, D>(q.at(b, ic, h), qf);
     load_cols<T, D>(go.at(b, ic, h), gf);
     float dl = 0.f;
     {
-        typename Mma<T>::v8 of[D / 16];
+        v8 of[D / 16];
         load_cols<T, D>(out.at(b, ic, h), of);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
@@ -89,75 +138,101 @@ __device__ __forceinline__ void attn_gq(T (&s_tile)[2][2][Tile<D>::ELEMS], const
     }
     // a query that saw nothing has lse = -inf: P = exp2(S - inf) = 0; so has
     // one past the end, for the pass over the keys
-    const float ls = lse[bh * a.tokens_q + ic], nl = ls == -INFINITY || i >= a.tokens_q ? -INFINITY : -ls * LOG2E;
-    if (hi == 0) {
-        float* row = rows + id * 2 * QG + wave * 32 + lane;
-        row[0] = nl;
-        row[QG] = dl;
-    }
+    float nl = lse[(int64_t)bh * tokens_q + ic];
+    nl = nl == -INFINITY || i >= tokens_q ? -INFINITY : -nl * LOG2E;
     acc16 acc[D / 32];
 #pragma unroll
     for (int t = 0; t < D / 32; ++t) acc[t] = zero16();
-    auto block = [&](const T* kt, const T* vt, auto masked, int limit) __attribute__((always_inline)) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            acc16 s = zero16(), p = zero16();
-#pragma unroll
-            for (int x = 0; x < D / 16; ++x) s = Mma<T>::mma(read_rows<T, D>(kt, t * 32, x), qf[x], s);
-#pragma unroll
-            for (int x = 0; x < D / 16; ++x) p = Mma<T>::mma(read_rows<T, D>(vt, t * 32, x), gf[x], p);
-            interleave<D / 8, D / 8, 4>();
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s[r] = exp2_fast(fmaf(s[r], c, nl));
-            if constexpr (decltype(masked)::value) {
-                const int rows = limit - 4 * hi;  // against constants: no registers for the rows
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = t * 32 + c_row(r, 0) < rows ? s[r] : 0.f;
-            }
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s[r] *= p[r] - dl;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const typename Mma<T>::v8 ds = as_operand<T>(s, x);
-#pragma unroll
-                for (int y = 0; y < D / 32; ++y)
-                    acc[y] = Mma<T>::mma(read_cols<T, D>(kt, t * 32 + x * 16, y * 32), ds, acc[y]);
-            }
-            interleave<D / 8, D / 16, 4>();
-            __builtin_amdgcn_sched_barrier(0);  // keeps the halves' registers apart
-        }
-    };
-    auto step = [&](int S, auto masked) __attribute__((always_inline)) {
+    float total = 0.f, weight = 0.f, mean[D / 64] = {};  // R; of c, and c's dimensions lane, lane + 64
+    const float* block_means = means + ((int64_t)b * a.heads_k + hk) * a.blocks * D;
+    LaneAddresses<T, D> at(0);
+    auto step = [&](int stage, auto masked) __attribute__((always_inline)) {
         const int next = walk.next();
         wait_loads();
         __syncthreads();
+        float mu[D / 64];  // before the loads to LDS, which it would else wait for
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) mu[x] = (block_means + (int64_t)blk * D)[lane + 64 * x];
         if (next >= 0) {
-            load_k(s_tile[S ^ 1][0], kb, (int64_t)next * KB, len - 1, wave);
-            load_v(s_tile[S ^ 1][1], vb, (int64_t)next * KB, len - 1, wave);
+            char* to = lds + (stage ^ 1) * M::STAGE;
+            load_k((T*)to, kb, (int64_t)next * KB, len - 1, wave);
+            load_v((T*)(to + M::TILE), vb, (int64_t)next * KB, len - 1, wave);
         }
-        const int64_t k0 = (int64_t)blk * KB, rest = mine - k0;
-        block(s_tile[S][0], s_tile[S][1], masked, (int)(rest < 0 ? 0 : (rest < KB ? rest : KB)));
+        float part = 0.f;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            acc16 s = zero16(), p = zero16();
+            constexpr uint32_t HALF = 32 * D * sizeof(T), STEP = 16 * D * sizeof(T);
+            __builtin_amdgcn_sched_barrier(0);  // keeps the parts' registers apart
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) s = Mma<T>::mma(at.rows(x, t * HALF), qf[x], s);
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) p = Mma<T>::mma(at.rows(x, M::TILE + t * HALF), gf[x], p);
+            interleave<D / 8, D / 8, 4>();
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[r] = exp2_fast(fmaf(s[r], c, nl));
+            if constexpr (decltype(masked)::value) {
+                const int upto = mine - blk * KB - 4 * hi - t * 32;  // against constants: no registers for the rows
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[r] = c_row(r, 0) < upto ? s[r] : 0.f;
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                if (t == 0) part += s[r];
+                s[r] *= p[r] - dl;
+            }
+            const v8 ds0 = as_operand<T>(s, 0), ds1 = as_operand<T>(s, 1);
+            total = add8(ds1, add8(ds0, total));
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int y = 0; y < D / 32; ++y)
+                    acc[y] = Mma<T>::mma(at.cols(y, t * HALF + x * STEP), x ? ds1 : ds0, acc[y]);
+            interleave<D / 8, D / 16, 8>();
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        part = wave_sum(part);
+        weight += part;
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) mean[x] = fmaf(part, mu[x], mean[x]);
+        at.move(stage ? (uint32_t)-1 * M::STAGE : M::STAGE);
         blk = next;
     };
-    walk_blocks(step, [&] { return blk >= 0; }, [&] { return (int64_t)blk * KB + KB > least; });
-    if (i >= a.tokens_q) return;
+    walk_blocks(step, [&] { return blk >= 0; }, [&] { return blk * KB + KB > least; });
+    total += __shfl_xor(total, 32);
+    if (hi == 0) {
+        float* row = rows + id * 2 * QG + wave * 32 + lane;
+        row[0] = nl;
+        row[QG] = dl + total;
+    }
+    // c to LDS and back, to the lanes that hold its dimensions (of this wave only)
+    float* cs = (float*)(lds + M::MEAN) + wave * D;
+    const float inv = weight > 0.f ? 1.f / weight : 0.f;
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) cs[lane + 64 * x] = mean[x] * inv;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (i >= tokens_q) return;
     T* o = gq.at(b, i, h);
 #pragma unroll
     for (int t = 0; t < D / 32; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            store4<T>(o + t * 32 + r * 8 + hi * 4, acc[t][4 * r] * a.scale, acc[t][4 * r + 1] * a.scale,
-                      acc[t][4 * r + 2] * a.scale, acc[t][4 * r + 3] * a.scale);
+        for (int r = 0; r < 4; ++r) {
+            const float4v x = *(const float4v*)(cs + t * 32 + r * 8 + hi * 4) * total;
+            store4<T>(o + t * 32 + r * 8 + hi * 4, (acc[t][4 * r] - x[0]) * a.scale, (acc[t][4 * r + 1] - x[1]) * a.scale,
+                      (acc[t][4 * r + 2] - x[2]) * a.scale, (acc[t][4 * r + 3] - x[3]) * a.scale);
+        }
 }
 
 template <typename T, int D>
 __global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_gq(View<const T> go, View<const T> q, View<const T> k,
                                                             View<const T> v, View<const T> out, const float* lse,
-                                                            const int32_t* lists, const int32_t* kv_len, View<T> gq,
-                                                            float* rows, const AttnArgs a)
+                                                            const int32_t* lists, const int32_t* kv_len,
+                                                            const float* means, View<T> gq, float* rows, const AttnArgs a)
 {
-    __shared__ alignas(16) T s_tile[2][2][Tile<D>::ELEMS];
-    attn_gq<T, D>(s_tile, go, q, k, v, out, lse, lists, kv_len, gq, rows, a);
+    extern __shared__ __align__(16) char s_lds[];
+    attn_gq<T, D>(s_lds, go, q, k, v, out, lse, lists, kv_len, means, gq, rows, a);
 }
 
 // Walks the (head of the key head, group of queries) pairs that list a block;
@@ -462,14 +537,23 @@ template <typename T, int D>
 static gs_status attn_bwd_launch(const gs_tokens* go, const gs_tokens* q, const gs_tokens* k, const gs_tokens* v,
                                  const gs_tokens* out, const float* lse, const int32_t* list, const int32_t* kv_len,
                                  const gs_tokens* gq, const gs_tokens* gk, const gs_tokens* gv, float* rows,
-                                 uint32_t* bits, uint32_t* order, int64_t batch, const AttnArgs& a, hipStream_t s)
+                                 float* means, uint32_t* bits, uint32_t* order, int64_t batch, const AttnArgs& a, hipStream_t s)
 {
     const int64_t lists = batch * a.heads_q * a.groups, blocks = batch * a.heads_k * a.blocks;
     const int64_t words = batch * a.heads_q * a.blocks * ((a.groups + 31) / 32);
     if (lists > 0) {
-        hipLaunchKernelGGL((k_attn_gq<T, D>), dim3((unsigned)lists), dim3(ATT_THREADS), 0, s, view_of<const T>(go),
+        if (blocks > 0) {
+            hipLaunchKernelGGL((k_key_means<T, D>), dim3(grid_for((uint64_t)blocks, ATT_THREADS / 64)), dim3(ATT_THREADS), 0,
+                               s, view_of<const T>(k), kv_len, means, blocks, a);
+            GS_CHECK_LAUNCH();
+        }
+        constexpr uint32_t lds = GqLds<T, D>::BYTES;
+        if (lds > 65536 && hipFuncSetAttribute((const void*)k_attn_gq<T, D>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)lds) != hipSuccess)
+            return GS_ERR_HIP;
+        hipLaunchKernelGGL((k_attn_gq<T, D>), dim3((unsigned)lists), dim3(ATT_THREADS), lds, s, view_of<const T>(go),
                            view_of<const T>(q), view_of<const T>(k), view_of<const T>(v), view_of<const T>(out), lse, list,
-                           kv_len, view_of<T>(gq), rows, a);
+                           kv_len, means, view_of<T>(gq), rows, a);
         GS_CHECK_LAUNCH();
     }
     if (blocks > 0) {
@@ -515,7 +599,8 @@ size_t gs_block_attn_bwd_workspace_bytes(int64_t batch, int64_t tokens_q, int64_
     using namespace gs;
     if (attn_check(batch, tokens_q, tokens_k, heads_q, heads_k, dim, GS_BF16, 1, 1.f) != GS_OK) return 0;
     const int64_t groups = (tokens_q + QG - 1) / QG, blocks = (tokens_k + KB - 1) / KB;
-    return row_bytes(batch, tokens_q, heads_q) + (size_t)(bits_words(batch, groups, blocks, heads_q) + batch * heads_k * blocks) * 4 + 16;
+    return row_bytes(batch, tokens_q, heads_q) +
+           (size_t)(bits_words(batch, groups, blocks, heads_q) + batch * heads_k * blocks * (dim + 1)) * 4 + 16;
 }
 
 gs_status gs_block_attn_bwd(const gs_tokens* gout, const gs_tokens* q, const gs_tokens* k, const gs_tokens* v,
@@ -544,14 +629,15 @@ gs_status gs_block_attn_bwd(const gs_tokens* gout, const gs_tokens* q, const gs_
     const AttnArgs a{tokens_q, tokens_k, (tokens_q + QG - 1) / QG, (tokens_k + KB - 1) / KB, heads_q, heads_k,
                      causal != 0, top, 1, sm_scale};
     float* rows = (float*)ws;
-    uint32_t* bits = (uint32_t*)((char*)ws + row_bytes(batch, tokens_q, heads_q));
+    float* means = rows + row_bytes(batch, tokens_q, heads_q) / 4;
+    uint32_t* bits = (uint32_t*)(means + batch * heads_k * a.blocks * dim);
     uint32_t* order = bits + bits_words(batch, a.groups, a.blocks, heads_q);
     const hipStream_t s = (hipStream_t)stream;
     if (dtype == GS_BF16)
-        return dim == 128 ? attn_bwd_launch<bf16, 128>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, rows, bits, order, batch, a, s)
-                          : attn_bwd_launch<bf16, 64>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, rows, bits, order, batch, a, s);
-    return dim == 128 ? attn_bwd_launch<f16, 128>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, rows, bits, order, batch, a, s)
-                      : attn_bwd_launch<f16, 64>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, rows, bits, order, batch, a, s);
+        return dim == 128 ? attn_bwd_launch<bf16, 128>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, rows, means, bits, order, batch, a, s)
+                          : attn_bwd_launch<bf16, 64>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, rows, means, bits, order, batch, a, s);
+    return dim == 128 ? attn_bwd_launch<f16, 128>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, rows, means, bits, order, batch, a, s)
+                      : attn_bwd_launch<f16, 64>(gout, q, k, v, out, lse, list, kv_len, gq, gk, gv, rows, means, bits, order, batch, a, s);
 }
 
 }  // extern "C"
