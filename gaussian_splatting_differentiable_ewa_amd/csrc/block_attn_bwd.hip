@@ -84,7 +84,10 @@ __global__ __launch_bounds__(ATT_THREADS) void k_key_means(View<const T> k, cons
 // add to zero, so with R the sum of the rounded ones gq - R c is gq's value
 // for any vector c, without either error's part along c. c is the mean key as
 // this wave's 32 queries weigh the blocks (from the first half of each; an
-// estimate is enough), and D + R goes to the other pass.
+// estimate is enough). In the blocks that masks cut, where the first queries of
+// a causal sequence have all their few keys and nothing averages out, dS is
+// kept in two parts. D with the sum of the unrounded ones added, -e, goes to
+// the other pass.
 // LDS of the workgroup, in bytes (dynamic, so that it begins at LDS address 0):
 // two stages of K and V, then c of the four waves.
 template <typename T, int D>
@@ -143,7 +146,8 @@ __device__ __forceinline__ void attn_gq(char* lds, const View<const T>& go, cons
     acc16 acc[D / 32];
 #pragma unroll
     for (int t = 0; t < D / 32; ++t) acc[t] = zero16();
-    float total = 0.f, weight = 0.f, mean[D / 64] = {};  // R; of c, and c's dimensions lane, lane + 64
+    float whole = 0.f, total = 0.f;              // sums of dS, as it is and rounded (R)
+    float weight = 0.f, mean[D / 64] = {};  // of c, and c's dimensions lane, lane + 64
     const float* block_means = means + ((int64_t)b * a.heads_k + hk) * a.blocks * D;
     LaneAddresses<T, D> at(0);
     auto step = [&](int stage, auto masked) __attribute__((always_inline)) {
@@ -181,6 +185,7 @@ __device__ __forceinline__ void attn_gq(char* lds, const View<const T>& go, cons
             for (int r = 0; r < 16; ++r) {
                 if (t == 0) part += s[r];
                 s[r] *= p[r] - dl;
+                whole += s[r];
             }
             const v8 ds0 = as_operand<T>(s, 0), ds1 = as_operand<T>(s, 1);
             total = add8(ds1, add8(ds0, total));
@@ -192,6 +197,20 @@ __device__ __forceinline__ void attn_gq(char* lds, const View<const T>& go, cons
                     acc[y] = Mma<T>::mma(at.cols(y, t * HALF + x * STEP), x ? ds1 : ds0, acc[y]);
             interleave<D / 8, D / 16, 8>();
             __builtin_amdgcn_sched_barrier(0);
+            if constexpr (decltype(masked)::value) {
+                // what rounding left, as a second operand
+#pragma unroll
+                for (int r = 0; r < 8; ++r) s[r] -= (float)ds0[r], s[8 + r] -= (float)ds1[r];
+                const v8 rest0 = as_operand<T>(s, 0), rest1 = as_operand<T>(s, 1);
+                total = add8(rest1, add8(rest0, total));
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int y = 0; y < D / 32; ++y)
+                        acc[y] = Mma<T>::mma(at.cols(y, t * HALF + x * STEP), x ? rest1 : rest0, acc[y]);
+                interleave<D / 8, D / 16, 8>();
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
         part = wave_sum(part);
         weight += part;
@@ -202,10 +221,11 @@ __device__ __forceinline__ void attn_gq(char* lds, const View<const T>& go, cons
     };
     walk_blocks(step, [&] { return blk >= 0; }, [&] { return blk * KB + KB > least; });
     total += __shfl_xor(total, 32);
+    whole += __shfl_xor(whole, 32);
     if (hi == 0) {
         float* row = rows + id * 2 * QG + wave * 32 + lane;
         row[0] = nl;
-        row[QG] = dl + total;
+        row[QG] = dl + whole;
     }
     // c to LDS and back, to the lanes that hold its dimensions (of this wave only)
     float* cs = (float*)(lds + M::MEAN) + wave * D;
