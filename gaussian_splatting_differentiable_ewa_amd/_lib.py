@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -440,13 +441,38 @@ def gs_stream_copy(dst, src, nbytes=None, stream=None):
 
 # ---- token operators -----------------------------------------------------------
 # Token tensors are [batch][tokens][heads][dim] (any strides, dim contiguous).
+def _current(t, stream):
+    """The given stream's handle, or that of the tensor's device's current one
+    (looked up once by name: torch.cuda.current_stream builds an object)."""
+    global _RAW_STREAM
+    if stream is not None:
+        return stream.cuda_stream
+    if _RAW_STREAM is None:
+        import torch
+        _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _RAW_STREAM(t.get_device())
+
+
+_RAW_STREAM = None
+_DTYPES = {}
+_Pairs = ctypes.c_int32 * 3
+
+
 def dtype_of(t) -> int:
     """gs_dtype of a tensor (raises for other types)."""
-    import torch
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: GS_F32, torch.float16: GS_F16, torch.bfloat16: GS_BF16})
     try:
-        return {torch.float32: GS_F32, torch.float16: GS_F16, torch.bfloat16: GS_BF16}[t.dtype]
+        return _DTYPES[t.dtype]
     except KeyError:
         raise GsError(f"unsupported element type {t.dtype}") from None
+
+
+# gs_tokens as bytes: a third of the time of a ctypes structure, and small
+# calls are bound by the host
+_pack_tokens = struct.Struct("@Pqqq").pack
 
 
 def _tok(t):
@@ -455,14 +481,15 @@ def _tok(t):
     sb, st, sh, sd = t.stride()
     if sd != 1 and t.shape[3] > 1:
         raise GsError("the last dimension of a token tensor must be contiguous")
-    return ctypes.byref(GsTokens(t.data_ptr(), sb, st, sh))
+    return _pack_tokens(t.data_ptr(), sb, st, sh)
 
 
 def _blk(t):
     """A summary [batch][heads][blocks](dim) as a token tensor of blocks."""
     if t.dim() == 4 and t.stride(3) != 1 and t.shape[3] > 1:
         raise GsError("the last dimension of a summary must be contiguous")
-    return ctypes.byref(GsTokens(t.data_ptr(), t.stride(0), t.stride(2), t.stride(1)))
+    st = t.stride()
+    return _pack_tokens(t.data_ptr(), st[0], st[2], st[1])
 
 
 def _ws(ws):
@@ -474,15 +501,15 @@ def gs_rope_axes(q, k, q_out, k_out, pos, freq, pairs, interleaved=False, invers
     b, n, hq, d = q.shape
     _check(lib().gs_rope_axes(_tok(q), _tok(k), _tok(q_out), _tok(k_out), b, n, hq, 0 if k is None else k.shape[2], d,
                               dtype_of(q), _ptr(pos), 0 if pos.shape[0] == 1 else pos.stride(0), _ptr(freq),
-                              (ctypes.c_int32 * 3)(*pairs), int(bool(interleaved)), int(bool(inverse)),
-                              _stream(stream)), "gs_rope_axes")
+                              _Pairs(*pairs), int(bool(interleaved)), int(bool(inverse)),
+                              _current(q, stream)), "gs_rope_axes")
 
 
 def gs_norm_gate_fwd(x, f, gate, w_post, w_pre, y, h, stats, rows_per_gate, scale=1.0, eps=1e-6, stream=None):
     """x, f, y, h [rows][channels] contiguous; f, gate, w_post, w_pre may be None."""
     rows, c = x.shape
     _check(lib().gs_norm_gate_fwd(_ptr(x), _ptr(f), _ptr(gate), _ptr(w_post), _ptr(w_pre), _ptr(y), _ptr(h), _ptr(stats),
-                                  rows, c, rows_per_gate, scale, eps, dtype_of(x), _stream(stream)), "gs_norm_gate_fwd")
+                                  rows, c, rows_per_gate, scale, eps, dtype_of(x), _current(x, stream)), "gs_norm_gate_fwd")
 
 
 def norm_gate_bwd_workspace_bytes(rows: int, channels: int, rows_per_gate: int) -> int:
@@ -495,7 +522,7 @@ def gs_norm_gate_bwd(gy, gh, x, f, gate, w_post, w_pre, stats, gx, gf, ggate, gw
     rows, c = x.shape
     _check(lib().gs_norm_gate_bwd(_ptr(gy), _ptr(gh), _ptr(x), _ptr(f), _ptr(gate), _ptr(w_post), _ptr(w_pre),
                                   _ptr(stats), _ptr(gx), _ptr(gf), _ptr(ggate), _ptr(gw_post), _ptr(gw_pre), rows, c,
-                                  rows_per_gate, scale, dtype_of(x), *_ws(ws), _stream(stream)), "gs_norm_gate_bwd")
+                                  rows_per_gate, scale, dtype_of(x), *_ws(ws), _current(x, stream)), "gs_norm_gate_bwd")
 
 
 def gs_block_summary(k, sum8, scale, kv_len=None, block0=0, blocks=None, stream=None):
@@ -505,14 +532,14 @@ def gs_block_summary(k, sum8, scale, kv_len=None, block0=0, blocks=None, stream=
     every = (n + GS_KEY_BLOCK - 1) // GS_KEY_BLOCK
     _check(lib().gs_block_summary(_tok(k), b, n, h, d, dtype_of(k), _ptr(kv_len), block0,
                                   every - block0 if blocks is None else blocks, _blk(sum8), _blk(scale),
-                                  _stream(stream)), "gs_block_summary")
+                                  _current(k, stream)), "gs_block_summary")
 
 
 def gs_block_select(q, sum8, scale, tokens_k, heads_k, lists, kv_len=None, causal=False, stream=None):
     """lists int32 [batch][heads_q][ceil(tokens_q / 128)][top]."""
     b, n, h, d = q.shape
     _check(lib().gs_block_select(_tok(q), _blk(sum8), _blk(scale), b, n, tokens_k, h, heads_k, d, dtype_of(q),
-                                 _ptr(kv_len), int(bool(causal)), lists.shape[3], _ptr(lists), _stream(stream)),
+                                 _ptr(kv_len), int(bool(causal)), lists.shape[3], _ptr(lists), _current(q, stream)),
            "gs_block_select")
 
 
@@ -526,7 +553,7 @@ def gs_block_attn_fwd(q, k, v, lists, out, lse, ws=None, kv_len=None, causal=Fal
     _check(lib().gs_block_attn_fwd(_tok(q), _tok(k), _tok(v), _ptr(lists), b, n, k.shape[1], h, k.shape[2], d,
                                    dtype_of(q), _ptr(kv_len), int(bool(causal)), lists.shape[3],
                                    d ** -0.5 if sm_scale is None else sm_scale, _tok(out), _ptr(lse), *_ws(ws),
-                                   _stream(stream)), "gs_block_attn_fwd")
+                                   _current(q, stream)), "gs_block_attn_fwd")
 
 
 def block_attn_bwd_workspace_bytes(batch: int, tokens_q: int, tokens_k: int, heads_q: int, heads_k: int, dim: int) -> int:
@@ -539,4 +566,4 @@ def gs_block_attn_bwd(gout, q, k, v, out, lse, lists, gq, gk, gv, ws, kv_len=Non
     _check(lib().gs_block_attn_bwd(_tok(gout), _tok(q), _tok(k), _tok(v), _tok(out), _ptr(lse), _ptr(lists), b, n,
                                    k.shape[1], h, k.shape[2], d, dtype_of(q), _ptr(kv_len), int(bool(causal)),
                                    lists.shape[3], d ** -0.5 if sm_scale is None else sm_scale, _tok(gq), _tok(gk),
-                                   _tok(gv), *_ws(ws), _stream(stream)), "gs_block_attn_bwd")
+                                   _tok(gv), *_ws(ws), _current(q, stream)), "gs_block_attn_bwd")

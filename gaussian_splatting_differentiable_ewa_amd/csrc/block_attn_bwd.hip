@@ -3,7 +3,8 @@
 // Two passes without atomics, so the bits repeat: one over the query groups
 // (gq, and D = sum gout out), one over the key blocks (gk, gv), which walks
 // the groups that list its block. Those come from a bit matrix
-// [batch][head][block][groups / 32], set from the lists (an OR: any order).
+// [batch][head][block][groups / 32], which the first pass sets from its lists
+// (an OR: any order).
 // Both passes form S and P again from lse: 7 products in all where the
 // formula's 5 would need fp32 atomics on gq.
 #include <algorithm>
@@ -12,42 +13,17 @@
 
 namespace gs {
 
-__global__ __launch_bounds__(ATT_THREADS) void k_zero_words(uint32_t* __restrict__ p, int64_t n)
-{
-    for (int64_t i = (int64_t)blockIdx.x * ATT_THREADS + threadIdx.x; i < n; i += (int64_t)gridDim.x * ATT_THREADS) p[i] = 0;
-}
-
-__device__ __forceinline__ void set_bit(const int32_t* __restrict__ lists, const int32_t* __restrict__ kv_len,
-                                        uint32_t* __restrict__ bits, int64_t e, const AttnArgs& a)
-{
-    const int64_t id = e / a.top, bh = id / a.groups, g = id - bh * a.groups;
-    const int64_t len = seq_len(kv_len, bh / a.heads_q, a.tokens_k), past = len - a.tokens_q;
-    const int64_t end = g * QG + QG < a.tokens_q ? g * QG + QG : a.tokens_q;
-    const int64_t most = a.causal && past + end < len ? past + end : len;
-    const int64_t visible = most > 0 ? (most + KB - 1) / KB : 0;
-    const int j = (int)(e - id * a.top);
-    if (!entry_ok(lists + id * a.top, j, visible)) return;
-    const int64_t words = (a.groups + 31) / 32;
-    atomicOr(&bits[(bh * a.blocks + lists[e]) * words + g / 32], 1u << (g & 31));
-}
-
-// A thread per list entry.
-__global__ __launch_bounds__(ATT_THREADS) void k_list_bits(const int32_t* __restrict__ lists,
-                                                           const int32_t* __restrict__ kv_len,
-                                                           uint32_t* __restrict__ bits, int64_t entries,
-                                                           const AttnArgs a)
-{
-    for (int64_t e = (int64_t)blockIdx.x * ATT_THREADS + threadIdx.x; e < entries; e += (int64_t)gridDim.x * ATT_THREADS)
-        set_bit(lists, kv_len, bits, e, a);
-}
-
-// Mean key of every block, fp32 [batch][head][block][D]; zero without valid
-// keys. One wave a block: D / 8 lanes across, the others along the keys.
+// What the passes need first: the mean key of every block, fp32
+// [batch][head][block][D], zero without valid keys (one wave a block: D / 8
+// lanes across, the others along the keys), and a cleared bit matrix.
 template <typename T, int D>
-__global__ __launch_bounds__(ATT_THREADS) void k_key_means(View<const T> k, const int32_t* __restrict__ kv_len,
-                                                           float* __restrict__ means, int64_t count, const AttnArgs a)
+__global__ __launch_bounds__(ATT_THREADS) void k_attn_prepare(View<const T> k, const int32_t* __restrict__ kv_len,
+                                                              float* __restrict__ means, uint32_t* __restrict__ bits,
+                                                              int64_t words, int64_t count, const AttnArgs a)
 {
     constexpr int ACROSS = D / 8, ALONG = 64 / ACROSS;
+    for (int64_t i = (int64_t)blockIdx.x * ATT_THREADS + threadIdx.x; i < words; i += (int64_t)gridDim.x * ATT_THREADS)
+        bits[i] = 0;
     const int64_t id = (int64_t)blockIdx.x * (ATT_THREADS / 64) + (threadIdx.x >> 6);
     if (id >= count) return;
     const int64_t bh = id / a.blocks, blk = id - bh * a.blocks, b = bh / a.heads_k, h = bh - b * a.heads_k;
@@ -88,8 +64,8 @@ __global__ __launch_bounds__(ATT_THREADS) void k_key_means(View<const T> k, cons
 // a causal sequence have all their few keys and nothing averages out, dS is
 // kept in two parts. D with the sum of the unrounded ones added, -e, goes to
 // the other pass.
-// LDS of the workgroup, in bytes (dynamic, so that it begins at LDS address 0):
-// two stages of K and V, then c of the four waves.
+// LDS of the workgroup, in bytes (the kernel's only LDS object, which so begins
+// at LDS address 0): two stages of K and V, then c of the four waves.
 template <typename T, int D>
 struct GqLds {
     static constexpr uint32_t TILE = Tile<D>::ELEMS * sizeof(T), STAGE = 2 * TILE, MEAN = 2 * STAGE;
@@ -100,8 +76,8 @@ template <typename T, int D>
 __device__ __forceinline__ void attn_gq(char* lds, const View<const T>& go, const View<const T>& q, const View<const T>& k,
                                         const View<const T>& v, const View<const T>& out, const float* __restrict__ lse,
                                         const int32_t* __restrict__ lists, const int32_t* __restrict__ kv_len,
-                                        const float* __restrict__ means, const View<T>& gq, float* __restrict__ rows,
-                                        const AttnArgs& a)
+                                        const float* __restrict__ means, uint32_t* __restrict__ bits,
+                                        const View<T>& gq, float* __restrict__ rows, const AttnArgs& a)
 {
     using M = GqLds<T, D>;
     typedef typename Mma<T>::v8 v8;
@@ -120,7 +96,12 @@ __device__ __forceinline__ void attn_gq(char* lds, const View<const T>& go, cons
     const T* kb = k.at(b, 0, hk);
     const T* vb = v.at(b, 0, hk);
     const TileLoad<T, D, 4> load_k(k.st), load_v(v.st);
-    ListWalk walk(lists + id * a.top, a.top, most > 0 ? (most + KB - 1) / KB : 0);
+    const int visible = most > 0 ? (most + KB - 1) / KB : 0;
+    ListWalk walk(lists + id * a.top, a.top, visible);
+    // the group's bit at each of its blocks, for the other pass
+    for (int j = threadIdx.x; j < a.top; j += ATT_THREADS)
+        if (entry_ok(lists + id * a.top, j, visible))
+            atomicOr(&bits[(bh * a.blocks + lists[id * a.top + j]) * ((a.groups + 31) / 32) + g / 32], 1u << (g & 31));
     int blk = walk.next();
     if (blk >= 0) {
         load_k((T*)lds, kb, (int64_t)blk * KB, len - 1, wave);
@@ -249,10 +230,11 @@ template <typename T, int D>
 __global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_gq(View<const T> go, View<const T> q, View<const T> k,
                                                             View<const T> v, View<const T> out, const float* lse,
                                                             const int32_t* lists, const int32_t* kv_len,
-                                                            const float* means, View<T> gq, float* rows, const AttnArgs a)
+                                                            const float* means, uint32_t* bits, View<T> gq,
+                                                            float* rows, const AttnArgs a)
 {
-    extern __shared__ __align__(16) char s_lds[];
-    attn_gq<T, D>(s_lds, go, q, k, v, out, lse, lists, kv_len, means, gq, rows, a);
+    __shared__ __align__(16) char s_lds[GqLds<T, D>::BYTES];
+    attn_gq<T, D>(s_lds, go, q, k, v, out, lse, lists, kv_len, means, bits, gq, rows, a);
 }
 
 // Walks the (head of the key head, group of queries) pairs that list a block;
@@ -296,7 +278,8 @@ struct Walk {
 
 // Blocks of one key head by the number of groups that list them, most first:
 // the grid takes them in this order, so that the launch does not end on a
-// block that many groups list. A counting sort on min(groups, ORDER_CLASSES - 1).
+// block that many groups list (with no more blocks than CUs all start at once
+// and none is needed). A counting sort on min(groups, ORDER_CLASSES - 1).
 // Ties may fall in any order: a block's result does not depend on its place.
 constexpr int ORDER_CLASSES = 1024;
 
@@ -349,7 +332,8 @@ __global__ __launch_bounds__(ATT_THREADS) void k_block_order(const uint32_t* __r
 // kind.
 constexpr int GKV_THREADS = 512;
 
-// LDS of the workgroup, in bytes (dynamic, so that it begins at LDS address 0).
+// LDS of the workgroup, in bytes (the kernel's only LDS object, which so begins
+// at LDS address 0).
 template <typename T, int D>
 struct GkvLds {
     static constexpr uint32_t TILE = Tile<D>::ELEMS * sizeof(T);          // q or gout of 64 queries
@@ -529,7 +513,7 @@ __device__ __forceinline__ void attn_gkv(char* lds, const View<const T>& go, con
 {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t id = xcd_contiguous(blockIdx.x, gridDim.x);
-    const int bh = (int)(id / a.blocks), blk = (int)order[id];
+    const int bh = (int)(id / a.blocks), blk = order ? (int)order[id] : (int)(id - (int64_t)bh * a.blocks);
     const int b = bh / a.heads_k, hk = bh - b * a.heads_k, per = a.heads_q / a.heads_k;
     const int len = (int)seq_len(kv_len, b, a.tokens_k);
     const int words = (int)((a.groups + 31) / 32);
@@ -549,8 +533,15 @@ __global__ __launch_bounds__(GKV_THREADS, 2) void k_attn_gkv(View<const T> go, V
                                                              const uint32_t* order, const int32_t* kv_len, View<T> gk,
                                                              View<T> gv, const AttnArgs a)
 {
+    // dynamic: with a static array of the same size the compiler's order of the
+    // reads costs 4 %
     extern __shared__ __align__(16) char s_lds[];
     attn_gkv<T, D>(s_lds, go, q, k, v, rows, bits, order, kv_len, gk, gv, a);
+}
+
+static int64_t bits_words(int64_t batch, int64_t groups, int64_t blocks, int32_t heads_q)
+{
+    return batch * heads_q * blocks * ((groups + 31) / 32);
 }
 
 template <typename T, int D>
@@ -560,40 +551,31 @@ static gs_status attn_bwd_launch(const gs_tokens* go, const gs_tokens* q, const 
                                  float* means, uint32_t* bits, uint32_t* order, int64_t batch, const AttnArgs& a, hipStream_t s)
 {
     const int64_t lists = batch * a.heads_q * a.groups, blocks = batch * a.heads_k * a.blocks;
-    const int64_t words = batch * a.heads_q * a.blocks * ((a.groups + 31) / 32);
+    const int64_t words = bits_words(batch, a.groups, a.blocks, a.heads_q);
+    if (blocks > 0) {
+        hipLaunchKernelGGL((k_attn_prepare<T, D>), dim3(grid_for((uint64_t)blocks, ATT_THREADS / 64)), dim3(ATT_THREADS), 0,
+                           s, view_of<const T>(k), kv_len, means, bits, words, blocks, a);
+        GS_CHECK_LAUNCH();
+    }
     if (lists > 0) {
-        if (blocks > 0) {
-            hipLaunchKernelGGL((k_key_means<T, D>), dim3(grid_for((uint64_t)blocks, ATT_THREADS / 64)), dim3(ATT_THREADS), 0,
-                               s, view_of<const T>(k), kv_len, means, blocks, a);
-            GS_CHECK_LAUNCH();
-        }
-        constexpr uint32_t lds = GqLds<T, D>::BYTES;
-        if (lds > 65536 && hipFuncSetAttribute((const void*)k_attn_gq<T, D>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)lds) != hipSuccess)
-            return GS_ERR_HIP;
-        hipLaunchKernelGGL((k_attn_gq<T, D>), dim3((unsigned)lists), dim3(ATT_THREADS), lds, s, view_of<const T>(go),
+        hipLaunchKernelGGL((k_attn_gq<T, D>), dim3((unsigned)lists), dim3(ATT_THREADS), 0, s, view_of<const T>(go),
                            view_of<const T>(q), view_of<const T>(k), view_of<const T>(v), view_of<const T>(out), lse, list,
-                           kv_len, means, view_of<T>(gq), rows, a);
+                           kv_len, means, bits, view_of<T>(gq), rows, a);
         GS_CHECK_LAUNCH();
     }
     if (blocks > 0) {
-        if (words > 0) {
-            hipLaunchKernelGGL(k_zero_words, dim3(std::min(grid_for((uint64_t)words, ATT_THREADS), 65536u)), dim3(ATT_THREADS), 0, s, bits,
-                               words);
-            GS_CHECK_LAUNCH();
-            hipLaunchKernelGGL(k_list_bits, dim3((unsigned)std::min<int64_t>((lists * a.top + ATT_THREADS - 1) / ATT_THREADS, 65536)), dim3(ATT_THREADS), 0, s,
-                               list, kv_len, bits, lists * a.top, a);
+        const bool ordered = blocks > 256 && words > 0;
+        if (ordered) {
+            hipLaunchKernelGGL(k_block_order, dim3((unsigned)(batch * a.heads_k)), dim3(ATT_THREADS), 0, s, bits, order, a);
             GS_CHECK_LAUNCH();
         }
-        hipLaunchKernelGGL(k_block_order, dim3((unsigned)(batch * a.heads_k)), dim3(ATT_THREADS), 0, s, bits, order, a);
-        GS_CHECK_LAUNCH();
         constexpr uint32_t lds = GkvLds<T, D>::BYTES;
         if (lds > 65536 && hipFuncSetAttribute((const void*)k_attn_gkv<T, D>, hipFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)lds) != hipSuccess)
             return GS_ERR_HIP;
         hipLaunchKernelGGL((k_attn_gkv<T, D>), dim3((unsigned)blocks), dim3(GKV_THREADS), lds, s, view_of<const T>(go),
-                           view_of<const T>(q), view_of<const T>(k), view_of<const T>(v), rows, bits, order, kv_len,
-                           view_of<T>(gk), view_of<T>(gv), a);
+                           view_of<const T>(q), view_of<const T>(k), view_of<const T>(v), rows, bits,
+                           ordered ? order : nullptr, kv_len, view_of<T>(gk), view_of<T>(gv), a);
         GS_CHECK_LAUNCH();
     }
     return GS_OK;
@@ -602,11 +584,6 @@ static gs_status attn_bwd_launch(const gs_tokens* go, const gs_tokens* q, const 
 static size_t row_bytes(int64_t batch, int64_t tokens_q, int32_t heads_q)
 {
     return (size_t)(batch * heads_q * ((tokens_q + QG - 1) / QG)) * 2 * QG * 4;
-}
-
-static int64_t bits_words(int64_t batch, int64_t groups, int64_t blocks, int32_t heads_q)
-{
-    return batch * heads_q * blocks * ((groups + 31) / 32);
 }
 
 }  // namespace gs

@@ -22,22 +22,24 @@ from . import _lib as L
 GROUP, BLOCK = L.GS_QUERY_GROUP, L.GS_KEY_BLOCK
 
 
+# The checks build their messages only when they fail, and compare device
+# numbers rather than devices: small calls are bound by the host.
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
 
 
 def _tokens(name, t, like=None):
-    _need(t.dim() == 4, f"{name} must be [batch, tokens, heads, dim], got {tuple(t.shape)}")
-    _need(t.is_cuda, f"{name} must be on the GPU")
-    if like is not None:
-        _need(t.dtype == like.dtype and t.device == like.device, f"{name} must have the type and device of its partner")
+    if t.dim() != 4 or not t.is_cuda:
+        raise ValueError(f"{name} must be [batch, tokens, heads, dim] on the GPU, got {tuple(t.shape)} on {t.device}")
+    if like is not None and (t.dtype is not like.dtype or t.get_device() != like.get_device()):
+        raise ValueError(f"{name} must have the type and device of its partner")
 
 
 def _vector(name, t, shape, like, dtype=torch.float32):
-    if t is not None:
-        _need(tuple(t.shape) == tuple(shape) and t.dtype == dtype and t.device == like.device and t.is_contiguous(),
-              f"{name} must be contiguous {dtype} {tuple(shape)} on {like.device}")
+    if t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous()
+                          or t.get_device() != like.get_device()):
+        raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)} on {like.device}")
 
 
 def _aligned(t, bytes=16):
@@ -133,10 +135,12 @@ def _length(kv_len, q):
 
 
 def _summary(name, s, shape, like):
-    _need(tuple(s[0].shape) == shape and s[0].dtype == torch.int8 and tuple(s[1].shape) == shape[:3]
-          and s[1].dtype == torch.float32 and s[0].device == s[1].device == like.device
-          and (s[0].stride(3) == 1 or shape[3] <= 1),
-          f"{name} must be int8 {shape} (its last dimension contiguous) and float32 {shape[:3]} on {like.device}")
+    sum8, scale = s
+    if (sum8.shape != shape or sum8.dtype is not torch.int8 or scale.shape != shape[:3] or scale.dtype is not torch.float32
+            or sum8.get_device() != like.get_device() or scale.get_device() != like.get_device()
+            or (sum8.stride(3) != 1 and shape[3] > 1)):
+        raise ValueError(f"{name} must be int8 {shape} (its last dimension contiguous) and float32 {shape[:3]} on "
+                         f"{like.device}")
 
 
 def block_summary(k, kv_len=None, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None, block0: int = 0):
