@@ -97,8 +97,8 @@ __global__ __launch_bounds__(SEL_THREADS) void k_block_summary(View<const T> k, 
 }
 
 struct SelArgs {
-    int64_t tokens_q, tokens_k, groups, blocks;
-    int32_t heads_q, heads_k, dim, causal, top;
+    int64_t tokens_q, tokens_k, groups, blocks, lists;
+    int32_t heads_q, heads_k, dim, causal, top, wide;  // wide: summary rows on 16 bytes
 };
 
 // Order-preserving map of finite floats to uint32 (never 0 or 0xffffffff).
@@ -108,22 +108,54 @@ __device__ __forceinline__ uint32_t rank_key(float x)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One workgroup per (batch, query head, group). Dynamic LDS: the blocks' keys.
-template <typename T>
-__global__ __launch_bounds__(SEL_THREADS) void k_block_select(View<const T> q, View<const int8_t> sum8,
-                                                              View<const float> scale,
-                                                              const int32_t* __restrict__ kv_len,
-                                                              int32_t* __restrict__ list, const SelArgs a)
+__device__ __forceinline__ int dot16(const uint4& x, const uint4& y, int dot)
 {
-    constexpr int N = Chunk<T>::N;
-    extern __shared__ uint32_t s_key[];
-    __shared__ int s_sum[256];
-    __shared__ int s_max;
-    __shared__ alignas(16) int8_t s_q[256];
-    __shared__ uint32_t s_hist[256];
-    __shared__ uint32_t s_pick[2];
-    __shared__ uint32_t s_cnt[2][SEL_THREADS / 64];
-    const int64_t id = blockIdx.x;
+    dot = __builtin_amdgcn_sdot4((int)x.x, (int)y.x, dot, false);
+    dot = __builtin_amdgcn_sdot4((int)x.y, (int)y.y, dot, false);
+    dot = __builtin_amdgcn_sdot4((int)x.z, (int)y.z, dot, false);
+    return __builtin_amdgcn_sdot4((int)x.w, (int)y.w, dot, false);
+}
+
+// Sum over each eight consecutive lanes; all of them get it.
+__device__ __forceinline__ int sum8_lanes(int x)
+{
+    x += __builtin_amdgcn_update_dpp(0, x, 0xb1, 0xf, 0xf, false);   // quad_perm 1,0,3,2
+    x += __builtin_amdgcn_update_dpp(0, x, 0x4e, 0xf, 0xf, false);   // quad_perm 2,3,0,1
+    return x + __builtin_amdgcn_update_dpp(0, x, 0x141, 0xf, 0xf, false);  // row_half_mirror
+}
+
+// Between the W waves of a list: a barrier, or nothing but order within a wave.
+template <int W>
+__device__ __forceinline__ void list_sync()
+{
+    if constexpr (W > 1) __syncthreads();
+    else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// One list (batch, query head, group) per W waves: the scores stay in
+// registers, KEYS a lane, block 64 W j + thread for j = 0 .. KEYS - 1, and the
+// top-th largest is found bit by bit from the top by counting (ballots and
+// scalar counts, no atomics: the scores of a list agree in their high bits, so
+// a histogram's additions would fall on few addresses).
+template <typename T, int W, int KEYS>
+__global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void k_block_select(View<const T> q, View<const int8_t> sum8,
+                                                                      View<const float> scale,
+                                                                      const int32_t* __restrict__ kv_len,
+                                                                      int32_t* __restrict__ list, const SelArgs a)
+{
+    constexpr int N = Chunk<T>::N, PER = W < 4 ? 4 / W : 1, THREADS = 64 * W;
+    __shared__ int s_sum[PER][256];
+    __shared__ int s_max[PER];
+    __shared__ int s_seen[PER];
+    __shared__ alignas(16) int8_t s_q[PER][256];
+    __shared__ uint32_t s_cnt[2][3][16];
+    __shared__ uint32_t s_start[W > 1 ? 2 * KEYS * W : 1];
+    __shared__ int s_dot[W == 1 ? PER : 1][W == 1 ? 64 * KEYS : 1];
+    const int which = threadIdx.x / THREADS, tid = threadIdx.x % THREADS, wave = tid >> 6;
+    const int64_t first_id = (int64_t)blockIdx.x * PER;
+    // past the last list: its work again, without its output
+    const bool extra = first_id + which >= a.lists;
+    const int64_t id = extra ? a.lists - 1 : first_id + which;
     const int64_t bh = id / a.groups, g = id - bh * a.groups;
     const int64_t b = bh / a.heads_q, h = bh - b * a.heads_q;
     const int64_t hk = h / (a.heads_q / a.heads_k);
@@ -136,111 +168,221 @@ __global__ __launch_bounds__(SEL_THREADS) void k_block_select(View<const T> q, V
     const int64_t low = t0 + len - a.tokens_q, high = low + n - 1;
     int64_t seen = len;
     if (a.causal && high + 1 < seen) seen = high + 1;
-    const int64_t visible = seen > 0 ? (seen + GS_KEY_BLOCK - 1) / GS_KEY_BLOCK : 0;
-    const int64_t held0 = a.causal ? (low > 0 ? low : 0) / GS_KEY_BLOCK : visible;
-    if (visible <= a.top) {  // all of them: nothing to rank
-        for (int64_t i = threadIdx.x; i < a.top; i += SEL_THREADS) out[i] = i < visible ? (int32_t)i : -1;
-        return;
-    }
+    const int visible = seen > 0 ? (int)((seen + GS_KEY_BLOCK - 1) / GS_KEY_BLOCK) : 0;
+    const int held0 = a.causal ? (int)((low > 0 ? low : 0) / GS_KEY_BLOCK) : visible;
+    const bool all = visible <= a.top;  // nothing to rank
+    if (all && !extra)
+        for (int i = tid; i < a.top; i += THREADS) out[i] = i < visible ? i : -1;
+    if (W > 1 && all) return;  // one list a workgroup; else the waves go on together
     // the group's 8-bit mean
-    for (int i = threadIdx.x; i < 256; i += SEL_THREADS) s_sum[i] = 0;
-    if (threadIdx.x == 0) s_max = 0;
-    __syncthreads();
-    const int chunks = a.dim / N, slices = SEL_THREADS / chunks;
-    const int c = threadIdx.x % chunks, slice = threadIdx.x / chunks;
-    if (slice < slices) {
+    for (int i = tid; i < 256; i += THREADS) s_sum[which][i] = 0;
+    if (tid == 0) s_max[which] = 0, s_seen[which] = visible;
+    list_sync<W>();
+    const int chunks = a.dim / N, slices = THREADS / chunks;
+    const int c = tid % chunks, slice = tid / chunks;
+    if (slice < slices && slice < n) {
         int acc[N] = {};
         sum_rows<T>(q.at(b, t0, h), q.st, 0, n, slice, slices, c, acc);
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (n > slice) atomicAdd(&s_sum[c * N + i], acc[i]);
+        for (int i = 0; i < N; ++i) atomicAdd(&s_sum[which][c * N + i], acc[i]);  // integers: any order
     }
-    __syncthreads();
-    const int d = threadIdx.x;
-    const int v = d < a.dim ? s_sum[d] : 0;
-    const int m = wave_max_int(abs(v));
-    if ((threadIdx.x & 63) == 0) atomicMax(&s_max, m);
-    __syncthreads();
-    if (d < a.dim) s_q[d] = (int8_t)to_eight(v, shift_of(s_max));
-    __syncthreads();
-    // scores of the visible blocks
+    list_sync<W>();
+    int m = 0;
+    for (int d = tid; d < a.dim; d += THREADS) m = max(m, abs(s_sum[which][d]));
+    m = wave_max_int(m);
+    if constexpr (W > 1) {
+        if (lane_id() == 0) atomicMax(&s_max[0], m);
+        __syncthreads();
+        m = s_max[0];
+    }
+    const int e = shift_of(m);
+    for (int d = tid; d < a.dim; d += THREADS) s_q[which][d] = (int8_t)to_eight(s_sum[which][d], e);
+    list_sync<W>();
+    // scores of the visible blocks; a key of 0 stands for none. Eight lanes
+    // read a row, 16 bytes each at a time, so that every line is read once and
+    // whole (a row per lane rereads its line for each 16 bytes once the waves'
+    // rows outgrow the L1); in step x lane l's eight take row 8 (l / 8) + x,
+    // whose sum lane 8 (l / 8) + x keeps.
     const int8_t* keys = sum8.at(b, 0, hk);
     const float* scales = scale.at(b, 0, hk);
-    const int words = a.dim / 8;
-    for (int64_t i = threadIdx.x; i < visible; i += SEL_THREADS) {
-        const uint2* row = (const uint2*)(keys + i * sum8.st);
-        int dot = 0;
-#pragma unroll 4
-        for (int w = 0; w < words; ++w) {
-            const uint2 x = row[w], y = ((const uint2*)s_q)[w];
-            dot = __builtin_amdgcn_sdot4((int)x.x, (int)y.x, dot, false);
-            dot = __builtin_amdgcn_sdot4((int)x.y, (int)y.y, dot, false);
-        }
-        // the product's one rounding; + 0 turns -0 into 0, which ties with it
-        const float s = (float)dot * scales[i * scale.st] + 0.f;
-        s_key[i] = i >= held0 ? 0xffffffffu : rank_key(s);
-    }
-    // the top-th largest key, 8 bits at a time
-    uint32_t prefix = 0, want = (uint32_t)a.top;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        s_hist[threadIdx.x] = 0;
+    const int sub = tid & 7, words = a.wide ? a.dim / 16 : 0;
+    uint32_t key[KEYS];
+    bool tiled = false;
+    if constexpr (W == 1) {
+        // The four lists of a workgroup share their key head nearly always:
+        // then its rows are read once for all four and multiplied by the
+        // matrix unit, 16 rows (columns of B) by the four means (rows of A),
+        // 64 dimensions at a time. (27 us of 62 by vector dot products, at 4080
+        // lists of 510 blocks and dim 128.)
         __syncthreads();
-        for (int64_t i = threadIdx.x; i < visible; i += SEL_THREADS) {
-            const uint32_t x = s_key[i];
-            if (shift == 24 || (x >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&s_hist[(x >> shift) & 255u], 1u);
-        }
-        __syncthreads();
-        if (threadIdx.x < 64) {
-            // lane t holds the four bins 255 - 4t .. 252 - 4t, largest first
-            uint32_t bin[4], sum = 0;
-            for (int i = 0; i < 4; ++i) sum += bin[i] = s_hist[255 - (threadIdx.x * 4 + i)];
-            uint32_t before = sum;
-            for (int off = 1; off < 64; off <<= 1) {
-                const uint32_t y = __shfl_up(before, off);
-                if ((int)threadIdx.x >= off) before += y;
-            }
-            before -= sum;
-            for (int i = 0; i < 4; ++i) {
-                if (before < want && before + bin[i] >= want) {
-                    s_pick[0] = 255u - (threadIdx.x * 4 + i);
-                    s_pick[1] = want - before;
+        const int64_t last_id = first_id + PER - 1 < a.lists ? first_id + PER - 1 : a.lists - 1;
+        const int per = a.heads_q / a.heads_k;
+        tiled = a.wide && a.dim % 64 == 0 && first_id / a.groups / per == last_id / a.groups / per;
+        if (tiled) {
+            typedef int int4v __attribute__((ext_vector_type(4)));
+            const int lane = lane_id(), part = lane >> 4, list_of = lane & 15;
+            int most = 0;
+            for (int w = 0; w < PER; ++w) most = max(most, s_seen[w]);
+            int4v mean[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                mean[t] = t * 64 < a.dim && list_of < PER ? ((const int4v*)s_q[list_of])[t * 4 + part] : int4v{0, 0, 0, 0};
+            for (int r0 = which * 16; r0 < most; r0 += PER * 16) {
+                const int r = min(r0 + list_of, most - 1);
+                const int4v* row = (const int4v*)(keys + r * sum8.st);
+                int4v acc = {0, 0, 0, 0};
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    if (t * 64 < a.dim) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(mean[t], row[t * 4 + part], acc, 0, 0, 0);
+                // C: column = lane & 15, rows 4 (lane >> 4) + i: the four lists are in the first 16 lanes
+                if (part == 0) {
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) s_dot[i][r0 + list_of] = acc[i];
                 }
-                before += bin[i];
             }
         }
         __syncthreads();
-        prefix |= s_pick[0] << shift;
-        want = s_pick[1];
+        if (all || extra) return;
     }
-    // keys above `prefix` are all in, of those equal to it the `want` lowest
-    // blocks; each thread holds a run of blocks, so ids come out ascending
-    const int64_t per = (visible + SEL_THREADS - 1) / SEL_THREADS;
-    const int64_t lo = threadIdx.x * per, hi = lo + per < visible ? lo + per : visible;
-    uint32_t above = 0, equal = 0;
-    for (int64_t i = lo; i < hi; ++i) {
-        above += s_key[i] > prefix;
-        equal += s_key[i] == prefix;
-    }
-    uint32_t ia = above, ie = equal;
-    for (int off = 1; off < 64; off <<= 1) {
-        const uint32_t x = __shfl_up(ia, off), y = __shfl_up(ie, off);
-        if ((int)lane_id() >= off) ia += x, ie += y;
-    }
-    const int wave = threadIdx.x >> 6;
-    if (lane_id() == 63) s_cnt[0][wave] = ia, s_cnt[1][wave] = ie;
-    __syncthreads();
-    ia -= above;
-    ie -= equal;
-    for (int w = 0; w < wave; ++w) ia += s_cnt[0][w], ie += s_cnt[1][w];
-    for (int64_t i = lo; i < hi; ++i) {
-        const uint32_t x = s_key[i];
-        if (x > prefix) {
-            out[ia + min(ie, want)] = (int32_t)i;
-            ++ia;
-        } else if (x == prefix) {
-            if (ie < want) out[ia + ie] = (int32_t)i;
-            ++ie;
+    auto score = [&](int j) __attribute__((always_inline)) -> uint32_t {
+        const int first = j * THREADS + (tid & ~7);  // of the eight rows
+        int kept = 0;
+        if (W == 1 && tiled) {
+            kept = s_dot[which][j * THREADS + tid];
+        } else {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const int i = first + x;
+                int dot = 0;
+                if (i < visible) {
+                    const int8_t* row = keys + i * sum8.st;
+                    if (a.wide) {
+                        for (int w = sub; w < words; w += 8)
+                            dot = dot16(((const uint4*)row)[w], ((const uint4*)s_q[which])[w], dot);
+                    } else {
+                        for (int w = sub; w < a.dim / 8; w += 8) {
+                            const uint2 p = ((const uint2*)row)[w], r = ((const uint2*)s_q[which])[w];
+                            dot = __builtin_amdgcn_sdot4((int)p.x, (int)r.x, dot, false);
+                            dot = __builtin_amdgcn_sdot4((int)p.y, (int)r.y, dot, false);
+                        }
+                    }
+                }
+                dot = sum8_lanes(dot);
+                kept = x == sub ? dot : kept;
+            }
         }
+        const int i = j * THREADS + tid;
+        if (i >= visible) return 0;
+        // the product's one rounding; + 0 turns -0 into 0, which ties with it
+        const float s = (float)kept * scales[i * scale.st] + 0.f;
+        return i >= held0 ? 0xffffffffu : rank_key(s);
+    };
+    if constexpr (KEYS > 8) {
+        // through LDS: unrolled, the steps' addresses alone would fill the registers
+        __shared__ uint32_t s_key[KEYS * THREADS];
+#pragma unroll 1
+        for (int j = 0; j < KEYS; ++j) s_key[j * THREADS + tid] = j * THREADS < visible ? score(j) : 0;
+#pragma unroll
+        for (int j = 0; j < KEYS; ++j) key[j] = s_key[j * THREADS + tid];
+    } else {
+#pragma unroll
+        for (int j = 0; j < KEYS; ++j) key[j] = j * THREADS < visible ? score(j) : 0;
+    }
+    // the top-th largest key: the largest value that at least `top` keys reach
+    auto count = [&](uint32_t from) {
+        uint32_t n = 0;
+#pragma unroll
+        for (int j = 0; j < KEYS; ++j)
+            if (j * THREADS < visible) n += __popcll(ballot(key[j] >= from));
+        return n;
+    };
+    const uint32_t top = (uint32_t)a.top;
+    uint32_t cut = 0;
+    if constexpr (W == 1) {
+        for (int bit = 31; bit >= 0; --bit) {
+            const uint32_t from = cut | 1u << bit, have = count(from);
+            if (have < top) continue;
+            cut = from;
+            if (have == top) {  // these are they, with no ties to break
+                --cut;
+                break;
+            }
+        }
+    } else {
+        // two bits a barrier; the waves' counts are added across 16 lanes
+        for (int bit = 30; bit >= 0; bit -= 2) {
+            uint32_t(&cnt)[3][16] = s_cnt[bit >> 1 & 1];
+#pragma unroll
+            for (int k = 1; k < 4; ++k) {
+                const uint32_t c1 = count(cut | (uint32_t)k << bit);
+                if (lane_id() == 0) cnt[k - 1][wave] = c1;
+            }
+            __syncthreads();
+            uint32_t sum[3];
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                int x = (lane_id() & 15) < W ? (int)cnt[k][lane_id() & 15] : 0;
+                x = sum8_lanes(x);
+                sum[k] = (uint32_t)__builtin_amdgcn_readlane(x, 0) + (uint32_t)__builtin_amdgcn_readlane(x, 8);
+            }
+            const int k = sum[2] >= top ? 3 : (sum[1] >= top ? 2 : (sum[0] >= top ? 1 : 0));
+            cut |= (uint32_t)k << bit;
+            if (k > 0 && sum[k - 1] == top) {  // these are they, with no ties to break
+                --cut;
+                break;
+            }
+        }
+    }
+    // keys above `cut` are all in, of those equal to it the lowest blocks that
+    // are wanted; ids come out in ascending order
+    uint32_t above = 0, equal = 0;  // before this wave's keys of step j
+    if constexpr (W == 1) {
+#pragma unroll
+        for (int j = 0; j < KEYS; ++j)
+            if (j * THREADS < visible) above += __popcll(ballot(key[j] > cut));
+    } else {
+        // per (step, wave): keys above and equal, then their exclusive sums
+#pragma unroll
+        for (int j = 0; j < KEYS; ++j) {
+            const uint32_t x = __popcll(ballot(key[j] > cut)), y = __popcll(ballot(key[j] == cut));
+            if (lane_id() == 0) s_start[j * W + wave] = x, s_start[KEYS * W + j * W + wave] = y;
+        }
+        __syncthreads();
+        if (wave < 2) {
+            uint32_t* p = s_start + wave * KEYS * W;
+            constexpr int ALL = KEYS * W, EACH = (ALL + 63) / 64;
+            const int lane = lane_id();
+            uint32_t v[EACH], sum = 0;
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) sum += v[i] = lane * EACH + i < ALL ? p[lane * EACH + i] : 0;
+            uint32_t run = sum;
+            for (int off = 1; off < 64; off <<= 1) {
+                const uint32_t x = __shfl_up(run, off);
+                if (lane >= off) run += x;
+            }
+            if (wave == 0 && lane == 63) s_max[0] = (int)run;  // all above
+            run -= sum;
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) {
+                if (lane * EACH + i < ALL) p[lane * EACH + i] = run;
+                run += v[i];
+            }
+        }
+        __syncthreads();
+        above = (uint32_t)s_max[0];
+    }
+    const uint32_t want = top - above;  // of the equal ones
+    above = 0;
+#pragma unroll
+    for (int j = 0; j < KEYS; ++j) {
+        if (j * THREADS >= visible) continue;
+        const uint64_t is_above = ballot(key[j] > cut), is_equal = ballot(key[j] == cut);
+        if constexpr (W > 1) above = s_start[j * W + wave], equal = s_start[KEYS * W + j * W + wave];
+        const uint32_t ra = above + mask_rank(is_above), re = equal + mask_rank(is_equal);
+        const bool mine = key[j] > cut || (key[j] == cut && re < want);
+        if (mine) out[ra + min(re, want)] = j * THREADS + tid;
+        above += __popcll(is_above);
+        equal += __popcll(is_equal);
     }
 }
 
@@ -254,17 +396,27 @@ static gs_status summary_launch(const gs_tokens* k, const int32_t* kv_len, const
     return GS_OK;
 }
 
+template <typename T, int W, int KEYS>
+static void select_by_waves(const gs_tokens* q, const gs_tokens* sum8, const gs_tokens* scale, const int32_t* kv_len,
+                            int32_t* list, const SelArgs& a, hipStream_t s)
+{
+    constexpr int PER = W < 4 ? 4 / W : 1;
+    hipLaunchKernelGGL((k_block_select<T, W, KEYS>), dim3(grid_for((uint64_t)a.lists, PER)), dim3(W < 4 ? 256 : 64 * W), 0, s,
+                       view_of<const T>(q), view_of<const int8_t>(sum8), view_of<const float>(scale), kv_len, list, a);
+}
+
+// Waves a list: 8 scores a lane, so that they stay in registers; one wave up
+// to 512 blocks, sixteen where the lists are too few to fill the CUs (one new
+// token, 2040 blocks, 16 lists: 18.4 us with four waves and a histogram in
+// LDS) or too long for four.
 template <typename T>
 static gs_status select_launch(const gs_tokens* q, const gs_tokens* sum8, const gs_tokens* scale, const int32_t* kv_len,
-                               int32_t* list, int64_t lists, const SelArgs& a, hipStream_t s)
+                               int32_t* list, const SelArgs& a, hipStream_t s)
 {
-    // keys of every block that can be visible; above 64 KiB the kernel asks for more LDS
-    const size_t lds = (size_t)a.blocks * 4;
-    if (lds > 65536 - 8192 &&
-        hipFuncSetAttribute((const void*)k_block_select<T>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
-        return GS_ERR_HIP;
-    hipLaunchKernelGGL((k_block_select<T>), dim3((unsigned)lists), dim3(SEL_THREADS), lds, s, view_of<const T>(q),
-                       view_of<const int8_t>(sum8), view_of<const float>(scale), kv_len, list, a);
+    if (a.blocks > 8192) select_by_waves<T, 16, 32>(q, sum8, scale, kv_len, list, a, s);
+    else if (a.blocks > 2048 || (a.lists <= 256 && a.blocks > 64)) select_by_waves<T, 16, 8>(q, sum8, scale, kv_len, list, a, s);
+    else if (a.blocks > 512) select_by_waves<T, 4, 8>(q, sum8, scale, kv_len, list, a, s);
+    else select_by_waves<T, 1, 8>(q, sum8, scale, kv_len, list, a, s);
     GS_CHECK_LAUNCH();
     return GS_OK;
 }
@@ -313,18 +465,18 @@ gs_status gs_block_select(const gs_tokens* q, const gs_tokens* sum8, const gs_to
     const int64_t blocks = (tokens_k + GS_KEY_BLOCK - 1) / GS_KEY_BLOCK;
     if (batch == 0 || groups == 0) return GS_OK;
     if (!q->data || !list || (blocks > 0 && (!sum8->data || !scale->data))) return GS_ERR_INVALID_ARGUMENT;
-    const int64_t grid_most = (int64_t)1 << 23;
+    const int64_t grid_most = (int64_t)1 << 21;  // 1024 threads each, below 2^32 in all
     if (batch > grid_most || heads_q > grid_most / batch || groups > grid_most / (batch * heads_q))
         return GS_ERR_UNSUPPORTED;
     if (!rows_aligned(q, batch, tokens_q, heads_q, elem_bytes(dtype), 16)) return GS_ERR_UNSUPPORTED;
     if (!rows_aligned(sum8, batch, blocks, heads_k, 1, 8)) return GS_ERR_UNSUPPORTED;
-    const SelArgs a{tokens_q, tokens_k, groups, blocks, heads_q, heads_k, dim, causal != 0, top};
+    const SelArgs a{tokens_q, tokens_k, groups, blocks, batch * heads_q * groups, heads_q, heads_k, dim, causal != 0, top,
+                    dim % 16 == 0 && rows_aligned(sum8, batch, blocks, heads_k, 1, 16)};
     const hipStream_t s = (hipStream_t)stream;
-    const int64_t lists = batch * heads_q * groups;
     switch (dtype) {
-        case GS_F32: return select_launch<float>(q, sum8, scale, kv_len, list, lists, a, s);
-        case GS_F16: return select_launch<f16>(q, sum8, scale, kv_len, list, lists, a, s);
-        default: return select_launch<bf16>(q, sum8, scale, kv_len, list, lists, a, s);
+        case GS_F32: return select_launch<float>(q, sum8, scale, kv_len, list, a, s);
+        case GS_F16: return select_launch<f16>(q, sum8, scale, kv_len, list, a, s);
+        default: return select_launch<bf16>(q, sum8, scale, kv_len, list, a, s);
     }
 }
 

@@ -238,79 +238,92 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm_bwd(const NormArgs
     if (pf) col.store_vec(a.part_a + (run + seg) * a.channels, sum_a);
 }
 
-// Sums over runs, 64 columns by 16 slices of the runs a workgroup, each slice
+// Sums over runs, 32 columns by 32 slices of the runs a workgroup, each slice
 // in order and the slices in order. The workgroups of gate s: A[s] from the
-// slots s + (runs that hold rows of s), times scale; the last ones: gw_pre.
-constexpr int SUMS_SLICES = 16;
+// slots s + (runs that hold rows of s), times scale; then those of gw_pre;
+// then, with few gates, those of gw_post, which add the gates' sums again
+// instead of waiting for them in a launch of their own.
+constexpr int SUMS_COLS = 32, SUMS_SLICES = 32, SUMS_GATES = 64;
 
-__device__ __forceinline__ float slice_sum(const float* p, int64_t first, int64_t count, int64_t stride, int c, bool on,
-                                           float (*s_buf)[64])
+__device__ __forceinline__ float slice_sum(const float* __restrict__ p, int64_t first, int64_t count, int64_t stride, int c,
+                                           bool on, float (*s_buf)[SUMS_COLS])
 {
-    const int slice = threadIdx.x >> 6;
+    const int slice = threadIdx.x / SUMS_COLS, col = threadIdx.x % SUMS_COLS;
     float s = 0.f;
     if (on) {
         const int64_t per = (count + SUMS_SLICES - 1) / SUMS_SLICES;
         const int64_t lo = slice * per, hi = lo + per < count ? lo + per : count;
+#pragma unroll 8
         for (int64_t k = lo; k < hi; ++k) s += p[(first + k) * stride + c];
     }
-    s_buf[slice][threadIdx.x & 63] = s;
+    s_buf[slice][col] = s;
     __syncthreads();
     s = 0.f;
-    for (int k = 0; k < SUMS_SLICES; ++k) s += s_buf[k][threadIdx.x & 63];
+#pragma unroll
+    for (int k = 0; k < SUMS_SLICES; ++k) s += s_buf[k][col];
     __syncthreads();
     return s;
 }
 
-__global__ __launch_bounds__(64 * SUMS_SLICES) void k_norm_sums(const float* __restrict__ part_a,
-                                                                const float* __restrict__ part_w,
-                                                                const float* __restrict__ w_post,
-                                                                float* __restrict__ a_of_gate,
-                                                                float* __restrict__ ggate, float* __restrict__ gw_pre,
-                                                                int64_t rows, int64_t per_gate, int64_t gates,
-                                                                int64_t run, int64_t runs, int32_t channels,
-                                                                float scale)
+__global__ __launch_bounds__(SUMS_COLS* SUMS_SLICES) void k_norm_sums(
+    const float* __restrict__ part_a, const float* __restrict__ part_w, const float* __restrict__ gate,
+    const float* __restrict__ w_post, float* __restrict__ a_of_gate, float* __restrict__ ggate, float* __restrict__ gw_pre,
+    float* __restrict__ gw_post, int64_t rows, int64_t per_gate, int64_t gates, int64_t run, int64_t runs, int32_t channels,
+    float scale)
 {
-    __shared__ float s_buf[SUMS_SLICES][64];
-    const int columns = (channels + 63) / 64;
-    const int c = blockIdx.x % columns * 64 + (threadIdx.x & 63);
-    const bool on = c < channels;
+    __shared__ float s_buf[SUMS_SLICES][SUMS_COLS];
+    const int columns = (channels + SUMS_COLS - 1) / SUMS_COLS;
+    const int c = blockIdx.x % columns * SUMS_COLS + threadIdx.x % SUMS_COLS;
+    const bool on = c < channels, first = on && threadIdx.x < SUMS_COLS;
     const int64_t s = blockIdx.x / columns;
     if (s == gates) {
         const float t = slice_sum(part_w, 0, runs, channels, c, on, s_buf);
-        if (on && threadIdx.x < 64 && gw_pre) gw_pre[c] = t;
+        if (first && gw_pre) gw_pre[c] = t;
         return;
     }
-    const int64_t lo = s * per_gate, end = lo + per_gate < rows ? lo + per_gate : rows;
-    const int64_t c0 = lo / run, c1 = (end - 1) / run;
-    const float t = scale * slice_sum(part_a, s + c0, c1 - c0 + 1, channels, c, on, s_buf);
-    if (on && threadIdx.x < 64) {
+    const auto of_gate = [&](int64_t g) {
+        const int64_t lo = g * per_gate, end = lo + per_gate < rows ? lo + per_gate : rows;
+        const int64_t c0 = lo / run, c1 = (end - 1) / run;
+        return scale * slice_sum(part_a, g + c0, c1 - c0 + 1, channels, c, on, s_buf);
+    };
+    if (s > gates) {
+        float t = 0.f;
+        for (int64_t g = 0; g < gates; ++g) {
+            const float x = of_gate(g);
+            if (on) t += gate ? gate[g * channels + c] * x : x;
+        }
+        if (first) gw_post[c] = t;
+        return;
+    }
+    const float t = of_gate(s);
+    if (first) {
         a_of_gate[s * channels + c] = t;
         if (ggate) ggate[s * channels + c] = w_post ? w_post[c] * t : t;
     }
 }
 
-// gw_post = sum over gates of gate A.
-__global__ __launch_bounds__(64 * SUMS_SLICES) void k_norm_gw_post(const float* __restrict__ a_of_gate,
-                                                                   const float* __restrict__ gate, int64_t gates,
-                                                                   int32_t channels, float* __restrict__ gw_post)
+// gw_post = sum over (many) gates of gate A.
+__global__ __launch_bounds__(SUMS_COLS* SUMS_SLICES) void k_norm_gw_post(const float* __restrict__ a_of_gate,
+                                                                         const float* __restrict__ gate, int64_t gates,
+                                                                         int32_t channels, float* __restrict__ gw_post)
 {
-    __shared__ float s_buf[SUMS_SLICES][64];
-    const int c = blockIdx.x * 64 + (threadIdx.x & 63), slice = threadIdx.x >> 6;
-    const bool on = c < channels;
+    __shared__ float s_buf[SUMS_SLICES][SUMS_COLS];
+    const int col = threadIdx.x % SUMS_COLS, slice = threadIdx.x / SUMS_COLS, c = blockIdx.x * SUMS_COLS + col;
     float s = 0.f;
-    if (on) {
+    if (c < channels) {
         const int64_t per = (gates + SUMS_SLICES - 1) / SUMS_SLICES;
         const int64_t lo = slice * per, hi = lo + per < gates ? lo + per : gates;
+#pragma unroll 8
         for (int64_t k = lo; k < hi; ++k) {
             const float x = a_of_gate[k * channels + c];
             s += gate ? gate[k * channels + c] * x : x;
         }
     }
-    s_buf[slice][threadIdx.x & 63] = s;
+    s_buf[slice][col] = s;
     __syncthreads();
-    if (threadIdx.x < 64 && on) {
+    if (threadIdx.x < SUMS_COLS && c < channels) {
         s = 0.f;
-        for (int k = 0; k < SUMS_SLICES; ++k) s += s_buf[k][threadIdx.x];
+        for (int k = 0; k < SUMS_SLICES; ++k) s += s_buf[k][col];
         gw_post[c] = s;
     }
 }
@@ -451,16 +464,18 @@ gs_status gs_norm_gate_bwd(const void* gy, const void* gh, const void* x, const 
     a.part_w = (float*)ws;
     a.part_a = a.part_w + (runs * channels + 3) / 4 * 4;
     float* a_of_gate = a.part_a + ((runs + gates) * channels + 3) / 4 * 4;
-    const unsigned columns = grid_for((uint64_t)channels, 64);
+    const unsigned columns = grid_for((uint64_t)channels, SUMS_COLS);
     // with f absent only gw_pre is summed (gates taken as 0)
     const int64_t g = f ? gates : 0;
-    if ((g + 1) * columns > ((int64_t)1 << 21)) return GS_ERR_UNSUPPORTED;  // 1024 threads each, below 2^32 in all
+    const bool with_post = f && gw_post && g > 0 && g <= SUMS_GATES;
+    if ((g + 2) * columns > ((int64_t)1 << 21)) return GS_ERR_UNSUPPORTED;  // 1024 threads each, below 2^32 in all
     if (rows > 0 && norm_dispatch(a, dtype, true, s) != hipSuccess) return GS_ERR_HIP;
-    hipLaunchKernelGGL(k_norm_sums, dim3((unsigned)(columns * (g + 1))), dim3(64 * SUMS_SLICES), 0, s, a.part_a, a.part_w,
-                       a.w_post, a_of_gate, ggate, gw_pre, rows, rows_per_gate, g, a.run, runs, channels, scale);
+    hipLaunchKernelGGL(k_norm_sums, dim3((unsigned)(columns * (g + 1 + with_post))), dim3(SUMS_COLS * SUMS_SLICES), 0, s,
+                       a.part_a, a.part_w, a.gate, a.w_post, a_of_gate, ggate, gw_pre, gw_post, rows, rows_per_gate, g, a.run,
+                       runs, channels, scale);
     GS_CHECK_LAUNCH();
-    if (gw_post && f) {
-        hipLaunchKernelGGL(k_norm_gw_post, dim3(columns), dim3(64 * SUMS_SLICES), 0, s, a_of_gate, a.gate, gates,
+    if (f && gw_post && !with_post) {
+        hipLaunchKernelGGL(k_norm_gw_post, dim3(columns), dim3(SUMS_COLS * SUMS_SLICES), 0, s, a_of_gate, a.gate, gates,
                            channels, gw_post);
         GS_CHECK_LAUNCH();
     }

@@ -766,7 +766,7 @@ size_t gs_norm_gate_bwd_workspace_bytes(int64_t rows, int32_t channels, int64_t 
  * gx may alias gy or x, gf may alias f or gh.
  *   ws  workspace of gs_norm_gate_bwd_workspace_bytes(...)
  * Errors: as gs_norm_gate_fwd, plus a small workspace or one off 16 bytes;
- * GS_ERR_UNSUPPORTED when gates x ceil(channels / 64) passes 2^21.
+ * GS_ERR_UNSUPPORTED when (gates + 2) x ceil(channels / 32) passes 2^21.
  */
 gs_status gs_norm_gate_bwd(const void* gy, const void* gh, const void* x, const void* f, const float* gate,
                            const float* w_post, const float* w_pre, const float* stats, void* gx, void* gf,
