@@ -257,14 +257,31 @@ __global__ __launch_bounds__(ATT_THREADS) void k_attn_join(const float* __restri
     const int d0 = threadIdx.x % TH * 4;
     const float* p = part + row * a.splits * (D + 4);
     float m = -INFINITY, total = 0.f;
-    for (int s = 0; s < a.splits; ++s) m = fmaxf(m, p[s * (D + 4)]);
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < a.splits; ++s) {
-        const float* ps = p + s * (D + 4);
-        const float f = m == -INFINITY ? 0.f : exp2_fast(ps[0] - m);
-        const float4 y = *(const float4*)(ps + 4 + d0);
-        total += f * ps[1];
-        x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
+    // eight splits at a time, all their loads in flight at once
+    for (int s0 = 0; s0 < a.splits; s0 += 8) {
+        float2 ml[8];
+        float4 y[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const float* ps = p + (s0 + s < a.splits ? s0 + s : a.splits - 1) * (D + 4);
+            ml[s] = *(const float2*)ps;
+            y[s] = *(const float4*)(ps + 4 + d0);
+        }
+        float most = m;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) most = s0 + s < a.splits ? fmaxf(most, ml[s].x) : most;
+        if (most == -INFINITY) continue;  // these splits saw nothing either
+        const float old = exp2_fast(m - most);
+        total *= old;
+        x.x *= old, x.y *= old, x.z *= old, x.w *= old;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const float f = s0 + s < a.splits ? exp2_fast(ml[s].x - most) : 0.f;
+            total = fmaf(f, ml[s].y, total);
+            x.x = fmaf(f, y[s].x, x.x), x.y = fmaf(f, y[s].y, x.y), x.z = fmaf(f, y[s].z, x.z), x.w = fmaf(f, y[s].w, x.w);
+        }
+        m = most;
     }
     const float inv = total > 0.f ? 1.f / total : 0.f;
     const int64_t bh = row / a.tokens_q, i = row - bh * a.tokens_q, b = bh / a.heads_q, h = bh - b * a.heads_q;
@@ -290,17 +307,22 @@ gs_status attn_check(int64_t batch, int64_t tokens_q, int64_t tokens_k, int32_t 
     return GS_OK;
 }
 
-// The split of few queries: while a group's workgroups do not fill the CUs.
+// The split of few queries: while a workgroup per group would leave most of
+// the 256 CUs idle. It reads each block for 32 queries where the other kernel
+// reads it for 128, so it must not be kept longer. Lists of 16 blocks, one
+// workgroup per group against this one: dim 128, 64 groups 27 against 20 us,
+// 116 groups 29 against 34; dim 64, 128 groups 24 against 22, 256 groups 25
+// against 32.
 struct Plan {
     bool few;
     int splits;
 };
 
-static Plan attn_plan(int64_t batch, int64_t tokens_q, int32_t heads_q, int32_t top)
+static Plan attn_plan(int64_t batch, int64_t tokens_q, int32_t heads_q, int32_t dim, int32_t top)
 {
     const int64_t groups = (tokens_q + QG - 1) / QG, tiles = (tokens_q + 31) / 32, bh = batch * heads_q;
     Plan p{};
-    p.few = bh * groups < 512;
+    p.few = bh * groups < (dim == 128 ? 96 : 192);
     p.splits = 1;
     if (p.few) {
         const int64_t want = (256 + bh * tiles - 1) / (bh * tiles), most = (top + 3) / 4;
@@ -344,7 +366,7 @@ size_t gs_block_attn_fwd_workspace_bytes(int64_t batch, int64_t tokens_q, int32_
     using namespace gs;
     if (attn_check(batch, tokens_q, 0, heads_q, 1, dim, GS_BF16, top, 1.f) != GS_OK) return 0;
     if (batch == 0 || tokens_q == 0) return 0;
-    const Plan p = attn_plan(batch, tokens_q, heads_q, top);
+    const Plan p = attn_plan(batch, tokens_q, heads_q, dim, top);
     return p.splits > 1 ? (size_t)(batch * heads_q * tokens_q) * p.splits * (dim + 4) * 4 : 0;
 }
 
@@ -365,7 +387,7 @@ gs_status gs_block_attn_fwd(const gs_tokens* q, const gs_tokens* k, const gs_tok
         return GS_ERR_UNSUPPORTED;
     const size_t need = gs_block_attn_fwd_workspace_bytes(batch, tokens_q, heads_q, dim, top);
     if (need > 0 && (!ws || ((uintptr_t)ws & 15) || ws_bytes < need)) return GS_ERR_INVALID_ARGUMENT;
-    const Plan plan = attn_plan(batch, tokens_q, heads_q, top);
+    const Plan plan = attn_plan(batch, tokens_q, heads_q, dim, top);
     const AttnArgs a{tokens_q, tokens_k, (tokens_q + QG - 1) / QG, (tokens_k + KB - 1) / KB, heads_q, heads_k,
                      causal != 0, top, plan.splits, sm_scale};
     const hipStream_t s = (hipStream_t)stream;
