@@ -143,18 +143,20 @@ def _summary(name, s, shape, like):
                          f"{like.device}")
 
 
-def block_summary(k, kv_len=None, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None, block0: int = 0):
-    """(sum8, scale) of the keys' blocks of 64, or of those from block0 on written
-    into `out` (a growing cache renews its last blocks). See gs_block_summary."""
+def block_summary(k, kv_len=None, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None, block0: int = 0,
+                  blocks: Optional[int] = None):
+    """(sum8, scale) of the keys' blocks of 64, or of `blocks` of them (the rest)
+    from block0 on written into `out` (a growing cache renews its last blocks).
+    See gs_block_summary."""
     _tokens("k", k)
     _length(kv_len, k)
     b, n, h, d = k.shape
     if out is None:
-        _need(block0 == 0, "block0 needs out")
+        _need(block0 == 0 and blocks is None, "block0 and blocks need out")
         out = (torch.empty(b, h, _blocks(n), d, dtype=torch.int8, device=k.device),
                torch.empty(b, h, _blocks(n), dtype=torch.float32, device=k.device))
     _summary("out", out, (b, h, _blocks(n), d), k)
-    L.gs_block_summary(_aligned(k), out[0], out[1], kv_len, block0)
+    L.gs_block_summary(_aligned(k), out[0], out[1], kv_len, block0, blocks)
     return out
 
 
