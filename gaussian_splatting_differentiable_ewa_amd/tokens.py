@@ -45,6 +45,8 @@ def _vector(name, t, shape, like, dtype=torch.float32):
 def _aligned(t, bytes=16):
     """t itself, or a copy, so that every row [dim] starts on that many bytes."""
     per = bytes // t.element_size()
+    if t.is_contiguous() and t.data_ptr() % bytes == 0 and t.shape[3] % per == 0:
+        return t
     sb, st, sh, sd = t.stride()
     b, n, h, d = t.shape
     if ((sd == 1 or d <= 1) and t.data_ptr() % bytes == 0 and (b <= 1 or sb % per == 0) and (n <= 1 or st % per == 0)
