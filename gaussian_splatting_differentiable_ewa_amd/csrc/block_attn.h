@@ -344,8 +344,7 @@ __device__ __forceinline__ void store4(T* p, float a, float b, float c, float d)
     *(typename Mma<T>::v4*)p = v;
 }
 
-// Host: the checks both directions share. GS_OK with `empty` when there is
-// nothing to do for the queries.
+// Host: the checks of sizes that both directions share.
 gs_status attn_check(int64_t batch, int64_t tokens_q, int64_t tokens_k, int32_t heads_q, int32_t heads_k, int32_t dim,
                      int32_t dtype, int32_t top, float sm_scale);
 

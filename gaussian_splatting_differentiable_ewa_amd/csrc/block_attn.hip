@@ -84,6 +84,16 @@ __device__ __forceinline__ void attend_block(const T* kt, const T* vt, const typ
 
 // Many queries: a workgroup per (batch, head, group), four waves of 32
 // queries, the listed blocks one after the other through two LDS stages.
+// A block is read once for 128 queries (128 x 64 x 4 x dim operations for 64 x
+// 2 x dim x 2 bytes: 128 a byte, from L2 mostly), and two workgroups a CU (four
+// at dim 64) let one wave's exponentials run behind another's matrix
+// instructions. Per block and wave at dim 128: 32 matrix instructions of 32
+// cycles each and 32 exponentials, maxima, sums and roundings a lane beside
+// them; at dim 64 half the former and all of the latter, which then bound it.
+// Measured: dim 128, 16 heads, 255 groups, 32 blocks each 578 us, 950 TFLOP/s
+// (large library product: 1350; matrix unit busy 47 %, no LDS bank conflicts);
+// dim 64, 16 heads on 4 key heads, 254 groups of 16 blocks, causal 180 us, 745
+// TFLOP/s.
 template <typename T, int D>
 __device__ __forceinline__ void attn_fwd(T (&s_tile)[2][2][Tile<D>::ELEMS], const View<const T>& q, const View<const T>& k,
                                          const View<const T>& v, const int32_t* __restrict__ lists,
@@ -161,6 +171,8 @@ __global__ __launch_bounds__(ATT_THREADS, D == 64 ? 4 : 2) void k_attn_fwd(View<
 // at the end (the softmax states of disjoint key sets add after rescaling to
 // the common maximum). With more than one split the joined states go to the
 // workspace and k_attn_join ends the work.
+// Bound by latency: one query, 16 heads of dim 128, 32 blocks: 8.5 us and 2.7
+// for the join (16 MB of keys and values, 3.3 us at the copy rate).
 template <typename T, int D>
 __global__ __launch_bounds__(ATT_THREADS, 1) void k_attn_few(View<const T> q, View<const T> k, View<const T> v,
                                                              const int32_t* __restrict__ lists,

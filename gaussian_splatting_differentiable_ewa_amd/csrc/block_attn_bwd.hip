@@ -7,6 +7,10 @@
 // (an OR: any order).
 // Both passes form S and P again from lse: 7 products in all where the
 // formula's 5 would need fp32 atomics on gq.
+//
+// Measured, dim 128, bf16, 16 heads, 255 groups of 32 blocks, 510 blocks:
+// prepare 22 us, gq 830 us (3 products: 990 TFLOP/s, matrix unit busy 49 %), order 9 us,
+// gk and gv 1440 us (4 products: 760 TFLOP/s, 36 %).
 #include <algorithm>
 
 #include "block_attn.h"
@@ -330,6 +334,11 @@ __global__ __launch_bounds__(ATT_THREADS) void k_block_order(const uint32_t* __r
 // multiplies while the other computes. The first kind is the longer one, so
 // the other issues all loads. Three stages of queries: one loading, one per
 // kind.
+// What bounds it is that a stage's loads take about as long as a step: without
+// the loads, the sums or the scores alone the pass takes 1.2, 1.2 and 1.15 of
+// its 1.44 ms. A fourth stage, loads two steps ahead, leaves no LDS for two
+// buffers of operands; the second barrier a step that one buffer needs costs
+// more than the stage gains (1.45 -> 1.6 ms).
 constexpr int GKV_THREADS = 512;
 
 // LDS of the workgroup, in bytes (the kernel's only LDS object, which so begins
@@ -388,7 +397,7 @@ struct GkvSteps {
     }
 };
 
-// P and dS, tile by tile. LEAD waves run one step more than they compute.
+// P and dS, tile by tile.
 template <typename T, int D>
 __device__ __forceinline__ void gkv_scores(GkvSteps<T, D>& steps, const View<const T>& k, const View<const T>& v, int blk,
                                            int hk, int len, const AttnArgs& a, int wave)

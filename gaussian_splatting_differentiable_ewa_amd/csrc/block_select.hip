@@ -57,6 +57,8 @@ __device__ __forceinline__ void sum_rows(const T* base, int64_t row_stride, int 
 }
 
 // One workgroup per (batch, head, block): 256 threads = chunks x row slices.
+// Bound by the read of k: 32640 tokens, 16 heads of dim 128, bf16, 28.5 us,
+// 4.7 TB/s.
 template <typename T>
 __global__ __launch_bounds__(SEL_THREADS) void k_block_summary(View<const T> k, const int32_t* __restrict__ kv_len,
                                                                View<int8_t> sum8, View<float> scale,
@@ -137,6 +139,11 @@ __device__ __forceinline__ void list_sync()
 // top-th largest is found bit by bit from the top by counting (ballots and
 // scalar counts, no atomics: the scores of a list agree in their high bits, so
 // a histogram's additions would fall on few addresses).
+// Measured, dim 128, bf16: 4080 lists of 32 out of 510 blocks 48 us (reads q at
+// 2.8 TB/s; a third of it, the counting, is vector and scalar work that the
+// reads of other lists do not fully hide); one new token against 2040 blocks,
+// 16 lists 19 us, which is latency: the mean 4, the scores 5, counting and
+// output 9.
 template <typename T, int W, int KEYS>
 __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void k_block_select(View<const T> q, View<const int8_t> sum8,
                                                                       View<const float> scale,

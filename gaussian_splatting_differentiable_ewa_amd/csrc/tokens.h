@@ -1,6 +1,6 @@
 // Device-side helpers shared by the token operators (rope.hip, norm_gate.hip,
 // block_select.hip, block_attn.hip, block_attn_bwd.hip): element types,
-// vector loads, the token views, and the MFMA/LDS pieces of the attention.
+// vector loads and the token views.
 #pragma once
 
 #include "internal.h"

@@ -791,7 +791,8 @@ gs_status gs_norm_gate_bwd(const void* gy, const void* gh, const void* x, const 
  *   sum8           out int8, a token tensor of ceil(tokens / 64) blocks
  *   scale          out fp32, the same without dim (strides in elements)
  * Errors: null pointers, bad sizes or dtype, dim not a multiple of 8 or
- * outside 8..256; GS_ERR_UNSUPPORTED when rows of k are not 16-byte aligned.
+ * outside 8..256; GS_ERR_UNSUPPORTED when rows of k are not 16-byte aligned or
+ * past 2^23 blocks in all.
  */
 gs_status gs_block_summary(const gs_tokens* k, int64_t batch, int64_t tokens, int32_t heads, int32_t dim,
                            int32_t dtype, const int32_t* kv_len, int64_t block0, int64_t blocks,
@@ -815,7 +816,7 @@ gs_status gs_block_summary(const gs_tokens* k, int64_t batch, int64_t tokens, in
  * Errors: null pointers, bad sizes, heads_q not a multiple of heads_k, top
  * outside 1..32768, dim not a multiple of 8 or outside 8..256, tokens_k over
  * GS_MAX_SELECT_TOKENS; GS_ERR_UNSUPPORTED when rows of q are not 16-byte
- * aligned or rows of sum8 not 8-byte aligned.
+ * aligned, rows of sum8 not 8-byte aligned, or past 2^21 lists.
  */
 gs_status gs_block_select(const gs_tokens* q, const gs_tokens* sum8, const gs_tokens* scale, int64_t batch,
                           int64_t tokens_q, int64_t tokens_k, int32_t heads_q, int32_t heads_k, int32_t dim,
@@ -833,7 +834,8 @@ size_t gs_block_attn_fwd_workspace_bytes(int64_t batch, int64_t tokens_q, int32_
  * over keys j of the listed blocks with j < kv_len (or tokens_k) and, when
  * `causal`, j <= kv_len - tokens_q + i for query i. A query that sees no key
  * has out = 0 and lse = -infinity. Keys and values at or past kv_len are not
- * used, whatever they hold.
+ * used, whatever they hold; one that only the causal limit hides from a query
+ * enters the products as 0 times itself and has to be finite.
  *   list  int32 [batch][heads_q][ceil(tokens_q / 128)][top], ascending with
  *         -1 after the last (gs_block_select's). An entry that does not
  *         exceed the one before it or lies outside the visible blocks is
@@ -845,8 +847,10 @@ size_t gs_block_attn_fwd_workspace_bytes(int64_t batch, int64_t tokens_q, int32_
  * Scores, softmax statistics and sums are fp32; the probabilities are rounded
  * to the inputs' type for their product with v.
  * Errors: null pointers, bad sizes, heads_q not a multiple of heads_k, top <
- * 1, a small workspace; GS_ERR_UNSUPPORTED for another dtype or dim, or rows
- * that are not 16-byte aligned.
+ * 1, a small workspace; GS_ERR_UNSUPPORTED for another dtype or dim, rows that
+ * are not 16-byte aligned, a token stride outside 0 .. 2^27 - 1 elements, or
+ * where batch x heads_q x (the larger of ceil(tokens_q / 32) and
+ * ceil(tokens_k / 64)) passes 2^23.
  */
 gs_status gs_block_attn_fwd(const gs_tokens* q, const gs_tokens* k, const gs_tokens* v, const int32_t* list,
                             int64_t batch, int64_t tokens_q, int64_t tokens_k, int32_t heads_q, int32_t heads_k,
@@ -865,7 +869,9 @@ size_t gs_block_attn_bwd_workspace_bytes(int64_t batch, int64_t tokens_q, int64_
  * summed over the query heads that share a key head. Keys that no group lists
  * get zeros, those past kv_len too. Every element of gq, gk and gv is
  * written; the sums have a fixed order, so the bits repeat.
- * P and dS are rounded to the inputs' type for the products.
+ * P and dS are rounded to the inputs' type for the products. The error that
+ * D takes over from the rounded `out` is removed from gk (the dS of a query add
+ * to zero) and, along the mean key, from gq.
  *   ws  device workspace of gs_block_attn_bwd_workspace_bytes(...)
  * Errors: as gs_block_attn_fwd.
  */
