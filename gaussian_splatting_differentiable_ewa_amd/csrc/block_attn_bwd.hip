@@ -246,15 +246,17 @@ __global__ __launch_bounds__(ATT_THREADS, 2) void k_attn_gq(View<const T> go, Vi
 // lanes: a step costs a few scalar instructions instead of a dependent load.
 struct Walk {
     const uint32_t* bits;  // of the first head, this block
-    int64_t head_stride, total;
-    int words;
-    // state
-    int64_t base;
+    int64_t head_stride;
+    int words, total;
+    // state; lane l holds word base + l, its head and its first query (divided
+    // there, once per 64 words, instead of per step)
+    int base;
     uint64_t some;  // lanes with words left
     uint32_t held, left;
-    int h, at, q0;
+    int held_h, held_q, h, word_q, q0;
     __device__ __forceinline__ Walk(const uint32_t* p, int64_t stride, int n, int heads)
-        : bits(p), head_stride(stride), total((int64_t)n * heads), words(n), base(-64), some(0), held(0), left(0), h(0), at(0), q0(0)
+        : bits(p), head_stride(stride), words(n), total(n * heads), base(-64), some(0), held(0), left(0), held_h(0), held_q(0),
+          h(0), word_q(0), q0(0)
     {
     }
     __device__ __forceinline__ bool next()
@@ -263,19 +265,20 @@ struct Walk {
             while (some == 0) {
                 base += 64;
                 if (base >= total) return false;
-                const int64_t i = base + lane_id();
-                held = i < total ? bits[i / words * head_stride + i % words] : 0;
+                const int i = base + (int)lane_id();
+                held_h = (uint32_t)i / (uint32_t)words;
+                held_q = (i - held_h * words) * 32 * QG;
+                held = i < total ? bits[held_h * head_stride + (i - held_h * words)] : 0;
                 some = ballot(held != 0);
             }
-            at = __builtin_ctzll(some);
+            const int at = __builtin_ctzll(some);
             some &= some - 1;
             left = __builtin_amdgcn_readlane(held, at);
+            h = __builtin_amdgcn_readlane(held_h, at);
+            word_q = __builtin_amdgcn_readlane(held_q, at);
         }
-        const int bit = __builtin_ctz(left);
+        q0 = word_q + __builtin_ctz(left) * QG;
         left &= left - 1;
-        const int64_t i = base + at;
-        h = (int)(i / words);
-        q0 = ((int)(i - (int64_t)h * words) * 32 + bit) * QG;
         return true;
     }
 };
