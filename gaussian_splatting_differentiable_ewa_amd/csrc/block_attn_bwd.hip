@@ -337,11 +337,16 @@ __global__ __launch_bounds__(ATT_THREADS) void k_block_order(const uint32_t* __r
 // multiplies while the other computes. The first kind is the longer one, so
 // the other issues all loads. Three stages of queries: one loading, one per
 // kind.
-// What bounds it is that a stage's loads take about as long as a step: without
-// the loads, the sums or the scores alone the pass takes 1.2, 1.2 and 1.15 of
-// its 1.44 ms. A fourth stage, loads two steps ahead, leaves no LDS for two
-// buffers of operands; the second barrier a step that one buffer needs costs
-// more than the stage gains (1.45 -> 1.6 ms).
+// What bounds it: a step's chain of products, exponentials, operands and
+// barrier, and what a block costs besides its steps (bits, first loads, filling
+// and draining the three stages, with no second workgroup on the CU): with lists
+// of 8, 16, 32 and 64 blocks 0.54, 0.92, 1.5 and 2.8 ms at the size above, 10 us
+// of each workgroup's 45 at 32. Without the loads, the sums or the scores alone
+// the pass takes 1.2, 1.2 and 1.15 of its 1.44 ms. Loads two steps ahead in a
+// fourth stage (row values through registers) are no faster, nor are twice the
+// score waves, one half a step behind the other (1.75 ms), nor workgroups that
+// go on to their next block (1.75 ms: the bookkeeping in every step costs more
+// than the drain).
 constexpr int GKV_THREADS = 512;
 
 // LDS of the workgroup, in bytes (the kernel's only LDS object, which so begins
