@@ -310,8 +310,8 @@ gs_status attn_check(int64_t batch, int64_t tokens_q, int64_t tokens_k, int32_t 
         !(sm_scale < INFINITY))
         return GS_ERR_INVALID_ARGUMENT;
     if ((dim != 64 && dim != 128) || dtype == GS_F32) return GS_ERR_UNSUPPORTED;
-    // one workgroup of 256 threads per unit of 32 queries (or 64 keys): below 2^32 threads in all
-    const int64_t units = (int64_t)1 << 23;
+    // one workgroup of 256 threads per unit of 32 queries, of 512 per 64 keys: below 2^32 threads in all
+    const int64_t units = ((int64_t)1 << 23) - 1;
     const int64_t per = std::max((tokens_q + 31) / 32, (tokens_k + KB - 1) / KB);
     if (batch > units || (batch > 0 && heads_q > units / batch) ||
         (batch > 0 && per > units / (batch * heads_q)))

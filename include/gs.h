@@ -850,7 +850,7 @@ size_t gs_block_attn_fwd_workspace_bytes(int64_t batch, int64_t tokens_q, int32_
  * 1, a small workspace; GS_ERR_UNSUPPORTED for another dtype or dim, rows that
  * are not 16-byte aligned, a token stride outside 0 .. 2^27 - 1 elements, or
  * where batch x heads_q x (the larger of ceil(tokens_q / 32) and
- * ceil(tokens_k / 64)) passes 2^23.
+ * ceil(tokens_k / 64)) reaches 2^23.
  */
 gs_status gs_block_attn_fwd(const gs_tokens* q, const gs_tokens* k, const gs_tokens* v, const int32_t* list,
                             int64_t batch, int64_t tokens_q, int64_t tokens_k, int32_t heads_q, int32_t heads_k,
