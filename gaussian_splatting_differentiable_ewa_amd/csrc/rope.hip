@@ -22,9 +22,27 @@ struct RopeArgs {
     int32_t interleaved, inverse;
 };
 
+// Sine and cosine of x f for any whole x of 32 bits. In fp32 the product alone
+// would be off by up to half an ulp of itself, radians at far positions; so it
+// is formed in fp64, with what fp64 rounds off, and reduced to +-pi by a 2 pi
+// of two fp64 parts before it goes to fp32, again with its remainder e:
+// cos(t + e) = cos t - e sin t, sin(t + e) = sin t + e cos t (e^2 < 2^-46).
+__device__ __forceinline__ void turn_of(int32_t x, float f, float& sn, float& cs)
+{
+    constexpr double TWO_PI = 6.283185307179586477, TWO_PI_REST = 2.449293598294706e-16, PER = 0.15915494309189533577;
+    const double xd = (double)x, fd = (double)f, t = xd * fd, k = rint(t * PER);
+    double r = fma(-k, TWO_PI, t);
+    r = fma(-k, TWO_PI_REST, r) + fma(xd, fd, -t);
+    const float near = (float)r, e = (float)(r - (double)near);
+    float s0, c0;
+    sincosf(near, &s0, &c0);
+    cs = fmaf(-e, s0, c0);
+    sn = fmaf(e, c0, s0);
+}
+
 // VEC pairs at a time: contiguous elements of each half (or 2 VEC contiguous
-// elements when interleaved). Angles, sines and the rotation are fp32; each
-// result is rounded once.
+// elements when interleaved). Sines and the rotation are fp32; each result is
+// rounded once.
 template <typename T, int VEC>
 __global__ __launch_bounds__(ROPE_THREADS) void k_rope(View<const T> q, View<const T> k, View<T> qo, View<T> ko,
                                                        const int32_t* __restrict__ pos,
@@ -38,7 +56,7 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope(View<const T> q, View<con
     const int slice = (int)(at - token * a.slices);
     const int64_t b = token / a.tokens, l = token - b * a.tokens;
     const int32_t* p = pos + b * a.stride_pos_b + l * 3;
-    const float p0 = (float)p[0], p1 = (float)p[1], p2 = (float)p[2];
+    const int32_t p0 = p[0], p1 = p[1], p2 = p[2];
     float cs[VEC], sn[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
@@ -46,14 +64,7 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_rope(View<const T> q, View<con
         cs[i] = 1.f;
         sn[i] = 0.f;
         if (j < a.p0 + a.p1 + a.p2) {
-            const float x = j < a.p0 ? p0 : (j < a.p0 + a.p1 ? p1 : p2), f = freq[j];
-            // the product's rounding error e enters to first order:
-            // cos(t + e) = cos t - e sin t, sin(t + e) = sin t + e cos t
-            const float t = x * f, e = fmaf(x, f, -t);
-            float s0, c0;
-            sincosf(t, &s0, &c0);
-            cs[i] = fmaf(-e, s0, c0);
-            sn[i] = fmaf(e, c0, s0);
+            turn_of(j < a.p0 ? p0 : (j < a.p0 + a.p1 ? p1 : p2), freq[j], sn[i], cs[i]);
             if (a.inverse) sn[i] = -sn[i];
         }
     }

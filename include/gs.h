@@ -707,8 +707,9 @@ typedef struct gs_tokens {
  * turned by the angle t = pos[b][l][a(j)] * freq[j]:
  *   (x0, x1) -> (x0 cos t - x1 sin t, x0 sin t + x1 cos t)
  * With `inverse` the angle is -t: the inverse rotation, which is also the
- * gradient's way back (the rotation is orthogonal). The angle's product is
- * not rounded before the sine (its rounding error is carried).
+ * gradient's way back (the rotation is orthogonal). The angle is not rounded
+ * to fp32 before the sine, so far positions turn as exactly as near ones
+ * (|t| up to 2^52).
  *   q, k         inputs (k may be NULL); q_out, k_out outputs, which may be
  *                the inputs themselves
  *   heads_q/_k   heads of each (heads_k 0 without k)
