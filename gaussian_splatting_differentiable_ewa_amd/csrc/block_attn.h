@@ -287,36 +287,54 @@ __device__ __forceinline__ int64_t seq_len(const int32_t* kv_len, int64_t b, int
     return n < 0 ? 0 : (n > tokens ? tokens : n);
 }
 
-// Whether entry j of a list counts: ascending, inside the visible blocks.
-__device__ __forceinline__ bool entry_ok(const int32_t* list, int j, int64_t visible)
-{
-    const int id = list[j], before = j > 0 ? list[j - 1] : -1;
-    return id >= 0 && id > before && id < visible;
-}
-
-// Walks the entries of a list that count, 64 of them held by the wave's lanes:
-// a step costs a few scalar instructions instead of a dependent load.
+// Walks the entries of a list that count, those that exceed every entry before
+// them and lie inside the visible blocks: so none counts twice, in either
+// direction, whatever the list holds. 64 entries are held by the wave's lanes:
+// a step costs a few scalar instructions instead of a dependent load. With
+// `step` only the entries `first`, first + step, ... are walked.
 struct ListWalk {
     const int32_t* list;
     int64_t visible;
-    int top, base, ids;  // ids: lane l holds entry base + l
+    int top, base, ids, most, first, step;  // ids: lane l holds entry base + l; most: the largest before them
     uint64_t left;
-    __device__ __forceinline__ ListWalk(const int32_t* l, int n, int64_t vis) : list(l), visible(vis), top(n), base(0) { fetch(); }
+    __device__ __forceinline__ ListWalk(const int32_t* l, int n, int64_t vis, int from = 0, int by = 1)
+        : list(l), visible(vis), top(n), base(0), most(-1), first(from), step(by)
+    {
+        fetch();
+    }
     __device__ __forceinline__ void fetch()
     {
         const int j = base + (int)lane_id();
         ids = j < top ? list[j] : -1;
         const int before = j > 0 && j < top ? list[j - 1] : -1;
-        left = ballot(ids >= 0 && ids > before && ids < visible);
+        const uint64_t up = ballot(ids > before);
+        left = ballot(ids > max(before, most));
+        if ((up & (up + 1)) == 0) {
+            // as selected: rising entries, then none that rises, so the neighbour is the largest before
+            if (up) most = max(most, __builtin_amdgcn_readlane(ids, __popcll(up) - 1));
+        } else {
+            left = 0;
+#pragma unroll 1
+            for (int i = 0; i < 64; ++i) {
+                const int id = __builtin_amdgcn_readlane(ids, i);
+                if (id > most) most = id, left |= 1ull << i;
+            }
+        }
+        left &= ballot(ids < visible && (step == 1 || j % step == first));
+    }
+    // The next 64 entries, if there are any.
+    __device__ __forceinline__ bool more()
+    {
+        base += 64;
+        if (base >= top) return false;
+        fetch();
+        return true;
     }
     // The next block, or -1.
     __device__ __forceinline__ int next()
     {
-        while (left == 0) {
-            base += 64;
-            if (base >= top) return -1;
-            fetch();
-        }
+        while (left == 0)
+            if (!more()) return -1;
         const int j = __builtin_ctzll(left);
         left &= left - 1;
         return __builtin_amdgcn_readlane(ids, j);

@@ -205,9 +205,9 @@ __global__ __launch_bounds__(ATT_THREADS, 1) void k_attn_few(View<const T> q, Vi
     const T* kb = k.at(b, 0, hk);
     const T* vb = v.at(b, 0, hk);
     const TileLoad<T, D, 1> load_k(k.st), load_v(v.st);
-    for (int j = split * 4 + wave; j < a.top; j += 4 * a.splits) {
-        if (!entry_ok(list, j, visible)) continue;
-        const int64_t k0 = (int64_t)list[j] * KB, rest = mine - k0;
+    ListWalk walk(list, a.top, visible, split * 4 + wave, 4 * a.splits);
+    for (int blk = walk.next(); blk >= 0; blk = walk.next()) {
+        const int64_t k0 = (int64_t)blk * KB, rest = mine - k0;
         // the wave's own reads of the tile's last contents are done: their
         // results were used
         load_k(s_tile[wave][0], kb, k0, len - 1, 0);

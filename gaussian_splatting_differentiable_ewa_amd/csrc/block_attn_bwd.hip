@@ -103,9 +103,12 @@ __device__ __forceinline__ void attn_gq(char* lds, const View<const T>& go, cons
     const int visible = most > 0 ? (most + KB - 1) / KB : 0;
     ListWalk walk(lists + id * a.top, a.top, visible);
     // the group's bit at each of its blocks, for the other pass
-    for (int j = threadIdx.x; j < a.top; j += ATT_THREADS)
-        if (entry_ok(lists + id * a.top, j, visible))
-            atomicOr(&bits[(bh * a.blocks + lists[id * a.top + j]) * ((a.groups + 31) / 32) + g / 32], 1u << (g & 31));
+    if (wave == 0) {
+        ListWalk all(walk);
+        do {
+            if (all.left >> lane & 1) atomicOr(&bits[(bh * a.blocks + all.ids) * ((a.groups + 31) / 32) + g / 32], 1u << (g & 31));
+        } while (all.more());
+    }
     int blk = walk.next();
     if (blk >= 0) {
         load_k((T*)lds, kb, (int64_t)blk * KB, len - 1, wave);

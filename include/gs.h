@@ -839,8 +839,9 @@ size_t gs_block_attn_fwd_workspace_bytes(int64_t batch, int64_t tokens_q, int32_
  * enters the products as 0 times itself and has to be finite.
  *   list  int32 [batch][heads_q][ceil(tokens_q / 128)][top], ascending with
  *         -1 after the last (gs_block_select's). An entry that does not
- *         exceed the one before it or lies outside the visible blocks is
- *         skipped, so no list leads out of k and v
+ *         exceed every entry before it or lies outside the visible blocks is
+ *         skipped, here and in the backward pass, so no block counts twice
+ *         and no list leads out of k and v
  *   sm_scale  > 0
  *   q, k, v, out  GS_F16 or GS_BF16, dim 64 or 128; key head of query head h:
  *         h / (heads_q / heads_k)
