@@ -25,6 +25,11 @@ struct Online {
 // block, at 64 multiplications a lane.
 constexpr float RISE = 8.f;
 
+// A sum of zero is a query that saw no key; a NaN (from its own row or a key it
+// sees) is none, and goes on.
+__device__ __forceinline__ float inverse_of(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
+__device__ __forceinline__ float lse_of(float m, float sum) { return sum == 0.f ? -INFINITY : (m + log2f(sum)) * LN2; }
+
 // One block of 64 keys: limit is the number of keys, counted from the block's
 // first, that this lane's query sees (>= 64: all of them).
 template <typename T, int D, bool MASKED>
@@ -145,7 +150,7 @@ __device__ __forceinline__ void attn_fwd(T (&s_tile)[2][2][Tile<D>::ELEMS], cons
     walk_blocks(step, [&] { return blk >= 0; }, [&] { return (int64_t)blk * KB + KB > least; });
     if (i >= a.tokens_q) return;
     const float l = st.l + __shfl_xor(st.l, 32);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = inverse_of(l);
     T* o = out.at(b, i, h);
 #pragma unroll
     for (int t = 0; t < D / 32; ++t)
@@ -153,7 +158,7 @@ __device__ __forceinline__ void attn_fwd(T (&s_tile)[2][2][Tile<D>::ELEMS], cons
         for (int r = 0; r < 4; ++r)
             store4<T>(o + t * 32 + r * 8 + hi * 4, st.o[t][4 * r] * inv, st.o[t][4 * r + 1] * inv,
                       st.o[t][4 * r + 2] * inv, st.o[t][4 * r + 3] * inv);
-    if (hi == 0) lse[bh * a.tokens_q + i] = l > 0.f ? (st.m + log2f(l)) * LN2 : -INFINITY;
+    if (hi == 0) lse[bh * a.tokens_q + i] = lse_of(st.m, l);
 }
 
 template <typename T, int D>
@@ -236,7 +241,7 @@ __global__ __launch_bounds__(ATT_THREADS, 1) void k_attn_few(View<const T> q, Vi
     }
     const int64_t at = i0 + col;
     if (at >= a.tokens_q) return;
-    const float inv = total > 0.f ? 1.f / total : 0.f;
+    const float inv = inverse_of(total);
     constexpr int PER = D / 8;  // dimensions of one thread
     const int d0 = (threadIdx.x >> 5) * PER;
     float x[PER];
@@ -249,7 +254,7 @@ __global__ __launch_bounds__(ATT_THREADS, 1) void k_attn_few(View<const T> q, Vi
         T* o = out.at(b, at, h) + d0;
 #pragma unroll
         for (int d = 0; d < PER; d += 4) store4<T>(o + d, x[d] * inv, x[d + 1] * inv, x[d + 2] * inv, x[d + 3] * inv);
-        if (d0 == 0) lse[bh * a.tokens_q + at] = total > 0.f ? (m + log2f(total)) * LN2 : -INFINITY;
+        if (d0 == 0) lse[bh * a.tokens_q + at] = lse_of(m, total);
     } else {
         float* p = part + ((bh * a.tokens_q + at) * a.splits + split) * (D + 4);
 #pragma unroll
@@ -283,22 +288,22 @@ __global__ __launch_bounds__(ATT_THREADS) void k_attn_join(const float* __restri
         float most = m;
 #pragma unroll
         for (int s = 0; s < 8; ++s) most = s0 + s < a.splits ? fmaxf(most, ml[s].x) : most;
-        if (most == -INFINITY) continue;  // these splits saw nothing either
-        const float old = exp2_fast(m - most);
+        // nothing seen so far: factors of zero (not skipped: a sum may be NaN)
+        const float ref = most == -INFINITY ? 0.f : most, old = exp2_fast(m - ref);
         total *= old;
         x.x *= old, x.y *= old, x.z *= old, x.w *= old;
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
-            const float f = s0 + s < a.splits ? exp2_fast(ml[s].x - most) : 0.f;
+            const float f = s0 + s < a.splits ? exp2_fast(ml[s].x - ref) : 0.f;
             total = fmaf(f, ml[s].y, total);
             x.x = fmaf(f, y[s].x, x.x), x.y = fmaf(f, y[s].y, x.y), x.z = fmaf(f, y[s].z, x.z), x.w = fmaf(f, y[s].w, x.w);
         }
         m = most;
     }
-    const float inv = total > 0.f ? 1.f / total : 0.f;
+    const float inv = inverse_of(total);
     const int64_t bh = row / a.tokens_q, i = row - bh * a.tokens_q, b = bh / a.heads_q, h = bh - b * a.heads_q;
     store4<T>(out.at(b, i, h) + d0, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-    if (d0 == 0) lse[row] = total > 0.f ? (m + log2f(total)) * LN2 : -INFINITY;
+    if (d0 == 0) lse[row] = lse_of(m, total);
 }
 
 gs_status attn_check(int64_t batch, int64_t tokens_q, int64_t tokens_k, int32_t heads_q, int32_t heads_k, int32_t dim,
