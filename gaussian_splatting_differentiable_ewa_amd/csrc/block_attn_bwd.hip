@@ -201,6 +201,7 @@ __device__ __forceinline__ void attn_gq(char* lds, const View<const T>& go, cons
             }
         }
         part = wave_sum(part);
+        part = part < INFINITY ? part : 0.f;  // a NaN row must not reach its neighbours through c
         weight += part;
 #pragma unroll
         for (int x = 0; x < D / 64; ++x) mean[x] = fmaf(part, mu[x], mean[x]);
