@@ -486,7 +486,8 @@ gs_status gs_norm_gate_bwd(const void* gy, const void* gh, const void* x, const 
                        a.part_a, a.part_w, a.gate, a.w_post, a_of_gate, ggate, gw_pre, gw_post, rows, rows_per_gate, g, a.run,
                        runs, channels, scale);
     GS_CHECK_LAUNCH();
-    if (f && gw_post && !with_post) {
+    // without rows f may be null because it is empty: its sum is zero, and written
+    if ((f || rows == 0) && gw_post && !with_post) {
         hipLaunchKernelGGL(k_norm_gw_post, dim3(columns), dim3(SUMS_COLS * SUMS_SLICES), 0, s, a_of_gate, a.gate, gates,
                            channels, gw_post);
         GS_CHECK_LAUNCH();

@@ -762,7 +762,8 @@ size_t gs_norm_gate_bwd_workspace_bytes(int64_t rows, int32_t channels, int64_t 
  *   x, f, gate, w_post, w_pre, scale, stats   as of the forward call; y is
  *                formed again from x and f
  *   gx           out, the type of x; gf out (not with f NULL)
- *   ggate, gw_post, gw_pre   out fp32, each may be NULL (not wanted)
+ *   ggate, gw_post, gw_pre   out fp32, each may be NULL (not wanted); zeros
+ *                when there are no rows
  * The sums over rows are taken in a fixed order: the same bits on every call.
  * gx may alias gy or x, gf may alias f or gh.
  *   ws  workspace of gs_norm_gate_bwd_workspace_bytes(...)
