@@ -26,6 +26,7 @@ from typing import List, Optional, Sequence, Tuple
 
 import torch
 import torch.nn.functional as F
+from torch.autograd.function import once_differentiable
 
 from . import _lib as L
 from . import tokens as T
@@ -51,6 +52,7 @@ class RenderL1(torch.autograd.Function):
         return buf.loss[0].float()
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         return ctx.saved_tensors[0] * g, None, None
 

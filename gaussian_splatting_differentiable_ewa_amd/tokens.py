@@ -16,6 +16,7 @@ from __future__ import annotations
 from typing import Optional, Sequence, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib as L
 
@@ -224,6 +225,8 @@ def block_attention_backward(gout, q, k, v, out, lse, lists, sm_scale: Optional[
 
 
 # ---- for torch.autograd ---------------------------------------------------------
+# Differentiable once: the backward kernels record no graph, so a gradient of
+# their gradients (create_graph=True) raises instead of lacking their part.
 class RopeAxes(torch.autograd.Function):
     """apply(q, k, pos, freq, pairs, interleaved=False) -> q', k' (gradients of q
     and k only)."""
@@ -235,6 +238,7 @@ class RopeAxes(torch.autograd.Function):
         return rope_axes(q, k, pos, freq, pairs, interleaved)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gq, gk):
         pos, freq = ctx.saved_tensors
         gq, gk = rope_axes(gq, gk, pos, freq, ctx.how[0], ctx.how[1], inverse=True)
@@ -253,6 +257,7 @@ class NormGate(torch.autograd.Function):
         return (x.view_as(x) if f is None else y), h
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gy, gh):
         gy = None if gy is None else gy.contiguous()
         grads = norm_gate_backward(gy, gh.contiguous(), *ctx.saved_tensors, scale=ctx.how[0], rows_per_gate=ctx.how[1])
@@ -270,6 +275,7 @@ class BlockAttention(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gout):
         q, k, v, out, lse, lists, kv_len = ctx.saved_tensors
         grads = block_attention_backward(gout, q, k, v, out, lse, lists, ctx.how[0], kv_len, ctx.how[1])
