@@ -7,8 +7,9 @@ workspace and makes one or two calls of the C ABI on the current stream
 (``_lib``); nothing is kept between calls. Token tensors are
 ``[batch, tokens, heads, dim]`` with any strides (views of a packed projection
 need no copy); a tensor whose rows do not start on 16 bytes is copied where the
-kernels need that. ``RopeAxes``, ``NormGate`` and ``BlockAttention`` are the
-same for ``torch.autograd``.
+kernels need that. The functions record no graph, and refuse tensors whose
+gradient would be lost that way; ``RopeAxes``, ``NormGate`` and
+``BlockAttention`` are the same for ``torch.autograd``.
 """
 
 from __future__ import annotations
@@ -43,6 +44,13 @@ def _vector(name, t, shape, like, dtype=torch.float32):
         raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)} on {like.device}")
 
 
+def _no_graph(form, *tensors):
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError(f"the results would carry no gradient: use {form}.apply, torch.no_grad() or detached tensors")
+
+
 def _aligned(t, bytes=16):
     """t itself, or a copy, so that every row [dim] starts on that many bytes."""
     per = bytes // t.element_size()
@@ -70,6 +78,7 @@ def rope_axes(q, k, pos, freq, pairs: Sequence[int], interleaved: bool = False, 
     row, column), freq fp32 [dim / 2] in radians per position, pairs: the pairs
     of each axis; see gs_rope_axes."""
     _tokens("q", q)
+    _no_graph("RopeAxes", q, k)
     b, n, hq, d = q.shape
     _need(d % 2 == 0, "dim must be even")
     if k is not None:
@@ -99,6 +108,7 @@ def _norm_args(x, f, gate, w_post, w_pre, rows_per_gate):
     _vector("gate", gate, ((rows + per - 1) // per, c), x)
     _vector("w_post", w_post, (c,), x)
     _vector("w_pre", w_pre, (c,), x)
+    _no_graph("NormGate", x, f, gate, w_post, w_pre)
     return rows, c, per
 
 
@@ -121,6 +131,7 @@ def norm_gate_backward(gy, gh, x, f, gate, w_post, w_pre, stats, scale: float = 
     rows, c, per = _norm_args(x, f, gate, w_post, w_pre, rows_per_gate)
     _vector("gy", gy, x.shape, x, x.dtype)
     _vector("gh", gh, x.shape, x, x.dtype)
+    _no_graph("NormGate", gy, gh)
     _vector("stats", stats, (2, rows), x)
     gx = torch.empty_like(x)
     gf = None if f is None else torch.empty_like(x)
@@ -190,6 +201,7 @@ def _attn_args(q, k, v, lists, kv_len):
     _need(lists.dim() == 4, "lists must be [batch, heads, groups, top]")
     _vector("lists", lists, (b, h, _groups(n), lists.shape[3]), q, torch.int32)
     _length(kv_len, q)
+    _no_graph("BlockAttention", q, k, v)
 
 
 def block_attention(q, k, v, lists, sm_scale: Optional[float] = None, kv_len=None, causal: bool = False):
@@ -211,6 +223,7 @@ def block_attention_backward(gout, q, k, v, out, lse, lists, sm_scale: Optional[
     _attn_args(q, k, v, lists, kv_len)
     _tokens("gout", gout, q)
     _tokens("out", out, q)
+    _no_graph("BlockAttention", gout, out)
     _need(gout.shape == q.shape and out.shape == q.shape, "gout and out must have q's shape")
     b, n, h, d = q.shape
     _vector("lse", lse, (b, h, n), q)
