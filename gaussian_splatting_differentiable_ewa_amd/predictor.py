@@ -10,10 +10,12 @@ camera rays (SH degree 0, 14 parameters); ``RenderL1`` renders them with
 ``gs_preprocess``, ``gs_tile_lists`` and ``gs_rasterize_fwd_bwd_l1`` and hands
 the parameters' gradients back. Linear layers are plain library products.
 
-``TileNet.forward`` takes all views at once (training); ``TileNet.extend``
-takes the next view against a ``TileCache`` of the views seen so far (serving):
-its keys, values and block summaries are kept, and only the blocks it touches
-are summarised again.
+``TileNet.forward`` takes all views at once (training), each attending to every
+view or, with ``causal``, to itself and the views before it; ``TileNet.extend``
+takes the next view against a ``TileCache`` of the views seen so far (serving)
+and computes what the causal form does: its keys, values and block summaries
+are kept, and only the blocks it touches are summarised again. ``train`` fits
+the causal form unless told otherwise.
 
     python -m gaussian_splatting_differentiable_ewa_amd.predictor --steps 60
 """
@@ -159,16 +161,36 @@ class TileNet(torch.nn.Module):
         return torch.cat([mean, scales, quat, raw[..., 10:11] + 1.0, raw[..., 11:14]], -1).flatten(0, 2).t()
 
     def forward(self, images, cams: Sequence, causal: bool = False):
+        """causal: a view attends to itself and the views before it, as in
+        ``extend``; else every view to all of them."""
         v, _, h, w = images.shape
         ty, tx = (h + L.GS_TILE - 1) // L.GS_TILE, (w + L.GS_TILE - 1) // L.GS_TILE
+        n = ty * tx
         pos = self._positions(0, v, ty, tx, images.device)
 
         def attend(i, q, k, v):
             with torch.no_grad():
-                lists = T.select_blocks(q, T.block_summary(k), k.shape[1], self.top, None, causal)
-            return T.BlockAttention.apply(q, k, v, lists, None, None, causal)
+                lists = T.select_blocks(q, T.block_summary(k), k.shape[1], self.top)
+            return T.BlockAttention.apply(q, k, v, lists)
 
-        return self._gaussians(self._layers(self._tiles(images), pos, ty * tx, 0, attend), cams, ty, tx)
+        def attend_by_view(i, q, k, v):
+            # its groups of queries begin with the view, and the summaries hold no later view's keys
+            blocks = (k.shape[1] + T.BLOCK - 1) // T.BLOCK
+            eight = torch.empty(1, self.kv_heads, blocks, DIM, dtype=torch.int8, device=k.device)
+            scale = torch.empty(1, self.kv_heads, blocks, dtype=torch.float32, device=k.device)
+            out = []
+            for before in range(0, k.shape[1], n):
+                upto = before + n
+                blocks = (upto + T.BLOCK - 1) // T.BLOCK
+                mine, sums = q[:, before:upto], (eight[:, :, :blocks], scale[:, :, :blocks])
+                with torch.no_grad():
+                    T.block_summary(k[:, :upto], None, sums, before // T.BLOCK)
+                    lists = T.select_blocks(mine, sums, upto, self.top)
+                out.append(T.BlockAttention.apply(mine, k[:, :upto], v[:, :upto], lists))
+            return torch.cat(out, 1)
+
+        h = self._layers(self._tiles(images), pos, n, 0, attend_by_view if causal else attend)
+        return self._gaussians(h, cams, ty, tx)
 
     @torch.no_grad()
     def extend(self, image, cam, cache: TileCache):
@@ -189,8 +211,9 @@ class TileNet(torch.nn.Module):
             cache.k[i][:, before: before + n] = k
             cache.v[i][:, before: before + n] = v
             T.block_summary(cache.k[i], cache.length, cache.sums[i], first, blocks)
-            lists = T.select_blocks(q, cache.sums[i], cache.capacity, self.top, cache.length, True)
-            return T.block_attention(q, cache.k[i], cache.v[i], lists, None, cache.length, True)[0]
+            # the length hides what comes after the view; inside it every tile sees every other
+            lists = T.select_blocks(q, cache.sums[i], cache.capacity, self.top, cache.length)
+            return T.block_attention(q, cache.k[i], cache.v[i], lists, None, cache.length)[0]
 
         tokens = self._layers(self._tiles(image[None]), pos, n, view, attend)
         cache.tokens = before + n
@@ -198,8 +221,9 @@ class TileNet(torch.nn.Module):
 
 
 def train(images, cams: Sequence, steps: int = 60, lr: float = 2e-3, net: Optional[TileNet] = None,
-          report=None) -> Tuple[TileNet, List[float]]:
-    """Fits a network to posed views; the network and the loss of every step."""
+          report=None, causal: bool = True) -> Tuple[TileNet, List[float]]:
+    """Fits a network to posed views; the network and the loss of every step.
+    causal: in the form that ``extend`` serves; else with every view seeing all."""
     net = (net or TileNet()).to(images.device)
     v, _, h, w = images.shape
     tiles = ((h + L.GS_TILE - 1) // L.GS_TILE) * ((w + L.GS_TILE - 1) // L.GS_TILE)
@@ -207,7 +231,7 @@ def train(images, cams: Sequence, steps: int = 60, lr: float = 2e-3, net: Option
     adam = torch.optim.Adam(net.parameters(), lr=lr)
     losses = []
     for s in range(steps):
-        loss = RenderL1.apply(net(images, cams), buf, images)
+        loss = RenderL1.apply(net(images, cams, causal=causal), buf, images)
         adam.zero_grad(set_to_none=True)
         loss.backward()
         adam.step()
