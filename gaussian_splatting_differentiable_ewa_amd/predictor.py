@@ -64,7 +64,7 @@ class TileCache:
     layer, with room for ``capacity`` tokens."""
 
     def __init__(self, layers: int, capacity: int, heads: int, dtype=torch.bfloat16, device="cuda"):
-        self.capacity, self.tokens = capacity, 0
+        self.capacity, self.tokens, self.views = capacity, 0, 0
         self.length = torch.zeros(1, dtype=torch.int32, device=device)
         blocks = (capacity + T.BLOCK - 1) // T.BLOCK
         self.k = [torch.empty(1, capacity, heads, DIM, dtype=dtype, device=device) for _ in range(layers)]
@@ -84,7 +84,7 @@ class TileNet(torch.nn.Module):
         if channels % 8 or heads % kv_heads:
             raise ValueError("channels must be a multiple of 8 and heads of kv_heads")
         self.channels, self.heads, self.kv_heads, self.layers = channels, heads, kv_heads, layers
-        self.per_tile, self.top, self.depth, self.dtype = per_tile, top, depth, dtype
+        self.per_tile, self.top, self.depth, self.dtype, self.views = per_tile, top, depth, dtype, views
         g = torch.Generator().manual_seed(seed)
 
         def weight(*shape, scale=1.0):
@@ -195,13 +195,15 @@ class TileNet(torch.nn.Module):
     @torch.no_grad()
     def extend(self, image, cam, cache: TileCache):
         """The Gaussians of the next view ([3, H, W]), its tokens attending to
-        themselves and to all views before it."""
+        themselves and to all views before it. Views may differ in size: the cache
+        counts them."""
         _, h, w = image.shape
         ty, tx = (h + L.GS_TILE - 1) // L.GS_TILE, (w + L.GS_TILE - 1) // L.GS_TILE
-        n, before = ty * tx, cache.tokens
+        n, before, view = ty * tx, cache.tokens, cache.views
         if before + n > cache.capacity:
             raise ValueError(f"the cache holds {cache.capacity} tokens, {before + n} are needed")
-        view = before // n
+        if view >= self.views:
+            raise ValueError(f"the network has gates for {self.views} views, and the cache holds {view}")
         pos = self._positions(view, 1, ty, tx, image.device)
         cache.length.fill_(before + n)
         first = before // T.BLOCK
@@ -216,7 +218,7 @@ class TileNet(torch.nn.Module):
             return T.block_attention(q, cache.k[i], cache.v[i], lists, None, cache.length)[0]
 
         tokens = self._layers(self._tiles(image[None]), pos, n, view, attend)
-        cache.tokens = before + n
+        cache.tokens, cache.views = before + n, view + 1
         return self._gaussians(tokens, [cam], ty, tx)
 
 
