@@ -441,24 +441,42 @@ def gs_stream_copy(dst, src, nbytes=None, stream=None):
 
 # ---- token operators -----------------------------------------------------------
 # Token tensors are [batch][tokens][heads][dim] (any strides, dim contiguous).
-def _launch(name, t, stream, *args):
-    """One call on the device of tensor t (a launch on the default stream goes to
-    the current one), on the given stream or that device's current one (looked
-    up by its handle: torch.cuda.current_stream builds an object)."""
-    global _RAW_STREAM, _DEVICE
+def _current(t, stream):
+    """The given stream's handle, or that of the tensor's device's current one
+    (looked up once by name: torch.cuda.current_stream builds an object)."""
+    global _RAW_STREAM
+    if stream is not None:
+        return stream.cuda_stream
     if _RAW_STREAM is None:
         import torch
         _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _RAW_STREAM(t.get_device())
+
+
+class _Elsewhere:
+    """The library with another device made current around each call."""
+
+    def __init__(self, device):
+        self.device = device
+
+    def __getattr__(self, name):
+        def call(*args):
+            import torch
+            with torch.cuda.device(self.device):
+                return getattr(lib(), name)(*args)
+        return call
+
+
+def _at(t):
+    """The library for a call on tensor t's device: a launch on a default stream
+    goes to the device that is current, whatever its arguments."""
+    global _DEVICE
+    if _DEVICE is None:
+        import torch
         _DEVICE = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     device = t.get_device()
-    raw = _RAW_STREAM(device) if stream is None else stream.cuda_stream
-    if device == _DEVICE():
-        _check(getattr(lib(), name)(*args, raw), name)
-        return
-    import torch
-    with torch.cuda.device(device):
-        _check(getattr(lib(), name)(*args, raw), name)
+    return lib() if device == _DEVICE() else _Elsewhere(device)
 
 
 _RAW_STREAM = _DEVICE = None
@@ -506,16 +524,17 @@ def _ws(ws):
 def gs_rope_axes(q, k, q_out, k_out, pos, freq, pairs, interleaved=False, inverse=False, stream=None):
     """pos int32 [batch or 1][tokens][3] contiguous; k and k_out may be None."""
     b, n, hq, d = q.shape
-    _launch("gs_rope_axes", q, stream, _tok(q), _tok(k), _tok(q_out), _tok(k_out), b, n, hq, 0 if k is None else
-            k.shape[2], d, dtype_of(q), _ptr(pos), 0 if pos.shape[0] == 1 else pos.stride(0), _ptr(freq),
-            _Pairs(*pairs), int(bool(interleaved)), int(bool(inverse)))
+    _check(_at(q).gs_rope_axes(_tok(q), _tok(k), _tok(q_out), _tok(k_out), b, n, hq, 0 if k is None else k.shape[2], d,
+                              dtype_of(q), _ptr(pos), 0 if pos.shape[0] == 1 else pos.stride(0), _ptr(freq),
+                              _Pairs(*pairs), int(bool(interleaved)), int(bool(inverse)),
+                              _current(q, stream)), "gs_rope_axes")
 
 
 def gs_norm_gate_fwd(x, f, gate, w_post, w_pre, y, h, stats, rows_per_gate, scale=1.0, eps=1e-6, stream=None):
     """x, f, y, h [rows][channels] contiguous; f, gate, w_post, w_pre may be None."""
     rows, c = x.shape
-    _launch("gs_norm_gate_fwd", x, stream, _ptr(x), _ptr(f), _ptr(gate), _ptr(w_post), _ptr(w_pre), _ptr(y), _ptr(h),
-            _ptr(stats), rows, c, rows_per_gate, scale, eps, dtype_of(x))
+    _check(_at(x).gs_norm_gate_fwd(_ptr(x), _ptr(f), _ptr(gate), _ptr(w_post), _ptr(w_pre), _ptr(y), _ptr(h), _ptr(stats),
+                                  rows, c, rows_per_gate, scale, eps, dtype_of(x), _current(x, stream)), "gs_norm_gate_fwd")
 
 
 def norm_gate_bwd_workspace_bytes(rows: int, channels: int, rows_per_gate: int) -> int:
@@ -526,9 +545,9 @@ def gs_norm_gate_bwd(gy, gh, x, f, gate, w_post, w_pre, stats, gx, gf, ggate, gw
                      scale=1.0, stream=None):
     """gy, f, gate, w_post, w_pre and the fp32 outputs may be None."""
     rows, c = x.shape
-    _launch("gs_norm_gate_bwd", x, stream, _ptr(gy), _ptr(gh), _ptr(x), _ptr(f), _ptr(gate), _ptr(w_post), _ptr(w_pre),
-            _ptr(stats), _ptr(gx), _ptr(gf), _ptr(ggate), _ptr(gw_post), _ptr(gw_pre), rows, c, rows_per_gate, scale,
-            dtype_of(x), *_ws(ws))
+    _check(_at(x).gs_norm_gate_bwd(_ptr(gy), _ptr(gh), _ptr(x), _ptr(f), _ptr(gate), _ptr(w_post), _ptr(w_pre),
+                                  _ptr(stats), _ptr(gx), _ptr(gf), _ptr(ggate), _ptr(gw_post), _ptr(gw_pre), rows, c,
+                                  rows_per_gate, scale, dtype_of(x), *_ws(ws), _current(x, stream)), "gs_norm_gate_bwd")
 
 
 def gs_block_summary(k, sum8, scale, kv_len=None, block0=0, blocks=None, stream=None):
@@ -536,15 +555,17 @@ def gs_block_summary(k, sum8, scale, kv_len=None, block0=0, blocks=None, stream=
     any strides, dim contiguous."""
     b, n, h, d = k.shape
     every = (n + GS_KEY_BLOCK - 1) // GS_KEY_BLOCK
-    _launch("gs_block_summary", k, stream, _tok(k), b, n, h, d, dtype_of(k), _ptr(kv_len), block0, every - block0 if
-            blocks is None else blocks, _blk(sum8), _blk(scale))
+    _check(_at(k).gs_block_summary(_tok(k), b, n, h, d, dtype_of(k), _ptr(kv_len), block0,
+                                  every - block0 if blocks is None else blocks, _blk(sum8), _blk(scale),
+                                  _current(k, stream)), "gs_block_summary")
 
 
 def gs_block_select(q, sum8, scale, tokens_k, heads_k, lists, kv_len=None, causal=False, stream=None):
     """lists int32 [batch][heads_q][ceil(tokens_q / 128)][top]."""
     b, n, h, d = q.shape
-    _launch("gs_block_select", q, stream, _tok(q), _blk(sum8), _blk(scale), b, n, tokens_k, h, heads_k, d, dtype_of(q),
-            _ptr(kv_len), int(bool(causal)), lists.shape[3], _ptr(lists))
+    _check(_at(q).gs_block_select(_tok(q), _blk(sum8), _blk(scale), b, n, tokens_k, h, heads_k, d, dtype_of(q),
+                                 _ptr(kv_len), int(bool(causal)), lists.shape[3], _ptr(lists), _current(q, stream)),
+           "gs_block_select")
 
 
 def block_attn_fwd_workspace_bytes(batch: int, tokens_q: int, heads_q: int, dim: int, top: int) -> int:
@@ -554,9 +575,10 @@ def block_attn_fwd_workspace_bytes(batch: int, tokens_q: int, heads_q: int, dim:
 def gs_block_attn_fwd(q, k, v, lists, out, lse, ws=None, kv_len=None, causal=False, sm_scale=None, stream=None):
     """sm_scale: dim ** -0.5 by default."""
     b, n, h, d = q.shape
-    _launch("gs_block_attn_fwd", q, stream, _tok(q), _tok(k), _tok(v), _ptr(lists), b, n, k.shape[1], h, k.shape[2], d,
-            dtype_of(q), _ptr(kv_len), int(bool(causal)), lists.shape[3], d ** -0.5 if sm_scale is None else sm_scale,
-            _tok(out), _ptr(lse), *_ws(ws))
+    _check(_at(q).gs_block_attn_fwd(_tok(q), _tok(k), _tok(v), _ptr(lists), b, n, k.shape[1], h, k.shape[2], d,
+                                   dtype_of(q), _ptr(kv_len), int(bool(causal)), lists.shape[3],
+                                   d ** -0.5 if sm_scale is None else sm_scale, _tok(out), _ptr(lse), *_ws(ws),
+                                   _current(q, stream)), "gs_block_attn_fwd")
 
 
 def block_attn_bwd_workspace_bytes(batch: int, tokens_q: int, tokens_k: int, heads_q: int, heads_k: int, dim: int) -> int:
@@ -566,6 +588,7 @@ def block_attn_bwd_workspace_bytes(batch: int, tokens_q: int, tokens_k: int, hea
 def gs_block_attn_bwd(gout, q, k, v, out, lse, lists, gq, gk, gv, ws, kv_len=None, causal=False, sm_scale=None,
                       stream=None):
     b, n, h, d = q.shape
-    _launch("gs_block_attn_bwd", q, stream, _tok(gout), _tok(q), _tok(k), _tok(v), _tok(out), _ptr(lse), _ptr(lists), b,
-            n, k.shape[1], h, k.shape[2], d, dtype_of(q), _ptr(kv_len), int(bool(causal)), lists.shape[3], d ** -0.5 if
-            sm_scale is None else sm_scale, _tok(gq), _tok(gk), _tok(gv), *_ws(ws))
+    _check(_at(q).gs_block_attn_bwd(_tok(gout), _tok(q), _tok(k), _tok(v), _tok(out), _ptr(lse), _ptr(lists), b, n,
+                                   k.shape[1], h, k.shape[2], d, dtype_of(q), _ptr(kv_len), int(bool(causal)),
+                                   lists.shape[3], d ** -0.5 if sm_scale is None else sm_scale, _tok(gq), _tok(gk),
+                                   _tok(gv), *_ws(ws), _current(q, stream)), "gs_block_attn_bwd")

@@ -44,11 +44,10 @@ def _vector(name, t, shape, like, dtype=torch.float32):
         raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)} on {like.device}")
 
 
-def _no_graph(form, *tensors):
+def _lost(form):
+    """For tensors that require a gradient: refuses where one would be lost."""
     if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                raise ValueError(f"the results would carry no gradient: use {form}.apply, torch.no_grad() or detached tensors")
+        raise ValueError(f"the results would carry no gradient: use {form}.apply, torch.no_grad() or detached tensors")
 
 
 def _aligned(t, bytes=16):
@@ -78,7 +77,8 @@ def rope_axes(q, k, pos, freq, pairs: Sequence[int], interleaved: bool = False, 
     row, column), freq fp32 [dim / 2] in radians per position, pairs: the pairs
     of each axis; see gs_rope_axes."""
     _tokens("q", q)
-    _no_graph("RopeAxes", q, k)
+    if q.requires_grad or k is not None and k.requires_grad:
+        _lost("RopeAxes")
     b, n, hq, d = q.shape
     _need(d % 2 == 0, "dim must be even")
     if k is not None:
@@ -88,27 +88,33 @@ def rope_axes(q, k, pos, freq, pairs: Sequence[int], interleaved: bool = False, 
     _vector("pos", pos, (pos.shape[0], n, 3), q, torch.int32)
     _vector("freq", freq, (d // 2,), q)
     q = q if q.stride(3) == 1 else q.contiguous()
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    q_out = torch.empty(b, n, hq, d, dtype=q.dtype, device=q.device)
     k_out = None
     if k is not None:
         k = k if k.stride(3) == 1 else k.contiguous()
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        k_out = torch.empty(b, n, k.shape[2], d, dtype=q.dtype, device=q.device)
     L.gs_rope_axes(q, k, q_out, k_out, pos, freq, pairs, interleaved, inverse)
     return q_out, k_out
 
 
 # ---- norms around a block -------------------------------------------------------
 def _norm_args(x, f, gate, w_post, w_pre, rows_per_gate):
-    _need(x.dim() == 2 and x.is_cuda, "x must be [rows, channels] on the GPU")
-    rows, c = x.shape
+    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be contiguous [rows, channels] on the GPU")
+    rows, c = shape = x.shape
     per = rows if rows_per_gate is None else int(rows_per_gate)
-    per = max(per, 1)
-    _need(x.is_contiguous(), "x must be contiguous")
-    _vector("f", f, x.shape, x, x.dtype)
-    _vector("gate", gate, ((rows + per - 1) // per, c), x)
-    _vector("w_post", w_post, (c,), x)
-    _vector("w_pre", w_pre, (c,), x)
-    _no_graph("NormGate", x, f, gate, w_post, w_pre)
+    if per < 1:
+        per = 1
+    _vector("f", f, shape, x, x.dtype)
+    if gate is not None:
+        _vector("gate", gate, ((rows + per - 1) // per, c), x)
+    if w_post is not None:
+        _vector("w_post", w_post, (c,), x)
+    if w_pre is not None:
+        _vector("w_pre", w_pre, (c,), x)
+    if (x.requires_grad or f is not None and f.requires_grad or gate is not None and gate.requires_grad
+            or w_post is not None and w_post.requires_grad or w_pre is not None and w_pre.requires_grad):
+        _lost("NormGate")
     return rows, c, per
 
 
@@ -131,7 +137,8 @@ def norm_gate_backward(gy, gh, x, f, gate, w_post, w_pre, stats, scale: float = 
     rows, c, per = _norm_args(x, f, gate, w_post, w_pre, rows_per_gate)
     _vector("gy", gy, x.shape, x, x.dtype)
     _vector("gh", gh, x.shape, x, x.dtype)
-    _no_graph("NormGate", gy, gh)
+    if gh.requires_grad or gy is not None and gy.requires_grad:
+        _lost("NormGate")
     _vector("stats", stats, (2, rows), x)
     gx = torch.empty_like(x)
     gf = None if f is None else torch.empty_like(x)
@@ -196,12 +203,17 @@ def _attn_args(q, k, v, lists, kv_len):
     _tokens("k", k, q)
     _tokens("v", v, q)
     b, n, h, d = q.shape
-    _need(k.shape == v.shape and k.shape[0] == b and k.shape[3] == d, "k and v must have q's batch and dim")
-    _need(k.shape[2] > 0 and h % k.shape[2] == 0, "q's heads must be a multiple of k's")
-    _need(lists.dim() == 4, "lists must be [batch, heads, groups, top]")
+    kb, _, hk, kd = k.shape
+    if kb != b or kd != d or v.shape != k.shape:
+        raise ValueError("k and v must have q's batch and dim")
+    if hk == 0 or h % hk != 0:
+        raise ValueError("q's heads must be a multiple of k's")
+    if lists.dim() != 4:
+        raise ValueError("lists must be [batch, heads, groups, top]")
     _vector("lists", lists, (b, h, _groups(n), lists.shape[3]), q, torch.int32)
     _length(kv_len, q)
-    _no_graph("BlockAttention", q, k, v)
+    if q.requires_grad or k.requires_grad or v.requires_grad:
+        _lost("BlockAttention")
 
 
 def block_attention(q, k, v, lists, sm_scale: Optional[float] = None, kv_len=None, causal: bool = False):
@@ -223,14 +235,16 @@ def block_attention_backward(gout, q, k, v, out, lse, lists, sm_scale: Optional[
     _attn_args(q, k, v, lists, kv_len)
     _tokens("gout", gout, q)
     _tokens("out", out, q)
-    _no_graph("BlockAttention", gout, out)
+    if gout.requires_grad or out.requires_grad:
+        _lost("BlockAttention")
     _need(gout.shape == q.shape and out.shape == q.shape, "gout and out must have q's shape")
     b, n, h, d = q.shape
     _vector("lse", lse, (b, h, n), q)
-    gq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    gk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    gv = torch.empty(v.shape, dtype=v.dtype, device=v.device)
-    need = L.block_attn_bwd_workspace_bytes(b, n, k.shape[1], h, k.shape[2], d)
+    m, hk = k.shape[1:3]
+    gq = torch.empty(b, n, h, d, dtype=q.dtype, device=q.device)
+    gk = torch.empty(b, m, hk, d, dtype=q.dtype, device=q.device)
+    gv = torch.empty(b, m, hk, d, dtype=q.dtype, device=q.device)
+    need = L.block_attn_bwd_workspace_bytes(b, n, m, h, hk, d)
     ws = torch.empty(need, dtype=torch.uint8, device=q.device)
     L.gs_block_attn_bwd(_aligned(gout), _aligned(q), _aligned(k), _aligned(v), _aligned(out), lse, lists, gq, gk, gv, ws,
                         kv_len, causal, sm_scale)
