@@ -177,23 +177,29 @@ __device__ __forceinline__ typename Mma<T>::v8 read_cols(const T* tile, int r0, 
     return u.v;
 }
 
-// The same reads with the lane's LDS addresses held in registers, for a kernel
-// whose tiles begin at LDS address 0: moving to another stage is one addition
+// Address in LDS.
+__device__ __forceinline__ uint32_t lds_address(const char* p)
+{
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
+}
+
+// The same reads with the lane's LDS addresses held in registers, of rows r0 ..
+// of a tile that begins at `tile`: moving to another stage is one addition
 // each, and the operand, the half and rows are offsets of the instruction.
 template <typename T, int D>
 struct LaneAddresses {
     uint32_t row[D / 16], col[D / 32][2];
-    __device__ __forceinline__ LaneAddresses(uint32_t r0)
+    __device__ __forceinline__ LaneAddresses(uint32_t tile, uint32_t r0)
     {
         const int l = lane_id(), hi = l >> 5;
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) row[x] = (r0 * D + Tile<D>::at(l & 31, x * 2 + hi)) * sizeof(T);
+        for (int x = 0; x < D / 16; ++x) row[x] = tile + (r0 * D + Tile<D>::at(l & 31, x * 2 + hi)) * sizeof(T);
 #pragma unroll
         for (int y = 0; y < D / 32; ++y)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int c = y * 32 + (l & 16) + 4 * (l & 3);
-                col[y][i] = (r0 * D + Tile<D>::at(8 * i + 4 * hi + ((l & 15) >> 2), c >> 3) + (c & 7)) * sizeof(T);
+                col[y][i] = tile + (r0 * D + Tile<D>::at(8 * i + 4 * hi + ((l & 15) >> 2), c >> 3) + (c & 7)) * sizeof(T);
             }
     }
     __device__ __forceinline__ void move(uint32_t by)

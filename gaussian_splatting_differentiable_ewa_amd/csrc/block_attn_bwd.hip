@@ -68,8 +68,7 @@ __global__ __launch_bounds__(ATT_THREADS) void k_attn_prepare(View<const T> k, c
 // a causal sequence have all their few keys and nothing averages out, dS is
 // kept in two parts. D with the sum of the unrounded ones added, -e, goes to
 // the other pass.
-// LDS of the workgroup, in bytes (the kernel's only LDS object, which so begins
-// at LDS address 0): two stages of K and V, then c of the four waves.
+// LDS of the workgroup, in bytes: two stages of K and V, then c of the four waves.
 template <typename T, int D>
 struct GqLds {
     static constexpr uint32_t TILE = Tile<D>::ELEMS * sizeof(T), STAGE = 2 * TILE, MEAN = 2 * STAGE;
@@ -137,7 +136,7 @@ __device__ __forceinline__ void attn_gq(char* lds, const View<const T>& go, cons
     float whole = 0.f, total = 0.f;              // sums of dS, as it is and rounded (R)
     float weight = 0.f, mean[D / 64] = {};  // of c, and c's dimensions lane, lane + 64
     const float* block_means = means + ((int64_t)b * a.heads_k + hk) * a.blocks * D;
-    LaneAddresses<T, D> at(0);
+    LaneAddresses<T, D> at(lds_address(lds), 0);
     auto step = [&](int stage, auto masked) __attribute__((always_inline)) {
         const int next = walk.next();
         wait_loads();
@@ -353,8 +352,7 @@ __global__ __launch_bounds__(ATT_THREADS) void k_block_order(const uint32_t* __r
 // than the drain).
 constexpr int GKV_THREADS = 512;
 
-// LDS of the workgroup, in bytes (the kernel's only LDS object, which so begins
-// at LDS address 0).
+// LDS of the workgroup, in bytes.
 template <typename T, int D>
 struct GkvLds {
     static constexpr uint32_t TILE = Tile<D>::ELEMS * sizeof(T);          // q or gout of 64 queries
@@ -427,7 +425,7 @@ __device__ __forceinline__ void gkv_scores(GkvSteps<T, D>& steps, const View<con
         load_cols<T, D>(k.at(steps.b, kc, hk), kf);
         load_cols<T, D>(v.at(steps.b, kc, hk), vf);
     }
-    LaneAddresses<T, D> at(qh * 32);
+    LaneAddresses<T, D> at(lds_address(steps.lds), qh * 32);
     uint32_t stage = 0, buffer = 0;
     while (steps.next()) {
         __syncthreads();
@@ -480,7 +478,7 @@ __device__ __forceinline__ void gkv_sums(GkvSteps<T, D>& steps, const View<T>& r
     acc16 acc[D / 32];
 #pragma unroll
     for (int t = 0; t < D / 32; ++t) acc[t] = zero16();
-    LaneAddresses<T, D> at(0);
+    LaneAddresses<T, D> at(lds_address(steps.lds), 0);
     auto sum = [&](uint32_t buffer) __attribute__((always_inline)) {
         const v8* op = (const v8*)(steps.lds + M::OPS + buffer * M::BUFFER + (FOR_V ? 0 : M::ARRAY) + kh * 4 * M::OP) + lane;
         __builtin_amdgcn_sched_barrier(0);
