@@ -30,8 +30,13 @@ constexpr float RISE = 8.f;
 __device__ __forceinline__ float inverse_of(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
 __device__ __forceinline__ float lse_of(float m, float sum) { return sum == 0.f ? -INFINITY : (m + log2f(sum)) * LN2; }
 
-// One block of 64 keys: limit is the number of keys, counted from the block's
-// first, that this lane's query sees (>= 64: all of them).
+// One block of 64 keys. Probabilities are rounded to the inputs' type for their
+// product with the values, which the matrix unit takes in that type; their sum
+// is of the unrounded ones, so the roundings average out instead of shifting a
+// row. At 510 blocks of 64, 32 listed, dim 128, bf16: out is 2.3e-3 of its norm
+// off, 1.66e-3 of which is its own rounding.
+// limit is the number of keys, counted from the block's first, that this lane's
+// query sees (>= 64: all of them).
 template <typename T, int D, bool MASKED>
 __device__ __forceinline__ void attend_block(const T* kt, const T* vt, const typename Mma<T>::v8 (&q)[D / 16],
                                              Online<D>& st, float c, int limit)

@@ -330,7 +330,9 @@ __global__ __launch_bounds__(ATT_THREADS) void k_block_order(const uint32_t* __r
 // either kind on each SIMD.
 //   Four form P and dS of a 32 x 32 tile each (keys 32 kh, queries 32 qh), with
 //   queries as rows, so that a lane holds one key, and leave them in LDS as the
-//   operands they are for: what lane l rounded, lane l reads.
+//   operands they are for, rounded to the inputs' type, which is what the matrix
+//   unit multiplies (gk and gv 2.35e-3 of their norm off in bf16, 1.66e-3 of it
+//   their own rounding): what lane l rounded, lane l reads.
 //   Four take the step before: gv^T += gout^T P or gk^T += q^T dS of 32 keys.
 // Registers decide the shape. One wave with both sums (128 registers at dim
 // 128), k and v (64) and S, dP (32) needs 340 and leaves a SIMD with one wave,

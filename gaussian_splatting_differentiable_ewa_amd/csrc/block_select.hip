@@ -3,10 +3,10 @@
 //
 // Everything up to the score's one rounding is whole-number arithmetic: a
 // mean of 64 keys in fixed point, 8 bits of it and a power-of-two exponent,
-// an integer dot product below 2^21. So the ranking is the same whatever the
-// order of the sums, and near-ties cannot flip between runs or variants. The
-// choice costs one read of q and k (HBM-bound) plus blocks x dim byte
-// products per group, 1 / 128 of the attention's own.
+// an integer dot product of at most 2^22 (dim 256), exact in fp32. So the
+// ranking is the same whatever the order of the sums, and near-ties cannot flip
+// between runs or variants. The choice costs one read of q and k (HBM-bound)
+// plus blocks x dim byte products per group, 1 / 128 of the attention's own.
 #include "tokens.h"
 
 namespace gs {

@@ -168,7 +168,7 @@ def block_summary(k, kv_len=None, out: Optional[Tuple[torch.Tensor, torch.Tensor
                   blocks: Optional[int] = None):
     """(sum8, scale) of the keys' blocks of 64, or of `blocks` of them (the rest)
     from block0 on written into `out` (a growing cache renews its last blocks).
-    See gs_block_summary."""
+    The means are in steps of 2^-8: for keys of order one. See gs_block_summary."""
     _tokens("k", k)
     _length(kv_len, k)
     b, n, h, d = k.shape
@@ -218,7 +218,9 @@ def _attn_args(q, k, v, lists, kv_len):
 
 def block_attention(q, k, v, lists, sm_scale: Optional[float] = None, kv_len=None, causal: bool = False):
     """(out, lse): attention of each query over its group's listed key blocks;
-    fp16 or bf16, dim 64 or 128. See gs_block_attn_fwd."""
+    fp16 or bf16, dim 64 or 128. causal: the last query is the last key (of
+    kv_len); sequences padded on the right for training take no kv_len. See
+    gs_block_attn_fwd."""
     _attn_args(q, k, v, lists, kv_len)
     b, n, h, d = q.shape
     out = torch.empty(b, n, h, d, dtype=q.dtype, device=q.device)
@@ -231,7 +233,8 @@ def block_attention(q, k, v, lists, sm_scale: Optional[float] = None, kv_len=Non
 
 def block_attention_backward(gout, q, k, v, out, lse, lists, sm_scale: Optional[float] = None, kv_len=None,
                              causal: bool = False):
-    """(gq, gk, gv) of block_attention. See gs_block_attn_bwd."""
+    """(gq, gk, gv) of block_attention; in fp16 the scores' gradients have to fit
+    the type. See gs_block_attn_bwd."""
     _attn_args(q, k, v, lists, kv_len)
     _tokens("gout", gout, q)
     _tokens("out", out, q)

@@ -783,7 +783,9 @@ gs_status gs_norm_gate_bwd(const void* gy, const void* gh, const void* x, const 
  *   S = sum of fixed over the block's valid keys, per dimension
  *   e = max(0, bits(max |S|) - 7)       (bits(0) = 0)
  *   sum8 = min(127, (S + (e ? 2^(e-1) : 0)) >> e),  scale = 2^e * fl(1 / valid keys)
- * (a block without valid keys has zeros and scale 1).
+ * (a block without valid keys has zeros and scale 1). The fixed point's step is
+ * 2^-8, so it is meant for keys and queries after a norm, of order one: means
+ * below 2^-9 in magnitude are lost, and blocks of such keys all score alike.
  *   k              keys, GS_F16, GS_BF16 or GS_F32
  *   kv_len         device int32 [batch]: keys at or past it are not read into
  *                  the sums; or NULL (all `tokens` are valid)
@@ -838,6 +840,11 @@ size_t gs_block_attn_fwd_workspace_bytes(int64_t batch, int64_t tokens_q, int32_
  * has out = 0 and lse = -infinity. Keys and values at or past kv_len are not
  * used, whatever they hold; one that only the causal limit hides from a query
  * enters the products as 0 times itself and has to be finite.
+ * The causal positions are those of queries that end a cache: the last query is
+ * the last key. Sequences padded on the right for training (tokens_q =
+ * tokens_k) take kv_len NULL instead: query i then sees keys 0 .. i, all of
+ * them its sequence's, and the padding's own rows get no gradient from a gout
+ * of zero (gs_block_summary still takes the lengths).
  *   list  int32 [batch][heads_q][ceil(tokens_q / 128)][top], ascending with
  *         -1 after the last (gs_block_select's). An entry that does not
  *         exceed every entry before it or lies outside the visible blocks is
@@ -872,9 +879,12 @@ size_t gs_block_attn_bwd_workspace_bytes(int64_t batch, int64_t tokens_q, int64_
  * summed over the query heads that share a key head. Keys that no group lists
  * get zeros, those past kv_len too. Every element of gq, gk and gv is
  * written; the sums have a fixed order, so the bits repeat.
- * P and dS are rounded to the inputs' type for the products. The error that
- * D takes over from the rounded `out` is removed from gk (the dS of a query add
- * to zero) and, along the mean key, from gq.
+ * P and dS are rounded to the inputs' type for the products: with GS_F16 a dS
+ * past 65504 becomes infinite and one below 2^-25 zero, so gout . v has to stay
+ * inside that range (a loss scale; GS_BF16 has fp32's). The error that D takes
+ * over from the rounded `out` is removed from gk (the dS of a query add to zero)
+ * and, along the mean key, from gq. Queries and gout of a query that sees no
+ * key enter the products as 0 times themselves and have to be finite.
  *   ws  device workspace of gs_block_attn_bwd_workspace_bytes(...)
  * Errors: as gs_block_attn_fwd.
  */
