@@ -101,9 +101,10 @@ __device__ __forceinline__ void attend_block(const T* kt, const T* vt, const typ
 // cycles each and 32 exponentials, maxima, sums and roundings a lane beside
 // them; at dim 64 half the former and all of the latter, which then bound it.
 // Measured: dim 128, 16 heads, 255 groups, 32 blocks each 578 us, 950 TFLOP/s
-// (large library product: 1350; matrix unit busy 47 %, no LDS bank conflicts);
-// dim 64, 16 heads on 4 key heads, 254 groups of 16 blocks, causal 180 us, 745
-// TFLOP/s.
+// (656 after seconds of load, where the clocks fall; large library product:
+// 1350; matrix unit busy 47 %, vector instructions in 45 % of the cycles, no LDS
+// bank conflicts); dim 64, 16 heads on 4 key heads, 254 groups of 16 blocks,
+// causal 170 to 195 us (39 % and 73 %).
 template <typename T, int D>
 __device__ __forceinline__ void attn_fwd(T (&s_tile)[2][2][Tile<D>::ELEMS], const View<const T>& q, const View<const T>& k,
                                          const View<const T>& v, const int32_t* __restrict__ lists,
@@ -331,10 +332,14 @@ gs_status attn_check(int64_t batch, int64_t tokens_q, int64_t tokens_k, int32_t 
 
 // The split of few queries: while a workgroup per group would leave most of
 // the 256 CUs idle. It reads each block for 32 queries where the other kernel
-// reads it for 128, so it must not be kept longer. Lists of 16 blocks, one
-// workgroup per group against this one: dim 128, 64 groups 27 against 20 us,
-// 116 groups 29 against 34; dim 64, 128 groups 24 against 22, 256 groups 25
-// against 32.
+// reads it for 128, so it must not be kept longer. Whole calls in us, one
+// workgroup per group against this one, at lists of 4, 16 and 64 blocks:
+//   dim 128, 48 groups   15/15  26/28  86/60    dim 64,  96 groups  15/15  22/15  73/42
+//            64 groups   15/15  26/18  86/52            128 groups  15/15  22/16  74/46
+//            92 groups   15/17  26/33  87/90            188 groups  15/15  23/24  74/66
+//           128 groups   15/20  26/35  86/92            256 groups  15/16  24/29  74/80
+// A limit on groups alone cannot suit every length; where it errs it costs up to
+// a third (92 groups, 16 blocks).
 struct Plan {
     bool few;
     int splits;

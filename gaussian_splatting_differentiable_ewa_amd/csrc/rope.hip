@@ -7,7 +7,7 @@
 //
 // Measured: 32640 tokens, 16 + 16 heads of dim 128, bf16: 100 us, 5.3 TB/s of
 // reads and writes (the library's copy kernel: 5.1). 256 tokens, 8 + 8 heads of
-// dim 64: 5.8 us, the latency of one wave (position, frequencies, sine, data).
+// dim 64: 6 us, the latency of one wave (position, frequencies, sine, data).
 #include "tokens.h"
 
 namespace gs {

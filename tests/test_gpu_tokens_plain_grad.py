@@ -42,7 +42,7 @@ def test_plain_functions_refuse_to_lose_a_gradient():
 
 
 def test_a_layer_keeps_the_gradients_of_its_projections():
-    """A layer as the README writes it: every weight before the attention learns."""
+    """A layer in training: every weight before the attention learns."""
     h = rand(1, 200, 64)
     # scores of order one: a saturated softmax has no gradient to lose
     weights = list((rand(3, 64, 128) / 16).unbind(0))
