@@ -102,9 +102,9 @@ def _norm_args(x, f, gate, w_post, w_pre, rows_per_gate):
     if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be contiguous [rows, channels] on the GPU")
     rows, c = shape = x.shape
-    per = rows if rows_per_gate is None else int(rows_per_gate)
+    per = (rows or 1) if rows_per_gate is None else int(rows_per_gate)
     if per < 1:
-        per = 1
+        raise ValueError("rows_per_gate must be at least 1")
     _vector("f", f, shape, x, x.dtype)
     if gate is not None:
         _vector("gate", gate, ((rows + per - 1) // per, c), x)
