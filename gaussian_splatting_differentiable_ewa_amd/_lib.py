@@ -42,6 +42,7 @@ EXPORTS = (
     "gs_rope_axes", "gs_norm_gate_fwd", "gs_norm_gate_bwd", "gs_norm_gate_bwd_workspace_bytes",
     "gs_block_summary", "gs_block_select", "gs_block_attn_fwd", "gs_block_attn_fwd_workspace_bytes",
     "gs_block_attn_bwd", "gs_block_attn_bwd_workspace_bytes",
+    "gs_layer_norm_fwd", "gs_layer_norm_bwd", "gs_layer_norm_bwd_workspace_bytes",
 )
 GS_F32, GS_F16, GS_BF16 = range(3)
 GS_QUERY_GROUP, GS_KEY_BLOCK = 128, 64
@@ -65,6 +66,10 @@ class GsCamera(ctypes.Structure):
 class GsTokens(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64),
                 ("stride_h", ctypes.c_int64)]
+
+
+class GsMatrix(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64)]
 
 
 _P = ctypes.c_void_p
@@ -143,6 +148,9 @@ def lib():
             "gs_block_attn_bwd_workspace_bytes": ([_I64, _I64, _I64, _I32, _I32, _I32], _SZ),
             "gs_block_attn_bwd": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _P, _I32, _I32,
                                    _F32, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
+            "gs_layer_norm_fwd": ([_P, _P, _P, _P, _P, _I64, _I32, _F32, _I32, _P], ctypes.c_int),
+            "gs_layer_norm_bwd_workspace_bytes": ([_I64, _I32], _SZ),
+            "gs_layer_norm_bwd": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _P, _SZ, _P], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -592,3 +600,33 @@ def gs_block_attn_bwd(gout, q, k, v, out, lse, lists, gq, gk, gv, ws, kv_len=Non
                                    k.shape[1], h, k.shape[2], d, dtype_of(q), _ptr(kv_len), int(bool(causal)),
                                    lists.shape[3], d ** -0.5 if sm_scale is None else sm_scale, _tok(gq), _tok(gk),
                                    _tok(gv), *_ws(ws), _current(q, stream)), "gs_block_attn_bwd")
+
+
+# Matrices are [rows][columns], any row stride, columns contiguous.
+_pack_matrix = struct.Struct("@Pq").pack
+
+
+def _mat(t):
+    if t is None:
+        return None
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise GsError("the rows of a matrix must be contiguous")
+    return _pack_matrix(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def gs_layer_norm_fwd(x, w, b, y, stats, eps=1e-5, stream=None):
+    """x any row stride, y contiguous; w and b may be None."""
+    rows, c = x.shape
+    _check(_at(x).gs_layer_norm_fwd(_mat(x), _ptr(w), _ptr(b), _ptr(y), _ptr(stats), rows, c, eps, dtype_of(x),
+                                    _current(x, stream)), "gs_layer_norm_fwd")
+
+
+def layer_norm_bwd_workspace_bytes(rows: int, channels: int) -> int:
+    return lib().gs_layer_norm_bwd_workspace_bytes(rows, channels)
+
+
+def gs_layer_norm_bwd(gy, x, w, stats, gx, gw, gb, ws, stream=None):
+    """gy and x any row stride, gx contiguous; w, gw and gb may be None."""
+    rows, c = x.shape
+    _check(_at(x).gs_layer_norm_bwd(_mat(gy), _mat(x), _ptr(w), _ptr(stats), _ptr(gx), _ptr(gw), _ptr(gb), rows, c,
+                                    dtype_of(x), *_ws(ws), _current(x, stream)), "gs_layer_norm_bwd")

@@ -23,102 +23,9 @@
 // much occupancy as it gains), sums 15 us. 7200 rows of 1027 fp32 channels
 // (rows off 16 bytes, so 4 bytes an access): 21, 34 and 10 us, 5.6 and 5.2
 // TB/s (it fits the last-level cache).
-#include "tokens.h"
+#include "norm.h"
 
 namespace gs {
-
-// Sums of N values over the NT threads that share a row. `buf` holds 2 x
-// (NT / 64) x N floats and alternates by `flip`, so one barrier per call is
-// enough: a wave can be at most one call ahead of the slowest.
-template <int NT, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float* buf, int flip)
-{
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-    if constexpr (NT > 64) {
-        constexpr int W = NT / 64;
-        float* mine = buf + flip * W * N;
-        const int wave = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) mine[wave * N + i] = v[i];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float s = 0.f;
-#pragma unroll
-            for (int w = 0; w < W; ++w) s += mine[w * N + i];
-            v[i] = s;
-        }
-    }
-}
-
-// The columns a thread holds: pack i covers [(i NT + t) VEC, + VEC), all of
-// it below the channel count or none of it.
-template <int VEC, int NV, int NT>
-struct Cols {
-    int base;
-    bool on[NV];
-    __device__ __forceinline__ Cols(int t, int channels) : base(t * VEC)
-    {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) on[i] = base + i * NT * VEC < channels;
-    }
-    __device__ __forceinline__ int at(int i) const { return base + i * NT * VEC; }
-    template <typename T>
-    __device__ __forceinline__ void load(const T* p, float (&out)[NV][VEC], float other = 0.f) const
-    {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (on[i] && p) {
-                load_f32<T, VEC>(p + at(i), out[i]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) out[i][e] = other;
-            }
-        }
-    }
-    // fp32 vectors of the channels: 16 bytes at a time where VEC allows
-    __device__ __forceinline__ void load_vec(const float* p, float (&out)[NV][VEC], float other) const
-    {
-        constexpr int Q = VEC >= 4 ? 4 : VEC;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-#pragma unroll
-            for (int e = 0; e < VEC; e += Q) {
-                float x[Q];
-#pragma unroll
-                for (int j = 0; j < Q; ++j) x[j] = other;
-                if (on[i] && p) load_f32<float, Q>(p + at(i) + e, x);
-#pragma unroll
-                for (int j = 0; j < Q; ++j) out[i][e + j] = x[j];
-            }
-        }
-    }
-    template <typename T>
-    __device__ __forceinline__ void store(T* p, const float (&in)[NV][VEC]) const
-    {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (on[i]) store_f32<T, VEC>(p + at(i), in[i]);
-    }
-    __device__ __forceinline__ void store_vec(float* p, const float (&in)[NV][VEC]) const
-    {
-        constexpr int Q = VEC >= 4 ? 4 : VEC;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (!on[i]) continue;
-#pragma unroll
-            for (int e = 0; e < VEC; e += Q) {
-                float x[Q];
-#pragma unroll
-                for (int j = 0; j < Q; ++j) x[j] = in[i][e + j];
-                store_f32<float, Q>(p + at(i) + e, x);
-            }
-        }
-    }
-};
 
 struct NormArgs {
     const void *x, *f, *gy, *gh;
@@ -130,11 +37,6 @@ struct NormArgs {
     int32_t channels;
     float scale, eps;
 };
-
-#define GS_EACH(body)                        \
-    _Pragma("unroll") for (int i = 0; i < NV; ++i) { \
-        _Pragma("unroll") for (int e = 0; e < VEC; ++e) { body; } \
-    }
 
 // One run of rows per NT threads (256 / NT runs per workgroup when NT < 256).
 template <typename T, int VEC, int NV, int NT>
@@ -248,32 +150,11 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm_bwd(const NormArgs
     if (pf) col.store_vec(a.part_a + (run + seg) * a.channels, sum_a);
 }
 
-// Sums over runs, 32 columns by 32 slices of the runs a workgroup, each slice
-// in order and the slices in order. The workgroups of gate s: A[s] from the
+// Sums over runs (slice_sum). The workgroups of gate s: A[s] from the
 // slots s + (runs that hold rows of s), times scale; then those of gw_pre;
 // then, with few gates, those of gw_post, which add the gates' sums again
 // instead of waiting for them in a launch of their own.
-constexpr int SUMS_COLS = 32, SUMS_SLICES = 32, SUMS_GATES = 64;
-
-__device__ __forceinline__ float slice_sum(const float* __restrict__ p, int64_t first, int64_t count, int64_t stride, int c,
-                                           bool on, float (*s_buf)[SUMS_COLS])
-{
-    const int slice = threadIdx.x / SUMS_COLS, col = threadIdx.x % SUMS_COLS;
-    float s = 0.f;
-    if (on) {
-        const int64_t per = (count + SUMS_SLICES - 1) / SUMS_SLICES;
-        const int64_t lo = slice * per, hi = lo + per < count ? lo + per : count;
-#pragma unroll 8
-        for (int64_t k = lo; k < hi; ++k) s += p[(first + k) * stride + c];
-    }
-    s_buf[slice][col] = s;
-    __syncthreads();
-    s = 0.f;
-#pragma unroll
-    for (int k = 0; k < SUMS_SLICES; ++k) s += s_buf[k][col];
-    __syncthreads();
-    return s;
-}
+constexpr int SUMS_GATES = 64;
 
 __global__ __launch_bounds__(SUMS_COLS* SUMS_SLICES) void k_norm_sums(
     const float* __restrict__ part_a, const float* __restrict__ part_w, const float* __restrict__ gate,
@@ -337,13 +218,6 @@ __global__ __launch_bounds__(SUMS_COLS* SUMS_SLICES) void k_norm_gw_post(const f
         gw_post[c] = s;
     }
 }
-
-// Rows per run: enough runs to fill the 256 CUs several times over. The
-// backward writes 1 or 2 fp32 rows of sums per run, so it takes fewer (512 or
-// 768 of them leave CUs idle at the end and are slower than 1024).
-static int64_t run_rows(int64_t rows, int64_t want) { return std::max<int64_t>(1, (rows + want - 1) / want); }
-
-constexpr int64_t FWD_RUNS = 4096, BWD_RUNS = 1024;
 
 template <typename T, int VEC, int NV, int NT>
 static hipError_t norm_launch(NormArgs& a, bool backward, hipStream_t s)

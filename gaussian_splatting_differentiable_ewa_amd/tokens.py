@@ -8,8 +8,8 @@ workspace and makes one or two calls of the C ABI on the current stream
 ``[batch, tokens, heads, dim]`` with any strides (views of a packed projection
 need no copy); a tensor whose rows do not start on 16 bytes is copied where the
 kernels need that. The functions record no graph, and refuse tensors whose
-gradient would be lost that way; ``RopeAxes``, ``NormGate`` and
-``BlockAttention`` are the same for ``torch.autograd``.
+gradient would be lost that way; ``RopeAxes``, ``NormGate``,
+``LayerNorm`` and ``BlockAttention`` are the same for ``torch.autograd``.
 """
 
 from __future__ import annotations
@@ -148,6 +148,53 @@ def norm_gate_backward(gy, gh, x, f, gate, w_post, w_pre, stats, scale: float = 
     ws = torch.empty(L.norm_gate_bwd_workspace_bytes(rows, c, per), dtype=torch.uint8, device=x.device)
     L.gs_norm_gate_bwd(gy, gh, x, f, gate, w_post, w_pre, stats, gx, gf, ggate, gw_post, gw_pre, per, ws, scale)
     return gx, gf, ggate, gw_post, gw_pre
+
+
+# ---- layer norm -----------------------------------------------------------------
+def _rows(name, t, columns=None, like=None):
+    """A matrix on the GPU, of that many columns and its partner's type."""
+    if t.dim() != 2 or not t.is_cuda or columns is not None and t.shape[1] != columns:
+        raise ValueError(f"{name} must be [rows, {columns or 'columns'}] on the GPU, got {tuple(t.shape)} on {t.device}")
+    if like is not None and (t.dtype is not like.dtype or t.get_device() != like.get_device()):
+        raise ValueError(f"{name} must have the type and device of its partner")
+
+
+def _packed(t):
+    """t itself, or a copy, so that its rows are contiguous and do not run backwards or far apart."""
+    return t if (t.stride(1) == 1 or t.shape[1] == 1) and t.stride(0) < 1 << 20 else t.contiguous()
+
+
+def layer_norm(x, w=None, b=None, eps: float = 1e-5):
+    """(y, stats): the layer norm of each row of x [rows, channels], times w plus
+    b (fp32 [channels], each may be None). See gs_layer_norm_fwd."""
+    _rows("x", x)
+    rows, c = x.shape
+    _vector("w", w, (c,), x)
+    _vector("b", b, (c,), x)
+    if x.requires_grad or w is not None and w.requires_grad or b is not None and b.requires_grad:
+        _lost("LayerNorm")
+    y = torch.empty(rows, c, dtype=x.dtype, device=x.device)
+    stats = torch.empty(2, rows, dtype=torch.float32, device=x.device)
+    L.gs_layer_norm_fwd(_packed(x), w, b, y, stats, eps)
+    return y, stats
+
+
+def layer_norm_backward(gy, x, w, stats, bias: bool = True):
+    """(gx, gw, gb); gw is None without w, gb without `bias`. See gs_layer_norm_bwd."""
+    _rows("x", x)
+    rows, c = x.shape
+    _rows("gy", gy, c, x)
+    _need(gy.shape[0] == rows, "gy must have x's rows")
+    _vector("w", w, (c,), x)
+    _vector("stats", stats, (2, rows), x)
+    if gy.requires_grad or x.requires_grad or w is not None and w.requires_grad:
+        _lost("LayerNorm")
+    gx = torch.empty(rows, c, dtype=x.dtype, device=x.device)
+    gw = None if w is None else torch.empty_like(w)
+    gb = torch.empty(c, dtype=torch.float32, device=x.device) if bias else None
+    ws = torch.empty(L.layer_norm_bwd_workspace_bytes(rows, c), dtype=torch.uint8, device=x.device)
+    L.gs_layer_norm_bwd(_packed(gy), _packed(x), w, stats, gx, gw, gb, ws)
+    return gx, gw, gb
 
 
 # ---- choice of key blocks -------------------------------------------------------
@@ -292,6 +339,22 @@ class NormGate(torch.autograd.Function):
         gy = None if gy is None else gy.contiguous()
         grads = norm_gate_backward(gy, gh.contiguous(), *ctx.saved_tensors, scale=ctx.how[0], rows_per_gate=ctx.how[1])
         return (*grads, None, None, None)
+
+
+class LayerNorm(torch.autograd.Function):
+    """apply(x, w, b, eps=1e-5) -> y."""
+
+    @staticmethod
+    def forward(ctx, x, w, b, eps=1e-5):
+        y, stats = layer_norm(x, w, b, eps)
+        ctx.save_for_backward(x, w, stats)
+        ctx.bias = b is not None
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gy):
+        return (*layer_norm_backward(gy, *ctx.saved_tensors, bias=ctx.bias), None)
 
 
 class BlockAttention(torch.autograd.Function):

@@ -679,6 +679,7 @@ gs_status gs_stream_copy(void* dst, const void* src, uint64_t bytes, void* strea
  *   gs_block_summary        8-bit means of blocks of keys
  *   gs_block_select         the key blocks each group of queries attends to
  *   gs_block_attn_fwd/_bwd  attention over those blocks
+ *   gs_layer_norm_fwd/_bwd  layer norm
  *
  * Memory, streams and errors as for every entry point above (caller-owned
  * device memory, enqueue only, host checks first). The formulas are written
@@ -894,6 +895,45 @@ gs_status gs_block_attn_bwd(const gs_tokens* gout, const gs_tokens* q, const gs_
                             int32_t dtype, const int32_t* kv_len, int32_t causal, int32_t top, float sm_scale,
                             const gs_tokens* gq, const gs_tokens* gk, const gs_tokens* gv, void* ws, size_t ws_bytes,
                             void* stream);
+
+/* A matrix (host struct): device data and the elements from one row to the
+ * next; a row's elements are contiguous. */
+typedef struct gs_matrix {
+    void* data;
+    int64_t stride;
+} gs_matrix;
+
+/*
+ * gs_layer_norm_fwd -- layer norm of each row of [rows][channels]:
+ *   m = mean x,  r = 1 / sqrt(mean (x - m)^2 + eps),  y = (x - m) r w + b
+ *   x      any row stride >= 0 and alignment of its element
+ *   w, b   fp32 [channels], or NULL (ones, zeros)
+ *   y      out, the type of x, contiguous (may alias a contiguous x)
+ *   stats  out fp32 [2][rows]: m, r (for the backward pass)
+ * Errors: null pointers, rows < 0, channels outside 1..16384, a row stride
+ * outside 0 .. 2^20 - 1, data off its element's size, a bad dtype, eps < 0.
+ */
+gs_status gs_layer_norm_fwd(const gs_matrix* x, const float* w, const float* b, void* y, float* stats, int64_t rows,
+                            int32_t channels, float eps, int32_t dtype, void* stream);
+
+/* Workspace of gs_layer_norm_bwd (bytes); 0 on invalid sizes. */
+size_t gs_layer_norm_bwd_workspace_bytes(int64_t rows, int32_t channels);
+
+/*
+ * gs_layer_norm_bwd -- gradients of gs_layer_norm_fwd. With xh = (x - m) r,
+ * d = gy w:
+ *   gx = r (d - mean d - xh mean(d xh)),  gw = sum gy xh,  gb = sum gy
+ *   x, w, stats  as of the forward call; gx out, the type of x, contiguous
+ *                (may alias a contiguous x or gy)
+ *   gw, gb       out fp32 [channels], each may be NULL (not wanted); zeros
+ *                when there are no rows
+ * The sums over rows are taken in a fixed order: the same bits on every call.
+ *   ws  workspace of gs_layer_norm_bwd_workspace_bytes(...)
+ * Errors: as gs_layer_norm_fwd, plus a small workspace or one off 16 bytes.
+ */
+gs_status gs_layer_norm_bwd(const gs_matrix* gy, const gs_matrix* x, const float* w, const float* stats, void* gx,
+                            float* gw, float* gb, int64_t rows, int32_t channels, int32_t dtype, void* ws,
+                            size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,60 @@
+"""Refusals of layer norm, the gated feed-forward block and 4-bit linear layers:
+every invalid argument returns its status before any HIP call (so without a
+GPU), and the tensor functions raise."""
+
+import ctypes
+import os
+
+import pytest
+import torch
+
+from gaussian_splatting_differentiable_ewa_amd import _lib as L
+from gaussian_splatting_differentiable_ewa_amd import tokens as T
+
+INV, UNS, OK = L.GS_ERR_INVALID_ARGUMENT, L.GS_ERR_UNSUPPORTED, L.GS_OK
+FAKE = ctypes.c_void_p(4096)  # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(L.LIB_PATH):
+        from gaussian_splatting_differentiable_ewa_amd import build
+        build.build()
+    return L.lib()
+
+
+def mat(data=4096, stride=1024):
+    return ctypes.byref(L.GsMatrix(data, stride))
+
+
+def call(f, defaults, **kw):
+    assert not set(kw) - set(defaults), kw
+    return f(*{**defaults, **kw}.values())
+
+
+def test_layer_norm_refusals(lib):
+    fwd = dict(x=mat(), w=FAKE, b=FAKE, y=FAKE, st=FAKE, rows=10, c=64, eps=1e-5, t=L.GS_BF16, s=None)
+    for bad in (dict(x=None), dict(x=mat(0)), dict(x=mat(4097)), dict(x=mat(stride=-1)), dict(x=mat(stride=1 << 20)),
+                dict(y=None), dict(st=None), dict(rows=-1), dict(rows=1 << 41), dict(c=0), dict(c=16385), dict(eps=-1.0),
+                dict(eps=float("nan")), dict(t=3), dict(t=-1)):
+        assert call(lib.gs_layer_norm_fwd, fwd, **bad) == INV, bad
+    assert call(lib.gs_layer_norm_fwd, fwd, rows=0, x=None) == OK
+    need = L.layer_norm_bwd_workspace_bytes(10, 64)
+    assert need > 0 and L.layer_norm_bwd_workspace_bytes(-1, 64) == 0 and L.layer_norm_bwd_workspace_bytes(1, 0) == 0
+    bwd = dict(gy=mat(), x=mat(), w=FAKE, st=FAKE, gx=FAKE, gw=FAKE, gb=FAKE, rows=10, c=64, t=L.GS_F32, ws=FAKE, wsb=need,
+               s=None)
+    for bad in (dict(gy=None), dict(x=None), dict(gy=mat(0)), dict(gy=mat(4098)), dict(x=mat(stride=1 << 20)), dict(st=None),
+                dict(gx=None), dict(ws=None), dict(ws=ctypes.c_void_p(4100)), dict(wsb=need - 1), dict(rows=-1), dict(c=0),
+                dict(t=9)):
+        assert call(lib.gs_layer_norm_bwd, bwd, **bad) == INV, bad
+
+
+def test_tensor_functions_refuse(lib):
+    """Shapes, types and devices, before the library is called."""
+    cpu = torch.zeros(4, 64)
+    with pytest.raises(ValueError):
+        T.layer_norm(cpu)
+    with pytest.raises(ValueError):
+        T.layer_norm(torch.zeros(64))
+    with pytest.raises(ValueError):
+        T.layer_norm_backward(cpu, cpu, None, torch.zeros(2, 4))
