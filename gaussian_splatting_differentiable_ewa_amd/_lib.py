@@ -43,10 +43,12 @@ EXPORTS = (
     "gs_block_summary", "gs_block_select", "gs_block_attn_fwd", "gs_block_attn_fwd_workspace_bytes",
     "gs_block_attn_bwd", "gs_block_attn_bwd_workspace_bytes",
     "gs_layer_norm_fwd", "gs_layer_norm_bwd", "gs_layer_norm_bwd_workspace_bytes",
+    "gs_gated_ff_fwd", "gs_gated_ff_fwd_workspace_bytes", "gs_gated_ff_bwd", "gs_gated_ff_bwd_workspace_bytes",
 )
 GS_F32, GS_F16, GS_BF16 = range(3)
 GS_QUERY_GROUP, GS_KEY_BLOCK = 128, 64
 GS_MAX_SELECT_TOKENS = 2097152
+GS_SILU, GS_GELU = range(2)
 
 
 class GsError(RuntimeError):
@@ -151,6 +153,12 @@ def lib():
             "gs_layer_norm_fwd": ([_P, _P, _P, _P, _P, _I64, _I32, _F32, _I32, _P], ctypes.c_int),
             "gs_layer_norm_bwd_workspace_bytes": ([_I64, _I32], _SZ),
             "gs_layer_norm_bwd": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _P, _SZ, _P], ctypes.c_int),
+            "gs_gated_ff_fwd_workspace_bytes": ([_I64, _I32, _I32, _I32], _SZ),
+            "gs_gated_ff_fwd": ([_P, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _SZ, _P],
+                                ctypes.c_int),
+            "gs_gated_ff_bwd_workspace_bytes": ([_I64, _I32, _I32, _I32], _SZ),
+            "gs_gated_ff_bwd": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _SZ,
+                                 _P], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -630,3 +638,27 @@ def gs_layer_norm_bwd(gy, x, w, stats, gx, gw, gb, ws, stream=None):
     rows, c = x.shape
     _check(_at(x).gs_layer_norm_bwd(_mat(gy), _mat(x), _ptr(w), _ptr(stats), _ptr(gx), _ptr(gw), _ptr(gb), rows, c,
                                     dtype_of(x), *_ws(ws), _current(x, stream)), "gs_layer_norm_bwd")
+
+
+def gated_ff_fwd_workspace_bytes(rows: int, channels: int, hidden: int, channels_out: int) -> int:
+    return lib().gs_gated_ff_fwd_workspace_bytes(rows, channels, hidden, channels_out)
+
+
+def gs_gated_ff_fwd(x, w_gate, w_up, w_down, act, h, pre, y, ws=None, stream=None):
+    """x, w_gate, w_up, w_down any row stride of 8 elements; pre may be None."""
+    rows, c = x.shape
+    _check(_at(x).gs_gated_ff_fwd(_mat(x), _mat(w_gate), _mat(w_up), _mat(w_down), rows, c, w_gate.shape[0],
+                                  w_down.shape[0], act, dtype_of(x), _ptr(h), _ptr(pre), _ptr(y), *_ws(ws),
+                                  _current(x, stream)), "gs_gated_ff_fwd")
+
+
+def gated_ff_bwd_workspace_bytes(rows: int, channels: int, hidden: int, channels_out: int) -> int:
+    return lib().gs_gated_ff_bwd_workspace_bytes(rows, channels, hidden, channels_out)
+
+
+def gs_gated_ff_bwd(gy, x, w_gate, w_up, w_down, h, pre, act, gx, gw_gate, gw_up, gw_down, ws, stream=None):
+    """gx, gw_gate with gw_up, and gw_down may be None."""
+    rows, c = x.shape
+    _check(_at(x).gs_gated_ff_bwd(_mat(gy), _mat(x), _mat(w_gate), _mat(w_up), _mat(w_down), _ptr(h), _ptr(pre), rows, c,
+                                  w_gate.shape[0], w_down.shape[0], act, dtype_of(x), _ptr(gx), _ptr(gw_gate), _ptr(gw_up),
+                                  _ptr(gw_down), *_ws(ws), _current(x, stream)), "gs_gated_ff_bwd")

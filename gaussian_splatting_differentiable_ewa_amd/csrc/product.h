@@ -1,0 +1,263 @@
+// Matrix products by tiles, shared by the gated feed-forward block
+// (gated_ff.hip) and the 4-bit linear layers (fp4.hip).
+//
+// A workgroup of four waves forms BM x BN elements of C = A B^T. Both operands
+// pass through LDS in stages of KB bytes of a row's k (two matrix steps per 64
+// bytes), loaded straight from memory STAGES - 1 stages ahead; there is one
+// barrier per stage, behind which the stage is whole for all waves and the one
+// before it is read out.
+//
+// Matrix tile: 32 x 32, 32 bytes of k a step. Lane l holds 16 bytes of k, half
+// l >> 5, of row l & 31 of either operand; of C column l & 31, rows
+// 8 (i >> 2) + 4 (l >> 5) + (i & 3) for registers i = 0..15.
+//
+// An operand lies in memory either along k (its rows' k contiguous) or across
+// it (TR: [k][rows], as the transposed matrices of a backward pass do); then
+// its 16-bit elements are turned on the way from LDS to registers.
+#pragma once
+
+#include "block_attn.h"
+
+namespace gs {
+
+// One operand's tile of ROWS rows in LDS, in chunks of 16 bytes, swizzled so
+// that a wave's reads do not share banks (64 of 4 bytes).
+//   along k:  [ROWS][KB]; chunk c of row r sits at c ^ f(r). 16 consecutive
+//             rows, the same chunk of each: every chunk of 256 bytes once.
+//   across:   [KB / 2][2 ROWS]; a turning read takes 4 rows of k, 64 bytes of
+//             each: every 64 bytes of 256 once.
+template <int ROWS, int KB, bool TR>
+struct Panel {
+    static constexpr int BYTES = ROWS * KB;
+    static constexpr int PITCH = TR ? ROWS * 2 : KB, CHUNKS = PITCH / 16;
+    static __device__ __forceinline__ int swizzle(int r)
+    {
+        if constexpr (!TR) return KB == 64 ? (r >> 2) & 3 : (r >> 1) & 7;
+        else if constexpr (ROWS >= 128) return ((r & 3) << 2) | ((r >> 2) & 3);
+        else return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+    }
+};
+
+constexpr uint32_t PAST = 0x80000000u;  // an offset past every buffer: such loads give zeros
+
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// Loads of a panel: WAVES waves, 16 bytes a lane, 1024 an instruction. The LDS
+// side of such a load is linear in the lane, so the swizzle is on the memory side.
+// With PAIR the panel's rows are of two matrices, 32 of one and 32 of the other
+// in turn, and a wave loads of one of them.
+template <int ROWS, int KB, bool TR, int WAVES, bool PAIR = false>
+struct PanelLoad {
+    using P = Panel<ROWS, KB, TR>;
+    static constexpr int PER = P::BYTES / 1024 / WAVES, RPI = 1024 / P::PITCH;
+    static_assert(PER * WAVES * 1024 == P::BYTES && RPI >= 1, "whole instructions");
+    static_assert(!PAIR || (!TR && ROWS / WAVES <= 32), "a wave loads of one matrix");
+    uint32_t off[PER];
+    int wave;
+    static __device__ __forceinline__ int row_of(int wave, int i) { return (wave * PER + i) * RPI + (int)lane_id() / P::CHUNKS; }
+    static __device__ __forceinline__ int chunk_of(int row) { return ((int)lane_id() % P::CHUNKS) ^ P::swizzle(row); }
+    // Which matrix of a pair the wave loads.
+    static __device__ __forceinline__ int second(int wave) { return (wave * (ROWS / WAVES)) >> 5 & 1; }
+    __device__ __forceinline__ PanelLoad(uint32_t ld, int w) : wave(w)
+    {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int r = row_of(w, i), m = PAIR ? (r >> 6) * 32 + (r & 31) : r;
+            off[i] = (uint32_t)m * ld + chunk_of(r) * 16;
+        }
+    }
+    // `bytes` from p to the end of the matrix (past it: zeros), `k` of them of
+    // this row's own.
+    __device__ __forceinline__ void operator()(char* lds, const char* p, uint32_t bytes, int k) const
+    {
+        const __amdgpu_buffer_rsrc_t src = __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, 0x00027000);
+        char* to = lds + wave * PER * 1024;
+        if (TR || k >= KB) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) one(src, to + i * 1024, off[i]);
+        } else {  // the last stage of k: a row goes on with what is not its own
+#pragma unroll
+            for (int i = 0; i < PER; ++i) one(src, to + i * 1024, chunk_of(row_of(wave, i)) * 16 < k ? off[i] : PAST);
+        }
+    }
+    static __device__ __forceinline__ void one(__amdgpu_buffer_rsrc_t src, char* to, uint32_t off)
+    {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)to, 16, off, 0, 0, 0);
+    }
+};
+
+// A lane's reads of 32 rows of a panel for one step: rows r0 + 32 t ..., where
+// r0 is the wave's first row.
+template <typename T, int ROWS, int KB, bool TR, int TILES>
+struct PanelRead {
+    using P = Panel<ROWS, KB, TR>;
+    using V = typename Mma<T>::v8;
+    static constexpr int STEPS = KB / 32, AT = TR ? 2 * TILES : STEPS;
+    uint32_t at[AT];
+    __device__ __forceinline__ explicit PanelRead(int r0)
+    {
+        const int l = lane_id(), hi = l >> 5;
+        if constexpr (!TR) {
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) at[s] = (r0 + (l & 31)) * KB + (((2 * s + hi) ^ P::swizzle(l & 31)) * 16);
+        } else {
+            // slots 0..3 and 4..7 of a lane's k are rows 8 hi and 8 hi + 4 on, as an operand along k has them
+#pragma unroll
+            for (int t = 0; t < TILES; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int row = 8 * hi + 4 * i + ((l & 15) >> 2), c = r0 + 32 * t + (l & 16) + 4 * (l & 3);
+                    at[2 * t + i] = row * P::PITCH + ((c >> 3) ^ P::swizzle(row)) * 16 + (c & 7) * 2;
+                }
+        }
+    }
+    __device__ __forceinline__ V operator()(const char* panel, int t, int s) const
+    {
+        if constexpr (!TR) {
+            return *(const V*)(panel + at[s] + t * 32 * KB);
+        } else {
+            union {
+                short4v h[2];
+                V v;
+            } u;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                u.h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) short4v*)(panel + at[2 * t + i] + s * 16 * P::PITCH));
+            return u.v;
+        }
+    }
+};
+
+// An operand as the host describes it. Along k: row r, element k at data +
+// r ld + k; across: data + k ld + r. A second matrix follows the first one along
+// k (segments of k elements each), or is the other one of a pair.
+struct Operand {
+    const char* data[2];
+    int64_t ld[2];  // bytes
+    int64_t rows;   // of one matrix
+};
+
+template <int BM_, int BN_, int WM_, int WN_, int KB_, int STAGES_>
+struct TileShape {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KB = KB_, STAGES = STAGES_;
+    static constexpr int WAVES = WM * WN, MT = BM / WM / 32, NT = BN / WN / 32;
+};
+
+// The stages a workgroup walks: [first, last) of all segments' stages.
+struct Walk {
+    int64_t k;   // elements of a segment
+    int stages;  // of a segment
+    int first, last;
+};
+
+template <typename T, typename S, bool ATR, bool BTR, bool PAIR>
+struct TileProduct {
+    static constexpr int KE = S::KB / 2;  // elements of a stage
+    using LoadA = PanelLoad<S::BM, S::KB, ATR, S::WAVES>;
+    using LoadB = PanelLoad<S::BN, S::KB, BTR, S::WAVES, PAIR>;
+    static constexpr int A_BYTES = LoadA::P::BYTES, STAGE = A_BYTES + LoadB::P::BYTES, LDS = STAGE * S::STAGES;
+    static constexpr int LOADS = LoadA::PER + LoadB::PER;
+
+    // An operand from the next stage on: its address, the bytes up to its end and
+    // what a stage adds to the one and takes from the other.
+    template <bool TR>
+    struct Feed {
+        const char* p;
+        int64_t bytes, step;
+        __device__ __forceinline__ void at(const Operand& o, int which, int64_t r0, int64_t k, int64_t k0)
+        {
+            const int64_t ld = o.ld[which];
+            p = o.data[which] + (TR ? k0 * ld + r0 * 2 : r0 * ld + k0 * 2);
+            bytes = TR ? (k - 1 - k0) * ld + (o.rows - r0) * 2 : (o.rows - 1 - r0) * ld + (k - k0) * 2;
+            step = TR ? KE * ld : KE * 2;
+        }
+        // as the 32 bits of a buffer's size (an operand's tile is below 2^31)
+        __device__ __forceinline__ uint32_t size(bool any) const
+        {
+            const uint32_t n = (uint32_t)(bytes >> 31) ? 0x7fffffffu : (uint32_t)bytes;
+            return any ? n : 0u;
+        }
+        __device__ __forceinline__ void next()
+        {
+            p += step;
+            bytes -= step;
+        }
+    };
+
+    static __device__ __forceinline__ void run(char* __restrict__ lds, const Operand& a, const Operand& b, int64_t m0,
+                                               int64_t n0, const Walk& w, int wave, acc16 (&acc)[S::MT][S::NT])
+    {
+        const LoadA load_a((uint32_t)a.ld[0], wave);
+        const int mine = PAIR ? LoadB::second(wave) : w.first >= w.stages;
+        LoadB load_b((uint32_t)b.ld[mine], wave);
+        const PanelRead<T, S::BM, S::KB, ATR, S::MT> read_a(wave / S::WN * (S::BM / S::WM));
+        const PanelRead<T, S::BN, S::KB, BTR, S::NT> read_b(wave % S::WN * (S::BN / S::WN));
+#pragma unroll
+        for (int i = 0; i < S::MT; ++i)
+#pragma unroll
+            for (int j = 0; j < S::NT; ++j) acc[i][j] = zero16();
+        int in = w.first - (w.first >= w.stages ? w.stages : 0);  // stage of its segment, the next to load
+        int left = w.last - w.first, k = (int)(w.k - (int64_t)in * KE) * 2;
+        Feed<ATR> fa;
+        Feed<BTR> fb;
+        fa.at(a, w.first >= w.stages, m0, w.k, (int64_t)in * KE);
+        fb.at(b, mine, n0, w.k, (int64_t)in * KE);
+        auto issue = [&](char* stage) __attribute__((always_inline)) {
+            load_a(stage, fa.p, fa.size(left > 0), k);
+            load_b(stage + A_BYTES, fb.p, fb.size(left > 0), k);
+            --left, ++in, k -= KE * 2;
+            fa.next();
+            fb.next();
+            if (!PAIR && in == w.stages && left > 0) {  // the second segment
+                k = (int)w.k * 2;
+                fa.at(a, 1, m0, w.k, 0);
+                fb.at(b, 1, n0, w.k, 0);
+                load_b = LoadB((uint32_t)b.ld[1], wave);
+            }
+        };
+#pragma unroll
+        for (int t = 0; t < S::STAGES - 1; ++t) issue(lds + t * STAGE);
+        int now = 0;
+        for (int t = w.first; t < w.last; ++t) {
+            // this stage's loads are done when only those of the later ones are out; reads of the last stage too
+            static_assert((S::STAGES - 2) * LOADS < 16, "fits the field used below");
+            __builtin_amdgcn_s_waitcnt(0x0070 | ((S::STAGES - 2) * LOADS));
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            const int to = now == 0 ? S::STAGES - 1 : now - 1;
+            issue(lds + to * STAGE);
+            const char* pa = lds + now * STAGE;
+            const char* pb = pa + A_BYTES;
+            typename Mma<T>::v8 ra[S::MT], rb[S::NT];
+#pragma unroll
+            for (int s = 0; s < S::KB / 32; ++s) {
+#pragma unroll
+                for (int j = 0; j < S::NT; ++j) rb[j] = read_b(pb, j, s);
+#pragma unroll
+                for (int i = 0; i < S::MT; ++i) ra[i] = read_a(pa, i, s);
+#pragma unroll
+                for (int i = 0; i < S::MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < S::NT; ++j) acc[i][j] = Mma<T>::mma(ra[i], rb[j], acc[i][j]);
+            }
+            now = now == S::STAGES - 1 ? 0 : now + 1;
+        }
+        wait_loads();  // what was loaded past the end lands before LDS is used again
+    }
+};
+
+// Workgroup -> tile: each XCD takes a contiguous range, in which 8 row tiles by
+// all column tiles come first, so that what runs at once shares rows of both
+// operands in its L2.
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t mt, uint32_t nt, uint32_t& m, uint32_t& n)
+{
+    constexpr uint32_t GROUP = 8;
+    const uint32_t g = id / (GROUP * nt), in = id - g * GROUP * nt;
+    const uint32_t rows = min(mt - g * GROUP, GROUP);
+    n = uniform(in / rows);
+    m = uniform(g * GROUP + (in - n * rows));
+}
+
+}  // namespace gs

@@ -9,7 +9,8 @@ workspace and makes one or two calls of the C ABI on the current stream
 need no copy); a tensor whose rows do not start on 16 bytes is copied where the
 kernels need that. The functions record no graph, and refuse tensors whose
 gradient would be lost that way; ``RopeAxes``, ``NormGate``,
-``LayerNorm`` and ``BlockAttention`` are the same for ``torch.autograd``.
+``LayerNorm``, ``GatedFF`` and ``BlockAttention`` are the same for
+``torch.autograd``.
 """
 
 from __future__ import annotations
@@ -197,6 +198,74 @@ def layer_norm_backward(gy, x, w, stats, bias: bool = True):
     return gx, gw, gb
 
 
+# ---- gated feed-forward block ---------------------------------------------------
+ACTS = {"silu": L.GS_SILU, "gelu": L.GS_GELU}
+
+
+def _on16(t):
+    """t itself, or a copy, so that every row starts on 16 bytes."""
+    if (t.stride(1) == 1 and t.data_ptr() % 16 == 0 and (t.shape[0] <= 1 or t.stride(0) % 8 == 0)
+            and t.stride(0) < 1 << 21):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+def _ff_args(x, w_gate, w_up, w_down, act):
+    _rows("x", x)
+    rows, c = x.shape
+    f = w_gate.shape[0]
+    _rows("w_gate", w_gate, c, x)
+    _rows("w_up", w_up, c, x)
+    _rows("w_down", w_down, f, x)
+    if w_up.shape[0] != f:
+        raise ValueError("w_up must have w_gate's rows")
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
+    if x.requires_grad or w_gate.requires_grad or w_up.requires_grad or w_down.requires_grad:
+        _lost("GatedFF")
+    return rows, c, f, w_down.shape[0]
+
+
+def _gated_ff(x, w_gate, w_up, w_down, act, keep):
+    rows, c, f, co = _ff_args(x, w_gate, w_up, w_down, act)
+    h = torch.empty(rows, f, dtype=x.dtype, device=x.device)
+    pre = torch.empty(rows, 2 * f, dtype=torch.float32, device=x.device) if keep else None
+    y = torch.empty(rows, co, dtype=x.dtype, device=x.device)
+    need = L.gated_ff_fwd_workspace_bytes(rows, c, f, co)
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    L.gs_gated_ff_fwd(_on16(x), _on16(w_gate), _on16(w_up), _on16(w_down), ACTS[act], h, pre, y, ws)
+    return y, h, pre
+
+
+def gated_ff(x, w_gate, w_up, w_down, act: str = "silu"):
+    """(act(x w_gate^T) * (x w_up^T)) w_down^T for x [rows, channels], w_gate and
+    w_up [hidden, channels], w_down [out, hidden]; fp16 or bf16, sizes of 8. See
+    gs_gated_ff_fwd."""
+    return _gated_ff(x, w_gate, w_up, w_down, act, False)[0]
+
+
+def gated_ff_train(x, w_gate, w_up, w_down, act: str = "silu"):
+    """(y, h, pre): gated_ff and what its backward pass takes, the hidden layer
+    and both projections (fp32 [rows, 2 hidden])."""
+    return _gated_ff(x, w_gate, w_up, w_down, act, True)
+
+
+def gated_ff_backward(gy, x, w_gate, w_up, w_down, h, pre, act: str = "silu"):
+    """(gx, gw_gate, gw_up, gw_down); in fp16 the projections' gradients have to
+    fit the type. See gs_gated_ff_bwd."""
+    rows, c, f, co = _ff_args(x, w_gate, w_up, w_down, act)
+    _rows("gy", gy, co, x)
+    _need(gy.shape[0] == rows, "gy must have x's rows")
+    _vector("h", h, (rows, f), x, x.dtype)
+    _vector("pre", pre, (rows, 2 * f), x)
+    if gy.requires_grad:
+        _lost("GatedFF")
+    grads = [torch.empty(s, dtype=x.dtype, device=x.device) for s in ((rows, c), (f, c), (f, c), (co, f))]
+    ws = torch.empty(L.gated_ff_bwd_workspace_bytes(rows, c, f, co), dtype=torch.uint8, device=x.device)
+    L.gs_gated_ff_bwd(_on16(gy), _on16(x), _on16(w_gate), _on16(w_up), _on16(w_down), h, pre, ACTS[act], *grads, ws)
+    return tuple(grads)
+
+
 # ---- choice of key blocks -------------------------------------------------------
 def _length(kv_len, q):
     _vector("kv_len", kv_len, (q.shape[0],), q, torch.int32)
@@ -355,6 +424,22 @@ class LayerNorm(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, gy):
         return (*layer_norm_backward(gy, *ctx.saved_tensors, bias=ctx.bias), None)
+
+
+class GatedFF(torch.autograd.Function):
+    """apply(x, w_gate, w_up, w_down, act="silu") -> y."""
+
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up, w_down, act="silu"):
+        y, h, pre = gated_ff_train(x, w_gate, w_up, w_down, act)
+        ctx.save_for_backward(x, w_gate, w_up, w_down, h, pre)
+        ctx.act = act
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gy):
+        return (*gated_ff_backward(gy, *ctx.saved_tensors, act=ctx.act), None)
 
 
 class BlockAttention(torch.autograd.Function):

@@ -680,6 +680,7 @@ gs_status gs_stream_copy(void* dst, const void* src, uint64_t bytes, void* strea
  *   gs_block_select         the key blocks each group of queries attends to
  *   gs_block_attn_fwd/_bwd  attention over those blocks
  *   gs_layer_norm_fwd/_bwd  layer norm
+ *   gs_gated_ff_fwd/_bwd    the gated feed-forward block
  *
  * Memory, streams and errors as for every entry point above (caller-owned
  * device memory, enqueue only, host checks first). The formulas are written
@@ -934,6 +935,54 @@ size_t gs_layer_norm_bwd_workspace_bytes(int64_t rows, int32_t channels);
 gs_status gs_layer_norm_bwd(const gs_matrix* gy, const gs_matrix* x, const float* w, const float* stats, void* gx,
                             float* gw, float* gb, int64_t rows, int32_t channels, int32_t dtype, void* ws,
                             size_t ws_bytes, void* stream);
+
+typedef enum gs_act { GS_SILU = 0, GS_GELU = 1 } gs_act;
+
+/* Workspace of gs_gated_ff_fwd (bytes); may be 0. */
+size_t gs_gated_ff_fwd_workspace_bytes(int64_t rows, int32_t channels, int32_t hidden, int32_t channels_out);
+
+/*
+ * gs_gated_ff_fwd -- the gated feed-forward block:
+ *   g = x w_gate^T,  u = x w_up^T,  h = act(g) u,  y = h w_down^T
+ * with act(g) = g / (1 + exp(-g)) (GS_SILU) or g times the normal distribution
+ * function (GS_GELU). Sums are fp32; h is rounded to the inputs' type for its
+ * product.
+ *   x        [rows][channels], GS_F16 or GS_BF16 as everything but pre
+ *   w_gate, w_up  [hidden][channels];  w_down  [channels_out][hidden]
+ *   h        out [rows][hidden] (for the backward pass, or scratch)
+ *   pre      out fp32 [rows][2 hidden], g and u (for the backward pass), or NULL
+ *   y        out [rows][channels_out]; h and y are contiguous
+ *   ws       workspace of gs_gated_ff_fwd_workspace_bytes(...), or NULL if that is 0
+ * Errors: null pointers, sizes that are not multiples of 8 or outside 8..2^17,
+ * rows outside 0..2^24, a bad act or dtype, a small workspace; GS_ERR_UNSUPPORTED
+ * for GS_F32, data or rows off 16 bytes, a row stride outside 0 .. 2^21 - 1, or
+ * past 2^23 tiles of a product (256 rows by 128 columns).
+ */
+gs_status gs_gated_ff_fwd(const gs_matrix* x, const gs_matrix* w_gate, const gs_matrix* w_up, const gs_matrix* w_down,
+                          int64_t rows, int32_t channels, int32_t hidden, int32_t channels_out, int32_t act, int32_t dtype,
+                          void* h, float* pre, void* y, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace of gs_gated_ff_bwd (bytes); 0 on invalid sizes. */
+size_t gs_gated_ff_bwd_workspace_bytes(int64_t rows, int32_t channels, int32_t hidden, int32_t channels_out);
+
+/*
+ * gs_gated_ff_bwd -- gradients of gs_gated_ff_fwd from that of y:
+ *   gh = gy w_down,  gg = gh u act'(g),  gu = gh act(g)
+ *   gx = gg w_gate + gu w_up,  gw_gate = gg^T x,  gw_up = gu^T x,  gw_down = gy^T h
+ *   h, pre   as the forward call wrote them
+ *   gx, gw_gate, gw_up, gw_down  out, contiguous, the inputs' type; each may be
+ *            NULL (not wanted), gw_gate and gw_up together; the weights' are
+ *            zeros when there are no rows
+ * gg and gu are rounded to the inputs' type for their products: with GS_F16 the
+ * loss has to be scaled so that they fit it. Sums are fp32 and have a fixed
+ * order: the same bits on every call.
+ *   ws       workspace of gs_gated_ff_bwd_workspace_bytes(...)
+ * Errors: as gs_gated_ff_fwd.
+ */
+gs_status gs_gated_ff_bwd(const gs_matrix* gy, const gs_matrix* x, const gs_matrix* w_gate, const gs_matrix* w_up,
+                          const gs_matrix* w_down, const void* h, const float* pre, int64_t rows, int32_t channels,
+                          int32_t hidden, int32_t channels_out, int32_t act, int32_t dtype, void* gx, void* gw_gate,
+                          void* gw_up, void* gw_down, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
