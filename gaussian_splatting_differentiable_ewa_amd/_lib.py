@@ -44,6 +44,7 @@ EXPORTS = (
     "gs_block_attn_bwd", "gs_block_attn_bwd_workspace_bytes",
     "gs_layer_norm_fwd", "gs_layer_norm_bwd", "gs_layer_norm_bwd_workspace_bytes",
     "gs_gated_ff_fwd", "gs_gated_ff_fwd_workspace_bytes", "gs_gated_ff_bwd", "gs_gated_ff_bwd_workspace_bytes",
+    "gs_quantise_fp4", "gs_dequantise_fp4", "gs_linear_fp4", "gs_linear_fp4_workspace_bytes",
 )
 GS_F32, GS_F16, GS_BF16 = range(3)
 GS_QUERY_GROUP, GS_KEY_BLOCK = 128, 64
@@ -157,6 +158,10 @@ def lib():
             "gs_gated_ff_fwd": ([_P, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _SZ, _P],
                                 ctypes.c_int),
             "gs_gated_ff_bwd_workspace_bytes": ([_I64, _I32, _I32, _I32], _SZ),
+            "gs_quantise_fp4": ([_P, _I64, _I32, _I32, _P, _P, _P], ctypes.c_int),
+            "gs_dequantise_fp4": ([_P, _P, _I64, _I32, _I32, _P, _P], ctypes.c_int),
+            "gs_linear_fp4_workspace_bytes": ([_I64, _I32, _I32], _SZ),
+            "gs_linear_fp4": ([_P, _P, _P, _I64, _I32, _I32, _I32, _P, _P, _SZ, _P], ctypes.c_int),
             "gs_gated_ff_bwd": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _SZ,
                                  _P], ctypes.c_int),
         }
@@ -662,3 +667,26 @@ def gs_gated_ff_bwd(gy, x, w_gate, w_up, w_down, h, pre, act, gx, gw_gate, gw_up
     _check(_at(x).gs_gated_ff_bwd(_mat(gy), _mat(x), _mat(w_gate), _mat(w_up), _mat(w_down), _ptr(h), _ptr(pre), rows, c,
                                   w_gate.shape[0], w_down.shape[0], act, dtype_of(x), _ptr(gx), _ptr(gw_gate), _ptr(gw_up),
                                   _ptr(gw_down), *_ws(ws), _current(x, stream)), "gs_gated_ff_bwd")
+
+
+def gs_quantise_fp4(x, codes, scales, stream=None):
+    """codes uint8 [rows][channels / 2], scales uint8 [rows][4 ceil(channels / 128)], contiguous."""
+    rows, c = x.shape
+    _check(_at(x).gs_quantise_fp4(_mat(x), rows, c, dtype_of(x), _ptr(codes), _ptr(scales), _current(x, stream)),
+           "gs_quantise_fp4")
+
+
+def gs_dequantise_fp4(codes, scales, out, stream=None):
+    rows, c = out.shape
+    _check(_at(out).gs_dequantise_fp4(_mat(codes), _mat(scales), rows, c, dtype_of(out), _ptr(out), _current(out, stream)),
+           "gs_dequantise_fp4")
+
+
+def linear_fp4_workspace_bytes(rows: int, channels: int, out: int) -> int:
+    return lib().gs_linear_fp4_workspace_bytes(rows, channels, out)
+
+
+def gs_linear_fp4(x, codes, scales, y, ws, stream=None):
+    rows, c = x.shape
+    _check(_at(x).gs_linear_fp4(_mat(x), _mat(codes), _mat(scales), rows, c, codes.shape[0], dtype_of(x), _ptr(y), *_ws(ws),
+                                _current(x, stream)), "gs_linear_fp4")

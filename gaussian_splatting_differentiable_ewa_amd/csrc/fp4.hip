@@ -1,0 +1,272 @@
+// gs_quantise_fp4, gs_dequantise_fp4 and gs_linear_fp4: microscaled 4-bit
+// floating point, blocks of 32 values along a row that share a power of two.
+//
+// The matrix unit takes such values as they are, with the blocks' exponents
+// beside them, at four times the rate of 16-bit ones: a product's tiles are the
+// 16-bit ones of product.h, four times as long in k.
+#include "product.h"
+
+namespace gs {
+
+constexpr int FP4_BLOCK = 32;
+
+// The power of two a block's byte stands for (255: NaN).
+__device__ __forceinline__ float power_of(uint32_t e)
+{
+    return __builtin_bit_cast(float, e == 0 ? 0x00400000u : (e == 255 ? 0x7fc00000u : e << 23));
+}
+
+// The byte of a block whose largest magnitude has these bits: its exponent less
+// that of 4, so that it lies in 4 .. 8 (6 is the largest of the grid; what is
+// over it rounds down). Infinities and NaN give 255, and a block of NaN.
+__device__ __forceinline__ uint32_t byte_of(uint32_t bits)
+{
+    const uint32_t e = bits >> 23;
+    return e == 255 ? 255 : (e > 2 ? e - 2 : 0);
+}
+
+// Eight values to codes, value i in bits 4 i; halves go to even codes.
+__device__ __forceinline__ uint32_t codes_of(const float (&v)[8], float power)
+{
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], power, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], power, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], power, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], power, 3);
+    return c;
+}
+
+__device__ __forceinline__ uint32_t largest_bits(const float (&v)[8])
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __builtin_bit_cast(uint32_t, v[i]) & 0x7fffffffu);
+    return m;
+}
+
+// The largest over the four lanes of a block.
+__device__ __forceinline__ uint32_t quad_max(uint32_t m)
+{
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xb1, 0xf, 0xf, false));  // quad_perm 1,0,3,2
+    return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4e, 0xf, 0xf, false));  // quad_perm 2,3,0,1
+}
+
+// A thread's place: eight values at column c of row r0 + k step, k = 0, 1, ...
+// Rows are dealt to `lanes` threads (a multiple of 4) or to several passes of
+// 256 of them.
+struct Eights {
+    int64_t row, step;
+    int c, stride;
+    bool on;
+    __device__ __forceinline__ explicit Eights(int channels)
+    {
+        const int lanes = channels / 8, t = threadIdx.x;
+        const int per = lanes < 256 ? 256 / lanes : 1;
+        const int r = lanes < 256 ? t / lanes : 0;
+        on = r < per;
+        row = (int64_t)blockIdx.x * per + r;
+        step = (int64_t)gridDim.x * per;
+        c = (lanes < 256 ? t - r * lanes : t) * 8;
+        stride = 256 * 8;
+    }
+};
+
+// Bound by HBM: a lane takes 16 or 32 bytes and gives 4, four lanes a block.
+template <typename T>
+__global__ __launch_bounds__(256) void k_fp4_quantise(const T* __restrict__ x, int64_t stride, uint8_t* __restrict__ codes,
+                                                      uint8_t* __restrict__ scales, int64_t rows, int32_t channels,
+                                                      int32_t scale_bytes)
+{
+    const Eights at(channels);
+    if (!at.on) return;
+    for (int64_t r = at.row; r < rows; r += at.step)
+        for (int c = at.c; c < channels; c += at.stride) {
+            float v[8];
+            load_f32<T, 8>(x + r * stride + c, v);
+            const uint32_t e = byte_of(quad_max(largest_bits(v)));
+            *(uint32_t*)(codes + r * (channels / 2) + c / 2) = codes_of(v, power_of(e));
+            if (c % FP4_BLOCK == 0) {
+                const int b = c / FP4_BLOCK;
+                scales[r * scale_bytes + b] = (uint8_t)e;
+                if (c + FP4_BLOCK == channels)  // the bytes a row is filled up with
+                    for (int i = b + 1; i < scale_bytes; ++i) scales[r * scale_bytes + i] = 0;
+            }
+        }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_fp4_dequantise(const uint8_t* __restrict__ codes, int64_t stride,
+                                                        const uint8_t* __restrict__ scales, int64_t scale_stride,
+                                                        T* __restrict__ out, int64_t rows, int32_t channels)
+{
+    typedef float float2v __attribute__((ext_vector_type(2)));
+    const Eights at(channels);
+    if (!at.on) return;
+    for (int64_t r = at.row; r < rows; r += at.step)
+        for (int c = at.c; c < channels; c += at.stride) {
+            const uint32_t w = *(const uint32_t*)(codes + r * stride + c / 2);
+            const float p = power_of(scales[r * scale_stride + c / FP4_BLOCK]);
+            const float2v a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 1);
+            const float2v d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 2), e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 3);
+            const float v[8] = {a[0] * p, a[1] * p, b[0] * p, b[1] * p, d[0] * p, d[1] * p, e[0] * p, e[1] * p};
+            store_f32<T, 8>(out + r * channels + c, v);
+        }
+}
+
+struct FourArgs {
+    Operand a, b;  // [0]: codes, [1]: scales
+    Walk walk;
+    void* y;
+    int64_t m, n;
+    uint32_t mt, nt;
+};
+
+using FourTile = TileShape<256, 128, 2, 2, 64, 3>;
+using FourSmall = TileShape<64, 64, 2, 2, 64, 3>;
+
+template <typename T, typename S>
+__device__ __forceinline__ void four_product(char* __restrict__ lds, const FourArgs& p)
+{
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), hi = lane >> 5;
+    uint32_t mi, ni;
+    tile_of(xcd_contiguous(blockIdx.x, gridDim.x), p.mt, p.nt, mi, ni);
+    const int64_t m0 = (int64_t)mi * S::BM, n0 = (int64_t)ni * S::BN;
+    acc16 acc[S::MT][S::NT];
+    TileProduct<fp4, S, false, false, false>::run(lds, p.a, p.b, m0, n0, p.walk, wave, acc);
+    const int64_t row0 = m0 + wave / S::WN * (S::BM / S::WM), col0 = n0 + wave % S::WN * (S::BN / S::WN) + (lane & 31);
+#pragma unroll
+    for (int i = 0; i < S::MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int64_t row = row0 + 32 * i + c_row(r, hi);
+            if (row >= p.m) continue;
+#pragma unroll
+            for (int j = 0; j < S::NT; ++j)
+                if (col0 + 32 * j < p.n) ((T*)p.y)[row * p.n + col0 + 32 * j] = (T)acc[i][j][r];
+        }
+}
+
+template <typename T, typename S>
+__global__ __launch_bounds__(S::WAVES * 64, 2) void k_fp4_product(const FourArgs p)
+{
+    __shared__ alignas(16) char s_lds[TileProduct<fp4, S, false, false, false>::LDS];
+    four_product<T, S>(s_lds, p);
+}
+
+static int64_t scale_bytes_of(int32_t channels) { return (channels + 127) / 128 * 4; }
+
+static unsigned eights_grid(int64_t rows, int32_t channels)
+{
+    const int64_t lanes = channels / 8, per = lanes < 256 ? 256 / lanes : 1;
+    return (unsigned)std::min<int64_t>((rows + per - 1) / per, 8192);
+}
+
+template <typename T>
+static hipError_t quantise(const void* x, int64_t stride, void* codes, void* scales, int64_t rows, int32_t channels, hipStream_t s)
+{
+    hipLaunchKernelGGL((k_fp4_quantise<T>), dim3(eights_grid(rows, channels)), dim3(256), 0, s, (const T*)x, stride,
+                       (uint8_t*)codes, (uint8_t*)scales, rows, channels, (int32_t)scale_bytes_of(channels));
+    return hipGetLastError();
+}
+
+static hipError_t quantise_as(int32_t dtype, const gs_matrix* x, void* codes, void* scales, int64_t rows, int32_t channels,
+                              hipStream_t s)
+{
+    return dtype == GS_F32   ? quantise<float>(x->data, x->stride, codes, scales, rows, channels, s)
+           : dtype == GS_F16 ? quantise<f16>(x->data, x->stride, codes, scales, rows, channels, s)
+                             : quantise<bf16>(x->data, x->stride, codes, scales, rows, channels, s);
+}
+
+template <typename T>
+static hipError_t dequantise(const gs_matrix* codes, const gs_matrix* scales, void* out, int64_t rows, int32_t channels,
+                             hipStream_t s)
+{
+    hipLaunchKernelGGL((k_fp4_dequantise<T>), dim3(eights_grid(rows, channels)), dim3(256), 0, s, (const uint8_t*)codes->data,
+                       codes->stride, (const uint8_t*)scales->data, scales->stride, (T*)out, rows, channels);
+    return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t product_as(FourArgs& p, hipStream_t s)
+{
+    const bool large = ((p.m + 255) / 256) * ((p.n + 127) / 128) >= 256;
+    p.mt = (uint32_t)((p.m + (large ? 255 : 63)) / (large ? 256 : 64));
+    p.nt = (uint32_t)((p.n + (large ? 127 : 63)) / (large ? 128 : 64));
+    if (large) hipLaunchKernelGGL((k_fp4_product<T, FourTile>), dim3(p.mt * p.nt), dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((k_fp4_product<T, FourSmall>), dim3(p.mt * p.nt), dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+static bool four_sizes_ok(int64_t rows, int32_t channels)
+{
+    return rows >= 0 && rows <= (1 << 24) && channels >= FP4_BLOCK && channels <= (1 << 17) && channels % FP4_BLOCK == 0;
+}
+
+// Rows of `bytes` a unit on 16 bytes, those of a tile within 31 bits.
+static bool four_rows_ok(const gs_matrix* m, int unit, int align)
+{
+    return (uintptr_t)m->data % align == 0 && m->stride >= 0 && m->stride < (1 << 21) && m->stride * unit % align == 0;
+}
+
+}  // namespace gs
+
+extern "C" {
+
+gs_status gs_quantise_fp4(const gs_matrix* x, int64_t rows, int32_t channels, int32_t dtype, void* codes, void* scales,
+                          void* stream)
+{
+    using namespace gs;
+    if (!four_sizes_ok(rows, channels) || !dtype_ok(dtype)) return GS_ERR_INVALID_ARGUMENT;
+    if (rows == 0) return GS_OK;
+    if (!x || !x->data || !codes || !scales) return GS_ERR_INVALID_ARGUMENT;
+    if (!four_rows_ok(x, elem_bytes(dtype), 16) || ((uintptr_t)codes & 15) || ((uintptr_t)scales & 3)) return GS_ERR_UNSUPPORTED;
+    return quantise_as(dtype, x, codes, scales, rows, channels, (hipStream_t)stream) == hipSuccess ? GS_OK : GS_ERR_HIP;
+}
+
+gs_status gs_dequantise_fp4(const gs_matrix* codes, const gs_matrix* scales, int64_t rows, int32_t channels, int32_t dtype,
+                            void* out, void* stream)
+{
+    using namespace gs;
+    if (!four_sizes_ok(rows, channels) || !dtype_ok(dtype)) return GS_ERR_INVALID_ARGUMENT;
+    if (rows == 0) return GS_OK;
+    if (!codes || !codes->data || !scales || !scales->data || !out) return GS_ERR_INVALID_ARGUMENT;
+    if (!four_rows_ok(codes, 1, 16) || !four_rows_ok(scales, 1, 4) || ((uintptr_t)out & 15)) return GS_ERR_UNSUPPORTED;
+    const hipStream_t s = (hipStream_t)stream;
+    const auto f = dtype == GS_F32 ? dequantise<float> : (dtype == GS_F16 ? dequantise<f16> : dequantise<bf16>);
+    return f(codes, scales, out, rows, channels, s) == hipSuccess ? GS_OK : GS_ERR_HIP;
+}
+
+size_t gs_linear_fp4_workspace_bytes(int64_t rows, int32_t channels, int32_t out)
+{
+    using namespace gs;
+    if (!four_sizes_ok(rows, channels) || out < 1 || out > (1 << 17)) return 0;
+    return ((size_t)rows * (channels / 2) + 15) / 16 * 16 + (size_t)rows * scale_bytes_of(channels) + 64;
+}
+
+gs_status gs_linear_fp4(const gs_matrix* x, const gs_matrix* codes, const gs_matrix* scales, int64_t rows, int32_t channels,
+                        int32_t out, int32_t dtype, void* y, void* ws, size_t ws_bytes, void* stream)
+{
+    using namespace gs;
+    if (!four_sizes_ok(rows, channels) || out < 1 || out > (1 << 17) || !dtype_ok(dtype)) return GS_ERR_INVALID_ARGUMENT;
+    if (rows == 0) return GS_OK;
+    if (!x || !x->data || !codes || !codes->data || !scales || !scales->data || !y) return GS_ERR_INVALID_ARGUMENT;
+    if (!ws || ((uintptr_t)ws & 15) || ws_bytes < gs_linear_fp4_workspace_bytes(rows, channels, out)) return GS_ERR_INVALID_ARGUMENT;
+    if (!four_rows_ok(x, elem_bytes(dtype), 16) || !four_rows_ok(codes, 1, 16) || !four_rows_ok(scales, 1, 4) ||
+        (uintptr_t)y % elem_bytes(dtype) || ((rows + 63) / 64) * ((out + 63) / 64) >= (1 << 23))
+        return GS_ERR_UNSUPPORTED;
+    const hipStream_t s = (hipStream_t)stream;
+    char* xc = (char*)ws;
+    char* xs = xc + ((size_t)rows * (channels / 2) + 15) / 16 * 16;
+    if (quantise_as(dtype, x, xc, xs, rows, channels, s) != hipSuccess) return GS_ERR_HIP;
+    FourArgs p{};
+    p.a = {{xc, xs}, {channels / 2, scale_bytes_of(channels)}, rows};
+    p.b = {{(const char*)codes->data, (const char*)scales->data}, {codes->stride, scales->stride}, out};
+    p.walk = {channels / 4, (channels + 127) / 128, 0, (channels + 127) / 128};
+    p.y = y;
+    p.m = rows;
+    p.n = out;
+    const hipError_t e = dtype == GS_F32 ? product_as<float>(p, s) : (dtype == GS_F16 ? product_as<f16>(p, s) : product_as<bf16>(p, s));
+    return e == hipSuccess ? GS_OK : GS_ERR_HIP;
+}
+
+}  // extern "C"

@@ -11,6 +11,11 @@
 // l >> 5, of row l & 31 of either operand; of C column l & 31, rows
 // 8 (i >> 2) + 4 (l >> 5) + (i & 3) for registers i = 0..15.
 //
+// 4-bit elements take 8 to the place of two 16-bit ones: sizes of k below are in
+// units of 2 bytes. A step then covers 64 of them, and a lane's 16 bytes are one
+// block of 32 with its scale; the lane halves take the blocks of a stage in the
+// order (2 hi + step), so that a lane's scales of all its steps are neighbours.
+//
 // An operand lies in memory either along k (its rows' k contiguous) or across
 // it (TR: [k][rows], as the transposed matrices of a backward pass do); then
 // its 16-bit elements are turned on the way from LDS to registers.
@@ -19,6 +24,21 @@
 #include "block_attn.h"
 
 namespace gs {
+
+// Two values of 4 bits a byte, of either operand of a scaled product.
+struct fp4 {};
+template <>
+struct Mma<fp4> {
+    typedef int v8 __attribute__((ext_vector_type(4)));
+    typedef int v8i __attribute__((ext_vector_type(8)));
+    // Scales: byte `s` of sa and sb, as exponents off 127.
+    static __device__ __forceinline__ acc16 mma(v8 a, v8 b, acc16 c, int s, int sa, int sb)
+    {
+        const v8i x = {a[0], a[1], a[2], a[3], 0, 0, 0, 0}, y = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
+        return s == 0 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 0, sa, 0, sb)
+                      : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 1, sa, 1, sb);
+    }
+};
 
 // One operand's tile of ROWS rows in LDS, in chunks of 16 bytes, swizzled so
 // that a wave's reads do not share banks (64 of 4 bytes).
@@ -99,7 +119,10 @@ struct PanelRead {
         const int l = lane_id(), hi = l >> 5;
         if constexpr (!TR) {
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s) at[s] = (r0 + (l & 31)) * KB + (((2 * s + hi) ^ P::swizzle(l & 31)) * 16);
+            for (int s = 0; s < STEPS; ++s) {
+                const int c = std::is_same<T, fp4>::value ? STEPS * hi + s : 2 * s + hi;
+                at[s] = (r0 + (l & 31)) * KB + (c ^ P::swizzle(l & 31)) * 16;
+            }
         } else {
             // slots 0..3 and 4..7 of a lane's k are rows 8 hi and 8 hi + 4 on, as an operand along k has them
 #pragma unroll
@@ -185,9 +208,37 @@ struct TileProduct {
         }
     };
 
+    // A lane's scales of one operand: 4 bytes a stage and row, the two of this lane's half in the low ones.
+    template <int TILES>
+    struct Scales {
+        __amdgpu_buffer_rsrc_t src;
+        uint32_t off, rows32;
+        __device__ __forceinline__ Scales(const Operand& o, int64_t r0, int row, int stages)
+        {
+            const int64_t ld = o.ld[1], bytes = (o.rows - 1 - r0) * ld + 4 * stages;
+            src = __builtin_amdgcn_make_buffer_rsrc((void*)(o.data[1] + r0 * ld), 0,
+                                                    bytes < 0x7fffffff ? (int)bytes : 0x7fffffff, 0x00027000);
+            off = (uint32_t)(row + (lane_id() & 31)) * (uint32_t)ld;
+            rows32 = 32 * (uint32_t)ld;
+        }
+        __device__ __forceinline__ void load(int stage, int (&out)[TILES]) const
+        {
+#pragma unroll
+            for (int i = 0; i < TILES; ++i) out[i] = __builtin_amdgcn_raw_buffer_load_b32(src, off, i * rows32 + stage * 4, 0);
+        }
+        // `blocks` of the 4 count; the bytes behind them may hold anything.
+        static __device__ __forceinline__ int mine(int x, int blocks)
+        {
+            if (blocks < 4) x &= (1 << 8 * blocks) - 1;
+            return (uint32_t)x >> (lane_id() >> 5) * 16;
+        }
+    };
+
     static __device__ __forceinline__ void run(char* __restrict__ lds, const Operand& a, const Operand& b, int64_t m0,
                                                int64_t n0, const Walk& w, int wave, acc16 (&acc)[S::MT][S::NT])
     {
+        constexpr bool FOUR = std::is_same<T, fp4>::value;
+        static_assert(!FOUR || S::KB == 64, "one dword of scales a stage");
         const LoadA load_a((uint32_t)a.ld[0], wave);
         const int mine = PAIR ? LoadB::second(wave) : w.first >= w.stages;
         LoadB load_b((uint32_t)b.ld[mine], wave);
@@ -219,14 +270,37 @@ struct TileProduct {
 #pragma unroll
         for (int t = 0; t < S::STAGES - 1; ++t) issue(lds + t * STAGE);
         int now = 0;
+        const Scales<S::MT> scale_a(a, m0, wave / S::WN * (S::BM / S::WM), w.stages);
+        const Scales<S::NT> scale_b(b, n0, wave % S::WN * (S::BN / S::WN), w.stages);
+        int sa[S::MT], sb[S::NT], next_sa[S::MT], next_sb[S::NT];
+        if constexpr (FOUR) {
+            scale_a.load(w.first, next_sa);
+            scale_b.load(w.first, next_sb);
+        }
         for (int t = w.first; t < w.last; ++t) {
             // this stage's loads are done when only those of the later ones are out; reads of the last stage too
-            static_assert((S::STAGES - 2) * LOADS < 16, "fits the field used below");
-            __builtin_amdgcn_s_waitcnt(0x0070 | ((S::STAGES - 2) * LOADS));
+            constexpr int LATER = (S::STAGES - 2) * LOADS;
+            static_assert(LATER < 16, "fits the field used below");
+            if constexpr (FOUR) {  // the scales' loads, the latest ones, are waited for with the stage's
+                __builtin_amdgcn_s_waitcnt(0x0070);
+            } else {
+                __builtin_amdgcn_s_waitcnt(0x0070 | LATER);
+            }
             asm volatile("" ::: "memory");
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
             const int to = now == 0 ? S::STAGES - 1 : now - 1;
+            if constexpr (FOUR) {
+                const int blocks = (int)(w.k - (int64_t)t * KE) / 8;
+#pragma unroll
+                for (int i = 0; i < S::MT; ++i) sa[i] = Scales<S::MT>::mine(next_sa[i], blocks);
+#pragma unroll
+                for (int j = 0; j < S::NT; ++j) sb[j] = Scales<S::NT>::mine(next_sb[j], blocks);
+                if (t + 1 < w.last) {
+                    scale_a.load(t + 1, next_sa);
+                    scale_b.load(t + 1, next_sb);
+                }
+            }
             issue(lds + to * STAGE);
             const char* pa = lds + now * STAGE;
             const char* pb = pa + A_BYTES;
@@ -240,7 +314,10 @@ struct TileProduct {
 #pragma unroll
                 for (int i = 0; i < S::MT; ++i)
 #pragma unroll
-                    for (int j = 0; j < S::NT; ++j) acc[i][j] = Mma<T>::mma(ra[i], rb[j], acc[i][j]);
+                    for (int j = 0; j < S::NT; ++j) {
+                        if constexpr (FOUR) acc[i][j] = Mma<T>::mma(ra[i], rb[j], acc[i][j], s, sa[i], sb[j]);
+                        else acc[i][j] = Mma<T>::mma(ra[i], rb[j], acc[i][j]);
+                    }
             }
             now = now == S::STAGES - 1 ? 0 : now + 1;
         }

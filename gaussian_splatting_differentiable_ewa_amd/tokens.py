@@ -266,6 +266,69 @@ def gated_ff_backward(gy, x, w_gate, w_up, w_down, h, pre, act: str = "silu"):
     return tuple(grads)
 
 
+# ---- linear layers in 4 bits ----------------------------------------------------
+FOUR = 32  # values that share a scale
+
+
+def _on16_rows(t):
+    """t itself, or a copy, so that every row starts on 16 bytes, whatever its type."""
+    if (t.stride(1) == 1 and t.data_ptr() % 16 == 0 and (t.shape[0] <= 1 or t.stride(0) * t.element_size() % 16 == 0)
+            and t.stride(0) < 1 << 21):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+def _four(four, channels, like):
+    codes, scales = four
+    for name, t, columns in (("codes", codes, channels // 2), ("scales", scales, (channels + 127) // 128 * 4)):
+        if (t.dim() != 2 or t.dtype is not torch.uint8 or t.shape[1] != columns or t.shape[0] != codes.shape[0]
+                or t.get_device() != like.get_device() or t.stride(1) != 1 or t.stride(0) % 4 or t.data_ptr() % 4):
+            raise ValueError(f"{name} must be uint8 [rows, {columns}] on {like.device}, rows on 4 bytes, as quantise4's")
+    return _on16_rows(codes), scales
+
+
+def quantise4(x):
+    """(codes, scales): x [rows, channels] in microscaled 4-bit floating point,
+    uint8 [rows, channels / 2] and [rows, 4 ceil(channels / 128)]; channels of
+    32. For weights once, and inside linear4 for its input. See gs_quantise_fp4."""
+    _rows("x", x)
+    rows, c = x.shape
+    _need(c % FOUR == 0 and c > 0, "channels must be a multiple of 32")
+    if x.requires_grad:
+        _lost("a 16-bit layer")
+    codes = torch.empty(rows, c // 2, dtype=torch.uint8, device=x.device)
+    scales = torch.empty(rows, (c + 127) // 128 * 4, dtype=torch.uint8, device=x.device)
+    L.gs_quantise_fp4(_on16_rows(x), codes, scales)
+    return codes, scales
+
+
+def dequantise4(four, dtype=torch.float32):
+    """The values [rows, channels] of quantise4's pair."""
+    _rows("codes", four[0])
+    c = four[0].shape[1] * 2
+    _need(c % FOUR == 0 and c > 0, "channels must be a multiple of 32")
+    codes, scales = _four(four, c, four[0])
+    out = torch.empty(codes.shape[0], c, dtype=dtype, device=codes.device)
+    L.gs_dequantise_fp4(codes, scales, out)
+    return out
+
+
+def linear4(x, weights):
+    """x [rows, channels], in 4 bits, times the transpose of quantise4's weights
+    ([out, channels]), in x's type; for serving. See gs_linear_fp4."""
+    _rows("x", x)
+    rows, c = x.shape
+    _need(c % FOUR == 0 and c > 0, "channels must be a multiple of 32")
+    codes, scales = _four(weights, c, x)
+    if x.requires_grad:
+        _lost("a 16-bit layer")
+    y = torch.empty(rows, codes.shape[0], dtype=x.dtype, device=x.device)
+    if codes.shape[0]:
+        ws = torch.empty(L.linear_fp4_workspace_bytes(rows, c, codes.shape[0]), dtype=torch.uint8, device=x.device)
+        L.gs_linear_fp4(_on16_rows(x), codes, scales, y, ws)
+    return y
+
+
 # ---- choice of key blocks -------------------------------------------------------
 def _length(kv_len, q):
     _vector("kv_len", kv_len, (q.shape[0],), q, torch.int32)

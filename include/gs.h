@@ -681,6 +681,7 @@ gs_status gs_stream_copy(void* dst, const void* src, uint64_t bytes, void* strea
  *   gs_block_attn_fwd/_bwd  attention over those blocks
  *   gs_layer_norm_fwd/_bwd  layer norm
  *   gs_gated_ff_fwd/_bwd    the gated feed-forward block
+ *   gs_quantise_fp4, gs_dequantise_fp4, gs_linear_fp4   4-bit linear layers
  *
  * Memory, streams and errors as for every entry point above (caller-owned
  * device memory, enqueue only, host checks first). The formulas are written
@@ -983,6 +984,54 @@ gs_status gs_gated_ff_bwd(const gs_matrix* gy, const gs_matrix* x, const gs_matr
                           const gs_matrix* w_down, const void* h, const float* pre, int64_t rows, int32_t channels,
                           int32_t hidden, int32_t channels_out, int32_t act, int32_t dtype, void* gx, void* gw_gate,
                           void* gw_up, void* gw_down, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * gs_quantise_fp4 -- rows to microscaled 4-bit floating point: each block of 32
+ * consecutive values v shares the scale 2^(e - 127), with
+ *   e = max(0, 127 + floor(log2 max |v|) - 2)    (0 for a block of zeros)
+ * and a value is the code of the nearest v / 2^(e - 127) among
+ *   0, 1/2, 1, 3/2, 2, 3, 4, 6  (codes 0..7, and 8 + those for negative values),
+ * the even code of two equally near ones, and 6 for what is over it. A block
+ * that holds an infinity or NaN has e = 255 and stands for NaN.
+ *   x       [rows][channels], GS_F32, GS_F16 or GS_BF16
+ *   codes   out [rows][channels / 2], value 2 i in the low half of byte i
+ *   scales  out uint8 [rows][4 ceil(channels / 128)]: e of every block, the
+ *           bytes a row is filled up with zero
+ * Errors: null pointers, channels not a multiple of 32 or outside 32..2^17, rows
+ * outside 0..2^24, a bad dtype; GS_ERR_UNSUPPORTED for data or rows off 16 bytes
+ * (scales: 4), a row stride outside 0 .. 2^21 - 1.
+ */
+gs_status gs_quantise_fp4(const gs_matrix* x, int64_t rows, int32_t channels, int32_t dtype, void* codes, void* scales,
+                          void* stream);
+
+/*
+ * gs_dequantise_fp4 -- the values that codes and scales stand for, rounded to
+ * the output's type (GS_F32 and GS_BF16 hold them exactly).
+ *   codes, scales  as gs_quantise_fp4 writes them, strides in bytes
+ *   out            [rows][channels], contiguous
+ * Errors: as gs_quantise_fp4.
+ */
+gs_status gs_dequantise_fp4(const gs_matrix* codes, const gs_matrix* scales, int64_t rows, int32_t channels, int32_t dtype,
+                            void* out, void* stream);
+
+/* Workspace of gs_linear_fp4 (bytes); 0 on invalid sizes. */
+size_t gs_linear_fp4_workspace_bytes(int64_t rows, int32_t channels, int32_t out);
+
+/*
+ * gs_linear_fp4 -- a linear layer in 4 bits: y = q(x) w^T with q(x) the values
+ * of gs_quantise_fp4 and w those of codes and scales; products are exact, sums
+ * are fp32, y is rounded once.
+ *   x       [rows][channels], GS_F32, GS_F16 or GS_BF16
+ *   codes   [out][channels / 2], scales [out][4 ceil(channels / 128)] of the
+ *           weights (strides in bytes; a row's last bytes, behind its blocks,
+ *           are not used)
+ *   y       out [rows][out], contiguous, the type of x
+ *   ws      workspace of gs_linear_fp4_workspace_bytes(...)
+ * Errors: as gs_quantise_fp4, out outside 1..2^17, a small workspace;
+ * GS_ERR_UNSUPPORTED also past 2^23 tiles of 64 x 64.
+ */
+gs_status gs_linear_fp4(const gs_matrix* x, const gs_matrix* codes, const gs_matrix* scales, int64_t rows, int32_t channels,
+                        int32_t out, int32_t dtype, void* y, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -86,3 +86,38 @@ def gated_ff(x, w_gate, w_up, w_down, act, gy=None):
     w = gy.T @ h
     out.append((w, gy.abs().T @ dh + chain(rows) * (gy.abs().T @ h.abs()) + u8 * w.abs() + tiny))
     return [(v, 1.01 * d) for v, d in out]
+
+
+GRID = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def quantise4(x):
+    """(codes [rows, channels], e [rows, channels / 32], values in 64 bits)."""
+    rows, c = x.shape
+    v = x.double().view(rows, c // 32, 32)
+    top = v.abs().amax(-1)
+    fine = torch.isfinite(top) & ~torch.isnan(v).any(-1)
+    # the exponent by comparison with powers of two, not by a logarithm
+    e = torch.zeros(rows, c // 32, dtype=torch.long, device=x.device)
+    for p in range(-124, 128):  # floor(log2 top) - 2 + 127 where that is over 0
+        e += (top >= 2.0 ** p).long() * fine
+    power = torch.exp2(e.double() - 127)
+    m = torch.where(fine[..., None], v.abs() / power[..., None], 0.0)
+    grid = torch.tensor(GRID, dtype=torch.double, device=x.device)
+    d = (m[..., None] - grid).abs()
+    near = d == d.amin(-1, keepdim=True)
+    # of two the even code
+    order = torch.tensor([0, 8, 1, 9, 2, 10, 3, 11], device=x.device)
+    code = torch.where(near, order, 99).argmin(-1)
+    value = torch.where(fine[..., None], torch.copysign(grid[code], v) * power[..., None], float("nan"))
+    code = code + 8 * torch.signbit(v).long()
+    return code.view(rows, c), torch.where(fine, e, 255), value.view(rows, c), fine
+
+
+def unpack4(codes, scales, channels):
+    """The values of a packed pair, in 64 bits."""
+    both = torch.stack([codes & 15, codes >> 4], -1).flatten(1).long()
+    grid = torch.tensor([*GRID, *(-g for g in GRID)], dtype=torch.double, device=codes.device)
+    e = scales[:, : channels // 32].long()
+    power = torch.where(e == 255, float("nan"), torch.exp2(e.double() - 127))
+    return grid[both] * power.repeat_interleave(32, 1)

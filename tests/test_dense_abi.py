@@ -82,6 +82,38 @@ def test_gated_ff_refusals(lib):
     assert call(lib.gs_gated_ff_bwd, bwd, rows=0, gwg=None, gwu=None, gwd=None) == OK
 
 
+def test_fp4_refusals(lib):
+    quant = dict(x=mat(), rows=10, c=64, t=L.GS_BF16, codes=FAKE, scales=FAKE, s=None)
+    back = dict(codes=mat(), scales=mat(), rows=10, c=64, t=L.GS_F32, out=FAKE, s=None)
+    need = L.linear_fp4_workspace_bytes(10, 64, 40)
+    assert need > 0 and L.linear_fp4_workspace_bytes(10, 48, 40) == 0 and L.linear_fp4_workspace_bytes(10, 64, 0) == 0
+    linear = dict(x=mat(), codes=mat(), scales=mat(), rows=10, c=64, n=40, t=L.GS_BF16, y=FAKE, ws=FAKE, wsb=need, s=None)
+    sizes = (dict(rows=-1), dict(rows=(1 << 24) + 1), dict(c=0), dict(c=48), dict(c=(1 << 17) + 32), dict(t=3), dict(t=-1))
+    for f, ok in ((lib.gs_quantise_fp4, quant), (lib.gs_dequantise_fp4, back), (lib.gs_linear_fp4, linear)):
+        for bad in sizes:
+            assert call(f, ok, **bad) == INV, bad
+        assert call(f, ok, rows=0) == OK
+    odd = ctypes.c_void_p(4104)
+    for bad in (dict(x=None), dict(x=mat(0)), dict(codes=None), dict(scales=None)):
+        assert call(lib.gs_quantise_fp4, quant, **bad) == INV, bad
+    for bad in (dict(x=mat(4104)), dict(x=mat(stride=1028)), dict(x=mat(stride=-8)), dict(x=mat(stride=1 << 21)), dict(codes=odd),
+                dict(scales=ctypes.c_void_p(4098))):
+        assert call(lib.gs_quantise_fp4, quant, **bad) == UNS, bad
+    for bad in (dict(codes=None), dict(scales=None), dict(codes=mat(0)), dict(scales=mat(0)), dict(out=None)):
+        assert call(lib.gs_dequantise_fp4, back, **bad) == INV, bad
+    for bad in (dict(codes=mat(4104)), dict(codes=mat(stride=1032)), dict(scales=mat(4098)), dict(scales=mat(stride=1026)),
+                dict(out=odd)):
+        assert call(lib.gs_dequantise_fp4, back, **bad) == UNS, bad
+    for bad in (dict(x=None), dict(codes=None), dict(scales=None), dict(x=mat(0)), dict(codes=mat(0)), dict(scales=mat(0)),
+                dict(n=0), dict(n=(1 << 17) + 1), dict(y=None), dict(ws=None), dict(ws=ctypes.c_void_p(4100)),
+                dict(wsb=need - 1)):
+        assert call(lib.gs_linear_fp4, linear, **bad) == INV, bad
+    for bad in (dict(x=mat(4104)), dict(x=mat(stride=1028)), dict(codes=mat(4104)), dict(codes=mat(stride=1032)),
+                dict(scales=mat(4098)), dict(scales=mat(stride=1026)), dict(scales=mat(stride=1 << 21)),
+                dict(y=ctypes.c_void_p(4097)), dict(rows=1 << 24, n=1 << 17)):
+        assert call(lib.gs_linear_fp4, linear, **bad, **({"wsb": 1 << 60} if "rows" in bad else {})) == UNS, bad
+
+
 def test_tensor_functions_refuse(lib):
     """Shapes, types and devices, before the library is called."""
     cpu = torch.zeros(4, 64)
@@ -97,3 +129,6 @@ def test_tensor_functions_refuse(lib):
             T.gated_ff(cpu, w, w, torch.zeros(64, 8), act)
     with pytest.raises(ValueError):
         T.gated_ff_backward(cpu, cpu, w, w, torch.zeros(64, 8), torch.zeros(4, 8), torch.zeros(4, 16))
+    for bad in (lambda: T.quantise4(cpu), lambda: T.linear4(cpu, (cpu, cpu)), lambda: T.dequantise4((cpu, cpu))):
+        with pytest.raises(ValueError):
+            bad()
