@@ -121,8 +121,8 @@ struct FourArgs {
     uint32_t mt, nt;
 };
 
-using FourTile = TileShape<256, 128, 2, 2, 64, 3>;
-using FourSmall = TileShape<64, 64, 2, 2, 64, 3>;
+using FourTile = TileShape<256, 256, 2, 4, 128, 2>;
+using FourSmall = TileShape<64, 64, 2, 2, 128, 3>;
 
 template <typename T, typename S>
 __device__ __forceinline__ void four_product(char* __restrict__ lds, const FourArgs& p)
@@ -189,10 +189,10 @@ static hipError_t dequantise(const gs_matrix* codes, const gs_matrix* scales, vo
 template <typename T>
 static hipError_t product_as(FourArgs& p, hipStream_t s)
 {
-    const bool large = ((p.m + 255) / 256) * ((p.n + 127) / 128) >= 256;
+    const bool large = ((p.m + 255) / 256) * ((p.n + 255) / 256) >= 128;
     p.mt = (uint32_t)((p.m + (large ? 255 : 63)) / (large ? 256 : 64));
-    p.nt = (uint32_t)((p.n + (large ? 127 : 63)) / (large ? 128 : 64));
-    if (large) hipLaunchKernelGGL((k_fp4_product<T, FourTile>), dim3(p.mt * p.nt), dim3(256), 0, s, p);
+    p.nt = (uint32_t)((p.n + (large ? 255 : 63)) / (large ? 256 : 64));
+    if (large) hipLaunchKernelGGL((k_fp4_product<T, FourTile>), dim3(p.mt * p.nt), dim3(512), 0, s, p);
     else hipLaunchKernelGGL((k_fp4_product<T, FourSmall>), dim3(p.mt * p.nt), dim3(256), 0, s, p);
     return hipGetLastError();
 }
@@ -261,7 +261,7 @@ gs_status gs_linear_fp4(const gs_matrix* x, const gs_matrix* codes, const gs_mat
     FourArgs p{};
     p.a = {{xc, xs}, {channels / 2, scale_bytes_of(channels)}, rows};
     p.b = {{(const char*)codes->data, (const char*)scales->data}, {codes->stride, scales->stride}, out};
-    p.walk = {channels / 4, (channels + 127) / 128, 0, (channels + 127) / 128};
+    p.walk = {channels / 4, (channels + 255) / 256, 0, (channels + 255) / 256};
     p.y = y;
     p.m = rows;
     p.n = out;

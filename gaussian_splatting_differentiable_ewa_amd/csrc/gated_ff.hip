@@ -158,7 +158,9 @@ __global__ __launch_bounds__(256) void k_ff_join(const Target o, int32_t splits)
     else store_one<T>(o, row, col, v);
 }
 
-using Large = TileShape<256, 128, 2, 2, 64, 3>;
+// Operands along k (rows of 128 bytes a stage), both across, and few tiles.
+using LargeK = TileShape<256, 256, 2, 4, 128, 2>;
+using LargeT = TileShape<256, 256, 2, 4, 128, 2>;
 using Small = TileShape<64, 128, 2, 2, 128, 3>;
 
 // How a product of m x n over k is cut.
@@ -168,14 +170,14 @@ struct Cut {
     int64_t mt, nt;
 };
 
-static Cut cut_of(int64_t m, int64_t n, int64_t k, int segments, bool pair)
+static Cut cut_of(int64_t m, int64_t n, int64_t k, int segments, bool pair, bool across)
 {
     Cut c;
-    const int64_t wide = pair ? 2 * n : n;
-    c.large = ((m + 255) / 256) * ((wide + 127) / 128) >= 256;
-    const int bm = c.large ? 256 : 64, ke = c.large ? 32 : 64;
+    const int64_t wide = pair ? 2 * n : n, rows = across ? LargeT::BM : LargeK::BM;
+    c.large = ((m + rows - 1) / rows) * ((wide + 255) / 256) >= 128;
+    const int bm = c.large ? (int)rows : Small::BM, ke = (c.large ? (across ? LargeT::KB : LargeK::KB) : Small::KB) / 2;
     c.mt = (m + bm - 1) / bm;
-    c.nt = (wide + 127) / 128;
+    c.nt = (wide + (c.large ? 255 : 127)) / (c.large ? 256 : 128);
     c.stages = (int32_t)((k + ke - 1) / ke);
     const int64_t total = (int64_t)c.stages * segments, tiles = c.mt * c.nt;
     int64_t splits = std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), total / 4));
@@ -192,7 +194,8 @@ static size_t part_bytes(const Cut& c, int64_t m, int64_t n, bool pair)
 template <typename T, bool ATR, bool BTR, int TO, int ACT>
 static hipError_t product(const Operand& a, const Operand& b, Target o, int64_t k, int segments, float* part, hipStream_t s)
 {
-    const Cut c = cut_of(o.m, o.n, k, segments, TO == TO_GATED);
+    using Large = std::conditional_t<ATR, LargeT, LargeK>;
+    const Cut c = cut_of(o.m, o.n, k, segments, TO == TO_GATED, ATR);
     ProductArgs p;
     p.a = a;
     p.b = b;
@@ -204,12 +207,12 @@ static hipError_t product(const Operand& a, const Operand& b, Target o, int64_t 
     p.per_split = c.per_split;
     const dim3 grid((unsigned)(c.mt * c.nt * c.splits));
     if (c.splits > 1) {
-        if (c.large) hipLaunchKernelGGL((k_ff_product<T, Large, ATR, BTR, TO, ACT, true>), grid, dim3(256), 0, s, p);
-        else hipLaunchKernelGGL((k_ff_product<T, Small, ATR, BTR, TO, ACT, true>), grid, dim3(256), 0, s, p);
+        if (c.large) hipLaunchKernelGGL((k_ff_product<T, Large, ATR, BTR, TO, ACT, true>), grid, dim3(c.large ? 512 : 256), 0, s, p);
+        else hipLaunchKernelGGL((k_ff_product<T, Small, ATR, BTR, TO, ACT, true>), grid, dim3(c.large ? 512 : 256), 0, s, p);
         hipLaunchKernelGGL((k_ff_join<T, TO, ACT>), dim3(grid_for((uint64_t)(o.m * o.n), 256)), dim3(256), 0, s, p.o, c.splits);
     } else {
-        if (c.large) hipLaunchKernelGGL((k_ff_product<T, Large, ATR, BTR, TO, ACT, false>), grid, dim3(256), 0, s, p);
-        else hipLaunchKernelGGL((k_ff_product<T, Small, ATR, BTR, TO, ACT, false>), grid, dim3(256), 0, s, p);
+        if (c.large) hipLaunchKernelGGL((k_ff_product<T, Large, ATR, BTR, TO, ACT, false>), grid, dim3(c.large ? 512 : 256), 0, s, p);
+        else hipLaunchKernelGGL((k_ff_product<T, Small, ATR, BTR, TO, ACT, false>), grid, dim3(c.large ? 512 : 256), 0, s, p);
     }
     return hipGetLastError();
 }
@@ -228,25 +231,25 @@ static bool sizes_ok(const Sizes& z)
 static bool tiles_ok(const Sizes& z)
 {
     const auto fits = [](const Cut& c) { return c.mt * c.nt < (1 << 23); };
-    return fits(cut_of(z.rows, z.f, z.c, 1, true)) && fits(cut_of(z.rows, z.co, z.f, 1, false)) &&
-           fits(cut_of(z.rows, z.c, z.f, 2, false)) && fits(cut_of(2 * z.f, z.c, z.rows, 1, false)) &&
-           fits(cut_of(z.co, z.f, z.rows, 1, false));
+    return fits(cut_of(z.rows, z.f, z.c, 1, true, false)) && fits(cut_of(z.rows, z.co, z.f, 1, false, false)) &&
+           fits(cut_of(z.rows, z.c, z.f, 2, false, false)) && fits(cut_of(2 * z.f, z.c, z.rows, 1, false, true)) &&
+           fits(cut_of(z.co, z.f, z.rows, 1, false, true));
 }
 
 static size_t fwd_bytes(const Sizes& z)
 {
-    return std::max(part_bytes(cut_of(z.rows, z.f, z.c, 1, true), z.rows, z.f, true),
-                    part_bytes(cut_of(z.rows, z.co, z.f, 1, false), z.rows, z.co, false));
+    return std::max(part_bytes(cut_of(z.rows, z.f, z.c, 1, true, false), z.rows, z.f, true),
+                    part_bytes(cut_of(z.rows, z.co, z.f, 1, false, false), z.rows, z.co, false));
 }
 
 static size_t grad_bytes(const Sizes& z) { return ((size_t)z.rows * z.f * 2 * 2 + 255) / 256 * 256; }  // gg | gu
 
 static size_t bwd_bytes(const Sizes& z)
 {
-    size_t part = part_bytes(cut_of(z.rows, z.f, z.co, 1, false), z.rows, z.f, false);
-    part = std::max(part, part_bytes(cut_of(z.rows, z.c, z.f, 2, false), z.rows, z.c, false));
-    part = std::max(part, part_bytes(cut_of(2 * z.f, z.c, z.rows, 1, false), 2 * z.f, z.c, false));
-    return grad_bytes(z) + std::max(part, part_bytes(cut_of(z.co, z.f, z.rows, 1, false), z.co, z.f, false));
+    size_t part = part_bytes(cut_of(z.rows, z.f, z.co, 1, false, false), z.rows, z.f, false);
+    part = std::max(part, part_bytes(cut_of(z.rows, z.c, z.f, 2, false, false), z.rows, z.c, false));
+    part = std::max(part, part_bytes(cut_of(2 * z.f, z.c, z.rows, 1, false, true), 2 * z.f, z.c, false));
+    return grad_bytes(z) + std::max(part, part_bytes(cut_of(z.co, z.f, z.rows, 1, false, true), z.co, z.f, false));
 }
 
 static Operand operand(const gs_matrix* m, int64_t rows) { return {{(const char*)m->data, nullptr}, {m->stride * 2, 0}, rows}; }

@@ -1,11 +1,13 @@
 // Matrix products by tiles, shared by the gated feed-forward block
 // (gated_ff.hip) and the 4-bit linear layers (fp4.hip).
 //
-// A workgroup of four waves forms BM x BN elements of C = A B^T. Both operands
-// pass through LDS in stages of KB bytes of a row's k (two matrix steps per 64
-// bytes), loaded straight from memory STAGES - 1 stages ahead; there is one
-// barrier per stage, behind which the stage is whole for all waves and the one
-// before it is read out.
+// A workgroup forms BM x BN elements of C = A B^T. Both operands pass through
+// LDS in stages of KB bytes of a row's k (32 bytes a matrix step), loaded
+// straight from memory into the stage that was read out last. A step's operands
+// are read into registers while the step before it is on the matrix unit, also
+// from one stage to the next: the one barrier per stage stands before its last
+// step, whose operands are in registers by then. Behind it the next stage is whole
+// and this one is free.
 //
 // Matrix tile: 32 x 32, 32 bytes of k a step. Lane l holds 16 bytes of k, half
 // l >> 5, of row l & 31 of either operand; of C column l & 31, rows
@@ -35,8 +37,12 @@ struct Mma<fp4> {
     static __device__ __forceinline__ acc16 mma(v8 a, v8 b, acc16 c, int s, int sa, int sb)
     {
         const v8i x = {a[0], a[1], a[2], a[3], 0, 0, 0, 0}, y = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
-        return s == 0 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 0, sa, 0, sb)
-                      : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 1, sa, 1, sb);
+        switch (s) {
+            case 0: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 0, sa, 0, sb);
+            case 1: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 1, sa, 1, sb);
+            case 2: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 2, sa, 2, sb);
+            default: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 3, sa, 3, sb);
+        }
     }
 };
 
@@ -174,6 +180,19 @@ struct Walk {
     int first, last;
 };
 
+// Order of the instructions around: LDS reads of the next step between matrix
+// instructions of this one.
+template <int READS, int MFMAS>
+__device__ __forceinline__ void spread()
+{
+    constexpr int EACH = (READS + MFMAS - 1) / MFMAS;
+#pragma unroll
+    for (int i = 0; i < MFMAS; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, EACH, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    }
+}
+
 template <typename T, typename S, bool ATR, bool BTR, bool PAIR>
 struct TileProduct {
     static constexpr int KE = S::KB / 2;  // elements of a stage
@@ -208,29 +227,29 @@ struct TileProduct {
         }
     };
 
-    // A lane's scales of one operand: 4 bytes a stage and row, the two of this lane's half in the low ones.
+    // A lane's scales of one operand: 8 bytes a stage and row, 4 of them each lane half's.
     template <int TILES>
     struct Scales {
         __amdgpu_buffer_rsrc_t src;
         uint32_t off, rows32;
-        __device__ __forceinline__ Scales(const Operand& o, int64_t r0, int row, int stages)
+        __device__ __forceinline__ Scales(const Operand& o, int64_t r0, int row, int bytes_of_row)
         {
-            const int64_t ld = o.ld[1], bytes = (o.rows - 1 - r0) * ld + 4 * stages;
+            const int64_t ld = o.ld[1], bytes = (o.rows - 1 - r0) * ld + bytes_of_row;
             src = __builtin_amdgcn_make_buffer_rsrc((void*)(o.data[1] + r0 * ld), 0,
                                                     bytes < 0x7fffffff ? (int)bytes : 0x7fffffff, 0x00027000);
-            off = (uint32_t)(row + (lane_id() & 31)) * (uint32_t)ld;
+            off = (uint32_t)(row + (lane_id() & 31)) * (uint32_t)ld + (lane_id() >> 5) * 4;
             rows32 = 32 * (uint32_t)ld;
         }
         __device__ __forceinline__ void load(int stage, int (&out)[TILES]) const
         {
 #pragma unroll
-            for (int i = 0; i < TILES; ++i) out[i] = __builtin_amdgcn_raw_buffer_load_b32(src, off, i * rows32 + stage * 4, 0);
+            for (int i = 0; i < TILES; ++i) out[i] = __builtin_amdgcn_raw_buffer_load_b32(src, off, i * rows32 + stage * 8, 0);
         }
-        // `blocks` of the 4 count; the bytes behind them may hold anything.
+        // `blocks` of the stage's 8 count; the bytes behind them may hold anything.
         static __device__ __forceinline__ int mine(int x, int blocks)
         {
-            if (blocks < 4) x &= (1 << 8 * blocks) - 1;
-            return (uint32_t)x >> (lane_id() >> 5) * 16;
+            const int n = blocks - 4 * (int)(lane_id() >> 5);
+            return n >= 4 ? x : (n <= 0 ? 0 : x & ((1 << 8 * n) - 1));
         }
     };
 
@@ -238,7 +257,9 @@ struct TileProduct {
                                                int64_t n0, const Walk& w, int wave, acc16 (&acc)[S::MT][S::NT])
     {
         constexpr bool FOUR = std::is_same<T, fp4>::value;
-        static_assert(!FOUR || S::KB == 64, "one dword of scales a stage");
+        static_assert(!FOUR || S::KB == 128, "one dword of scales a stage and lane half");
+        constexpr int STEPS = S::KB / 32, LATER = (S::STAGES - 2) * LOADS;
+        static_assert(STEPS % 2 == 0 && S::STAGES >= 2 && LATER < 16, "steps in pairs; loads out fit the wait's field");
         const LoadA load_a((uint32_t)a.ld[0], wave);
         const int mine = PAIR ? LoadB::second(wave) : w.first >= w.stages;
         LoadB load_b((uint32_t)b.ld[mine], wave);
@@ -267,59 +288,69 @@ struct TileProduct {
                 load_b = LoadB((uint32_t)b.ld[1], wave);
             }
         };
-#pragma unroll
-        for (int t = 0; t < S::STAGES - 1; ++t) issue(lds + t * STAGE);
-        int now = 0;
-        const Scales<S::MT> scale_a(a, m0, wave / S::WN * (S::BM / S::WM), w.stages);
-        const Scales<S::NT> scale_b(b, n0, wave % S::WN * (S::BN / S::WN), w.stages);
-        int sa[S::MT], sb[S::NT], next_sa[S::MT], next_sb[S::NT];
-        if constexpr (FOUR) {
-            scale_a.load(w.first, next_sa);
-            scale_b.load(w.first, next_sb);
-        }
-        for (int t = w.first; t < w.last; ++t) {
-            // this stage's loads are done when only those of the later ones are out; reads of the last stage too
-            constexpr int LATER = (S::STAGES - 2) * LOADS;
-            static_assert(LATER < 16, "fits the field used below");
-            if constexpr (FOUR) {  // the scales' loads, the latest ones, are waited for with the stage's
-                __builtin_amdgcn_s_waitcnt(0x0070);
-            } else {
-                __builtin_amdgcn_s_waitcnt(0x0070 | LATER);
-            }
+        // `out` loads may be left out; all LDS reads are done
+        auto ready = [&](auto out) __attribute__((always_inline)) {
+            __builtin_amdgcn_s_waitcnt(0x0070 | decltype(out)::value);
             asm volatile("" ::: "memory");
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
-            const int to = now == 0 ? S::STAGES - 1 : now - 1;
+        };
+        typename Mma<T>::v8 ra[2][S::MT], rb[2][S::NT];
+        auto read = [&](const char* stage, int step, int to) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < S::NT; ++j) rb[to][j] = read_b(stage + A_BYTES, j, step);
+#pragma unroll
+            for (int i = 0; i < S::MT; ++i) ra[to][i] = read_a(stage, i, step);
+        };
+        const int scale_row = (int)(w.k + 31) / 32 * 4;
+        const Scales<S::MT> scale_a(a, m0, wave / S::WN * (S::BM / S::WM), scale_row);
+        const Scales<S::NT> scale_b(b, n0, wave % S::WN * (S::BN / S::WN), scale_row);
+        int sa[S::MT], sb[S::NT], next_sa[S::MT], next_sb[S::NT];
+        auto multiply = [&](int step, int from) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < S::MT; ++i)
+#pragma unroll
+                for (int j = 0; j < S::NT; ++j) {
+                    if constexpr (FOUR) acc[i][j] = Mma<T>::mma(ra[from][i], rb[from][j], acc[i][j], step, sa[i], sb[j]);
+                    else acc[i][j] = Mma<T>::mma(ra[from][i], rb[from][j], acc[i][j]);
+                }
+        };
+#pragma unroll
+        for (int t = 0; t < S::STAGES; ++t) issue(lds + t * STAGE);
+        if constexpr (FOUR) {
+            scale_a.load(w.first, next_sa);
+            scale_b.load(w.first, next_sb);
+            ready(std::integral_constant<int, 0>{});
+        } else {
+            ready(std::integral_constant<int, LATER + LOADS>{});
+        }
+        read(lds, 0, 0);
+        int now = 0;
+        for (int t = w.first; t < w.last; ++t) {
+            const char* stage = lds + now * STAGE;
+            const int next = now == S::STAGES - 1 ? 0 : now + 1;
             if constexpr (FOUR) {
                 const int blocks = (int)(w.k - (int64_t)t * KE) / 8;
 #pragma unroll
                 for (int i = 0; i < S::MT; ++i) sa[i] = Scales<S::MT>::mine(next_sa[i], blocks);
 #pragma unroll
                 for (int j = 0; j < S::NT; ++j) sb[j] = Scales<S::NT>::mine(next_sb[j], blocks);
-                if (t + 1 < w.last) {
-                    scale_a.load(t + 1, next_sa);
-                    scale_b.load(t + 1, next_sb);
+                scale_a.load(t + 1, next_sa);  // past the row's end: not used
+                scale_b.load(t + 1, next_sb);
+            }
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                if (s < STEPS - 1) {
+                    read(stage, s + 1, (s + 1) & 1);
+                } else {
+                    ready(std::integral_constant<int, FOUR ? 0 : LATER>{});
+                    issue(lds + now * STAGE);
+                    read(lds + next * STAGE, 0, 0);
                 }
+                multiply(s, s & 1);
+                spread<(LoadA::P::PITCH == S::KB ? 1 : 2) * S::MT + (LoadB::P::PITCH == S::KB ? 1 : 2) * S::NT, S::MT * S::NT>();
             }
-            issue(lds + to * STAGE);
-            const char* pa = lds + now * STAGE;
-            const char* pb = pa + A_BYTES;
-            typename Mma<T>::v8 ra[S::MT], rb[S::NT];
-#pragma unroll
-            for (int s = 0; s < S::KB / 32; ++s) {
-#pragma unroll
-                for (int j = 0; j < S::NT; ++j) rb[j] = read_b(pb, j, s);
-#pragma unroll
-                for (int i = 0; i < S::MT; ++i) ra[i] = read_a(pa, i, s);
-#pragma unroll
-                for (int i = 0; i < S::MT; ++i)
-#pragma unroll
-                    for (int j = 0; j < S::NT; ++j) {
-                        if constexpr (FOUR) acc[i][j] = Mma<T>::mma(ra[i], rb[j], acc[i][j], s, sa[i], sb[j]);
-                        else acc[i][j] = Mma<T>::mma(ra[i], rb[j], acc[i][j]);
-                    }
-            }
-            now = now == S::STAGES - 1 ? 0 : now + 1;
+            now = next;
         }
         wait_loads();  // what was loaded past the end lands before LDS is used again
     }
