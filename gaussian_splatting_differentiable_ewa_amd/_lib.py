@@ -43,7 +43,8 @@ EXPORTS = (
     "gs_block_summary", "gs_block_select", "gs_block_attn_fwd", "gs_block_attn_fwd_workspace_bytes",
     "gs_block_attn_bwd", "gs_block_attn_bwd_workspace_bytes",
     "gs_layer_norm_fwd", "gs_layer_norm_bwd", "gs_layer_norm_bwd_workspace_bytes",
-    "gs_gated_ff_fwd", "gs_gated_ff_fwd_workspace_bytes", "gs_gated_ff_bwd", "gs_gated_ff_bwd_workspace_bytes",
+    "gs_gated_ff_fwd", "gs_gated_ff_kept_bytes", "gs_gated_ff_fwd_workspace_bytes", "gs_gated_ff_bwd",
+    "gs_gated_ff_bwd_workspace_bytes",
     "gs_quantise_fp4", "gs_dequantise_fp4", "gs_linear_fp4", "gs_linear_fp4_workspace_bytes",
 )
 GS_F32, GS_F16, GS_BF16 = range(3)
@@ -154,6 +155,7 @@ def lib():
             "gs_layer_norm_fwd": ([_P, _P, _P, _P, _P, _I64, _I32, _F32, _I32, _P], ctypes.c_int),
             "gs_layer_norm_bwd_workspace_bytes": ([_I64, _I32], _SZ),
             "gs_layer_norm_bwd": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _P, _SZ, _P], ctypes.c_int),
+            "gs_gated_ff_kept_bytes": ([_I64, _I32, _I32], _SZ),
             "gs_gated_ff_fwd_workspace_bytes": ([_I64, _I32, _I32, _I32], _SZ),
             "gs_gated_ff_fwd": ([_P, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _SZ, _P],
                                 ctypes.c_int),
@@ -552,7 +554,7 @@ def gs_rope_axes(q, k, q_out, k_out, pos, freq, pairs, interleaved=False, invers
 
 
 def gs_norm_gate_fwd(x, f, gate, w_post, w_pre, y, h, stats, rows_per_gate, scale=1.0, eps=1e-6, stream=None):
-    """x, f, y, h [rows][channels] contiguous; f, gate, w_post, w_pre may be None."""
+    """x, f, y, h [rows][channels] contiguous; f, gate, w_post, w_kept may be None."""
     rows, c = x.shape
     _check(_at(x).gs_norm_gate_fwd(_ptr(x), _ptr(f), _ptr(gate), _ptr(w_post), _ptr(w_pre), _ptr(y), _ptr(h), _ptr(stats),
                                   rows, c, rows_per_gate, scale, eps, dtype_of(x), _current(x, stream)), "gs_norm_gate_fwd")
@@ -645,15 +647,19 @@ def gs_layer_norm_bwd(gy, x, w, stats, gx, gw, gb, ws, stream=None):
                                     dtype_of(x), *_ws(ws), _current(x, stream)), "gs_layer_norm_bwd")
 
 
+def gated_ff_kept_bytes(rows: int, hidden: int, dtype: int) -> int:
+    return lib().gs_gated_ff_kept_bytes(rows, hidden, dtype)
+
+
 def gated_ff_fwd_workspace_bytes(rows: int, channels: int, hidden: int, channels_out: int) -> int:
     return lib().gs_gated_ff_fwd_workspace_bytes(rows, channels, hidden, channels_out)
 
 
-def gs_gated_ff_fwd(x, w_gate, w_up, w_down, act, h, pre, y, ws=None, stream=None):
-    """x, w_gate, w_up, w_down any row stride of 8 elements; pre may be None."""
+def gs_gated_ff_fwd(x, w_gate, w_up, w_down, act, h, kept, y, ws=None, stream=None):
+    """x, w_gate, w_up, w_down any row stride of 8 elements; kept may be None."""
     rows, c = x.shape
     _check(_at(x).gs_gated_ff_fwd(_mat(x), _mat(w_gate), _mat(w_up), _mat(w_down), rows, c, w_gate.shape[0],
-                                  w_down.shape[0], act, dtype_of(x), _ptr(h), _ptr(pre), _ptr(y), *_ws(ws),
+                                  w_down.shape[0], act, dtype_of(x), _ptr(h), _ptr(kept), _ptr(y), *_ws(ws),
                                   _current(x, stream)), "gs_gated_ff_fwd")
 
 
@@ -661,10 +667,10 @@ def gated_ff_bwd_workspace_bytes(rows: int, channels: int, hidden: int, channels
     return lib().gs_gated_ff_bwd_workspace_bytes(rows, channels, hidden, channels_out)
 
 
-def gs_gated_ff_bwd(gy, x, w_gate, w_up, w_down, h, pre, act, gx, gw_gate, gw_up, gw_down, ws, stream=None):
+def gs_gated_ff_bwd(gy, x, w_gate, w_up, w_down, h, kept, act, gx, gw_gate, gw_up, gw_down, ws, stream=None):
     """gx, gw_gate with gw_up, and gw_down may be None."""
     rows, c = x.shape
-    _check(_at(x).gs_gated_ff_bwd(_mat(gy), _mat(x), _mat(w_gate), _mat(w_up), _mat(w_down), _ptr(h), _ptr(pre), rows, c,
+    _check(_at(x).gs_gated_ff_bwd(_mat(gy), _mat(x), _mat(w_gate), _mat(w_up), _mat(w_down), _ptr(h), _ptr(kept), rows, c,
                                   w_gate.shape[0], w_down.shape[0], act, dtype_of(x), _ptr(gx), _ptr(gw_gate), _ptr(gw_up),
                                   _ptr(gw_down), *_ws(ws), _current(x, stream)), "gs_gated_ff_bwd")
 

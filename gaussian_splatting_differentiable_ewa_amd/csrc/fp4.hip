@@ -133,17 +133,37 @@ __device__ __forceinline__ void four_product(char* __restrict__ lds, const FourA
     const int64_t m0 = (int64_t)mi * S::BM, n0 = (int64_t)ni * S::BN;
     acc16 acc[S::MT][S::NT];
     TileProduct<fp4, S, false, false, false>::run(lds, p.a, p.b, m0, n0, p.walk, wave, acc);
-    const int64_t row0 = m0 + wave / S::WN * (S::BM / S::WM), col0 = n0 + wave % S::WN * (S::BN / S::WN) + (lane & 31);
+    // out through a scratch of the wave's own: whole rows, or where those do not lie on 16 bytes their elements
+    using Tiles = TileProduct<fp4, S, false, false, false>;
+    constexpr int SIZE = sizeof(T), PER = SIZE == 2 && S::NT > 1 ? 2 : 1, W = 32 * SIZE * PER;  // matrix tiles to a row of scratch
+    static_assert(S::NT % PER == 0 && Tiles::LDS / S::WAVES >= 32 * W, "a wave's scratch");
+    const Rows<W> at{lds + wave * (Tiles::LDS / S::WAVES)};
+    const int64_t col0 = n0 + wave % S::WN * (S::BN / S::WN);
+    const bool whole = p.n * SIZE % 16 == 0 && ((uintptr_t)p.y & 15) == 0;
 #pragma unroll
-    for (int i = 0; i < S::MT; ++i)
+    for (int i = 0; i < S::MT; ++i) {
+        const int64_t row0 = m0 + wave / S::WN * (S::BM / S::WM) + 32 * i;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int64_t row = row0 + 32 * i + c_row(r, hi);
-            if (row >= p.m) continue;
+        for (int j = 0; j < S::NT; j += PER) {
+            wait_lds();
 #pragma unroll
-            for (int j = 0; j < S::NT; ++j)
-                if (col0 + 32 * j < p.n) ((T*)p.y)[row * p.n + col0 + 32 * j] = (T)acc[i][j][r];
+            for (int q = 0; q < PER; ++q)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    struct alignas(4 * SIZE) {
+                        T v[4];
+                    } t;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) t.v[e] = (T)acc[i][j + q][4 * r + e];
+                    at.put((32 * q + 8 * r + 4 * hi) * SIZE, t);
+                }
+            wait_lds();
+            const int64_t col = col0 + 32 * j;
+            char* to = (char*)((T*)p.y + row0 * p.n + col);
+            if (whole) at.store(to, p.n * SIZE, p.m - row0, (p.n - col) * SIZE);
+            else at.template store_as<std::conditional_t<SIZE == 2, uint16_t, uint32_t>>(to, p.n * SIZE, p.m - row0, (p.n - col) * SIZE, 0);
         }
+    }
 }
 
 template <typename T, typename S>

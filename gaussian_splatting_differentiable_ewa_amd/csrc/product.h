@@ -10,8 +10,9 @@
 // and this one is free.
 //
 // Matrix tile: 32 x 32, 32 bytes of k a step. Lane l holds 16 bytes of k, half
-// l >> 5, of row l & 31 of either operand; of C column l & 31, rows
-// 8 (i >> 2) + 4 (l >> 5) + (i & 3) for registers i = 0..15.
+// l >> 5, of row l & 31 of either operand. B goes first into the instruction, so
+// that of C a lane holds row l & 31, columns 8 (i >> 2) + 4 (l >> 5) + (i & 3)
+// for registers i = 0..15: four neighbours at a time.
 //
 // 4-bit elements take 8 to the place of two 16-bit ones: sizes of k below are in
 // units of 2 bytes. A step then covers 64 of them, and a lane's 16 bytes are one
@@ -58,7 +59,7 @@ struct Panel {
     static constexpr int PITCH = TR ? ROWS * 2 : KB, CHUNKS = PITCH / 16;
     static __device__ __forceinline__ int swizzle(int r)
     {
-        if constexpr (!TR) return KB == 64 ? (r >> 2) & 3 : (r >> 1) & 7;
+        if constexpr (!TR) return KB == 32 ? (r >> 3) & 1 : (KB == 64 ? (r >> 2) & 3 : (r >> 1) & 7);
         else if constexpr (ROWS >= 128) return ((r & 3) << 2) | ((r >> 2) & 3);
         else return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
     }
@@ -311,8 +312,8 @@ struct TileProduct {
             for (int i = 0; i < S::MT; ++i)
 #pragma unroll
                 for (int j = 0; j < S::NT; ++j) {
-                    if constexpr (FOUR) acc[i][j] = Mma<T>::mma(ra[from][i], rb[from][j], acc[i][j], step, sa[i], sb[j]);
-                    else acc[i][j] = Mma<T>::mma(ra[from][i], rb[from][j], acc[i][j]);
+                    if constexpr (FOUR) acc[i][j] = Mma<T>::mma(rb[from][j], ra[from][i], acc[i][j], step, sb[j], sa[i]);
+                    else acc[i][j] = Mma<T>::mma(rb[from][j], ra[from][i], acc[i][j]);
                 }
         };
 #pragma unroll
@@ -332,9 +333,9 @@ struct TileProduct {
             if constexpr (FOUR) {
                 const int blocks = (int)(w.k - (int64_t)t * KE) / 8;
 #pragma unroll
-                for (int i = 0; i < S::MT; ++i) sa[i] = Scales<S::MT>::mine(next_sa[i], blocks);
+                for (int i = 0; i < S::MT; ++i) sa[i] = blocks < 8 ? Scales<S::MT>::mine(next_sa[i], blocks) : next_sa[i];
 #pragma unroll
-                for (int j = 0; j < S::NT; ++j) sb[j] = Scales<S::NT>::mine(next_sb[j], blocks);
+                for (int j = 0; j < S::NT; ++j) sb[j] = blocks < 8 ? Scales<S::NT>::mine(next_sb[j], blocks) : next_sb[j];
                 scale_a.load(t + 1, next_sa);  // past the row's end: not used
                 scale_b.load(t + 1, next_sb);
             }
@@ -352,9 +353,90 @@ struct TileProduct {
             }
             now = next;
         }
-        wait_loads();  // what was loaded past the end lands before LDS is used again
+        // what was loaded past the end has landed and all reads are done: LDS is free
+        ready(std::integral_constant<int, 0>{});
     }
 };
+
+// A wave's scratch in LDS for 32 rows of W bytes (32, 64 or 128), in chunks of 16
+// swizzled as a panel's: rows of C are written four columns at a time and leave
+// as whole rows, 16 bytes a lane (without it a store would hold 16 bytes of each
+// of 32 rows).
+template <int W>
+struct Rows {
+    char* p;
+    static __device__ __forceinline__ int at(int row, int byte)
+    {
+        return row * W + (((byte >> 4) ^ Panel<32, W, false>::swizzle(row)) << 4) + (byte & 15);
+    }
+    // This lane's row (l & 31), at a byte of it.
+    template <typename V>
+    __device__ __forceinline__ void put(int byte, const V& v) const
+    {
+        *(V*)(p + at(lane_id() & 31, byte)) = v;
+    }
+    template <typename V>
+    __device__ __forceinline__ V get(int byte) const
+    {
+        return *(const V*)(p + at(lane_id() & 31, byte));
+    }
+    // Rows first .. rows - 1 to memory, V at a time, `bytes` of each (a multiple of V's).
+    template <typename V>
+    __device__ __forceinline__ void store_as(char* to, int64_t ld, int64_t rows, int64_t bytes, int64_t first) const
+    {
+        constexpr int N = W / sizeof(V);
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) {
+            const int row = (k * 64 + lane_id()) / N, byte = (lane_id() % N) * sizeof(V);
+            const V v = *(const V*)(p + at(row, byte));
+            if (row >= first && row < rows && byte < bytes) *(V*)(to + row * ld + byte) = v;
+        }
+    }
+    __device__ __forceinline__ void store(char* to, int64_t ld, int64_t rows, int64_t bytes, int64_t first = 0) const
+    {
+        store_as<uint4>(to, ld, rows, bytes, first);
+    }
+    // The same from memory, all reads before the first is used.
+    template <typename V>
+    __device__ __forceinline__ void load_as(const char* from, int64_t ld, int64_t rows, int64_t bytes) const
+    {
+        constexpr int N = W / sizeof(V);
+        V v[N / 2];
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) {
+            const int row = (k * 64 + lane_id()) / N, byte = (lane_id() % N) * sizeof(V);
+            v[k] = V{};
+            if (row < rows && byte < bytes) v[k] = *(const V*)(from + row * ld + byte);
+        }
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) {
+            const int row = (k * 64 + lane_id()) / N, byte = (lane_id() % N) * sizeof(V);
+            *(V*)(p + at(row, byte)) = v[k];
+        }
+    }
+    __device__ __forceinline__ void load(const char* from, int64_t ld, int64_t rows, int64_t bytes) const
+    {
+        load_as<uint4>(from, ld, rows, bytes);
+    }
+    // Rows of a multiple of 8 bytes.
+    __device__ __forceinline__ void store8(char* to, int64_t ld, int64_t rows, int64_t bytes) const
+    {
+        store_as<uint2>(to, ld, rows, bytes, 0);
+    }
+    __device__ __forceinline__ void load8(const char* from, int64_t ld, int64_t rows, int64_t bytes) const
+    {
+        load_as<uint2>(from, ld, rows, bytes);
+    }
+};
+
+// Waits for this wave's LDS accesses (its lanes exchange values through a
+// scratch of its own, without a barrier).
+__device__ __forceinline__ void wait_lds()
+{
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0), the other counters as they are
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+}
 
 // Workgroup -> tile: each XCD takes a contiguous range, in which 8 row tiles by
 // all column tiles come first, so that what runs at once shares rows of both

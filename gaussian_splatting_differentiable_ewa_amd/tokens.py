@@ -229,12 +229,12 @@ def _ff_args(x, w_gate, w_up, w_down, act):
 def _gated_ff(x, w_gate, w_up, w_down, act, keep):
     rows, c, f, co = _ff_args(x, w_gate, w_up, w_down, act)
     h = torch.empty(rows, f, dtype=x.dtype, device=x.device)
-    pre = torch.empty(rows, 2 * f, dtype=torch.float32, device=x.device) if keep else None
+    kept = torch.empty(L.gated_ff_kept_bytes(rows, f, L.dtype_of(x)), dtype=torch.uint8, device=x.device) if keep else None
     y = torch.empty(rows, co, dtype=x.dtype, device=x.device)
     need = L.gated_ff_fwd_workspace_bytes(rows, c, f, co)
     ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-    L.gs_gated_ff_fwd(_on16(x), _on16(w_gate), _on16(w_up), _on16(w_down), ACTS[act], h, pre, y, ws)
-    return y, h, pre
+    L.gs_gated_ff_fwd(_on16(x), _on16(w_gate), _on16(w_up), _on16(w_down), ACTS[act], h, kept, y, ws)
+    return y, h, kept
 
 
 def gated_ff(x, w_gate, w_up, w_down, act: str = "silu"):
@@ -245,24 +245,24 @@ def gated_ff(x, w_gate, w_up, w_down, act: str = "silu"):
 
 
 def gated_ff_train(x, w_gate, w_up, w_down, act: str = "silu"):
-    """(y, h, pre): gated_ff and what its backward pass takes, the hidden layer
-    and both projections (fp32 [rows, 2 hidden])."""
+    """(y, h, kept): gated_ff and what its backward pass takes, the hidden layer
+    and both projections (in gs_gated_ff_kept_bytes of the kernels' own layout)."""
     return _gated_ff(x, w_gate, w_up, w_down, act, True)
 
 
-def gated_ff_backward(gy, x, w_gate, w_up, w_down, h, pre, act: str = "silu"):
+def gated_ff_backward(gy, x, w_gate, w_up, w_down, h, kept, act: str = "silu"):
     """(gx, gw_gate, gw_up, gw_down); in fp16 the projections' gradients have to
     fit the type. See gs_gated_ff_bwd."""
     rows, c, f, co = _ff_args(x, w_gate, w_up, w_down, act)
     _rows("gy", gy, co, x)
     _need(gy.shape[0] == rows, "gy must have x's rows")
     _vector("h", h, (rows, f), x, x.dtype)
-    _vector("pre", pre, (rows, 2 * f), x)
+    _vector("kept", kept, (L.gated_ff_kept_bytes(rows, f, L.dtype_of(x)),), x, torch.uint8)
     if gy.requires_grad:
         _lost("GatedFF")
     grads = [torch.empty(s, dtype=x.dtype, device=x.device) for s in ((rows, c), (f, c), (f, c), (co, f))]
     ws = torch.empty(L.gated_ff_bwd_workspace_bytes(rows, c, f, co), dtype=torch.uint8, device=x.device)
-    L.gs_gated_ff_bwd(_on16(gy), _on16(x), _on16(w_gate), _on16(w_up), _on16(w_down), h, pre, ACTS[act], *grads, ws)
+    L.gs_gated_ff_bwd(_on16(gy), _on16(x), _on16(w_gate), _on16(w_up), _on16(w_down), h, kept, ACTS[act], *grads, ws)
     return tuple(grads)
 
 
@@ -494,8 +494,8 @@ class GatedFF(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, w_gate, w_up, w_down, act="silu"):
-        y, h, pre = gated_ff_train(x, w_gate, w_up, w_down, act)
-        ctx.save_for_backward(x, w_gate, w_up, w_down, h, pre)
+        y, h, kept = gated_ff_train(x, w_gate, w_up, w_down, act)
+        ctx.save_for_backward(x, w_gate, w_up, w_down, h, kept)
         ctx.act = act
         return y
 

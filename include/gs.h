@@ -939,6 +939,10 @@ gs_status gs_layer_norm_bwd(const gs_matrix* gy, const gs_matrix* x, const float
 
 typedef enum gs_act { GS_SILU = 0, GS_GELU = 1 } gs_act;
 
+/* What gs_gated_ff_fwd keeps of g and u for the backward pass (bytes): 5 an
+ * element of the hidden layer with GS_BF16, 6 with GS_F16; 0 on invalid sizes. */
+size_t gs_gated_ff_kept_bytes(int64_t rows, int32_t hidden, int32_t dtype);
+
 /* Workspace of gs_gated_ff_fwd (bytes); may be 0. */
 size_t gs_gated_ff_fwd_workspace_bytes(int64_t rows, int32_t channels, int32_t hidden, int32_t channels_out);
 
@@ -948,10 +952,12 @@ size_t gs_gated_ff_fwd_workspace_bytes(int64_t rows, int32_t channels, int32_t h
  * with act(g) = g / (1 + exp(-g)) (GS_SILU) or g times the normal distribution
  * function (GS_GELU). Sums are fp32; h is rounded to the inputs' type for its
  * product.
- *   x        [rows][channels], GS_F16 or GS_BF16 as everything but pre
+ *   x        [rows][channels], GS_F16 or GS_BF16 as everything but kept
  *   w_gate, w_up  [hidden][channels];  w_down  [channels_out][hidden]
  *   h        out [rows][hidden] (for the backward pass, or scratch)
- *   pre      out fp32 [rows][2 hidden], g and u (for the backward pass), or NULL
+ *   kept     out, gs_gated_ff_kept_bytes(...): g and u (for the backward pass), 12
+ *            significant bits of each with GS_BF16, 16 with GS_F16, in fp32's
+ *            range; or NULL
  *   y        out [rows][channels_out]; h and y are contiguous
  *   ws       workspace of gs_gated_ff_fwd_workspace_bytes(...), or NULL if that is 0
  * Errors: null pointers, sizes that are not multiples of 8 or outside 8..2^17,
@@ -961,7 +967,7 @@ size_t gs_gated_ff_fwd_workspace_bytes(int64_t rows, int32_t channels, int32_t h
  */
 gs_status gs_gated_ff_fwd(const gs_matrix* x, const gs_matrix* w_gate, const gs_matrix* w_up, const gs_matrix* w_down,
                           int64_t rows, int32_t channels, int32_t hidden, int32_t channels_out, int32_t act, int32_t dtype,
-                          void* h, float* pre, void* y, void* ws, size_t ws_bytes, void* stream);
+                          void* h, void* kept, void* y, void* ws, size_t ws_bytes, void* stream);
 
 /* Workspace of gs_gated_ff_bwd (bytes); 0 on invalid sizes. */
 size_t gs_gated_ff_bwd_workspace_bytes(int64_t rows, int32_t channels, int32_t hidden, int32_t channels_out);
@@ -970,7 +976,7 @@ size_t gs_gated_ff_bwd_workspace_bytes(int64_t rows, int32_t channels, int32_t h
  * gs_gated_ff_bwd -- gradients of gs_gated_ff_fwd from that of y:
  *   gh = gy w_down,  gg = gh u act'(g),  gu = gh act(g)
  *   gx = gg w_gate + gu w_up,  gw_gate = gg^T x,  gw_up = gu^T x,  gw_down = gy^T h
- *   h, pre   as the forward call wrote them
+ *   h, kept  as the forward call wrote them
  *   gx, gw_gate, gw_up, gw_down  out, contiguous, the inputs' type; each may be
  *            NULL (not wanted), gw_gate and gw_up together; the weights' are
  *            zeros when there are no rows
@@ -981,7 +987,7 @@ size_t gs_gated_ff_bwd_workspace_bytes(int64_t rows, int32_t channels, int32_t h
  * Errors: as gs_gated_ff_fwd.
  */
 gs_status gs_gated_ff_bwd(const gs_matrix* gy, const gs_matrix* x, const gs_matrix* w_gate, const gs_matrix* w_up,
-                          const gs_matrix* w_down, const void* h, const float* pre, int64_t rows, int32_t channels,
+                          const gs_matrix* w_down, const void* h, const void* kept, int64_t rows, int32_t channels,
                           int32_t hidden, int32_t channels_out, int32_t act, int32_t dtype, void* gx, void* gw_gate,
                           void* gw_up, void* gw_down, void* ws, size_t ws_bytes, void* stream);
 

@@ -73,6 +73,9 @@ def gated_ff(x, w_gate, w_up, w_down, act, gy=None):
     if gy is None:
         return [(y, 1.01 * dy)]
     gy = gy.double()
+    # the backward pass's g and u are rounded to 12 or 16 significant bits
+    cut = {torch.float16: 2.0 ** -16, torch.bfloat16: 2.0 ** -12}[kind]
+    dg, du = dg + cut * g.abs(), du + cut * u.abs()
     gh, dgh = gy @ w_down, chain(co) * (gy.abs() @ w_down.abs())
     gg, gu = gh * u * da, gh * a
     dgg = dgh * (u * da).abs() + gh.abs() * (du * da.abs() + u.abs() * (0.8 * dg + off_d)) + u8 * gg.abs() + tiny

@@ -51,17 +51,19 @@ def test_layer_norm_refusals(lib):
 
 def test_gated_ff_refusals(lib):
     fwd = dict(x=mat(), wg=mat(), wu=mat(), wd=mat(), rows=10, c=64, hid=128, co=64, act=L.GS_SILU, t=L.GS_BF16, h=FAKE,
-               pre=FAKE, y=FAKE, ws=FAKE, wsb=1 << 40, s=None)
+               kept=FAKE, y=FAKE, ws=FAKE, wsb=1 << 40, s=None)
     need = L.gated_ff_bwd_workspace_bytes(10, 64, 128, 64)
     assert need > 0 and L.gated_ff_bwd_workspace_bytes(10, 64, 12, 64) == 0
+    assert L.gated_ff_kept_bytes(10, 128, L.GS_BF16) == 6400 and L.gated_ff_kept_bytes(10, 128, L.GS_F16) == 7680
+    assert L.gated_ff_kept_bytes(10, 128, L.GS_F32) == 0 and L.gated_ff_kept_bytes(10, 12, L.GS_F16) == 0
     assert L.gated_ff_fwd_workspace_bytes(-1, 64, 128, 64) == 0
-    bwd = dict(gy=mat(), x=mat(), wg=mat(), wu=mat(), wd=mat(), h=FAKE, pre=FAKE, rows=10, c=64, hid=128, co=64, act=L.GS_SILU,
+    bwd = dict(gy=mat(), x=mat(), wg=mat(), wu=mat(), wd=mat(), h=FAKE, kept=FAKE, rows=10, c=64, hid=128, co=64, act=L.GS_SILU,
                t=L.GS_BF16, gx=FAKE, gwg=FAKE, gwu=FAKE, gwd=FAKE, ws=FAKE, wsb=need, s=None)
     both = (dict(x=None), dict(wg=None), dict(wu=None), dict(wd=None), dict(x=mat(0)), dict(wd=mat(0)), dict(h=None),
             dict(rows=-1), dict(rows=(1 << 24) + 1), dict(c=0), dict(c=60), dict(hid=4), dict(hid=-8), dict(co=12),
             dict(c=(1 << 17) + 8), dict(hid=1 << 18), dict(act=2), dict(act=-1), dict(t=3))
     odd = (dict(t=L.GS_F32), dict(x=mat(4104)), dict(wg=mat(stride=1028)), dict(wu=mat(stride=-8)), dict(wd=mat(stride=1 << 21)),
-           dict(h=ctypes.c_void_p(4104)), dict(rows=1 << 24, hid=1 << 17))
+           dict(h=ctypes.c_void_p(4104)), dict(kept=ctypes.c_void_p(4104)), dict(rows=1 << 24, hid=1 << 17))
     for f, ok in ((lib.gs_gated_ff_fwd, fwd), (lib.gs_gated_ff_bwd, bwd)):
         big = {"wsb": 1 << 60} if ok is bwd else {}
         for bad in both:
@@ -75,7 +77,7 @@ def test_gated_ff_refusals(lib):
         assert call(lib.gs_gated_ff_fwd, fwd, **bad) == INV, bad
     assert call(lib.gs_gated_ff_fwd, fwd, y=ctypes.c_void_p(4104)) == UNS
     assert call(lib.gs_gated_ff_fwd, fwd, rows=0, x=None) == OK
-    for bad in (dict(gy=None), dict(pre=None), dict(gwg=None), dict(gwu=None), dict(ws=None), dict(wsb=need - 1),
+    for bad in (dict(gy=None), dict(kept=None), dict(gwg=None), dict(gwu=None), dict(ws=None), dict(wsb=need - 1),
                 dict(ws=ctypes.c_void_p(4100))):
         assert call(lib.gs_gated_ff_bwd, bwd, **bad) == INV, bad
     assert call(lib.gs_gated_ff_bwd, bwd, gx=ctypes.c_void_p(4104)) == UNS

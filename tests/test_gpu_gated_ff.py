@@ -43,13 +43,13 @@ def test_both_ways(dtype, act, rows, c, f, co):
     g = gen(rows + c)
     x, wg, wu, wd, gy = case(g, rows, c, f, co, dtype)
     want = O.gated_ff(x, wg, wu, wd, act, gy)
-    y, h, pre = T.gated_ff_train(x, wg, wu, wd, act)
-    got = [y, *T.gated_ff_backward(gy, x, wg, wu, wd, h, pre, act)]
+    y, h, kept = T.gated_ff_train(x, wg, wu, wd, act)
+    got = [y, *T.gated_ff_backward(gy, x, wg, wu, wd, h, kept, act)]
     for name, p, (w, bound) in zip(NAMES, got, want):
         assert p.dtype is dtype
         O.within(p, w, bound, name)
     assert torch.equal(T.gated_ff(x, wg, wu, wd, act), y)
-    again = T.gated_ff_backward(gy, x, wg, wu, wd, h, pre, act)
+    again = T.gated_ff_backward(gy, x, wg, wu, wd, h, kept, act)
     assert all(torch.equal(p, r) for p, r in zip(got[1:], again))
 
 
@@ -86,20 +86,20 @@ def test_strides_and_alignment():
         x, gy = wide[:, first: first + c], wide[:, first + c: first + 2 * c]
         wg, wu = packed[:f, first: first + c], packed[f:, first: first + c]
         wd = down.t().contiguous().t() if first == 3 else down
-        y, h, pre = T.gated_ff_train(x, wg, wu, wd)
-        grads = T.gated_ff_backward(gy, x, wg, wu, wd, h, pre)
+        y, h, kept = T.gated_ff_train(x, wg, wu, wd)
+        grads = T.gated_ff_backward(gy, x, wg, wu, wd, h, kept)
         same = [t.contiguous() for t in (x, wg, wu, wd)]
-        y2, h2, pre2 = T.gated_ff_train(*same)
-        assert torch.equal(y, y2) and torch.equal(h, h2) and torch.equal(pre, pre2)
-        for p, r in zip(grads, T.gated_ff_backward(gy.contiguous(), *same, h2, pre2)):
+        y2, h2, kept2 = T.gated_ff_train(*same)
+        assert torch.equal(y, y2) and torch.equal(h, h2) and torch.equal(kept, kept2)
+        for p, r in zip(grads, T.gated_ff_backward(gy.contiguous(), *same, h2, kept2)):
             assert torch.equal(p, r)
     # one row for all (a row stride of zero), as x and as the gradient of a sum
     one = wide[:1, :c].expand(rows, c)
-    y, h, pre = T.gated_ff_train(one, *same[1:])
-    y2, h2, pre2 = T.gated_ff_train(one.contiguous(), *same[1:])
+    y, h, kept = T.gated_ff_train(one, *same[1:])
+    y2, h2, kept2 = T.gated_ff_train(one.contiguous(), *same[1:])
     assert torch.equal(y, y2)
-    for p, r in zip(T.gated_ff_backward(one, one, *same[1:], h, pre),
-                    T.gated_ff_backward(one.contiguous(), one.contiguous(), *same[1:], h2, pre2)):
+    for p, r in zip(T.gated_ff_backward(one, one, *same[1:], h, kept),
+                    T.gated_ff_backward(one.contiguous(), one.contiguous(), *same[1:], h2, kept2)):
         assert torch.equal(p, r)
 
 
@@ -116,17 +116,17 @@ def test_what_is_not_finite_stays_in_its_row(rows):
     wg2 = torch.full((f + 1, c + 8), float("nan"), device=DEV, dtype=BF16)
     wg2[:f, :c] = wg
     clean = T.gated_ff_train(x0, wg, wu, wd)
-    y, h, pre = T.gated_ff_train(x, wg2[:f, :c], wu, wd)
+    y, h, kept = T.gated_ff_train(x, wg2[:f, :c], wu, wd)
     assert torch.equal(y, clean[0])
-    gx = T.gated_ff_backward(gy, x, wg2[:f, :c], wu, wd, h, pre)[0]
+    gx = T.gated_ff_backward(gy, x, wg2[:f, :c], wu, wd, h, kept)[0]
     x[1, 3], x[3, 5] = float("nan"), float("inf")
-    y2, h2, pre2 = T.gated_ff_train(x, wg2[:f, :c], wu, wd)
+    y2, h2, kept2 = T.gated_ff_train(x, wg2[:f, :c], wu, wd)
     ok = torch.ones(rows, dtype=torch.bool, device=DEV)
     ok[[1, 3]] = False
     assert torch.equal(y2[ok], y[ok]) and torch.isnan(y2[1]).all() and not torch.isfinite(y2[3]).any()
     gy2 = gy.clone()
     gy2[4] = float("nan")
-    gx2 = T.gated_ff_backward(gy2, x, wg2[:f, :c], wu, wd, h2, pre2)[0]
+    gx2 = T.gated_ff_backward(gy2, x, wg2[:f, :c], wu, wd, h2, kept2)[0]
     ok[4] = False
     assert torch.equal(gx2[ok], gx[ok]) and torch.isnan(gx2[4]).all()
 
@@ -134,16 +134,16 @@ def test_what_is_not_finite_stays_in_its_row(rows):
 def test_no_rows_and_partial_gradients():
     g = gen(6)
     x, wg, wu, wd, gy = case(g, 0, 64, 96, 40, BF16)
-    y, h, pre = T.gated_ff_train(x, wg, wu, wd)
-    grads = T.gated_ff_backward(gy, x, wg, wu, wd, h, pre)
+    y, h, kept = T.gated_ff_train(x, wg, wu, wd)
+    grads = T.gated_ff_backward(gy, x, wg, wu, wd, h, kept)
     assert y.shape == (0, 40) and grads[0].shape == (0, 64) and not any(t.any() for t in grads[1:])
     x, wg, wu, wd, gy = case(g, 50, 64, 96, 40, BF16)
-    y, h, pre = T.gated_ff_train(x, wg, wu, wd)
-    want = T.gated_ff_backward(gy, x, wg, wu, wd, h, pre)
+    y, h, kept = T.gated_ff_train(x, wg, wu, wd)
+    want = T.gated_ff_backward(gy, x, wg, wu, wd, h, kept)
     ws = torch.empty(L.gated_ff_bwd_workspace_bytes(50, 64, 96, 40), dtype=torch.uint8, device=DEV)
     for keep in ((0,), (1, 2), (3,)):
         got = [torch.full_like(t, 7.0) if n in keep else None for n, t in enumerate(want)]
-        L.gs_gated_ff_bwd(gy, x, wg, wu, wd, h, pre, L.GS_SILU, *got, ws)
+        L.gs_gated_ff_bwd(gy, x, wg, wu, wd, h, kept, L.GS_SILU, *got, ws)
         assert all(torch.equal(got[n], want[n]) for n in keep)
 
 
@@ -152,10 +152,10 @@ def test_large_values():
     eye = torch.eye(8, device=DEV, dtype=BF16)
     x = torch.tensor([[-3e38, -1e4, -200.0, -90.0, 90.0, 200.0, 1e4, 1e18]], device=DEV).to(BF16)
     for act in ("silu", "gelu"):
-        y, h, pre = T.gated_ff_train(x, eye, torch.full_like(eye, 0.0) + eye * 0.5, eye, act)
+        y, h, kept = T.gated_ff_train(x, eye, torch.full_like(eye, 0.0) + eye * 0.5, eye, act)
         want = torch.where(x < 0, 0.0, x.float() ** 2 / 2).to(BF16)
         assert torch.equal(y.abs(), want), act
-        gx, *_ = T.gated_ff_backward(torch.ones_like(x), x, eye, eye * 0.5, eye, h, pre, act)
+        gx, *_ = T.gated_ff_backward(torch.ones_like(x), x, eye, eye * 0.5, eye, h, kept, act)
         assert torch.equal(gx.abs(), torch.where(x < 0, 0.0, x.float()).to(BF16)), act
 
 
@@ -166,8 +166,8 @@ def test_replays_equal_eager_calls():
         return list(case(gen(seed), 300, 136, 264, 72, BF16))
 
     def run(x, wg, wu, wd, gy):
-        y, h, pre = T.gated_ff_train(x, wg, wu, wd, "gelu")
-        return [y, h, pre, *T.gated_ff_backward(gy, x, wg, wu, wd, h, pre, "gelu"), T.gated_ff(x[:1], wg, wu, wd)]
+        y, h, kept = T.gated_ff_train(x, wg, wu, wd, "gelu")
+        return [y, h, kept, *T.gated_ff_backward(gy, x, wg, wu, wd, h, kept, "gelu"), T.gated_ff(x[:1], wg, wu, wd)]
 
     held = inputs(0)
     side = torch.cuda.Stream()
