@@ -328,10 +328,8 @@ __global__ __launch_bounds__(256) void k_ff_join(const Target o, int32_t splits)
     }
 }
 
-// Operands along k and few tiles' worth of waiting behind a product (two
-// workgroups a CU), otherwise the largest tile, and few tiles.
+// Many tiles, and few.
 using Wide = TileShape<256, 256, 2, 4, 128, 2>;
-using Twice = TileShape<192, 128, 2, 2, 128, 2>;
 using Small = TileShape<64, 128, 2, 2, 128, 3>;
 
 // How a product of m x n over k is cut.
@@ -360,7 +358,7 @@ static Cut cut_of(int64_t m, int64_t n, int64_t k, int segments, int to)
 {
     const int64_t wide = to == TO_GATED ? 2 * n : n;
     if (((m + 255) / 256) * ((wide + 255) / 256) < 128) return cut_as<Small>(false, m, wide, k, segments, 512);
-    return to == TO_STORE ? cut_as<Wide>(true, m, wide, k, segments, 256) : cut_as<Twice>(true, m, wide, k, segments, 512);
+    return cut_as<Wide>(true, m, wide, k, segments, 256);
 }
 
 static size_t part_bytes(const Cut& c, int64_t m, int64_t n, int to)
@@ -371,7 +369,6 @@ static size_t part_bytes(const Cut& c, int64_t m, int64_t n, int to)
 template <typename T, bool ATR, bool BTR, int TO, int ACT>
 static hipError_t product(const Operand& a, const Operand& b, Target o, int64_t k, int segments, float* part, hipStream_t s)
 {
-    using Large = std::conditional_t<TO == TO_STORE, Wide, Twice>;
     const Cut c = cut_of(o.m, o.n, k, segments, TO);
     ProductArgs p;
     p.a = a;
@@ -382,13 +379,13 @@ static hipError_t product(const Operand& a, const Operand& b, Target o, int64_t 
     p.mt = (uint32_t)c.mt;
     p.nt = (uint32_t)c.nt;
     p.per_split = c.per_split;
-    const dim3 grid((unsigned)(c.mt * c.nt * c.splits)), block((c.large ? Large::WAVES : Small::WAVES) * 64);
+    const dim3 grid((unsigned)(c.mt * c.nt * c.splits)), block((c.large ? Wide::WAVES : Small::WAVES) * 64);
     if (c.splits > 1) {
-        if (c.large) hipLaunchKernelGGL((k_ff_product<T, Large, ATR, BTR, TO, ACT, true>), grid, block, 0, s, p);
+        if (c.large) hipLaunchKernelGGL((k_ff_product<T, Wide, ATR, BTR, TO, ACT, true>), grid, block, 0, s, p);
         else hipLaunchKernelGGL((k_ff_product<T, Small, ATR, BTR, TO, ACT, true>), grid, block, 0, s, p);
         hipLaunchKernelGGL((k_ff_join<T, TO, ACT>), dim3(grid_for((uint64_t)(o.m * o.n / 4), 256)), dim3(256), 0, s, p.o, c.splits);
     } else {
-        if (c.large) hipLaunchKernelGGL((k_ff_product<T, Large, ATR, BTR, TO, ACT, false>), grid, block, 0, s, p);
+        if (c.large) hipLaunchKernelGGL((k_ff_product<T, Wide, ATR, BTR, TO, ACT, false>), grid, block, 0, s, p);
         else hipLaunchKernelGGL((k_ff_product<T, Small, ATR, BTR, TO, ACT, false>), grid, block, 0, s, p);
     }
     return hipGetLastError();
