@@ -121,8 +121,8 @@ struct FourArgs {
     uint32_t mt, nt;
 };
 
-using FourTile = TileShape<256, 256, 2, 4, 128, 2>;
-using FourSmall = TileShape<64, 64, 2, 2, 128, 3>;
+using FourTile = TileShape<256, 256, 2, 4, 64, 4>;
+using FourSmall = TileShape<64, 64, 2, 2, 64, 4>;
 
 template <typename T, typename S>
 __device__ __forceinline__ void four_product(char* __restrict__ lds, const FourArgs& p)
@@ -281,7 +281,7 @@ gs_status gs_linear_fp4(const gs_matrix* x, const gs_matrix* codes, const gs_mat
     FourArgs p{};
     p.a = {{xc, xs}, {channels / 2, scale_bytes_of(channels)}, rows};
     p.b = {{(const char*)codes->data, (const char*)scales->data}, {codes->stride, scales->stride}, out};
-    p.walk = {channels / 4, (channels + 255) / 256, 0, (channels + 255) / 256};
+    p.walk = {channels / 4, (channels + 127) / 128, 0, (channels + 127) / 128};
     p.y = y;
     p.m = rows;
     p.n = out;

@@ -252,7 +252,7 @@ __device__ __forceinline__ void finish(char* __restrict__ scratch, const Target&
     }
 }
 
-template <typename T, typename S, bool ATR, bool BTR, int TO, int ACT, bool PART>
+template <typename T, typename S, bool ATR, bool BTR, int TO, int ACT, bool PART, bool TWO>
 __device__ __forceinline__ void ff_product(char* __restrict__ lds, const ProductArgs& p)
 {
     constexpr bool PAIR = TO == TO_GATED;
@@ -265,18 +265,18 @@ __device__ __forceinline__ void ff_product(char* __restrict__ lds, const Product
     w.first = split * p.per_split;
     w.last = min(w.last, w.first + p.per_split);
     acc16 acc[S::MT][S::NT];
-    using Tiles = TileProduct<T, S, ATR, BTR, PAIR>;
+    using Tiles = TileProduct<T, S, ATR, BTR, PAIR, TWO>;
     Tiles::run(lds, p.a, p.b, m0, n0, w, wave, acc);
     static_assert(Tiles::LDS / S::WAVES >= 32 * 64 * 4 * 2, "a wave's scratch");
     finish<T, S, TO, ACT, PART>(lds + wave * (Tiles::LDS / S::WAVES), p.o, acc, m0 + wave / S::WN * (S::BM / S::WM),
                                 n0 + wave % S::WN * (S::BN / S::WN / (PAIR ? 2 : 1)), split);
 }
 
-template <typename T, typename S, bool ATR, bool BTR, int TO, int ACT, bool PART>
+template <typename T, typename S, bool ATR, bool BTR, int TO, int ACT, bool PART, bool TWO>
 __global__ __launch_bounds__(S::WAVES * 64, 2) void k_ff_product(const ProductArgs p)
 {
-    __shared__ alignas(16) char s_lds[TileProduct<T, S, ATR, BTR, TO == TO_GATED>::LDS];
-    ff_product<T, S, ATR, BTR, TO, ACT, PART>(s_lds, p);
+    __shared__ alignas(16) char s_lds[TileProduct<T, S, ATR, BTR, TO == TO_GATED, TWO>::LDS];
+    ff_product<T, S, ATR, BTR, TO, ACT, PART, TWO>(s_lds, p);
 }
 
 // The splits' sums, in order, and what becomes of them; four columns a thread.
@@ -366,9 +366,10 @@ static size_t part_bytes(const Cut& c, int64_t m, int64_t n, int to)
     return c.splits > 1 ? (size_t)c.splits * m * n * (to == TO_GATED ? 2 : 1) * 4 : 0;
 }
 
-template <typename T, bool ATR, bool BTR, int TO, int ACT>
-static hipError_t product(const Operand& a, const Operand& b, Target o, int64_t k, int segments, float* part, hipStream_t s)
+template <typename T, bool ATR, bool BTR, int TO, int ACT, bool TWO = false>
+static hipError_t product(const Operand& a, const Operand& b, Target o, int64_t k, float* part, hipStream_t s)
 {
+    constexpr int segments = TWO ? 2 : 1;
     const Cut c = cut_of(o.m, o.n, k, segments, TO);
     ProductArgs p;
     p.a = a;
@@ -381,12 +382,12 @@ static hipError_t product(const Operand& a, const Operand& b, Target o, int64_t 
     p.per_split = c.per_split;
     const dim3 grid((unsigned)(c.mt * c.nt * c.splits)), block((c.large ? Wide::WAVES : Small::WAVES) * 64);
     if (c.splits > 1) {
-        if (c.large) hipLaunchKernelGGL((k_ff_product<T, Wide, ATR, BTR, TO, ACT, true>), grid, block, 0, s, p);
-        else hipLaunchKernelGGL((k_ff_product<T, Small, ATR, BTR, TO, ACT, true>), grid, block, 0, s, p);
+        if (c.large) hipLaunchKernelGGL((k_ff_product<T, Wide, ATR, BTR, TO, ACT, true, TWO>), grid, block, 0, s, p);
+        else hipLaunchKernelGGL((k_ff_product<T, Small, ATR, BTR, TO, ACT, true, TWO>), grid, block, 0, s, p);
         hipLaunchKernelGGL((k_ff_join<T, TO, ACT>), dim3(grid_for((uint64_t)(o.m * o.n / 4), 256)), dim3(256), 0, s, p.o, c.splits);
     } else {
-        if (c.large) hipLaunchKernelGGL((k_ff_product<T, Wide, ATR, BTR, TO, ACT, false>), grid, block, 0, s, p);
-        else hipLaunchKernelGGL((k_ff_product<T, Small, ATR, BTR, TO, ACT, false>), grid, block, 0, s, p);
+        if (c.large) hipLaunchKernelGGL((k_ff_product<T, Wide, ATR, BTR, TO, ACT, false, TWO>), grid, block, 0, s, p);
+        else hipLaunchKernelGGL((k_ff_product<T, Small, ATR, BTR, TO, ACT, false, TWO>), grid, block, 0, s, p);
     }
     return hipGetLastError();
 }
@@ -445,10 +446,10 @@ static hipError_t ff_fwd(const Sizes& z, const gs_matrix* x, const gs_matrix* wg
                          void* h, void* kept, void* y, float* part, hipStream_t s)
 {
     hipError_t e = product<T, false, false, TO_GATED, ACT>(operand(x, z.rows), operand(wg, wu, z.f),
-                                                           target(h, z.f, z.rows, z.f, kept), z.c, 1, part, s);
+                                                           target(h, z.f, z.rows, z.f, kept), z.c, part, s);
     if (e == hipSuccess)
         e = product<T, false, false, TO_STORE, ACT_SILU>(dense(h, z.f, z.rows), operand(wd, z.co), target(y, z.co, z.rows, z.co),
-                                                         z.f, 1, part, s);
+                                                         z.f, part, s);
     return e;
 }
 
@@ -460,21 +461,21 @@ static hipError_t ff_bwd(const Sizes& z, const gs_matrix* gy, const gs_matrix* x
     char* g = (char*)ws;  // gg | gu
     float* part = (float*)(g + grad_bytes(z));
     hipError_t e = product<T, false, true, TO_GRAD, ACT>(operand(gy, z.rows), operand(wd, z.f),
-                                                         target(g, 2 * z.f, z.rows, z.f, (void*)kept), z.co, 1, part, s);
+                                                         target(g, 2 * z.f, z.rows, z.f, (void*)kept), z.co, part, s);
     if (e == hipSuccess && gx) {
         Operand a{{g, g + z.f * 2}, {z.f * 4, z.f * 4}, z.rows};
-        e = product<T, false, true, TO_STORE, ACT_SILU>(a, operand(wg, wu, z.c), target(gx, z.c, z.rows, z.c), z.f, 2, part, s);
+        e = product<T, false, true, TO_STORE, ACT_SILU, true>(a, operand(wg, wu, z.c), target(gx, z.c, z.rows, z.c), z.f, part, s);
     }
     if (e == hipSuccess && gwg) {
         Target o = target(gwg, z.c, 2 * z.f, z.c);
         o.out[1] = gwu;
         o.ld[1] = z.c;
         o.half = z.f;
-        e = product<T, true, true, TO_STORE, ACT_SILU>(dense(g, 2 * z.f, 2 * z.f), operand(x, z.c), o, z.rows, 1, part, s);
+        e = product<T, true, true, TO_STORE, ACT_SILU>(dense(g, 2 * z.f, 2 * z.f), operand(x, z.c), o, z.rows, part, s);
     }
     if (e == hipSuccess && gwd)
         e = product<T, true, true, TO_STORE, ACT_SILU>(operand(gy, z.co), dense(h, z.f, z.f), target(gwd, z.f, z.co, z.f), z.rows,
-                                                       1, part, s);
+                                                       part, s);
     return e;
 }
 

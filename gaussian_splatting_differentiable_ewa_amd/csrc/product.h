@@ -7,7 +7,9 @@
 // are read into registers while the step before it is on the matrix unit, also
 // from one stage to the next: the one barrier per stage stands before its last
 // step, whose operands are in registers by then. Behind it the next stage is whole
-// and this one is free.
+// and this one is free. A stage's loads are spread over the steps that follow:
+// issued at once they fill the CU's one address path, and every wave behind it
+// waits with its matrix instructions.
 //
 // Matrix tile: 32 x 32, 32 bytes of k a step. Lane l holds 16 bytes of k, half
 // l >> 5, of row l & 31 of either operand. B goes first into the instruction, so
@@ -93,23 +95,15 @@ struct PanelLoad {
             off[i] = (uint32_t)m * ld + chunk_of(r) * 16;
         }
     }
-    // `bytes` from p to the end of the matrix (past it: zeros), `k` of them of
-    // this row's own.
-    __device__ __forceinline__ void operator()(char* lds, const char* p, uint32_t bytes, int k) const
+    // Load i of a stage from what is left of the matrix, `k` bytes of them of the
+    // rows' own (behind the last stage of k a row goes on with what is not).
+    __device__ __forceinline__ void one(__amdgpu_buffer_rsrc_t src, char* lds, int i, int k) const
     {
-        const __amdgpu_buffer_rsrc_t src = __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, 0x00027000);
-        char* to = lds + wave * PER * 1024;
-        if (TR || k >= KB) {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) one(src, to + i * 1024, off[i]);
-        } else {  // the last stage of k: a row goes on with what is not its own
-#pragma unroll
-            for (int i = 0; i < PER; ++i) one(src, to + i * 1024, chunk_of(row_of(wave, i)) * 16 < k ? off[i] : PAST);
-        }
-    }
-    static __device__ __forceinline__ void one(__amdgpu_buffer_rsrc_t src, char* to, uint32_t off)
-    {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)to, 16, off, 0, 0, 0);
+        static_assert(TR || KB == 64 || PER % 2 == 0, "a load's chunk goes by whether it is odd");
+        const int chunk = chunk_of(row_of(wave, KB == 64 ? 0 : i & 1));
+        const uint32_t at = TR || chunk * 16 < k ? off[i] : PAST;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            src, (__attribute__((address_space(3))) void*)(lds + (wave * PER + i) * 1024), 16, at, 0, 0, 0);
     }
 };
 
@@ -181,20 +175,7 @@ struct Walk {
     int first, last;
 };
 
-// Order of the instructions around: LDS reads of the next step between matrix
-// instructions of this one.
-template <int READS, int MFMAS>
-__device__ __forceinline__ void spread()
-{
-    constexpr int EACH = (READS + MFMAS - 1) / MFMAS;
-#pragma unroll
-    for (int i = 0; i < MFMAS; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x100, EACH, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    }
-}
-
-template <typename T, typename S, bool ATR, bool BTR, bool PAIR>
+template <typename T, typename S, bool ATR, bool BTR, bool PAIR, bool TWO = false>
 struct TileProduct {
     static constexpr int KE = S::KB / 2;  // elements of a stage
     using LoadA = PanelLoad<S::BM, S::KB, ATR, S::WAVES>;
@@ -215,11 +196,11 @@ struct TileProduct {
             bytes = TR ? (k - 1 - k0) * ld + (o.rows - r0) * 2 : (o.rows - 1 - r0) * ld + (k - k0) * 2;
             step = TR ? KE * ld : KE * 2;
         }
-        // as the 32 bits of a buffer's size (an operand's tile is below 2^31)
-        __device__ __forceinline__ uint32_t size(bool any) const
+        // as a buffer (an operand's tile is below 2^31), or an empty one
+        __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(bool any) const
         {
             const uint32_t n = (uint32_t)(bytes >> 31) ? 0x7fffffffu : (uint32_t)bytes;
-            return any ? n : 0u;
+            return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, any ? (int)n : 0, 0x00027000);
         }
         __device__ __forceinline__ void next()
         {
@@ -228,7 +209,7 @@ struct TileProduct {
         }
     };
 
-    // A lane's scales of one operand: 8 bytes a stage and row, 4 of them each lane half's.
+    // A lane's scales of one operand: 4 bytes a stage and row, the upper two the upper lane half's.
     template <int TILES>
     struct Scales {
         __amdgpu_buffer_rsrc_t src;
@@ -238,19 +219,19 @@ struct TileProduct {
             const int64_t ld = o.ld[1], bytes = (o.rows - 1 - r0) * ld + bytes_of_row;
             src = __builtin_amdgcn_make_buffer_rsrc((void*)(o.data[1] + r0 * ld), 0,
                                                     bytes < 0x7fffffff ? (int)bytes : 0x7fffffff, 0x00027000);
-            off = (uint32_t)(row + (lane_id() & 31)) * (uint32_t)ld + (lane_id() >> 5) * 4;
+            off = (uint32_t)(row + (lane_id() & 31)) * (uint32_t)ld;
             rows32 = 32 * (uint32_t)ld;
         }
         __device__ __forceinline__ void load(int stage, int (&out)[TILES]) const
         {
 #pragma unroll
-            for (int i = 0; i < TILES; ++i) out[i] = __builtin_amdgcn_raw_buffer_load_b32(src, off, i * rows32 + stage * 8, 0);
+            for (int i = 0; i < TILES; ++i) out[i] = __builtin_amdgcn_raw_buffer_load_b32(src, off, i * rows32 + stage * 4, 0);
         }
-        // `blocks` of the stage's 8 count; the bytes behind them may hold anything.
+        // `blocks` of the stage's 4 count; the bytes behind them may hold anything.
         static __device__ __forceinline__ int mine(int x, int blocks)
         {
-            const int n = blocks - 4 * (int)(lane_id() >> 5);
-            return n >= 4 ? x : (n <= 0 ? 0 : x & ((1 << 8 * n) - 1));
+            if (blocks < 4) x &= (1 << 8 * blocks) - 1;
+            return (uint32_t)x >> (lane_id() >> 5) * 16;
         }
     };
 
@@ -258,9 +239,13 @@ struct TileProduct {
                                                int64_t n0, const Walk& w, int wave, acc16 (&acc)[S::MT][S::NT])
     {
         constexpr bool FOUR = std::is_same<T, fp4>::value;
-        static_assert(!FOUR || S::KB == 128, "one dword of scales a stage and lane half");
-        constexpr int STEPS = S::KB / 32, LATER = (S::STAGES - 2) * LOADS;
-        static_assert(STEPS % 2 == 0 && S::STAGES >= 2 && LATER < 16, "steps in pairs; loads out fit the wait's field");
+        static_assert(!FOUR || S::KB == 64, "one dword of scales a stage");
+        // loads that may be out when a stage has to be there (the fewest that follow its own: in the first
+        // iteration scales are loaded once behind them, later more often), and the first part of a stage's
+        constexpr int STEPS = S::KB / 32, LATER = (S::STAGES - 2) * LOADS + (FOUR ? S::MT + S::NT : 0);
+        // a step is MT groups of matrix instructions; loads go EACH to a group, from the last step's on
+        constexpr int EACH = (LOADS + S::MT * STEPS - 1) / (S::MT * STEPS), FIRST = LOADS < EACH * S::MT ? LOADS : EACH * S::MT;
+        static_assert(STEPS % 2 == 0 && S::STAGES >= 2 && LATER + FIRST < 64, "steps in pairs; loads out fit the wait's field");
         const LoadA load_a((uint32_t)a.ld[0], wave);
         const int mine = PAIR ? LoadB::second(wave) : w.first >= w.stages;
         LoadB load_b((uint32_t)b.ld[mine], wave);
@@ -276,13 +261,29 @@ struct TileProduct {
         Feed<BTR> fb;
         fa.at(a, w.first >= w.stages, m0, w.k, (int64_t)in * KE);
         fb.at(b, mine, n0, w.k, (int64_t)in * KE);
-        auto issue = [&](char* stage) __attribute__((always_inline)) {
-            load_a(stage, fa.p, fa.size(left > 0), k);
-            load_b(stage + A_BYTES, fb.p, fb.size(left > 0), k);
+        __amdgpu_buffer_rsrc_t from_a, from_b;  // of the stage whose loads are being issued, and where to
+        int k_of;
+        char* to;
+        auto prepare = [&](char* stage) __attribute__((always_inline)) {
+            from_a = fa.buffer(left > 0);
+            from_b = fb.buffer(left > 0);
+            k_of = k;
+            to = stage;
             --left, ++in, k -= KE * 2;
             fa.next();
             fb.next();
-            if (!PAIR && in == w.stages && left > 0) {  // the second segment
+        };
+        // the loads of group `g` behind the barrier
+        auto load = [&](int g) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = g * EACH; i < (g + 1) * EACH && i < LOADS; ++i) {
+                if (i < LoadA::PER) load_a.one(from_a, to, i, k_of);
+                else load_b.one(from_b, to + A_BYTES, i - LoadA::PER, k_of);
+            }
+        };
+        // after a stage's last load: on to the second segment?
+        auto turn = [&]() __attribute__((always_inline)) {
+            if (TWO && in == w.stages && left > 0) {
                 k = (int)w.k * 2;
                 fa.at(a, 1, m0, w.k, 0);
                 fb.at(b, 1, n0, w.k, 0);
@@ -291,41 +292,45 @@ struct TileProduct {
         };
         // `out` loads may be left out; all LDS reads are done
         auto ready = [&](auto out) __attribute__((always_inline)) {
-            __builtin_amdgcn_s_waitcnt(0x0070 | decltype(out)::value);
+            constexpr int N = decltype(out)::value;
+            __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | (N >> 4) << 14);
             asm volatile("" ::: "memory");
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
         };
         typename Mma<T>::v8 ra[2][S::MT], rb[2][S::NT];
-        auto read = [&](const char* stage, int step, int to) __attribute__((always_inline)) {
-#pragma unroll
-            for (int j = 0; j < S::NT; ++j) rb[to][j] = read_b(stage + A_BYTES, j, step);
-#pragma unroll
-            for (int i = 0; i < S::MT; ++i) ra[to][i] = read_a(stage, i, step);
+        // operand i of a step's: B's, then A's
+        auto read = [&](const char* stage, int step, int to, int i) __attribute__((always_inline)) {
+            if (i < S::NT) rb[to][i] = read_b(stage + A_BYTES, i, step);
+            else ra[to][i - S::NT] = read_a(stage, i - S::NT, step);
         };
+        constexpr int READS = S::NT + S::MT;
         const int scale_row = (int)(w.k + 31) / 32 * 4;
         const Scales<S::MT> scale_a(a, m0, wave / S::WN * (S::BM / S::WM), scale_row);
         const Scales<S::NT> scale_b(b, n0, wave % S::WN * (S::BN / S::WN), scale_row);
         int sa[S::MT], sb[S::NT], next_sa[S::MT], next_sb[S::NT];
-        auto multiply = [&](int step, int from) __attribute__((always_inline)) {
+        auto multiply = [&](int step, int i) __attribute__((always_inline)) {
+            const int from = step & 1;
 #pragma unroll
-            for (int i = 0; i < S::MT; ++i)
-#pragma unroll
-                for (int j = 0; j < S::NT; ++j) {
-                    if constexpr (FOUR) acc[i][j] = Mma<T>::mma(rb[from][j], ra[from][i], acc[i][j], step, sb[j], sa[i]);
-                    else acc[i][j] = Mma<T>::mma(rb[from][j], ra[from][i], acc[i][j]);
-                }
+            for (int j = 0; j < S::NT; ++j) {
+                if constexpr (FOUR) acc[i][j] = Mma<T>::mma(rb[from][j], ra[from][i], acc[i][j], step, sb[j], sa[i]);
+                else acc[i][j] = Mma<T>::mma(rb[from][j], ra[from][i], acc[i][j]);
+            }
         };
-#pragma unroll
-        for (int t = 0; t < S::STAGES; ++t) issue(lds + t * STAGE);
         if constexpr (FOUR) {
             scale_a.load(w.first, next_sa);
             scale_b.load(w.first, next_sb);
-            ready(std::integral_constant<int, 0>{});
-        } else {
-            ready(std::integral_constant<int, LATER + LOADS>{});
         }
-        read(lds, 0, 0);
+#pragma unroll
+        for (int t = 0; t < S::STAGES; ++t) {
+            prepare(lds + t * STAGE);
+#pragma unroll
+            for (int g = 0; g < (t < S::STAGES - 1 ? S::MT * STEPS : S::MT); ++g) load(g);
+            if (t < S::STAGES - 1) turn();
+        }
+        ready(std::integral_constant<int, (S::STAGES - 2) * LOADS + FIRST>{});
+#pragma unroll
+        for (int i = 0; i < READS; ++i) read(lds, 0, 0, i);
         int now = 0;
         for (int t = w.first; t < w.last; ++t) {
             const char* stage = lds + now * STAGE;
@@ -333,23 +338,39 @@ struct TileProduct {
             if constexpr (FOUR) {
                 const int blocks = (int)(w.k - (int64_t)t * KE) / 8;
 #pragma unroll
-                for (int i = 0; i < S::MT; ++i) sa[i] = blocks < 8 ? Scales<S::MT>::mine(next_sa[i], blocks) : next_sa[i];
+                for (int i = 0; i < S::MT; ++i) sa[i] = Scales<S::MT>::mine(next_sa[i], blocks);
 #pragma unroll
-                for (int j = 0; j < S::NT; ++j) sb[j] = blocks < 8 ? Scales<S::NT>::mine(next_sb[j], blocks) : next_sb[j];
+                for (int j = 0; j < S::NT; ++j) sb[j] = Scales<S::NT>::mine(next_sb[j], blocks);
                 scale_a.load(t + 1, next_sa);  // past the row's end: not used
                 scale_b.load(t + 1, next_sb);
             }
+            // The order is kept as written: between two groups of matrix instructions go a few of the next
+            // step's reads and a load. Of the last step, one group stands before the barrier.
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
-                if (s < STEPS - 1) {
-                    read(stage, s + 1, (s + 1) & 1);
-                } else {
-                    ready(std::integral_constant<int, FOUR ? 0 : LATER>{});
-                    issue(lds + now * STAGE);
-                    read(lds + next * STAGE, 0, 0);
+                const bool last = s == STEPS - 1;
+#pragma unroll
+                for (int i = 0; i < S::MT; ++i) {
+                    if (i == 0 && s > 0 && TWO && s == STEPS - 1) turn();
+                    if (S::MT > 1) {
+                        multiply(s, i);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    if (last && i == 0) {
+                        ready(std::integral_constant<int, LATER>{});
+                        prepare(lds + now * STAGE);
+                    }
+                    // the reads before the last group, of which the last step has one fewer
+                    constexpr int G = S::MT > 2 ? S::MT - 1 : S::MT;
+                    const int parts = S::MT > 1 && last && G > 1 ? G - 1 : G, p = S::MT > 1 && last && G > 1 ? i - 1 : i;
+#pragma unroll
+                    for (int r = 0; r < READS; ++r)
+                        if (p >= 0 && p < parts && r * parts / READS == p)
+                            read(last ? lds + next * STAGE : stage, last ? 0 : s + 1, (s + 1) & 1, r);
+                    load(last ? i : (s + 1) * S::MT + i);
+                    if (S::MT > 1) __builtin_amdgcn_sched_barrier(0);
+                    else multiply(s, i);
                 }
-                multiply(s, s & 1);
-                spread<(LoadA::P::PITCH == S::KB ? 1 : 2) * S::MT + (LoadB::P::PITCH == S::KB ? 1 : 2) * S::NT, S::MT * S::NT>();
             }
             now = next;
         }
