@@ -273,7 +273,7 @@ __device__ __forceinline__ void ff_product(char* __restrict__ lds, const Product
 }
 
 template <typename T, typename S, bool ATR, bool BTR, int TO, int ACT, bool PART, bool TWO>
-__global__ __launch_bounds__(S::WAVES * 64, 2) void k_ff_product(const ProductArgs p)
+__global__ __launch_bounds__(S::WAVES * 64, S::PER_SIMD) void k_ff_product(const ProductArgs p)
 {
     __shared__ alignas(16) char s_lds[TileProduct<T, S, ATR, BTR, TO == TO_GATED, TWO>::LDS];
     ff_product<T, S, ATR, BTR, TO, ACT, PART, TWO>(s_lds, p);
@@ -326,6 +326,115 @@ __global__ __launch_bounds__(256) void k_ff_join(const Target o, int32_t splits)
         for (int e = 0; e < 4; ++e) t.v[e] = (T)v[e];
         *(Vec<T, 4>*)((T*)o.out[which] + (which ? row - o.half : row) * o.ld[which] + col) = t;
     }
+}
+
+// Few rows (16 at most): the weights are read once and bound it, so each wave
+// takes them straight from memory to registers, 16 rows of them and the tokens
+// beside them to a 16 x 16 tile of the result, and the waves of a workgroup
+// share the sum over k, 64 elements in turn: a lane's two pieces of 16 bytes and
+// its three neighbours' are 128 bytes of a row (the order of k inside a product
+// is free as long as both operands have the same). Their sums meet in LDS.
+constexpr int FEW = 16;
+
+struct FewArgs {
+    const char *x, *w[2];
+    int64_t ld_x, ld[2];  // bytes
+    Target o;
+    int32_t k;
+};
+
+template <typename T, int TO, int ACT, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void k_ff_few(const FewArgs p)
+{
+    constexpr int M = TO == TO_GATED ? 2 : 1, AHEAD = 4 / M;
+    typedef typename Mma<T>::v8 V;
+    typedef float4v acc4;
+    __shared__ acc4 s_sum[WAVES][M][64];
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int rows = (int)p.o.m;
+    const char* x = p.x + (r < rows ? r : rows - 1) * p.ld_x + q * 32;
+    const int64_t row = n0 + r < p.o.n ? n0 + r : p.o.n - 1;
+    const char* w[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) w[i] = p.w[i] + row * p.ld[i] + q * 32;
+    acc4 acc[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) acc[i] = acc4{0.f, 0.f, 0.f, 0.f};
+    const auto load = [&](const char* from, int k, int half) __attribute__((always_inline)) {
+        V v{};
+        if (k + q * 16 + half * 8 < p.k) v = *(const V*)(from + k * 2 + half * 16);
+        return v;
+    };
+    for (int k0 = wave * 64; k0 < p.k; k0 += WAVES * 64 * AHEAD) {
+        V vx[AHEAD][2], vw[AHEAD][M][2];
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = k0 + a * WAVES * 64;
+#pragma unroll
+                for (int i = 0; i < M; ++i) vw[a][i][h] = load(w[i], k, h);
+                vx[a][h] = load(x, k, h);
+            }
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < M; ++i) acc[i] = mma16<T>(vw[a][i][h], vx[a][h], acc[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < M; ++i) s_sum[wave][i][lane] = acc[i];
+    __syncthreads();
+    if (wave > 0) return;
+    float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] += s_sum[i][0][lane][e];
+            if (M > 1) u[e] += s_sum[i][M - 1][lane][e];
+        }
+    // of the result a lane holds token r, columns 4 q on
+    const int64_t col = n0 + 4 * q;
+    if (r >= rows || col >= p.o.n) return;
+    if constexpr (TO == TO_GATED) {
+        Vec<T, 4> h;
+        Vec<uint16_t, 4> kg, ku;
+        Vec<typename Kept<T>::Low, 4> low;
+        Four<T, ACT>::gate(v, u, h, kg, ku, low);
+        *(Vec<T, 4>*)((T*)p.o.out[0] + r * p.o.ld[0] + col) = h;
+        if (p.o.kept) {
+            const Kept<T> kept{p.o.kept, p.o.m * p.o.n};
+            const int64_t at = r * p.o.n + col;
+            *(Vec<uint16_t, 4>*)kept.g(at) = kg;
+            *(Vec<uint16_t, 4>*)kept.u(at) = ku;
+            *(Vec<typename Kept<T>::Low, 4>*)kept.low(at) = low;
+        }
+    } else {
+        Vec<T, 4> t;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t.v[e] = (T)v[e];
+        *(Vec<T, 4>*)((T*)p.o.out[0] + r * p.o.ld[0] + col) = t;
+    }
+}
+
+// Waves to a workgroup: enough for the chip where there are few columns.
+template <typename T, int TO, int ACT>
+static hipError_t few(const Operand& a, const Operand& b, const Target& o, int64_t k, hipStream_t s)
+{
+    FewArgs p;
+    p.x = a.data[0];
+    p.ld_x = a.ld[0];
+    for (int i = 0; i < 2; ++i) p.w[i] = b.data[i], p.ld[i] = b.ld[i];
+    p.o = o;
+    p.k = (int32_t)k;
+    const dim3 grid((unsigned)((o.n + 15) / 16));
+    if (k <= 512) hipLaunchKernelGGL((k_ff_few<T, TO, ACT, 4>), grid, dim3(256), 0, s, p);
+    else if (TO == TO_GATED || o.n > 4096) hipLaunchKernelGGL((k_ff_few<T, TO, ACT, 8>), grid, dim3(512), 0, s, p);
+    else hipLaunchKernelGGL((k_ff_few<T, TO, ACT, 16>), grid, dim3(1024), 0, s, p);
+    return hipGetLastError();
 }
 
 // Many tiles, and few.
@@ -413,6 +522,7 @@ static bool tiles_ok(const Sizes& z)
 
 static size_t fwd_bytes(const Sizes& z)
 {
+    if (z.rows <= FEW) return 0;
     return std::max(part_bytes(cut_of(z.rows, z.f, z.c, 1, TO_GATED), z.rows, z.f, TO_GATED),
                     part_bytes(cut_of(z.rows, z.co, z.f, 1, TO_STORE), z.rows, z.co, TO_STORE));
 }
@@ -445,6 +555,11 @@ template <typename T, int ACT>
 static hipError_t ff_fwd(const Sizes& z, const gs_matrix* x, const gs_matrix* wg, const gs_matrix* wu, const gs_matrix* wd,
                          void* h, void* kept, void* y, float* part, hipStream_t s)
 {
+    if (z.rows <= FEW) {
+        const hipError_t e = few<T, TO_GATED, ACT>(operand(x, z.rows), operand(wg, wu, z.f), target(h, z.f, z.rows, z.f, kept), z.c, s);
+        if (e != hipSuccess) return e;
+        return few<T, TO_STORE, ACT_SILU>(dense(h, z.f, z.rows), operand(wd, z.co), target(y, z.co, z.rows, z.co), z.f, s);
+    }
     hipError_t e = product<T, false, false, TO_GATED, ACT>(operand(x, z.rows), operand(wg, wu, z.f),
                                                            target(h, z.f, z.rows, z.f, kept), z.c, part, s);
     if (e == hipSuccess)

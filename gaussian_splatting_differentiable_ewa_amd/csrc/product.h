@@ -30,6 +30,15 @@
 
 namespace gs {
 
+// The 16 x 16 x 32 product: of A row, of B column l & 15, eight k from 8 (l >> 4);
+// of C column l & 15, rows 4 (l >> 4) on.
+template <typename T>
+__device__ __forceinline__ float4v mma16(typename Mma<T>::v8 a, typename Mma<T>::v8 b, float4v c)
+{
+    if constexpr (std::is_same<T, bf16>::value) return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    else return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
 // Two values of 4 bits a byte, of either operand of a scaled product.
 struct fp4 {};
 template <>
@@ -73,25 +82,26 @@ __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgc
 
 // Loads of a panel: WAVES waves, 16 bytes a lane, 1024 an instruction. The LDS
 // side of such a load is linear in the lane, so the swizzle is on the memory side.
-// With PAIR the panel's rows are of two matrices, 32 of one and 32 of the other
-// in turn, and a wave loads of one of them.
-template <int ROWS, int KB, bool TR, int WAVES, bool PAIR = false>
+// With PAIR the panel's rows are of two matrices, PAIR of one and as many of the
+// other in turn, and a wave loads of one of them.
+template <int ROWS, int KB, bool TR, int WAVES, int PAIR = 0>
 struct PanelLoad {
     using P = Panel<ROWS, KB, TR>;
     static constexpr int PER = P::BYTES / 1024 / WAVES, RPI = 1024 / P::PITCH;
     static_assert(PER * WAVES * 1024 == P::BYTES && RPI >= 1, "whole instructions");
-    static_assert(!PAIR || (!TR && ROWS / WAVES <= 32), "a wave loads of one matrix");
+    static_assert(!PAIR || (!TR && PAIR % (ROWS / WAVES) == 0), "a wave loads of one matrix");
+    static constexpr int HALF = PAIR ? PAIR : 1;
     uint32_t off[PER];
     int wave;
     static __device__ __forceinline__ int row_of(int wave, int i) { return (wave * PER + i) * RPI + (int)lane_id() / P::CHUNKS; }
     static __device__ __forceinline__ int chunk_of(int row) { return ((int)lane_id() % P::CHUNKS) ^ P::swizzle(row); }
     // Which matrix of a pair the wave loads.
-    static __device__ __forceinline__ int second(int wave) { return (wave * (ROWS / WAVES)) >> 5 & 1; }
+    static __device__ __forceinline__ int second(int wave) { return wave * (ROWS / WAVES) / HALF & 1; }
     __device__ __forceinline__ PanelLoad(uint32_t ld, int w) : wave(w)
     {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int r = row_of(w, i), m = PAIR ? (r >> 6) * 32 + (r & 31) : r;
+            const int r = row_of(w, i), m = PAIR ? r / (2 * HALF) * HALF + r % HALF : r;
             off[i] = (uint32_t)m * ld + chunk_of(r) * 16;
         }
     }
@@ -166,6 +176,7 @@ template <int BM_, int BN_, int WM_, int WN_, int KB_, int STAGES_>
 struct TileShape {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KB = KB_, STAGES = STAGES_;
     static constexpr int WAVES = WM * WN, MT = BM / WM / 32, NT = BN / WN / 32;
+    static constexpr int PER_SIMD = MT * NT > 8 ? 1 : 2;  // waves that share a SIMD's registers
 };
 
 // The stages a workgroup walks: [first, last) of all segments' stages.
@@ -179,7 +190,7 @@ template <typename T, typename S, bool ATR, bool BTR, bool PAIR, bool TWO = fals
 struct TileProduct {
     static constexpr int KE = S::KB / 2;  // elements of a stage
     using LoadA = PanelLoad<S::BM, S::KB, ATR, S::WAVES>;
-    using LoadB = PanelLoad<S::BN, S::KB, BTR, S::WAVES, PAIR>;
+    using LoadB = PanelLoad<S::BN, S::KB, BTR, S::WAVES, PAIR ? S::BN / S::WN / 2 : 0>;
     static constexpr int A_BYTES = LoadA::P::BYTES, STAGE = A_BYTES + LoadB::P::BYTES, LDS = STAGE * S::STAGES;
     static constexpr int LOADS = LoadA::PER + LoadB::PER;
 
