@@ -334,6 +334,9 @@ __global__ __launch_bounds__(256) void k_ff_join(const Target o, int32_t splits)
 // share the sum over k, 64 elements in turn: a lane's two pieces of 16 bytes and
 // its three neighbours' are 128 bytes of a row (the order of k inside a product
 // is free as long as both operands have the same). Their sums meet in LDS.
+// With PARTS = 2 a tile is 8 rows of the weights for 8 tokens, each twice, with
+// the first and the second half of k: of the 16 x 16 results the two 8 x 8 count
+// whose halves are the same. It makes twice the workgroups, for few columns.
 constexpr int FEW = 16;
 
 struct FewArgs {
@@ -343,40 +346,43 @@ struct FewArgs {
     int32_t k;
 };
 
-template <typename T, int TO, int ACT, int WAVES>
+template <typename T, int TO, int ACT, int WAVES, int PARTS>
 __global__ __launch_bounds__(WAVES * 64) void k_ff_few(const FewArgs p)
 {
-    constexpr int M = TO == TO_GATED ? 2 : 1, AHEAD = 4 / M;
+    constexpr int M = TO == TO_GATED ? 2 : 1, AHEAD = (WAVES < 16 ? 8 : 4) / M, SIDE = 16 / PARTS;
     typedef typename Mma<T>::v8 V;
-    typedef float4v acc4;
-    __shared__ acc4 s_sum[WAVES][M][64];
-    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
-    const int rows = (int)p.o.m;
-    const char* x = p.x + (r < rows ? r : rows - 1) * p.ld_x + q * 32;
+    __shared__ float4v s_sum[WAVES][M][64];
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane % SIDE, q = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * SIDE;
+    const int rows = (int)p.o.m, part = PARTS > 1 ? lane >> 3 & 1 : 0;
+    const int span = PARTS > 1 ? (p.k / 2 + 63) / 64 * 64 : p.k;  // of k a part has
+    const int first = part * span + q * 16, end = part * span + span < p.k ? part * span + span : p.k;
+    const char* x = p.x + (r < rows ? r : rows - 1) * p.ld_x;
     const int64_t row = n0 + r < p.o.n ? n0 + r : p.o.n - 1;
     const char* w[M];
 #pragma unroll
-    for (int i = 0; i < M; ++i) w[i] = p.w[i] + row * p.ld[i] + q * 32;
-    acc4 acc[M];
+    for (int i = 0; i < M; ++i) w[i] = p.w[i] + row * p.ld[i];
+    float4v acc[M];
 #pragma unroll
-    for (int i = 0; i < M; ++i) acc[i] = acc4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < M; ++i) acc[i] = float4v{0.f, 0.f, 0.f, 0.f};
     const auto load = [&](const char* from, int k, int half) __attribute__((always_inline)) {
+        const int at = first + k + half * 8;
         V v{};
-        if (k + q * 16 + half * 8 < p.k) v = *(const V*)(from + k * 2 + half * 16);
+        if (at < end) v = *(const V*)(from + at * 2);
         return v;
     };
-    for (int k0 = wave * 64; k0 < p.k; k0 += WAVES * 64 * AHEAD) {
+    for (int k0 = wave * 64; k0 < span; k0 += WAVES * 64 * AHEAD) {
         V vx[AHEAD][2], vw[AHEAD][M][2];
 #pragma unroll
         for (int a = 0; a < AHEAD; ++a)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = k0 + a * WAVES * 64;
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int i = 0; i < M; ++i) vw[a][i][h] = load(w[i], k, h);
-                vx[a][h] = load(x, k, h);
-            }
+                for (int i = 0; i < M; ++i) vw[a][i][h] = load(w[i], k0 + a * WAVES * 64, h);
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) vx[a][h] = load(x, k0 + a * WAVES * 64, h);
 #pragma unroll
         for (int a = 0; a < AHEAD; ++a)
 #pragma unroll
@@ -395,10 +401,15 @@ __global__ __launch_bounds__(WAVES * 64) void k_ff_few(const FewArgs p)
         for (int e = 0; e < 4; ++e) {
             v[e] += s_sum[i][0][lane][e];
             if (M > 1) u[e] += s_sum[i][M - 1][lane][e];
+            if (PARTS > 1) {  // token r's second half, rows 8 on of the tile: 8 lanes and two quarters further
+                const int other = (lane + 40) % 64;
+                v[e] += s_sum[i][0][other][e];
+                if (M > 1) u[e] += s_sum[i][M - 1][other][e];
+            }
         }
     // of the result a lane holds token r, columns 4 q on
     const int64_t col = n0 + 4 * q;
-    if (r >= rows || col >= p.o.n) return;
+    if (r >= rows || col >= p.o.n || part > 0 || 4 * q >= SIDE) return;
     if constexpr (TO == TO_GATED) {
         Vec<T, 4> h;
         Vec<uint16_t, 4> kg, ku;
@@ -430,10 +441,17 @@ static hipError_t few(const Operand& a, const Operand& b, const Target& o, int64
     for (int i = 0; i < 2; ++i) p.w[i] = b.data[i], p.ld[i] = b.ld[i];
     p.o = o;
     p.k = (int32_t)k;
-    const dim3 grid((unsigned)((o.n + 15) / 16));
-    if (k <= 512) hipLaunchKernelGGL((k_ff_few<T, TO, ACT, 4>), grid, dim3(256), 0, s, p);
-    else if (TO == TO_GATED || o.n > 4096) hipLaunchKernelGGL((k_ff_few<T, TO, ACT, 8>), grid, dim3(512), 0, s, p);
-    else hipLaunchKernelGGL((k_ff_few<T, TO, ACT, 16>), grid, dim3(1024), 0, s, p);
+    const auto launch = [&](auto waves, auto parts) {
+        constexpr int W = decltype(waves)::value, P = decltype(parts)::value;
+        hipLaunchKernelGGL((k_ff_few<T, TO, ACT, W, P>), dim3((unsigned)((o.n + 16 / P - 1) / (16 / P))), dim3(W * 64), 0, s, p);
+    };
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, 2> two;
+    const std::integral_constant<int, 4> four;
+    const std::integral_constant<int, 8> eight;
+    if (k <= 512) launch(four, one);
+    else if (o.m <= 8 && o.n <= 4096) launch(eight, two);
+    else launch(eight, one);
     return hipGetLastError();
 }
 
