@@ -125,19 +125,19 @@ using FourTile = TileShape<256, 256, 2, 4, 64, 4>;
 using FourSmall = TileShape<64, 64, 2, 2, 64, 4>;
 
 template <typename T, typename S>
-__device__ __forceinline__ void four_product(char* __restrict__ lds, const FourArgs& p)
+__device__ __forceinline__ void four_product(char* lds, const FourArgs& p)
 {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), hi = lane >> 5;
     uint32_t mi, ni;
     tile_of(xcd_contiguous(blockIdx.x, gridDim.x), p.mt, p.nt, mi, ni);
     const int64_t m0 = (int64_t)mi * S::BM, n0 = (int64_t)ni * S::BN;
     acc16 acc[S::MT][S::NT];
-    TileProduct<fp4, S, false, false, false>::run(lds, p.a, p.b, m0, n0, p.walk, wave, acc);
+    TileProduct<fp4, S, false, false, false>::run(lds, p.a, p.b, m0, n0, p.walk, 0, wave, acc);
     // out through a scratch of the wave's own: whole rows, or where those do not lie on 16 bytes their elements
     using Tiles = TileProduct<fp4, S, false, false, false>;
     constexpr int SIZE = sizeof(T), PER = SIZE == 2 && S::NT > 1 ? 2 : 1, W = 32 * SIZE * PER;  // matrix tiles to a row of scratch
-    static_assert(S::NT % PER == 0 && Tiles::LDS / S::WAVES >= 32 * W, "a wave's scratch");
-    const Rows<W> at{lds + wave * (Tiles::LDS / S::WAVES)};
+    static_assert(S::NT % PER == 0 && Tiles::SCRATCH >= 32 * W, "a wave's scratch");
+    const Rows<W> at{lds + wave * (Tiles::SCRATCH)};
     const int64_t col0 = n0 + wave % S::WN * (S::BN / S::WN);
     const bool whole = p.n * SIZE % 16 == 0 && ((uintptr_t)p.y & 15) == 0;
 #pragma unroll
@@ -167,7 +167,7 @@ __device__ __forceinline__ void four_product(char* __restrict__ lds, const FourA
 }
 
 template <typename T, typename S>
-__global__ __launch_bounds__(S::WAVES * 64, 2) void k_fp4_product(const FourArgs p)
+__global__ __launch_bounds__(S::THREADS, S::PER_SIMD) void k_fp4_product(const FourArgs p)
 {
     __shared__ alignas(16) char s_lds[TileProduct<fp4, S, false, false, false>::LDS];
     four_product<T, S>(s_lds, p);
@@ -212,8 +212,8 @@ static hipError_t product_as(FourArgs& p, hipStream_t s)
     const bool large = ((p.m + 255) / 256) * ((p.n + 255) / 256) >= 128;
     p.mt = (uint32_t)((p.m + (large ? 255 : 63)) / (large ? 256 : 64));
     p.nt = (uint32_t)((p.n + (large ? 255 : 63)) / (large ? 256 : 64));
-    if (large) hipLaunchKernelGGL((k_fp4_product<T, FourTile>), dim3(p.mt * p.nt), dim3(512), 0, s, p);
-    else hipLaunchKernelGGL((k_fp4_product<T, FourSmall>), dim3(p.mt * p.nt), dim3(256), 0, s, p);
+    if (large) hipLaunchKernelGGL((k_fp4_product<T, FourTile>), dim3(p.mt * p.nt), dim3(FourTile::THREADS), 0, s, p);
+    else hipLaunchKernelGGL((k_fp4_product<T, FourSmall>), dim3(p.mt * p.nt), dim3(FourSmall::THREADS), 0, s, p);
     return hipGetLastError();
 }
 

@@ -132,7 +132,7 @@ struct ProductArgs {
 // The wave's rows from m0 + 32 i on and columns from n0 on, for each i, out of
 // its accumulators through its scratch.
 template <typename T, typename S, int TO, int ACT, bool PART>
-__device__ __forceinline__ void finish(char* __restrict__ scratch, const Target& o, const acc16 (&acc)[S::MT][S::NT],
+__device__ __forceinline__ void finish(char* scratch, const Target& o, const acc16 (&acc)[S::MT][S::NT],
                                        int64_t m0, int64_t n0, int64_t split)
 {
     const int lane = lane_id(), hi = lane >> 5;
@@ -252,38 +252,62 @@ __device__ __forceinline__ void finish(char* __restrict__ scratch, const Target&
     }
 }
 
-template <typename T, typename S, bool ATR, bool BTR, int TO, int ACT, bool PART, bool TWO>
-__device__ __forceinline__ void ff_product(char* __restrict__ lds, const ProductArgs& p)
+// Block `id` of a product's.
+template <typename T, typename S, bool ATR, bool BTR, int TO, int ACT, bool TWO>
+__device__ __forceinline__ void ff_product(char* lds, const ProductArgs& p, uint32_t id)
 {
     constexpr bool PAIR = TO == TO_GATED;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t tiles = p.mt * p.nt, split = uniform(blockIdx.x / tiles);
+    const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), group = all / S::WAVES, wave = all % S::WAVES;
+    const uint32_t tiles = p.mt * p.nt, split = uniform(id / tiles);
     uint32_t mi, ni;
-    tile_of(xcd_contiguous(blockIdx.x - split * tiles, tiles), p.mt, p.nt, mi, ni);
+    tile_of(xcd_contiguous(id - split * tiles, tiles), p.mt, p.nt, mi, ni);
     const int64_t m0 = (int64_t)mi * S::BM, n0 = (int64_t)ni * (PAIR ? S::BN / 2 : S::BN);
     Walk w = p.walk;
     w.first = split * p.per_split;
-    w.last = min(w.last, w.first + p.per_split);
+    w.last = min(w.last, w.first + (int)p.per_split);
     acc16 acc[S::MT][S::NT];
     using Tiles = TileProduct<T, S, ATR, BTR, PAIR, TWO>;
-    Tiles::run(lds, p.a, p.b, m0, n0, w, wave, acc);
-    static_assert(Tiles::LDS / S::WAVES >= 32 * 64 * 4 * 2, "a wave's scratch");
-    finish<T, S, TO, ACT, PART>(lds + wave * (Tiles::LDS / S::WAVES), p.o, acc, m0 + wave / S::WN * (S::BM / S::WM),
-                                n0 + wave % S::WN * (S::BN / S::WN / (PAIR ? 2 : 1)), split);
+    Tiles::run(lds, p.a, p.b, m0, n0, w, group, wave, acc);
+    if (group > 0) return;
+    char* scratch = lds + wave * Tiles::SCRATCH;
+    const int64_t m = m0 + wave / S::WN * (S::BM / S::WM), n = n0 + wave % S::WN * (S::BN / S::WN / (PAIR ? 2 : 1));
+    static_assert(Tiles::SCRATCH >= 32 * 64 * 4 * 2, "a wave's scratch");
+    if (p.o.part) finish<T, S, TO, ACT, true>(scratch, p.o, acc, m, n, split);
+    else finish<T, S, TO, ACT, false>(scratch, p.o, acc, m, n, 0);
 }
 
-template <typename T, typename S, bool ATR, bool BTR, int TO, int ACT, bool PART, bool TWO>
-__global__ __launch_bounds__(S::WAVES * 64, S::PER_SIMD) void k_ff_product(const ProductArgs p)
+template <typename T, typename S, bool ATR, bool BTR, int TO, int ACT>
+__global__ __launch_bounds__(S::THREADS, S::PER_SIMD) void k_ff_product(const ProductArgs p)
 {
-    __shared__ alignas(16) char s_lds[TileProduct<T, S, ATR, BTR, TO == TO_GATED, TWO>::LDS];
-    ff_product<T, S, ATR, BTR, TO, ACT, PART, TWO>(s_lds, p);
+    __shared__ alignas(16) char s_lds[TileProduct<T, S, ATR, BTR, TO == TO_GATED>::LDS];
+    ff_product<T, S, ATR, BTR, TO, ACT, false>(s_lds, p, blockIdx.x);
+}
+
+// gx, the two projections' gradients and the last one's: blocks of each in turn.
+struct BackArgs {
+    ProductArgs p[3];
+    uint32_t blocks[3];
+};
+
+template <typename T, typename S>
+__global__ __launch_bounds__(S::THREADS, S::PER_SIMD) void k_ff_back(const BackArgs b)
+{
+    __shared__ alignas(16) char s_lds[TileProduct<T, S, true, true, false>::LDS];
+    uint32_t id = blockIdx.x;
+    if (id < b.blocks[0]) {
+        ff_product<T, S, false, true, TO_STORE, ACT_SILU, true>(s_lds, b.p[0], id);
+        return;
+    }
+    id -= b.blocks[0];
+    const int which = id < b.blocks[1] ? 1 : 2;
+    ff_product<T, S, true, true, TO_STORE, ACT_SILU, false>(s_lds, b.p[which], which == 1 ? id : id - b.blocks[1]);
 }
 
 // The splits' sums, in order, and what becomes of them; four columns a thread.
 template <typename T, int TO, int ACT>
-__global__ __launch_bounds__(256) void k_ff_join(const Target o, int32_t splits)
+__device__ __forceinline__ void ff_join(const Target& o, int32_t splits, uint32_t id)
 {
-    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    const int64_t at = ((int64_t)id * 256 + threadIdx.x) * 4;
     if (at >= o.m * o.n) return;
     const int64_t row = at / o.n, col = at - row * o.n, width = TO == TO_GATED ? 2 * o.n : o.n;
     float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
@@ -326,6 +350,27 @@ __global__ __launch_bounds__(256) void k_ff_join(const Target o, int32_t splits)
         for (int e = 0; e < 4; ++e) t.v[e] = (T)v[e];
         *(Vec<T, 4>*)((T*)o.out[which] + (which ? row - o.half : row) * o.ld[which] + col) = t;
     }
+}
+
+template <typename T, int TO, int ACT>
+__global__ __launch_bounds__(256) void k_ff_join(const Target o, int32_t splits)
+{
+    ff_join<T, TO, ACT>(o, splits, blockIdx.x);
+}
+
+struct JoinArgs {
+    Target o[3];
+    int32_t splits[3];
+    uint32_t blocks[3];
+};
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_ff_joins(const JoinArgs j)
+{
+    uint32_t id = blockIdx.x;
+    int which = 0;
+    while (which < 2 && id >= j.blocks[which]) id -= j.blocks[which++];
+    ff_join<T, TO_STORE, ACT_SILU>(j.o[which], j.splits[which], id);
 }
 
 // Few rows (16 at most): the weights are read once and bound it, so each wave
@@ -455,37 +500,59 @@ static hipError_t few(const Operand& a, const Operand& b, const Target& o, int64
     return hipGetLastError();
 }
 
-// Many tiles, and few.
+// The tiles. Smaller ones make more workgroups, and their groups of waves, which
+// share the sum over k, fill the CU that one workgroup has to itself.
 using Wide = TileShape<256, 256, 2, 4, 128, 2>;
-using Small = TileShape<64, 128, 2, 2, 128, 3>;
+using Mid = TileShape<128, 128, 2, 2, 128, 2, 2>;
+using Small = TileShape<64, 64, 2, 2, 128, 2, 4>;
+using SmallPair = TileShape<64, 64, 2, 1, 128, 2, 4>;
+enum { SMALL = 0, MID = 1, WIDE = 2 };
+constexpr int64_t CUS = 256;
 
-// How a product of m x n over k is cut.
+// How a product of m x n over k is cut into tiles of a shape and splits of the
+// sum, and the time one block takes: us a round of stages, as measured with
+// every CU at work, and a fixed part.
 struct Cut {
-    bool large;
     int32_t stages, splits, per_split;
-    int64_t mt, nt;
+    int64_t mt, nt, blocks;
+    double us;
 };
 
-template <typename S>
-static Cut cut_as(bool large, int64_t m, int64_t wide, int64_t k, int segments, int64_t slots)
+static Cut cut_as(int shape, int64_t m, int64_t wide, int64_t k, int segments, int64_t splits)
 {
+    static constexpr int64_t SIDE[3] = {64, 128, 256}, GROUPS[3] = {4, 2, 1};
+    static constexpr double ROUND[3] = {0.9, 1.2, 1.75};
     Cut c;
-    c.large = large;
-    c.mt = (m + S::BM - 1) / S::BM;
-    c.nt = (wide + S::BN - 1) / S::BN;
-    c.stages = (int32_t)((k + S::KB / 2 - 1) / (S::KB / 2));
-    const int64_t total = (int64_t)c.stages * segments, tiles = std::max<int64_t>(c.mt * c.nt, 1);
-    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(slots / tiles, total / 4));
+    c.mt = (m + SIDE[shape] - 1) / SIDE[shape];
+    c.nt = (wide + SIDE[shape] - 1) / SIDE[shape];
+    c.stages = (int32_t)((k + 63) / 64);
+    const int64_t total = (int64_t)c.stages * segments;
     c.per_split = (int32_t)std::max<int64_t>(1, (total + splits - 1) / splits);
     c.splits = (int32_t)std::max<int64_t>(1, (total + c.per_split - 1) / c.per_split);
+    c.blocks = c.mt * c.nt * c.splits;
+    c.us = 3.0 + ROUND[shape] * (double)((c.per_split + GROUPS[shape] - 1) / GROUPS[shape]);
     return c;
 }
 
-static Cut cut_of(int64_t m, int64_t n, int64_t k, int segments, int to)
+// Sums of splits are written, read and joined by another kernel: microseconds.
+static double join_us(const Cut& c, int64_t m, int64_t wide) { return c.splits > 1 ? 4.0 + (double)(c.splits * m * wide) * 3e-6 : 0.0; }
+
+constexpr int64_t MOST_SPLITS = 32;
+
+// The shape and splits that take the least time by the figures above.
+static Cut cut_of(int64_t m, int64_t n, int64_t k, int to, int* shape)
 {
     const int64_t wide = to == TO_GATED ? 2 * n : n;
-    if (((m + 255) / 256) * ((wide + 255) / 256) < 128) return cut_as<Small>(false, m, wide, k, segments, 512);
-    return cut_as<Wide>(true, m, wide, k, segments, 256);
+    Cut best{};
+    double least = 1e30;
+    for (int s = SMALL; s <= WIDE; ++s)
+        for (int64_t splits = 1; splits <= MOST_SPLITS; splits *= 2) {
+            const Cut c = cut_as(s, m, wide, k, 1, splits);
+            const double us = (double)((c.blocks + CUS - 1) / CUS) * c.us + join_us(c, m, wide);
+            if (us < least) least = us, best = c, *shape = s;
+            if (c.per_split <= 4) break;
+        }
+    return best;
 }
 
 static size_t part_bytes(const Cut& c, int64_t m, int64_t n, int to)
@@ -493,29 +560,33 @@ static size_t part_bytes(const Cut& c, int64_t m, int64_t n, int to)
     return c.splits > 1 ? (size_t)c.splits * m * n * (to == TO_GATED ? 2 : 1) * 4 : 0;
 }
 
-template <typename T, bool ATR, bool BTR, int TO, int ACT, bool TWO = false>
-static hipError_t product(const Operand& a, const Operand& b, Target o, int64_t k, float* part, hipStream_t s)
+static ProductArgs args_of(const Operand& a, const Operand& b, const Target& o, int64_t k, int segments, const Cut& c, float* part)
 {
-    constexpr int segments = TWO ? 2 : 1;
-    const Cut c = cut_of(o.m, o.n, k, segments, TO);
     ProductArgs p;
     p.a = a;
     p.b = b;
-    o.part = part;
     p.o = o;
+    p.o.part = c.splits > 1 ? part : nullptr;
     p.walk = {k, c.stages, 0, c.stages * segments};
     p.mt = (uint32_t)c.mt;
     p.nt = (uint32_t)c.nt;
-    p.per_split = c.per_split;
-    const dim3 grid((unsigned)(c.mt * c.nt * c.splits)), block((c.large ? Wide::WAVES : Small::WAVES) * 64);
-    if (c.splits > 1) {
-        if (c.large) hipLaunchKernelGGL((k_ff_product<T, Wide, ATR, BTR, TO, ACT, true, TWO>), grid, block, 0, s, p);
-        else hipLaunchKernelGGL((k_ff_product<T, Small, ATR, BTR, TO, ACT, true, TWO>), grid, block, 0, s, p);
+    p.per_split = (uint32_t)c.per_split;
+    return p;
+}
+
+template <typename T, bool BTR, int TO, int ACT>
+static hipError_t product(const Operand& a, const Operand& b, const Target& o, int64_t k, float* part, hipStream_t s)
+{
+    using Least = std::conditional_t<TO == TO_GATED, SmallPair, Small>;
+    int shape;
+    const Cut c = cut_of(o.m, o.n, k, TO, &shape);
+    const ProductArgs p = args_of(a, b, o, k, 1, c, part);
+    const dim3 grid((unsigned)c.blocks);
+    if (shape == WIDE) hipLaunchKernelGGL((k_ff_product<T, Wide, false, BTR, TO, ACT>), grid, dim3(Wide::THREADS), 0, s, p);
+    else if (shape == MID) hipLaunchKernelGGL((k_ff_product<T, Mid, false, BTR, TO, ACT>), grid, dim3(Mid::THREADS), 0, s, p);
+    else hipLaunchKernelGGL((k_ff_product<T, Least, false, BTR, TO, ACT>), grid, dim3(Least::THREADS), 0, s, p);
+    if (c.splits > 1)
         hipLaunchKernelGGL((k_ff_join<T, TO, ACT>), dim3(grid_for((uint64_t)(o.m * o.n / 4), 256)), dim3(256), 0, s, p.o, c.splits);
-    } else {
-        if (c.large) hipLaunchKernelGGL((k_ff_product<T, Wide, ATR, BTR, TO, ACT, false, TWO>), grid, block, 0, s, p);
-        else hipLaunchKernelGGL((k_ff_product<T, Small, ATR, BTR, TO, ACT, false, TWO>), grid, block, 0, s, p);
-    }
     return hipGetLastError();
 }
 
@@ -529,30 +600,73 @@ static bool sizes_ok(const Sizes& z)
            z.co <= (1 << 17) && z.c % 8 == 0 && z.f % 8 == 0 && z.co % 8 == 0;
 }
 
-// Whether every product's workgroups, of 256 threads, are below 2^32 threads.
+// The three products of the backward pass that need gg and gu, in one launch:
+// gx, gWg and gWu over each other, gWd.
+struct Back {
+    int shape;
+    Cut c[3];
+    int64_t m[3], n[3];
+    double us;
+};
+
+static Back back_of(const Sizes& z)
+{
+    const int64_t m[3] = {z.rows, 2 * z.f, z.co}, n[3] = {z.c, z.c, z.f}, k[3] = {z.f, z.rows, z.rows};
+    Back best{};
+    best.us = 1e30;
+    for (int s = SMALL; s <= WIDE; ++s) {
+        Back b{};
+        b.shape = s;
+        for (int i = 0; i < 3; ++i) b.m[i] = m[i], b.n[i] = n[i], b.c[i] = cut_as(s, m[i], n[i], k[i], i == 0 ? 2 : 1, 1);
+        // the longest blocks in splits, as long as that makes it shorter
+        for (;;) {
+            double sum = 0, longest = 0, joins = 0;
+            int64_t blocks = 0;
+            int which = 0;
+            for (int i = 0; i < 3; ++i) {
+                sum += b.c[i].us * (double)b.c[i].blocks;
+                blocks += b.c[i].blocks;
+                joins += join_us(b.c[i], m[i], n[i]);
+                if (b.c[i].us > longest) longest = b.c[i].us, which = i;
+            }
+            // whole rounds of the average block, or what the CUs do on average and half of the longest block
+            b.us = (blocks <= CUS ? longest : sum / CUS + longest / 2) + joins;
+            if (b.us < best.us) best = b;
+            if (b.c[which].splits * 2 > MOST_SPLITS || b.c[which].per_split <= 4) break;
+            b.c[which] = cut_as(s, m[which], n[which], k[which], which == 0 ? 2 : 1, b.c[which].splits * 2);
+        }
+    }
+    return best;
+}
+
+// Whether every product's workgroups, of 1024 threads at most, are below 2^32
+// threads.
 static bool tiles_ok(const Sizes& z)
 {
-    const auto fits = [](const Cut& c) { return c.mt * c.nt < (1 << 23); };
-    return fits(cut_of(z.rows, z.f, z.c, 1, TO_GATED)) && fits(cut_of(z.rows, z.co, z.f, 1, TO_STORE)) &&
-           fits(cut_of(z.rows, z.f, z.co, 1, TO_GRAD)) && fits(cut_of(z.rows, z.c, z.f, 2, TO_STORE)) && fits(cut_of(2 * z.f, z.c, z.rows, 1, TO_STORE)) &&
-           fits(cut_of(z.co, z.f, z.rows, 1, TO_STORE));
+    int shape;
+    const auto fits = [](int64_t blocks) { return blocks < (1 << 22); };
+    const Back b = back_of(z);
+    return fits(cut_of(z.rows, z.f, z.c, TO_GATED, &shape).blocks) && fits(cut_of(z.rows, z.co, z.f, TO_STORE, &shape).blocks) &&
+           fits(cut_of(z.rows, z.f, z.co, TO_GRAD, &shape).blocks) && fits(b.c[0].blocks + b.c[1].blocks + b.c[2].blocks);
 }
 
 static size_t fwd_bytes(const Sizes& z)
 {
     if (z.rows <= FEW) return 0;
-    return std::max(part_bytes(cut_of(z.rows, z.f, z.c, 1, TO_GATED), z.rows, z.f, TO_GATED),
-                    part_bytes(cut_of(z.rows, z.co, z.f, 1, TO_STORE), z.rows, z.co, TO_STORE));
+    int shape;
+    return std::max(part_bytes(cut_of(z.rows, z.f, z.c, TO_GATED, &shape), z.rows, z.f, TO_GATED),
+                    part_bytes(cut_of(z.rows, z.co, z.f, TO_STORE, &shape), z.rows, z.co, TO_STORE));
 }
 
 static size_t grad_bytes(const Sizes& z) { return ((size_t)z.rows * z.f * 2 * 2 + 255) / 256 * 256; }  // gg | gu
 
 static size_t bwd_bytes(const Sizes& z)
 {
-    size_t part = part_bytes(cut_of(z.rows, z.f, z.co, 1, TO_GRAD), z.rows, z.f, TO_GRAD);
-    part = std::max(part, part_bytes(cut_of(z.rows, z.c, z.f, 2, TO_STORE), z.rows, z.c, TO_STORE));
-    part = std::max(part, part_bytes(cut_of(2 * z.f, z.c, z.rows, 1, TO_STORE), 2 * z.f, z.c, TO_STORE));
-    return grad_bytes(z) + std::max(part, part_bytes(cut_of(z.co, z.f, z.rows, 1, TO_STORE), z.co, z.f, TO_STORE));
+    int shape;
+    const Back b = back_of(z);
+    size_t back = 0;
+    for (int i = 0; i < 3; ++i) back += part_bytes(b.c[i], b.m[i], b.n[i], TO_STORE);
+    return grad_bytes(z) + std::max(part_bytes(cut_of(z.rows, z.f, z.co, TO_GRAD, &shape), z.rows, z.f, TO_GRAD), back);
 }
 
 static Operand operand(const gs_matrix* m, int64_t rows) { return {{(const char*)m->data, nullptr}, {m->stride * 2, 0}, rows}; }
@@ -578,12 +692,11 @@ static hipError_t ff_fwd(const Sizes& z, const gs_matrix* x, const gs_matrix* wg
         if (e != hipSuccess) return e;
         return few<T, TO_STORE, ACT_SILU>(dense(h, z.f, z.rows), operand(wd, z.co), target(y, z.co, z.rows, z.co), z.f, s);
     }
-    hipError_t e = product<T, false, false, TO_GATED, ACT>(operand(x, z.rows), operand(wg, wu, z.f),
-                                                           target(h, z.f, z.rows, z.f, kept), z.c, part, s);
-    if (e == hipSuccess)
-        e = product<T, false, false, TO_STORE, ACT_SILU>(dense(h, z.f, z.rows), operand(wd, z.co), target(y, z.co, z.rows, z.co),
-                                                         z.f, part, s);
-    return e;
+    const hipError_t e = product<T, false, TO_GATED, ACT>(operand(x, z.rows), operand(wg, wu, z.f),
+                                                          target(h, z.f, z.rows, z.f, kept), z.c, part, s);
+    if (e != hipSuccess) return e;
+    return product<T, false, TO_STORE, ACT_SILU>(dense(h, z.f, z.rows), operand(wd, z.co), target(y, z.co, z.rows, z.co), z.f, part,
+                                                 s);
 }
 
 template <typename T, int ACT>
@@ -593,23 +706,37 @@ static hipError_t ff_bwd(const Sizes& z, const gs_matrix* gy, const gs_matrix* x
 {
     char* g = (char*)ws;  // gg | gu
     float* part = (float*)(g + grad_bytes(z));
-    hipError_t e = product<T, false, true, TO_GRAD, ACT>(operand(gy, z.rows), operand(wd, z.f),
-                                                         target(g, 2 * z.f, z.rows, z.f, (void*)kept), z.co, part, s);
-    if (e == hipSuccess && gx) {
-        Operand a{{g, g + z.f * 2}, {z.f * 4, z.f * 4}, z.rows};
-        e = product<T, false, true, TO_STORE, ACT_SILU, true>(a, operand(wg, wu, z.c), target(gx, z.c, z.rows, z.c), z.f, part, s);
+    const hipError_t e = product<T, true, TO_GRAD, ACT>(operand(gy, z.rows), operand(wd, z.f),
+                                                        target(g, 2 * z.f, z.rows, z.f, (void*)kept), z.co, part, s);
+    if (e != hipSuccess) return e;
+    const Back b = back_of(z);
+    const Operand gg{{g, g + z.f * 2}, {z.f * 4, z.f * 4}, z.rows};
+    Target o[3] = {target(gx, z.c, z.rows, z.c), target(gwg, z.c, 2 * z.f, z.c), target(gwd, z.f, z.co, z.f)};
+    o[1].out[1] = gwu;
+    o[1].ld[1] = z.c;
+    o[1].half = z.f;
+    BackArgs p{};
+    JoinArgs j{};
+    for (int i = 0, joins = 0; i < 3; ++i) {
+        if (!o[i].out[0]) continue;  // not wanted: no blocks
+        p.p[i] = i == 0   ? args_of(gg, operand(wg, wu, z.c), o[0], z.f, 2, b.c[0], part)
+                 : i == 1 ? args_of(dense(g, 2 * z.f, 2 * z.f), operand(x, z.c), o[1], z.rows, 1, b.c[1], part)
+                          : args_of(operand(gy, z.co), dense(h, z.f, z.f), o[2], z.rows, 1, b.c[2], part);
+        p.blocks[i] = (uint32_t)b.c[i].blocks;
+        if (b.c[i].splits == 1) continue;
+        part += part_bytes(b.c[i], b.m[i], b.n[i], TO_STORE) / 4;
+        j.o[joins] = p.p[i].o;
+        j.splits[joins] = b.c[i].splits;
+        j.blocks[joins++] = grid_for((uint64_t)(b.m[i] * b.n[i] / 4), 256);
     }
-    if (e == hipSuccess && gwg) {
-        Target o = target(gwg, z.c, 2 * z.f, z.c);
-        o.out[1] = gwu;
-        o.ld[1] = z.c;
-        o.half = z.f;
-        e = product<T, true, true, TO_STORE, ACT_SILU>(dense(g, 2 * z.f, 2 * z.f), operand(x, z.c), o, z.rows, part, s);
-    }
-    if (e == hipSuccess && gwd)
-        e = product<T, true, true, TO_STORE, ACT_SILU>(operand(gy, z.co), dense(h, z.f, z.f), target(gwd, z.f, z.co, z.f), z.rows,
-                                                       part, s);
-    return e;
+    const dim3 grid(p.blocks[0] + p.blocks[1] + p.blocks[2]);
+    if (grid.x == 0) return hipSuccess;
+    if (b.shape == WIDE) hipLaunchKernelGGL((k_ff_back<T, Wide>), grid, dim3(Wide::THREADS), 0, s, p);
+    else if (b.shape == MID) hipLaunchKernelGGL((k_ff_back<T, Mid>), grid, dim3(Mid::THREADS), 0, s, p);
+    else hipLaunchKernelGGL((k_ff_back<T, Small>), grid, dim3(Small::THREADS), 0, s, p);
+    if (j.blocks[0])
+        hipLaunchKernelGGL((k_ff_joins<T>), dim3(j.blocks[0] + j.blocks[1] + j.blocks[2]), dim3(256), 0, s, j);
+    return hipGetLastError();
 }
 
 // Rows on 16 bytes, and those of a tile within 31 bits.

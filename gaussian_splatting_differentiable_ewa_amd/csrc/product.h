@@ -78,6 +78,25 @@ struct Panel {
 
 constexpr uint32_t PAST = 0x80000000u;  // an offset past every buffer: such loads give zeros
 
+// `bytes` from p on, as the loads take it.
+typedef uint32_t Buffer __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ Buffer buffer_of(const char* p, uint32_t bytes)
+{
+    const uint64_t at = (uint64_t)p;
+    return Buffer{(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, bytes, 0x00027000u};
+}
+
+// 16 bytes a lane from a buffer straight to LDS, lane after lane. In assembly
+// because the compiler, which would have to keep these apart from reads of other
+// stages, waits for all of them at a read where it cannot (two products in one
+// kernel). They are waited for, and kept from reads, by `ready` below alone.
+// M0 and a buffer from vector instructions need the wait states in between.
+__device__ __forceinline__ void load_lds(Buffer src, uint32_t offset, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(src)
+                 : "memory", "m0");
+}
+
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
 
 // Loads of a panel: WAVES waves, 16 bytes a lane, 1024 an instruction. The LDS
@@ -107,13 +126,11 @@ struct PanelLoad {
     }
     // Load i of a stage from what is left of the matrix, `k` bytes of them of the
     // rows' own (behind the last stage of k a row goes on with what is not).
-    __device__ __forceinline__ void one(__amdgpu_buffer_rsrc_t src, char* lds, int i, int k) const
+    __device__ __forceinline__ void one(Buffer src, uint32_t lds, int i, int k) const
     {
         static_assert(TR || KB == 64 || PER % 2 == 0, "a load's chunk goes by whether it is odd");
         const int chunk = chunk_of(row_of(wave, KB == 64 ? 0 : i & 1));
-        const uint32_t at = TR || chunk * 16 < k ? off[i] : PAST;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            src, (__attribute__((address_space(3))) void*)(lds + (wave * PER + i) * 1024), 16, at, 0, 0, 0);
+        load_lds(src, TR || chunk * 16 < k ? off[i] : PAST, lds + (wave * PER + i) * 1024);
     }
 };
 
@@ -172,11 +189,13 @@ struct Operand {
     int64_t rows;   // of one matrix
 };
 
-template <int BM_, int BN_, int WM_, int WN_, int KB_, int STAGES_>
+// BM x BN elements by WM x WN waves. KG groups of such waves, each with stages of
+// its own, share the sum over k; their sums meet in LDS, in order, in the first.
+template <int BM_, int BN_, int WM_, int WN_, int KB_, int STAGES_, int KG_ = 1>
 struct TileShape {
-    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KB = KB_, STAGES = STAGES_;
-    static constexpr int WAVES = WM * WN, MT = BM / WM / 32, NT = BN / WN / 32;
-    static constexpr int PER_SIMD = MT * NT > 8 ? 1 : 2;  // waves that share a SIMD's registers
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KB = KB_, STAGES = STAGES_, KG = KG_;
+    static constexpr int WAVES = WM * WN, THREADS = WAVES * KG * 64, MT = BM / WM / 32, NT = BN / WN / 32;
+    static constexpr int PER_SIMD = (THREADS / 64 + 3) / 4;  // waves that share a SIMD's registers
 };
 
 // The stages a workgroup walks: [first, last) of all segments' stages.
@@ -191,7 +210,9 @@ struct TileProduct {
     static constexpr int KE = S::KB / 2;  // elements of a stage
     using LoadA = PanelLoad<S::BM, S::KB, ATR, S::WAVES>;
     using LoadB = PanelLoad<S::BN, S::KB, BTR, S::WAVES, PAIR ? S::BN / S::WN / 2 : 0>;
-    static constexpr int A_BYTES = LoadA::P::BYTES, STAGE = A_BYTES + LoadB::P::BYTES, LDS = STAGE * S::STAGES;
+    static constexpr int A_BYTES = LoadA::P::BYTES, STAGE = A_BYTES + LoadB::P::BYTES, GROUP = STAGE * S::STAGES, LDS = GROUP * S::KG;
+    // at the end: the other groups' sums, and below them a scratch for each wave of the first
+    static constexpr int SUMS = S::MT * S::NT * 4096, FREE = LDS - (S::KG - 1) * S::WAVES * SUMS, SCRATCH = FREE / S::WAVES / 16 * 16;
     static constexpr int LOADS = LoadA::PER + LoadB::PER;
 
     // An operand from the next stage on: its address, the bytes up to its end and
@@ -208,10 +229,10 @@ struct TileProduct {
             step = TR ? KE * ld : KE * 2;
         }
         // as a buffer (an operand's tile is below 2^31), or an empty one
-        __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(bool any) const
+        __device__ __forceinline__ Buffer buffer(bool any) const
         {
             const uint32_t n = (uint32_t)(bytes >> 31) ? 0x7fffffffu : (uint32_t)bytes;
-            return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, any ? (int)n : 0, 0x00027000);
+            return buffer_of(p, any ? n : 0u);
         }
         __device__ __forceinline__ void next()
         {
@@ -241,14 +262,19 @@ struct TileProduct {
         // `blocks` of the stage's 4 count; the bytes behind them may hold anything.
         static __device__ __forceinline__ int mine(int x, int blocks)
         {
-            if (blocks < 4) x &= (1 << 8 * blocks) - 1;
+            if (blocks < 4) x &= blocks > 0 ? (1 << 8 * blocks) - 1 : 0;
             return (uint32_t)x >> (lane_id() >> 5) * 16;
         }
     };
 
-    static __device__ __forceinline__ void run(char* __restrict__ lds, const Operand& a, const Operand& b, int64_t m0,
-                                               int64_t n0, const Walk& w, int wave, acc16 (&acc)[S::MT][S::NT])
+    // The sums of the first group's waves.
+    static __device__ __forceinline__ void run(char* all, const Operand& a, const Operand& b, int64_t m0,
+                                               int64_t n0, Walk w, int group, int wave, acc16 (&acc)[S::MT][S::NT])
     {
+        const int per = (w.last - w.first + S::KG - 1) / S::KG;
+        char* lds = all + group * GROUP;
+        w.first += group * per;
+        w.last = min(w.last, w.first + per);
         constexpr bool FOUR = std::is_same<T, fp4>::value;
         static_assert(!FOUR || S::KB == 64, "one dword of scales a stage");
         // loads that may be out when a stage has to be there (the fewest that follow its own: in the first
@@ -272,14 +298,14 @@ struct TileProduct {
         Feed<BTR> fb;
         fa.at(a, w.first >= w.stages, m0, w.k, (int64_t)in * KE);
         fb.at(b, mine, n0, w.k, (int64_t)in * KE);
-        __amdgpu_buffer_rsrc_t from_a, from_b;  // of the stage whose loads are being issued, and where to
+        Buffer from_a, from_b;  // of the stage whose loads are being issued, and where to
         int k_of;
-        char* to;
-        auto prepare = [&](char* stage) __attribute__((always_inline)) {
+        uint32_t to;
+        auto prepare = [&](const char* stage) __attribute__((always_inline)) {
             from_a = fa.buffer(left > 0);
             from_b = fb.buffer(left > 0);
             k_of = k;
-            to = stage;
+            to = uniform(lds_address(stage));
             --left, ++in, k -= KE * 2;
             fa.next();
             fb.next();
@@ -343,7 +369,7 @@ struct TileProduct {
 #pragma unroll
         for (int i = 0; i < READS; ++i) read(lds, 0, 0, i);
         int now = 0;
-        for (int t = w.first; t < w.last; ++t) {
+        for (int t = w.first, end = w.first + per; t < end; ++t) {
             const char* stage = lds + now * STAGE;
             const int next = now == S::STAGES - 1 ? 0 : now + 1;
             if constexpr (FOUR) {
@@ -387,6 +413,31 @@ struct TileProduct {
         }
         // what was loaded past the end has landed and all reads are done: LDS is free
         ready(std::integral_constant<int, 0>{});
+        if constexpr (S::KG > 1) {
+            float4v* at = (float4v*)(all + FREE + wave * SUMS) + lane_id();
+            const auto each = [&](auto f) __attribute__((always_inline)) {
+#pragma unroll
+                for (int i = 0; i < S::MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < S::NT; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) f(acc[i][j], r, ((i * S::NT + j) * 4 + r) * 64);
+            };
+            if (group > 0)
+                each([&](acc16& c, int r, int to) __attribute__((always_inline)) {
+                    at[(group - 1) * S::WAVES * (SUMS / 16) + to] = float4v{c[4 * r], c[4 * r + 1], c[4 * r + 2], c[4 * r + 3]};
+                });
+            __syncthreads();
+            if (group == 0) {
+#pragma unroll
+                for (int g = 0; g < S::KG - 1; ++g)
+                    each([&](acc16& c, int r, int to) __attribute__((always_inline)) {
+                        const float4v x = at[g * S::WAVES * (SUMS / 16) + to];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) c[4 * r + e] += x[e];
+                    });
+            }
+        }
     }
 };
 
