@@ -624,9 +624,10 @@ _pack_matrix = struct.Struct("@Pq").pack
 def _mat(t):
     if t is None:
         return None
-    if t.stride(1) != 1 and t.shape[1] > 1:
+    (rows, columns), (sr, sc) = t.shape, t.stride()
+    if sc != 1 and columns > 1:
         raise GsError("the rows of a matrix must be contiguous")
-    return _pack_matrix(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1])
+    return _pack_matrix(t.data_ptr(), sr if rows > 1 else columns)
 
 
 def gs_layer_norm_fwd(x, w, b, y, stats, eps=1e-5, stream=None):

@@ -174,8 +174,8 @@ def layer_norm(x, w=None, b=None, eps: float = 1e-5):
     _vector("b", b, (c,), x)
     if x.requires_grad or w is not None and w.requires_grad or b is not None and b.requires_grad:
         _lost("LayerNorm")
-    y = torch.empty(rows, c, dtype=x.dtype, device=x.device)
-    stats = torch.empty(2, rows, dtype=torch.float32, device=x.device)
+    y = x.new_empty(rows, c)
+    stats = x.new_empty(2, rows, dtype=torch.float32)
     L.gs_layer_norm_fwd(_packed(x), w, b, y, stats, eps)
     return y, stats
 
@@ -190,10 +190,10 @@ def layer_norm_backward(gy, x, w, stats, bias: bool = True):
     _vector("stats", stats, (2, rows), x)
     if gy.requires_grad or x.requires_grad or w is not None and w.requires_grad:
         _lost("LayerNorm")
-    gx = torch.empty(rows, c, dtype=x.dtype, device=x.device)
+    gx = x.new_empty(rows, c)
     gw = None if w is None else torch.empty_like(w)
-    gb = torch.empty(c, dtype=torch.float32, device=x.device) if bias else None
-    ws = torch.empty(L.layer_norm_bwd_workspace_bytes(rows, c), dtype=torch.uint8, device=x.device)
+    gb = x.new_empty(c, dtype=torch.float32) if bias else None
+    ws = x.new_empty(L.layer_norm_bwd_workspace_bytes(rows, c), dtype=torch.uint8)
     L.gs_layer_norm_bwd(_packed(gy), _packed(x), w, stats, gx, gw, gb, ws)
     return gx, gw, gb
 
@@ -204,35 +204,37 @@ ACTS = {"silu": L.GS_SILU, "gelu": L.GS_GELU}
 
 def _on16(t):
     """t itself, or a copy, so that every row starts on 16 bytes."""
-    if (t.stride(1) == 1 and t.data_ptr() % 16 == 0 and (t.shape[0] <= 1 or t.stride(0) % 8 == 0)
-            and t.stride(0) < 1 << 21):
-        return t
+    if t.data_ptr() % 16 == 0:
+        sr, sc = t.stride()
+        if sc == 1 and (sr % 8 == 0 and 0 <= sr < 1 << 21 or t.shape[0] <= 1):
+            return t
     return t.clone(memory_format=torch.contiguous_format)
 
 
 def _ff_args(x, w_gate, w_up, w_down, act):
     _rows("x", x)
     rows, c = x.shape
-    f = w_gate.shape[0]
-    _rows("w_gate", w_gate, c, x)
-    _rows("w_up", w_up, c, x)
-    _rows("w_down", w_down, f, x)
-    if w_up.shape[0] != f:
-        raise ValueError("w_up must have w_gate's rows")
+    shape, down, kind, device = w_gate.shape, w_down.shape, x.dtype, x.get_device()
+    if len(shape) != 2 or shape[1] != c or w_up.shape != shape or len(down) != 2 or down[1] != shape[0]:
+        raise ValueError(f"w_gate and w_up must be [hidden, {c}] and w_down [out, hidden], got {tuple(shape)}, "
+                         f"{tuple(w_up.shape)} and {tuple(down)}")
+    if (w_gate.dtype is not kind or w_up.dtype is not kind or w_down.dtype is not kind or w_gate.get_device() != device
+            or w_up.get_device() != device or w_down.get_device() != device):
+        raise ValueError("w_gate, w_up and w_down must have x's type and device")
     if act not in ACTS:
         raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
     if x.requires_grad or w_gate.requires_grad or w_up.requires_grad or w_down.requires_grad:
         _lost("GatedFF")
-    return rows, c, f, w_down.shape[0]
+    return rows, c, shape[0], down[0]
 
 
 def _gated_ff(x, w_gate, w_up, w_down, act, keep):
     rows, c, f, co = _ff_args(x, w_gate, w_up, w_down, act)
-    h = torch.empty(rows, f, dtype=x.dtype, device=x.device)
-    kept = torch.empty(L.gated_ff_kept_bytes(rows, f, L.dtype_of(x)), dtype=torch.uint8, device=x.device) if keep else None
-    y = torch.empty(rows, co, dtype=x.dtype, device=x.device)
+    h = x.new_empty(rows, f)
+    kept = x.new_empty(L.gated_ff_kept_bytes(rows, f, L.dtype_of(x)), dtype=torch.uint8) if keep else None
+    y = x.new_empty(rows, co)
     need = L.gated_ff_fwd_workspace_bytes(rows, c, f, co)
-    ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    ws = x.new_empty(need, dtype=torch.uint8) if need else None
     L.gs_gated_ff_fwd(_on16(x), _on16(w_gate), _on16(w_up), _on16(w_down), ACTS[act], h, kept, y, ws)
     return y, h, kept
 
@@ -260,10 +262,10 @@ def gated_ff_backward(gy, x, w_gate, w_up, w_down, h, kept, act: str = "silu"):
     _vector("kept", kept, (L.gated_ff_kept_bytes(rows, f, L.dtype_of(x)),), x, torch.uint8)
     if gy.requires_grad:
         _lost("GatedFF")
-    grads = [torch.empty(s, dtype=x.dtype, device=x.device) for s in ((rows, c), (f, c), (f, c), (co, f))]
-    ws = torch.empty(L.gated_ff_bwd_workspace_bytes(rows, c, f, co), dtype=torch.uint8, device=x.device)
+    grads = x.new_empty(rows, c), x.new_empty(f, c), x.new_empty(f, c), x.new_empty(co, f)
+    ws = x.new_empty(L.gated_ff_bwd_workspace_bytes(rows, c, f, co), dtype=torch.uint8)
     L.gs_gated_ff_bwd(_on16(gy), _on16(x), _on16(w_gate), _on16(w_up), _on16(w_down), h, kept, ACTS[act], *grads, ws)
-    return tuple(grads)
+    return grads
 
 
 # ---- linear layers in 4 bits ----------------------------------------------------
@@ -272,9 +274,10 @@ FOUR = 32  # values that share a scale
 
 def _on16_rows(t):
     """t itself, or a copy, so that every row starts on 16 bytes, whatever its type."""
-    if (t.stride(1) == 1 and t.data_ptr() % 16 == 0 and (t.shape[0] <= 1 or t.stride(0) * t.element_size() % 16 == 0)
-            and t.stride(0) < 1 << 21):
-        return t
+    if t.data_ptr() % 16 == 0:
+        sr, sc = t.stride()
+        if sc == 1 and (sr * t.element_size() % 16 == 0 and 0 <= sr < 1 << 21 or t.shape[0] <= 1):
+            return t
     return t.clone(memory_format=torch.contiguous_format)
 
 
@@ -322,9 +325,9 @@ def linear4(x, weights):
     codes, scales = _four(weights, c, x)
     if x.requires_grad:
         _lost("a 16-bit layer")
-    y = torch.empty(rows, codes.shape[0], dtype=x.dtype, device=x.device)
+    y = x.new_empty(rows, codes.shape[0])
     if codes.shape[0]:
-        ws = torch.empty(L.linear_fp4_workspace_bytes(rows, c, codes.shape[0]), dtype=torch.uint8, device=x.device)
+        ws = x.new_empty(L.linear_fp4_workspace_bytes(rows, c, codes.shape[0]), dtype=torch.uint8)
         L.gs_linear_fp4(_on16_rows(x), codes, scales, y, ws)
     return y
 
