@@ -96,6 +96,11 @@ __device__ __forceinline__ void load_lds(Buffer src, uint32_t offset, uint32_t l
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(src)
                  : "memory", "m0");
 }
+__device__ __forceinline__ void load_lds_4(Buffer src, uint32_t offset, uint32_t lds)  // 4 bytes a lane
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(src)
+                 : "memory", "m0");
+}
 
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
 
@@ -210,10 +215,12 @@ struct TileProduct {
     static constexpr int KE = S::KB / 2;  // elements of a stage
     using LoadA = PanelLoad<S::BM, S::KB, ATR, S::WAVES>;
     using LoadB = PanelLoad<S::BN, S::KB, BTR, S::WAVES, PAIR ? S::BN / S::WN / 2 : 0>;
-    static constexpr int A_BYTES = LoadA::P::BYTES, STAGE = A_BYTES + LoadB::P::BYTES, GROUP = STAGE * S::STAGES, LDS = GROUP * S::KG;
+    static constexpr int A_BYTES = LoadA::P::BYTES, STAGE = A_BYTES + LoadB::P::BYTES, GROUP = STAGE * S::STAGES;
+    static constexpr bool FOUR = std::is_same<T, fp4>::value;
+    static constexpr int LDS = GROUP * S::KG + (FOUR ? 3 * (S::BM + S::BN) * 16 : 0);
     // at the end: the other groups' sums, and below them a scratch for each wave of the first
-    static constexpr int SUMS = S::MT * S::NT * 4096, FREE = LDS - (S::KG - 1) * S::WAVES * SUMS, SCRATCH = FREE / S::WAVES / 16 * 16;
-    static constexpr int LOADS = LoadA::PER + LoadB::PER;
+    static constexpr int SUMS = S::MT * S::NT * 4096, FREE = GROUP * S::KG - (S::KG - 1) * S::WAVES * SUMS, SCRATCH = FREE / S::WAVES / 16 * 16;
+    static constexpr int PANEL_LOADS = LoadA::PER + LoadB::PER, LOADS = PANEL_LOADS + FOUR;
 
     // An operand from the next stage on: its address, the bytes up to its end and
     // what a stage adds to the one and takes from the other.
@@ -241,29 +248,41 @@ struct TileProduct {
         }
     };
 
-    // A lane's scales of one operand: 4 bytes a stage and row, the upper two the upper lane half's.
-    template <int TILES>
+    // Scales of 4-bit operands: 4 bytes a stage and row, loaded 4 stages at a time
+    // (16 bytes of each of 16 rows an instruction: a load of 4 bytes of each of 64
+    // rows takes the address path four times as long), [rows of A, rows of B][4
+    // stages] in a ring of three, a group ahead of its stages.
+    static constexpr int SCALE_GROUP = (S::BM + S::BN) * 16, SCALE_LOADS = SCALE_GROUP / 256 / S::WAVES;
     struct Scales {
-        __amdgpu_buffer_rsrc_t src;
-        uint32_t off, rows32;
-        __device__ __forceinline__ Scales(const Operand& o, int64_t r0, int row, int bytes_of_row)
+        static_assert(S::WAVES % 2 == 0 && S::BM == S::BN, "a wave loads of one operand");
+        Buffer src;
+        uint32_t off, rows16, lds;
+        __device__ __forceinline__ Scales(const Operand& a, const Operand& b, int64_t m0, int64_t n0, int bytes_of_row,
+                                          const char* at, int wave)
         {
-            const int64_t ld = o.ld[1], bytes = (o.rows - 1 - r0) * ld + bytes_of_row;
-            src = __builtin_amdgcn_make_buffer_rsrc((void*)(o.data[1] + r0 * ld), 0,
-                                                    bytes < 0x7fffffff ? (int)bytes : 0x7fffffff, 0x00027000);
-            off = (uint32_t)(row + (lane_id() & 31)) * (uint32_t)ld;
-            rows32 = 32 * (uint32_t)ld;
+            const int first = wave % (S::WAVES / 2) * SCALE_LOADS * 16;
+            const bool second = wave >= S::WAVES / 2;
+            const int64_t ld = second ? b.ld[1] : a.ld[1], r0 = second ? n0 : m0;
+            const int64_t bytes = ((second ? b.rows : a.rows) - 1 - r0) * ld + bytes_of_row;
+            src = buffer_of((second ? b.data[1] : a.data[1]) + r0 * ld, (uint32_t)(bytes >> 31) ? 0x7fffffffu : (uint32_t)bytes);
+            off = (uint32_t)(first + lane_id() / 4) * (uint32_t)ld + lane_id() % 4 * 4;
+            rows16 = 16 * (uint32_t)ld;
+            lds = uniform(lds_address(at)) + wave * SCALE_LOADS * 256;
         }
-        __device__ __forceinline__ void load(int stage, int (&out)[TILES]) const
+        __device__ __forceinline__ void load(int group, int i) const
         {
-#pragma unroll
-            for (int i = 0; i < TILES; ++i) out[i] = __builtin_amdgcn_raw_buffer_load_b32(src, off, i * rows32 + stage * 4, 0);
+            load_lds_4(src, off + (i * rows16 + group * 16), uniform(lds + group % 3 * SCALE_GROUP + i * 256));
         }
-        // `blocks` of the stage's 4 count; the bytes behind them may hold anything.
-        static __device__ __forceinline__ int mine(int x, int blocks)
+        // Those of the lane's row of 32 from `first` on (of both operands), and its half's two bytes of them,
+        // of the `blocks` that count of a stage's 4 (the others may hold anything).
+        static __device__ __forceinline__ uint32_t all(const char* at, int stage, int first)
         {
-            if (blocks < 4) x &= blocks > 0 ? (1 << 8 * blocks) - 1 : 0;
-            return (uint32_t)x >> (lane_id() >> 5) * 16;
+            return *(const uint32_t*)(at + stage / 4 % 3 * SCALE_GROUP + (first + (lane_id() & 31)) * 16 + stage % 4 * 4);
+        }
+        static __device__ __forceinline__ int half(uint32_t x, int blocks)
+        {
+            if (blocks < 4) x &= blocks > 0 ? (1u << 8 * blocks) - 1 : 0u;
+            return x >> (lane_id() >> 5) * 16;
         }
     };
 
@@ -275,11 +294,9 @@ struct TileProduct {
         char* lds = all + group * GROUP;
         w.first += group * per;
         w.last = min(w.last, w.first + per);
-        constexpr bool FOUR = std::is_same<T, fp4>::value;
-        static_assert(!FOUR || S::KB == 64, "one dword of scales a stage");
-        // loads that may be out when a stage has to be there (the fewest that follow its own: in the first
-        // iteration scales are loaded once behind them, later more often), and the first part of a stage's
-        constexpr int STEPS = S::KB / 32, LATER = (S::STAGES - 2) * LOADS + (FOUR ? S::MT + S::NT : 0);
+        static_assert(!FOUR || (S::KB == 64 && S::KG == 1 && S::STAGES == 4 && 4 % SCALE_LOADS == 0), "the ring of scales");
+        // loads that may be out when a stage has to be there
+        constexpr int STEPS = S::KB / 32, LATER = (S::STAGES - 2) * LOADS;
         // a step is MT groups of matrix instructions; loads go EACH to a group, from the last step's on
         constexpr int EACH = (LOADS + S::MT * STEPS - 1) / (S::MT * STEPS), FIRST = LOADS < EACH * S::MT ? LOADS : EACH * S::MT;
         static_assert(STEPS % 2 == 0 && S::STAGES >= 2 && LATER + FIRST < 64, "steps in pairs; loads out fit the wait's field");
@@ -298,6 +315,7 @@ struct TileProduct {
         Feed<BTR> fb;
         fa.at(a, w.first >= w.stages, m0, w.k, (int64_t)in * KE);
         fb.at(b, mine, n0, w.k, (int64_t)in * KE);
+        int of_stage = -1;  // whose loads are being issued, counted from the first
         Buffer from_a, from_b;  // of the stage whose loads are being issued, and where to
         int k_of;
         uint32_t to;
@@ -307,15 +325,22 @@ struct TileProduct {
             k_of = k;
             to = uniform(lds_address(stage));
             --left, ++in, k -= KE * 2;
+            ++of_stage;
             fa.next();
             fb.next();
         };
+        // with stage s, one of the loads of the scales of the four stages that follow the four of s
+        const int scale_row = (int)(w.k + 31) / 32 * 4;
+        const char* scales = all + GROUP * S::KG;
+        const Scales scale(a, b, m0, n0, scale_row, scales, wave);
+        auto scale_load = [&]() __attribute__((always_inline)) { scale.load(of_stage / 4 + 1, of_stage % SCALE_LOADS); };
         // the loads of group `g` behind the barrier
         auto load = [&](int g) __attribute__((always_inline)) {
 #pragma unroll
             for (int i = g * EACH; i < (g + 1) * EACH && i < LOADS; ++i) {
                 if (i < LoadA::PER) load_a.one(from_a, to, i, k_of);
-                else load_b.one(from_b, to + A_BYTES, i - LoadA::PER, k_of);
+                else if (i < PANEL_LOADS) load_b.one(from_b, to + A_BYTES, i - LoadA::PER, k_of);
+                else if constexpr (FOUR) scale_load();
             }
         };
         // after a stage's last load: on to the second segment?
@@ -342,10 +367,8 @@ struct TileProduct {
             else ra[to][i - S::NT] = read_a(stage, i - S::NT, step);
         };
         constexpr int READS = S::NT + S::MT;
-        const int scale_row = (int)(w.k + 31) / 32 * 4;
-        const Scales<S::MT> scale_a(a, m0, wave / S::WN * (S::BM / S::WM), scale_row);
-        const Scales<S::NT> scale_b(b, n0, wave % S::WN * (S::BN / S::WN), scale_row);
-        int sa[S::MT], sb[S::NT], next_sa[S::MT], next_sb[S::NT];
+        int sa[S::MT], sb[S::NT];
+        uint32_t next_sa[S::MT], next_sb[S::NT];
         auto multiply = [&](int step, int i) __attribute__((always_inline)) {
             const int from = step & 1;
 #pragma unroll
@@ -355,8 +378,8 @@ struct TileProduct {
             }
         };
         if constexpr (FOUR) {
-            scale_a.load(w.first, next_sa);
-            scale_b.load(w.first, next_sb);
+#pragma unroll
+            for (int i = 0; i < SCALE_LOADS; ++i) scale.load(0, i);
         }
 #pragma unroll
         for (int t = 0; t < S::STAGES; ++t) {
@@ -368,6 +391,13 @@ struct TileProduct {
         ready(std::integral_constant<int, (S::STAGES - 2) * LOADS + FIRST>{});
 #pragma unroll
         for (int i = 0; i < READS; ++i) read(lds, 0, 0, i);
+        auto next_scales = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < S::MT; ++i) next_sa[i] = Scales::all(scales, t, wave / S::WN * (S::BM / S::WM) + 32 * i);
+#pragma unroll
+            for (int j = 0; j < S::NT; ++j) next_sb[j] = Scales::all(scales, t, S::BM + wave % S::WN * (S::BN / S::WN) + 32 * j);
+        };
+        if constexpr (FOUR) next_scales(w.first);
         int now = 0;
         for (int t = w.first, end = w.first + per; t < end; ++t) {
             const char* stage = lds + now * STAGE;
@@ -375,11 +405,10 @@ struct TileProduct {
             if constexpr (FOUR) {
                 const int blocks = (int)(w.k - (int64_t)t * KE) / 8;
 #pragma unroll
-                for (int i = 0; i < S::MT; ++i) sa[i] = Scales<S::MT>::mine(next_sa[i], blocks);
+                for (int i = 0; i < S::MT; ++i) sa[i] = Scales::half(next_sa[i], blocks);
 #pragma unroll
-                for (int j = 0; j < S::NT; ++j) sb[j] = Scales<S::NT>::mine(next_sb[j], blocks);
-                scale_a.load(t + 1, next_sa);  // past the row's end: not used
-                scale_b.load(t + 1, next_sb);
+                for (int j = 0; j < S::NT; ++j) sb[j] = Scales::half(next_sb[j], blocks);
+                if (t + 1 < end) next_scales(t + 1);
             }
             // The order is kept as written: between two groups of matrix instructions go a few of the next
             // step's reads and a load. Of the last step, one group stands before the barrier.
