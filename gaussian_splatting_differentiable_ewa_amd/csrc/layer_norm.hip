@@ -98,7 +98,15 @@ struct LayerArgs {
     float eps;
 };
 
-template <typename T, int VEC, int NV, int NT>
+// 1 / sqrt(v), one rounding off at most; the hardware's takes no subnormals.
+__device__ __forceinline__ float inverse_root(float v)
+{
+    const bool tiny = v < 0x1p-100f;
+    return __builtin_amdgcn_rsqf(tiny ? v * 0x1p60f : v) * (tiny ? 0x1p30f : 1.f);
+}
+
+// FULL: the threads hold exactly a row; else what is past it is masked.
+template <typename T, int VEC, int NV, int NT, int AHEAD, bool FULL>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_fwd(const LayerArgs a)
 {
     constexpr int PER = NT < 256 ? 256 / NT : 1;
@@ -109,36 +117,43 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_fwd(const LayerAr
     const int64_t r0 = run * a.run, r1 = r0 + a.run < a.rows ? r0 + a.run : a.rows;
     if (r0 >= a.rows) return;  // whole waves (NT >= 64); with NT > 64 the whole workgroup
     const T* px = (const T*)a.x;
-    const float n = (float)a.channels;
-    typename C::template Raw<T> next;
-    col.load(px + r0 * a.stride_x, next);
-    float w[NV][VEC], b[NV][VEC];
+    const float inv = 1.f / (float)a.channels;
+    typename C::template Raw<T> next[AHEAD];
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d)
+        if (r0 + d < r1) col.load(px + (r0 + d) * a.stride_x, next[d]);
+    float w[NV][VEC], b[NV][VEC], mask[NV][VEC];
     col.load_vec(a.w, w, 1.f);
     col.load_vec(a.b, b, 0.f);
+    GS_EACH(mask[i][e] = col.has(i, e) ? 1.f : 0.f)
     int flip = 0;
-    for (int64_t r = r0; r < r1; ++r) {
+    const auto one = [&](int64_t r, typename C::template Raw<T>& raw) __attribute__((always_inline)) {
         float x[NV][VEC], sum[1] = {0.f};
-        GS_EACH(x[i][e] = (float)next.v[i][e]; sum[0] += x[i][e])
-        if (r + 1 < r1) col.load(px + (r + 1) * a.stride_x, next);
+        GS_EACH(x[i][e] = (float)raw.v[i][e]; sum[0] += x[i][e])
+        if (r + AHEAD < r1) col.load(px + (r + AHEAD) * a.stride_x, raw);
         row_sums<NT, 1>(sum, s_buf, flip);
         flip ^= 1;
-        const float mean = sum[0] / n;
+        const float mean = sum[0] * inv;
         float v[2] = {0.f, 0.f};
-        GS_EACH(x[i][e] -= mean; const float d = col.has(i, e) ? x[i][e] : 0.f; v[0] += d; v[1] = fmaf(d, d, v[1]))
+        GS_EACH(x[i][e] -= mean; const float d = FULL ? x[i][e] : x[i][e] * mask[i][e]; v[0] += d; v[1] = fmaf(d, d, v[1]))
         row_sums<NT, 2>(v, s_buf2, flip);
-        const float rest = v[0] / n, var = fmaf(-rest, rest, v[1] / n);
-        const float rs = 1.f / sqrtf((var < 0.f ? 0.f : var) + a.eps);
-        GS_EACH(x[i][e] -= rest)
-        GS_EACH(x[i][e] = fmaf(x[i][e] * rs, w[i][e], b[i][e]))
+        const float rest = v[0] * inv, var = fmaf(-rest, rest, v[1] * inv);
+        const float rs = inverse_root((var < 0.f ? 0.f : var) + a.eps);
+        const float shift = -rest * rs;
+        GS_EACH(x[i][e] = fmaf(fmaf(x[i][e], rs, shift), w[i][e], b[i][e]))
         col.store((T*)a.out + r * a.channels, x);
         if (threadIdx.x % NT == 0) {
             a.stats[r] = mean + rest;
             a.stats[a.rows + r] = rs;
         }
-    }
+    };
+    for (int64_t r = r0; r < r1; r += AHEAD)
+#pragma unroll
+        for (int d = 0; d < AHEAD; ++d)
+            if (r + d < r1) one(r + d, next[d]);
 }
 
-template <typename T, int VEC, int NV, int NT>
+template <typename T, int VEC, int NV, int NT, int AHEAD>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_bwd(const LayerArgs a)
 {
     constexpr int PER = NT < 256 ? 256 / NT : 1;
@@ -150,30 +165,38 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_bwd(const LayerAr
     if (r0 >= a.rows) return;  // whole waves (NT >= 64); with NT > 64 the whole workgroup
     const T *px = (const T*)a.x, *pg = (const T*)a.gy;
     const float inv = 1.f / (float)a.channels;
-    typename C::template Raw<T> next_x, next_g;
-    col.load(px + r0 * a.stride_x, next_x);
-    col.load(pg + r0 * a.stride_gy, next_g);
+    typename C::template Raw<T> next_x[AHEAD], next_g[AHEAD];
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d)
+        if (r0 + d < r1) {
+            col.load(px + (r0 + d) * a.stride_x, next_x[d]);
+            col.load(pg + (r0 + d) * a.stride_gy, next_g[d]);
+        }
     float w[NV][VEC], sum_w[NV][VEC], sum_b[NV][VEC];
     col.load_vec(a.w, w, 1.f);
     GS_EACH(sum_w[i][e] = 0.f; sum_b[i][e] = 0.f)
     int flip = 0;
-    for (int64_t r = r0; r < r1; ++r) {
+    const auto one = [&](int64_t r, typename C::template Raw<T>& raw_x, typename C::template Raw<T>& raw_g) __attribute__((always_inline)) {
         const float mean = a.stats[r], rs = a.stats[a.rows + r];
         float xh[NV][VEC], d[NV][VEC], v[2] = {0.f, 0.f};
         // past the channels gy is zero, and with it every term
-        GS_EACH(xh[i][e] = ((float)next_x.v[i][e] - mean) * rs; const float g = (float)next_g.v[i][e];
+        GS_EACH(xh[i][e] = ((float)raw_x.v[i][e] - mean) * rs; const float g = (float)raw_g.v[i][e];
                 sum_w[i][e] = fmaf(g, xh[i][e], sum_w[i][e]); sum_b[i][e] += g; d[i][e] = g * w[i][e];
                 v[0] += d[i][e]; v[1] = fmaf(d[i][e], xh[i][e], v[1]))
-        if (r + 1 < r1) {
-            col.load(px + (r + 1) * a.stride_x, next_x);
-            col.load(pg + (r + 1) * a.stride_gy, next_g);
+        if (r + AHEAD < r1) {
+            col.load(px + (r + AHEAD) * a.stride_x, raw_x);
+            col.load(pg + (r + AHEAD) * a.stride_gy, raw_g);
         }
         row_sums<NT, 2>(v, s_buf, flip);
         flip ^= 1;
         const float m0 = v[0] * inv, m1 = v[1] * inv;
         GS_EACH(d[i][e] = rs * fmaf(-m1, xh[i][e], d[i][e] - m0))
         col.store((T*)a.out + r * a.channels, d);
-    }
+    };
+    for (int64_t r = r0; r < r1; r += AHEAD)
+#pragma unroll
+        for (int d = 0; d < AHEAD; ++d)
+            if (r + d < r1) one(r + d, next_x[d], next_g[d]);
     if (a.part) {
         float* p = a.part + run * 2 * a.channels;
         col.store(p, sum_w);
@@ -198,11 +221,14 @@ template <typename T, int VEC, int NV, int NT>
 static hipError_t layer_launch(const LayerArgs& a, bool backward, hipStream_t s)
 {
     constexpr int PER = NT < 256 ? 256 / NT : 1, THREADS = NT < 256 ? 256 : NT;
+    constexpr int AHEAD = 2, BACK = 1;
     const dim3 grid(grid_for((uint64_t)((a.rows + a.run - 1) / a.run), PER));
     if (backward)
-        hipLaunchKernelGGL((k_layer_bwd<T, VEC, NV, NT>), grid, dim3(THREADS), 0, s, a);
+        hipLaunchKernelGGL((k_layer_bwd<T, VEC, NV, NT, BACK>), grid, dim3(THREADS), 0, s, a);
+    else if (a.channels == VEC * NV * NT)
+        hipLaunchKernelGGL((k_layer_fwd<T, VEC, NV, NT, AHEAD, true>), grid, dim3(THREADS), 0, s, a);
     else
-        hipLaunchKernelGGL((k_layer_fwd<T, VEC, NV, NT>), grid, dim3(THREADS), 0, s, a);
+        hipLaunchKernelGGL((k_layer_fwd<T, VEC, NV, NT, AHEAD, false>), grid, dim3(THREADS), 0, s, a);
     return hipGetLastError();
 }
 

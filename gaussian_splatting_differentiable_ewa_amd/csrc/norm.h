@@ -6,6 +6,13 @@
 
 namespace gs {
 
+// A barrier for LDS alone: __syncthreads also waits for the loads of the next
+// row and the stores of the last one.
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // Sums of N values over the NT threads that share a row. `buf` holds 2 x
 // (NT / 64) x N floats and alternates by `flip`, so one barrier per call is
 // enough: a wave can be at most one call ahead of the slowest.
@@ -22,7 +29,7 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* buf, int flip)
 #pragma unroll
             for (int i = 0; i < N; ++i) mine[wave * N + i] = v[i];
         }
-        __syncthreads();
+        lds_barrier();
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float s = 0.f;
