@@ -81,9 +81,15 @@ struct RaggedCols {
     __device__ __forceinline__ void load_vec(const float* p, float (&out)[NV][VEC], float other) const
     {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i) {
+            if (p && n[i] == VEC) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) out[i][e] = p && has(i, e) ? p[at(i) + e] : other;
+                for (int e = 0; e < VEC; e += 4) copy<float, 4>(out[i] + e, p + at(i) + e);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) out[i][e] = p && has(i, e) ? p[at(i) + e] : other;
+            }
+        }
     }
 };
 
