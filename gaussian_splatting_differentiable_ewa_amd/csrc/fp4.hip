@@ -122,6 +122,7 @@ struct FourArgs {
 };
 
 using FourTile = TileShape<256, 256, 2, 4, 64, 4>;
+using FourMid = TileShape<128, 128, 2, 2, 64, 4>;
 using FourSmall = TileShape<64, 64, 2, 2, 64, 4>;
 
 template <typename T, typename S>
@@ -167,10 +168,70 @@ __device__ __forceinline__ void four_product(char* lds, const FourArgs& p)
 }
 
 template <typename T, typename S>
-__global__ __launch_bounds__(S::THREADS, S::PER_SIMD) void k_fp4_product(const FourArgs p)
+__global__ __launch_bounds__(S::THREADS, 2) void k_fp4_product(const FourArgs p)
 {
     __shared__ alignas(16) char s_lds[TileProduct<fp4, S, false, false, false>::LDS];
     four_product<T, S>(s_lds, p);
+}
+
+// Few rows (16 at most): one launch. A wave takes 16 rows of the weights and the
+// tokens straight to registers, 128 values of each a step, a lane one block of
+// 32 of either with its scale; it quantises the tokens' blocks itself (every
+// workgroup does, which costs less than a launch before it). The waves of a
+// workgroup share the sum, and theirs meet in LDS.
+constexpr int FOUR_FEW = 16, FEW_WAVES = 8;
+
+template <typename T>
+__global__ __launch_bounds__(FEW_WAVES * 64) void k_fp4_few(const FourArgs p, const T* __restrict__ x, int64_t stride_x)
+{
+    typedef int v8i __attribute__((ext_vector_type(8)));
+    __shared__ float4v s_sum[FEW_WAVES][64];
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * 16, row = n0 + r < p.n ? n0 + r : p.n - 1;
+    const int rows = (int)p.m, blocks = (int)p.walk.k / 8;
+    const uint4* codes = (const uint4*)(p.b.data[0] + row * p.b.ld[0]);
+    const uint8_t* scales = (const uint8_t*)p.b.data[1] + row * p.b.ld[1];
+    const T* mine = x + (r < rows ? r : rows - 1) * stride_x;
+    float4v acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+    for (int b = wave * 4 + q; b < (blocks + 3) / 4 * 4; b += FEW_WAVES * 4) {
+        v8i w = {}, t = {};
+        int sw = 0, st = 0;
+        if (b < blocks) {
+            const uint4 c = codes[b];
+            sw = scales[b];
+            float v[4][8];
+            uint32_t most = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                load_f32<T, 8>(mine + b * FP4_BLOCK + i * 8, v[i]);
+                most = max(most, largest_bits(v[i]));
+            }
+            st = (int)byte_of(most);
+            const float power = power_of(st);
+            w[0] = c.x, w[1] = c.y, w[2] = c.z, w[3] = c.w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[i] = (int)codes_of(v[i], power);
+        }
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, t, acc, 4, 4, 0, sw, 0, st);
+    }
+    s_sum[wave][lane] = acc;
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int i = 1; i < FEW_WAVES; ++i) acc += s_sum[i][lane];
+    // of the result a lane holds token r, columns 4 q on
+    if (r >= rows) return;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (n0 + 4 * q + e < p.n) ((T*)p.y)[r * p.n + n0 + 4 * q + e] = (T)acc[e];
+}
+
+template <typename T>
+static hipError_t few_as(const FourArgs& p, const gs_matrix* x, hipStream_t s)
+{
+    hipLaunchKernelGGL((k_fp4_few<T>), dim3((unsigned)((p.n + 15) / 16)), dim3(FEW_WAVES * 64), 0, s, p, (const T*)x->data, x->stride);
+    return hipGetLastError();
 }
 
 static int64_t scale_bytes_of(int32_t channels) { return (channels + 127) / 128 * 4; }
@@ -206,15 +267,22 @@ static hipError_t dequantise(const gs_matrix* codes, const gs_matrix* scales, vo
     return hipGetLastError();
 }
 
+template <typename T, typename S>
+static hipError_t product_by(FourArgs& p, hipStream_t s)
+{
+    p.mt = (uint32_t)((p.m + S::BM - 1) / S::BM);
+    p.nt = (uint32_t)((p.n + S::BN - 1) / S::BN);
+    hipLaunchKernelGGL((k_fp4_product<T, S>), dim3(p.mt * p.nt), dim3(S::THREADS), 0, s, p);
+    return hipGetLastError();
+}
+
 template <typename T>
 static hipError_t product_as(FourArgs& p, hipStream_t s)
 {
-    const bool large = ((p.m + 255) / 256) * ((p.n + 255) / 256) >= 128;
-    p.mt = (uint32_t)((p.m + (large ? 255 : 63)) / (large ? 256 : 64));
-    p.nt = (uint32_t)((p.n + (large ? 255 : 63)) / (large ? 256 : 64));
-    if (large) hipLaunchKernelGGL((k_fp4_product<T, FourTile>), dim3(p.mt * p.nt), dim3(FourTile::THREADS), 0, s, p);
-    else hipLaunchKernelGGL((k_fp4_product<T, FourSmall>), dim3(p.mt * p.nt), dim3(FourSmall::THREADS), 0, s, p);
-    return hipGetLastError();
+    const auto tiles = [&](int64_t side) { return ((p.m + side - 1) / side) * ((p.n + side - 1) / side); };
+    if (tiles(256) >= 192) return product_by<T, FourTile>(p, s);
+    if (tiles(128) >= 160) return product_by<T, FourMid>(p, s);
+    return product_by<T, FourSmall>(p, s);
 }
 
 static bool four_sizes_ok(int64_t rows, int32_t channels)
@@ -259,7 +327,7 @@ gs_status gs_dequantise_fp4(const gs_matrix* codes, const gs_matrix* scales, int
 size_t gs_linear_fp4_workspace_bytes(int64_t rows, int32_t channels, int32_t out)
 {
     using namespace gs;
-    if (!four_sizes_ok(rows, channels) || out < 1 || out > (1 << 17)) return 0;
+    if (!four_sizes_ok(rows, channels) || out < 1 || out > (1 << 17) || rows <= FOUR_FEW) return 0;
     return ((size_t)rows * (channels / 2) + 15) / 16 * 16 + (size_t)rows * scale_bytes_of(channels) + 64;
 }
 
@@ -270,21 +338,28 @@ gs_status gs_linear_fp4(const gs_matrix* x, const gs_matrix* codes, const gs_mat
     if (!four_sizes_ok(rows, channels) || out < 1 || out > (1 << 17) || !dtype_ok(dtype)) return GS_ERR_INVALID_ARGUMENT;
     if (rows == 0) return GS_OK;
     if (!x || !x->data || !codes || !codes->data || !scales || !scales->data || !y) return GS_ERR_INVALID_ARGUMENT;
-    if (!ws || ((uintptr_t)ws & 15) || ws_bytes < gs_linear_fp4_workspace_bytes(rows, channels, out)) return GS_ERR_INVALID_ARGUMENT;
+    const size_t need = gs_linear_fp4_workspace_bytes(rows, channels, out);
+    if (need && (!ws || ((uintptr_t)ws & 15) || ws_bytes < need)) return GS_ERR_INVALID_ARGUMENT;
     if (!four_rows_ok(x, elem_bytes(dtype), 16) || !four_rows_ok(codes, 1, 16) || !four_rows_ok(scales, 1, 4) ||
         (uintptr_t)y % elem_bytes(dtype) || ((rows + 63) / 64) * ((out + 63) / 64) >= (1 << 23))
         return GS_ERR_UNSUPPORTED;
     const hipStream_t s = (hipStream_t)stream;
-    char* xc = (char*)ws;
-    char* xs = xc + ((size_t)rows * (channels / 2) + 15) / 16 * 16;
-    if (quantise_as(dtype, x, xc, xs, rows, channels, s) != hipSuccess) return GS_ERR_HIP;
     FourArgs p{};
-    p.a = {{xc, xs}, {channels / 2, scale_bytes_of(channels)}, rows};
     p.b = {{(const char*)codes->data, (const char*)scales->data}, {codes->stride, scales->stride}, out};
     p.walk = {channels / 4, (channels + 127) / 128, 0, (channels + 127) / 128};
     p.y = y;
     p.m = rows;
     p.n = out;
+    if (rows <= FOUR_FEW) {
+        const hipError_t e = dtype == GS_F32   ? few_as<float>(p, x, s)
+                             : dtype == GS_F16 ? few_as<f16>(p, x, s)
+                                               : few_as<bf16>(p, x, s);
+        return e == hipSuccess ? GS_OK : GS_ERR_HIP;
+    }
+    char* xc = (char*)ws;
+    char* xs = xc + ((size_t)rows * (channels / 2) + 15) / 16 * 16;
+    if (quantise_as(dtype, x, xc, xs, rows, channels, s) != hipSuccess) return GS_ERR_HIP;
+    p.a = {{xc, xs}, {channels / 2, scale_bytes_of(channels)}, rows};
     const hipError_t e = dtype == GS_F32 ? product_as<float>(p, s) : (dtype == GS_F16 ? product_as<f16>(p, s) : product_as<bf16>(p, s));
     return e == hipSuccess ? GS_OK : GS_ERR_HIP;
 }

@@ -283,10 +283,12 @@ def _on16_rows(t):
 
 def _four(four, channels, like):
     codes, scales = four
-    for name, t, columns in (("codes", codes, channels // 2), ("scales", scales, (channels + 127) // 128 * 4)):
-        if (t.dim() != 2 or t.dtype is not torch.uint8 or t.shape[1] != columns or t.shape[0] != codes.shape[0]
-                or t.get_device() != like.get_device() or t.stride(1) != 1 or t.stride(0) % 4 or t.data_ptr() % 4):
-            raise ValueError(f"{name} must be uint8 [rows, {columns}] on {like.device}, rows on 4 bytes, as quantise4's")
+    device, (rows, half), (sr, sc), (cr, cc) = like.get_device(), codes.shape, scales.stride(), codes.stride()
+    if (codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or half * 2 != channels
+            or scales.shape != (rows, (channels + 127) // 128 * 4) or codes.get_device() != device
+            or scales.get_device() != device or cc != 1 or sc != 1 or sr % 4 or scales.data_ptr() % 4):
+        raise ValueError(f"the weights must be quantise4's: uint8 [rows, {channels // 2}] and [rows, "
+                         f"{(channels + 127) // 128 * 4}] on {like.device}, scales on 4 bytes")
     return _on16_rows(codes), scales
 
 
@@ -327,7 +329,8 @@ def linear4(x, weights):
         _lost("a 16-bit layer")
     y = x.new_empty(rows, codes.shape[0])
     if codes.shape[0]:
-        ws = x.new_empty(L.linear_fp4_workspace_bytes(rows, c, codes.shape[0]), dtype=torch.uint8)
+        need = L.linear_fp4_workspace_bytes(rows, c, codes.shape[0])
+        ws = x.new_empty(need, dtype=torch.uint8) if need else None
         L.gs_linear_fp4(_on16_rows(x), codes, scales, y, ws)
     return y
 

@@ -1020,7 +1020,7 @@ gs_status gs_quantise_fp4(const gs_matrix* x, int64_t rows, int32_t channels, in
 gs_status gs_dequantise_fp4(const gs_matrix* codes, const gs_matrix* scales, int64_t rows, int32_t channels, int32_t dtype,
                             void* out, void* stream);
 
-/* Workspace of gs_linear_fp4 (bytes); 0 on invalid sizes. */
+/* Workspace of gs_linear_fp4 (bytes); may be 0. */
 size_t gs_linear_fp4_workspace_bytes(int64_t rows, int32_t channels, int32_t out);
 
 /*
@@ -1032,7 +1032,7 @@ size_t gs_linear_fp4_workspace_bytes(int64_t rows, int32_t channels, int32_t out
  *           weights (strides in bytes; a row's last bytes, behind its blocks,
  *           are not used)
  *   y       out [rows][out], contiguous, the type of x
- *   ws      workspace of gs_linear_fp4_workspace_bytes(...)
+ *   ws      workspace of gs_linear_fp4_workspace_bytes(...), or NULL if that is 0
  * Errors: as gs_quantise_fp4, out outside 1..2^17, a small workspace;
  * GS_ERR_UNSUPPORTED also past 2^23 tiles of 64 x 64.
  */

@@ -87,9 +87,9 @@ def test_gated_ff_refusals(lib):
 def test_fp4_refusals(lib):
     quant = dict(x=mat(), rows=10, c=64, t=L.GS_BF16, codes=FAKE, scales=FAKE, s=None)
     back = dict(codes=mat(), scales=mat(), rows=10, c=64, t=L.GS_F32, out=FAKE, s=None)
-    need = L.linear_fp4_workspace_bytes(10, 64, 40)
-    assert need > 0 and L.linear_fp4_workspace_bytes(10, 48, 40) == 0 and L.linear_fp4_workspace_bytes(10, 64, 0) == 0
-    linear = dict(x=mat(), codes=mat(), scales=mat(), rows=10, c=64, n=40, t=L.GS_BF16, y=FAKE, ws=FAKE, wsb=need, s=None)
+    need = L.linear_fp4_workspace_bytes(100, 64, 40)
+    assert need > 0 and L.linear_fp4_workspace_bytes(100, 48, 40) == 0 and L.linear_fp4_workspace_bytes(100, 64, 0) == 0
+    linear = dict(x=mat(), codes=mat(), scales=mat(), rows=100, c=64, n=40, t=L.GS_BF16, y=FAKE, ws=FAKE, wsb=need, s=None)
     sizes = (dict(rows=-1), dict(rows=(1 << 24) + 1), dict(c=0), dict(c=48), dict(c=(1 << 17) + 32), dict(t=3), dict(t=-1))
     for f, ok in ((lib.gs_quantise_fp4, quant), (lib.gs_dequantise_fp4, back), (lib.gs_linear_fp4, linear)):
         for bad in sizes:
