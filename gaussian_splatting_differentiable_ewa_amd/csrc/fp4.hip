@@ -290,10 +290,12 @@ static bool four_sizes_ok(int64_t rows, int32_t channels)
     return rows >= 0 && rows <= (1 << 24) && channels >= FP4_BLOCK && channels <= (1 << 17) && channels % FP4_BLOCK == 0;
 }
 
-// Rows of `bytes` a unit on 16 bytes, those of a tile within 31 bits.
-static bool four_rows_ok(const gs_matrix* m, int unit, int align)
+// Rows on `align` bytes, those of a tile within 31 bits; rows that are one, or
+// apart (`columns` of `unit` bytes each).
+static bool four_rows_ok(const gs_matrix* m, int64_t columns, int unit, int align)
 {
-    return (uintptr_t)m->data % align == 0 && m->stride >= 0 && m->stride < (1 << 21) && m->stride * unit % align == 0;
+    return (uintptr_t)m->data % align == 0 && (m->stride == 0 || m->stride >= columns) && m->stride < (1 << 21) &&
+           m->stride * unit % align == 0;
 }
 
 }  // namespace gs
@@ -307,7 +309,7 @@ gs_status gs_quantise_fp4(const gs_matrix* x, int64_t rows, int32_t channels, in
     if (!four_sizes_ok(rows, channels) || !dtype_ok(dtype)) return GS_ERR_INVALID_ARGUMENT;
     if (rows == 0) return GS_OK;
     if (!x || !x->data || !codes || !scales) return GS_ERR_INVALID_ARGUMENT;
-    if (!four_rows_ok(x, elem_bytes(dtype), 16) || ((uintptr_t)codes & 15) || ((uintptr_t)scales & 3)) return GS_ERR_UNSUPPORTED;
+    if (!four_rows_ok(x, channels, elem_bytes(dtype), 16) || ((uintptr_t)codes & 15) || ((uintptr_t)scales & 3)) return GS_ERR_UNSUPPORTED;
     return quantise_as(dtype, x, codes, scales, rows, channels, (hipStream_t)stream) == hipSuccess ? GS_OK : GS_ERR_HIP;
 }
 
@@ -318,7 +320,7 @@ gs_status gs_dequantise_fp4(const gs_matrix* codes, const gs_matrix* scales, int
     if (!four_sizes_ok(rows, channels) || !dtype_ok(dtype)) return GS_ERR_INVALID_ARGUMENT;
     if (rows == 0) return GS_OK;
     if (!codes || !codes->data || !scales || !scales->data || !out) return GS_ERR_INVALID_ARGUMENT;
-    if (!four_rows_ok(codes, 1, 16) || !four_rows_ok(scales, 1, 4) || ((uintptr_t)out & 15)) return GS_ERR_UNSUPPORTED;
+    if (!four_rows_ok(codes, channels / 2, 1, 16) || !four_rows_ok(scales, scale_bytes_of(channels), 1, 4) || ((uintptr_t)out & 15)) return GS_ERR_UNSUPPORTED;
     const hipStream_t s = (hipStream_t)stream;
     const auto f = dtype == GS_F32 ? dequantise<float> : (dtype == GS_F16 ? dequantise<f16> : dequantise<bf16>);
     return f(codes, scales, out, rows, channels, s) == hipSuccess ? GS_OK : GS_ERR_HIP;
@@ -340,7 +342,7 @@ gs_status gs_linear_fp4(const gs_matrix* x, const gs_matrix* codes, const gs_mat
     if (!x || !x->data || !codes || !codes->data || !scales || !scales->data || !y) return GS_ERR_INVALID_ARGUMENT;
     const size_t need = gs_linear_fp4_workspace_bytes(rows, channels, out);
     if (need && (!ws || ((uintptr_t)ws & 15) || ws_bytes < need)) return GS_ERR_INVALID_ARGUMENT;
-    if (!four_rows_ok(x, elem_bytes(dtype), 16) || !four_rows_ok(codes, 1, 16) || !four_rows_ok(scales, 1, 4) ||
+    if (!four_rows_ok(x, channels, elem_bytes(dtype), 16) || !four_rows_ok(codes, channels / 2, 1, 16) || !four_rows_ok(scales, scale_bytes_of(channels), 1, 4) ||
         (uintptr_t)y % elem_bytes(dtype) || ((rows + 63) / 64) * ((out + 63) / 64) >= (1 << 23))
         return GS_ERR_UNSUPPORTED;
     const hipStream_t s = (hipStream_t)stream;

@@ -86,14 +86,16 @@ __device__ __forceinline__ Buffer buffer_of(const char* p, uint32_t bytes)
     return Buffer{(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, bytes, 0x00027000u};
 }
 
-// 16 bytes a lane from a buffer straight to LDS, lane after lane. In assembly
+// 16 bytes a lane from a buffer, at a lane's offset and a uniform one that is
+// inside the buffer, straight to LDS, lane after lane. In assembly
 // because the compiler, which would have to keep these apart from reads of other
 // stages, waits for all of them at a read where it cannot (two products in one
 // kernel). They are waited for, and kept from reads, by `ready` below alone.
 // M0 and a buffer from vector instructions need the wait states in between.
-__device__ __forceinline__ void load_lds(Buffer src, uint32_t offset, uint32_t lds)
+__device__ __forceinline__ void load_lds(Buffer src, uint32_t offset, uint32_t further, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(src)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(offset), "s"(src),
+                 "s"(further)
                  : "memory", "m0");
 }
 __device__ __forceinline__ void load_lds_4(Buffer src, uint32_t offset, uint32_t lds)  // 4 bytes a lane
@@ -131,11 +133,11 @@ struct PanelLoad {
     }
     // Load i of a stage from what is left of the matrix, `k` bytes of them of the
     // rows' own (behind the last stage of k a row goes on with what is not).
-    __device__ __forceinline__ void one(Buffer src, uint32_t lds, int i, int k) const
+    __device__ __forceinline__ void one(Buffer src, uint32_t further, uint32_t lds, int i, int k) const
     {
         static_assert(TR || KB == 64 || PER % 2 == 0, "a load's chunk goes by whether it is odd");
         const int chunk = chunk_of(row_of(wave, KB == 64 ? 0 : i & 1));
-        load_lds(src, TR || chunk * 16 < k ? off[i] : PAST, lds + (wave * PER + i) * 1024);
+        load_lds(src, TR || chunk * 16 < k ? off[i] : PAST, further, lds + (wave * PER + i) * 1024);
     }
 };
 
@@ -222,29 +224,35 @@ struct TileProduct {
     static constexpr int SUMS = S::MT * S::NT * 4096, FREE = GROUP * S::KG - (S::KG - 1) * S::WAVES * SUMS, SCRATCH = FREE / S::WAVES / 16 * 16;
     static constexpr int PANEL_LOADS = LoadA::PER + LoadB::PER, LOADS = PANEL_LOADS + FOUR;
 
-    // An operand from the next stage on: its address, the bytes up to its end and
-    // what a stage adds to the one and takes from the other.
+    // An operand from the next stage on. Along k the buffer stays, and an offset
+    // goes on (a row's own end is kept by `one`, that of the rows by the buffer);
+    // across, rows of k pass, and their address goes on, past 32 bits, with the
+    // bytes that are left.
     template <bool TR>
     struct Feed {
+        Buffer src;
         const char* p;
         int64_t bytes, step;
+        uint32_t further;
+        static __device__ __forceinline__ uint32_t limit(int64_t n) { return (uint32_t)(n >> 31) ? 0x7fffffffu : (uint32_t)n; }
         __device__ __forceinline__ void at(const Operand& o, int which, int64_t r0, int64_t k, int64_t k0)
         {
             const int64_t ld = o.ld[which];
-            p = o.data[which] + (TR ? k0 * ld + r0 * 2 : r0 * ld + k0 * 2);
-            bytes = TR ? (k - 1 - k0) * ld + (o.rows - r0) * 2 : (o.rows - 1 - r0) * ld + (k - k0) * 2;
-            step = TR ? KE * ld : KE * 2;
+            if (TR) {
+                p = o.data[which] + k0 * ld + r0 * 2;
+                bytes = (k - 1 - k0) * ld + (o.rows - r0) * 2;
+                step = KE * ld;
+                further = 0;
+            } else {
+                src = buffer_of(o.data[which] + r0 * ld, limit((o.rows - 1 - r0) * ld + k * 2));
+                further = (uint32_t)k0 * 2;
+            }
         }
-        // as a buffer (an operand's tile is below 2^31), or an empty one
-        __device__ __forceinline__ Buffer buffer(bool any) const
-        {
-            const uint32_t n = (uint32_t)(bytes >> 31) ? 0x7fffffffu : (uint32_t)bytes;
-            return buffer_of(p, any ? n : 0u);
-        }
+        __device__ __forceinline__ Buffer buffer(bool any) const { return TR ? buffer_of(p, any ? limit(bytes) : 0u) : src; }
         __device__ __forceinline__ void next()
         {
-            p += step;
-            bytes -= step;
+            if (TR) p += step, bytes -= step;
+            else further += KE * 2;
         }
     };
 
@@ -269,21 +277,13 @@ struct TileProduct {
             rows16 = 16 * (uint32_t)ld;
             lds = uniform(lds_address(at)) + wave * SCALE_LOADS * 256;
         }
-        __device__ __forceinline__ void load(int group, int i) const
+        // Load i of group g's, into place `ring` of the three.
+        __device__ __forceinline__ void load(uint32_t g, uint32_t ring, int i) const
         {
-            load_lds_4(src, off + (i * rows16 + group * 16), uniform(lds + group % 3 * SCALE_GROUP + i * 256));
+            load_lds_4(src, off + (i * rows16 + g * 16), lds + ring * SCALE_GROUP + i * 256);
         }
-        // Those of the lane's row of 32 from `first` on (of both operands), and its half's two bytes of them,
-        // of the `blocks` that count of a stage's 4 (the others may hold anything).
-        static __device__ __forceinline__ uint32_t all(const char* at, int stage, int first)
-        {
-            return *(const uint32_t*)(at + stage / 4 % 3 * SCALE_GROUP + (first + (lane_id() & 31)) * 16 + stage % 4 * 4);
-        }
-        static __device__ __forceinline__ int half(uint32_t x, int blocks)
-        {
-            if (blocks < 4) x &= blocks > 0 ? (1u << 8 * blocks) - 1 : 0u;
-            return x >> (lane_id() >> 5) * 16;
-        }
+        // The two bytes of this lane half's of a stage's four.
+        static __device__ __forceinline__ int half(uint32_t x) { return x >> (lane_id() >> 5) * 16; }
     };
 
     // The sums of the first group's waves.
@@ -299,7 +299,7 @@ struct TileProduct {
         constexpr int STEPS = S::KB / 32, LATER = (S::STAGES - 2) * LOADS;
         // a step is MT groups of matrix instructions; loads go EACH to a group, from the last step's on
         constexpr int EACH = (LOADS + S::MT * STEPS - 1) / (S::MT * STEPS), FIRST = LOADS < EACH * S::MT ? LOADS : EACH * S::MT;
-        static_assert(STEPS % 2 == 0 && S::STAGES >= 2 && LATER + FIRST < 64, "steps in pairs; loads out fit the wait's field");
+        static_assert(STEPS % 2 == 0 && (S::STAGES == 2 || S::STAGES == 4) && LATER + FIRST < 64, "steps in pairs; loads out fit the wait's field");
         const LoadA load_a((uint32_t)a.ld[0], wave);
         const int mine = PAIR ? LoadB::second(wave) : w.first >= w.stages;
         LoadB load_b((uint32_t)b.ld[mine], wave);
@@ -315,32 +315,34 @@ struct TileProduct {
         Feed<BTR> fb;
         fa.at(a, w.first >= w.stages, m0, w.k, (int64_t)in * KE);
         fb.at(b, mine, n0, w.k, (int64_t)in * KE);
-        int of_stage = -1;  // whose loads are being issued, counted from the first
-        Buffer from_a, from_b;  // of the stage whose loads are being issued, and where to
+        // of the stage whose loads are being issued: where from and where to
+        Buffer from_a, from_b;
+        uint32_t further_a, further_b, to;
         int k_of;
-        uint32_t to;
         auto prepare = [&](const char* stage) __attribute__((always_inline)) {
-            from_a = fa.buffer(left > 0);
-            from_b = fb.buffer(left > 0);
-            k_of = k;
+            const bool any = left > 0;
+            from_a = fa.buffer(any);
+            from_b = fb.buffer(any);
+            further_a = any ? fa.further : 0;  // never past the buffer's size, from which it is taken off
+            further_b = any ? fb.further : 0;
+            k_of = any ? k : 0;
             to = uniform(lds_address(stage));
             --left, ++in, k -= KE * 2;
-            ++of_stage;
             fa.next();
             fb.next();
         };
-        // with stage s, one of the loads of the scales of the four stages that follow the four of s
-        const int scale_row = (int)(w.k + 31) / 32 * 4;
+        // with stage s goes load s % 4 of the scales of the four stages that follow the four of s
         const char* scales = all + GROUP * S::KG;
-        const Scales scale(a, b, m0, n0, scale_row, scales, wave);
-        auto scale_load = [&]() __attribute__((always_inline)) { scale.load(of_stage / 4 + 1, of_stage % SCALE_LOADS); };
+        const Scales scale(a, b, m0, n0, (int)(w.k + 31) / 32 * 4, scales, wave);
+        uint32_t scale_group = 1, scale_ring = 1;
+        int scale_part = 0;
         // the loads of group `g` behind the barrier
         auto load = [&](int g) __attribute__((always_inline)) {
 #pragma unroll
             for (int i = g * EACH; i < (g + 1) * EACH && i < LOADS; ++i) {
-                if (i < LoadA::PER) load_a.one(from_a, to, i, k_of);
-                else if (i < PANEL_LOADS) load_b.one(from_b, to + A_BYTES, i - LoadA::PER, k_of);
-                else if constexpr (FOUR) scale_load();
+                if (i < LoadA::PER) load_a.one(from_a, further_a, to, i, k_of);
+                else if (i < PANEL_LOADS) load_b.one(from_b, further_b, to + A_BYTES, i - LoadA::PER, k_of);
+                else if constexpr (FOUR) scale.load(scale_group, scale_ring, scale_part);
             }
         };
         // after a stage's last load: on to the second segment?
@@ -379,11 +381,12 @@ struct TileProduct {
         };
         if constexpr (FOUR) {
 #pragma unroll
-            for (int i = 0; i < SCALE_LOADS; ++i) scale.load(0, i);
+            for (int i = 0; i < SCALE_LOADS; ++i) scale.load(0, 0, i);
         }
 #pragma unroll
         for (int t = 0; t < S::STAGES; ++t) {
             prepare(lds + t * STAGE);
+            scale_part = t % SCALE_LOADS;
 #pragma unroll
             for (int g = 0; g < (t < S::STAGES - 1 ? S::MT * STEPS : S::MT); ++g) load(g);
             if (t < S::STAGES - 1) turn();
@@ -391,24 +394,33 @@ struct TileProduct {
         ready(std::integral_constant<int, (S::STAGES - 2) * LOADS + FIRST>{});
 #pragma unroll
         for (int i = 0; i < READS; ++i) read(lds, 0, 0, i);
-        auto next_scales = [&](int t) __attribute__((always_inline)) {
+        // this lane's scales of a stage, all four bytes of each row: place `ring`, stage `slot` of its four
+        const char* scale_rows = scales + (wave / S::WN * (S::BM / S::WM) + (lane_id() & 31)) * 16;
+        const char* scale_cols = scales + (S::BM + wave % S::WN * (S::BN / S::WN) + (lane_id() & 31)) * 16;
+        auto next_scales = [&](uint32_t ring, int slot) __attribute__((always_inline)) {
+            const char *rows = scale_rows + ring * SCALE_GROUP, *cols = scale_cols + ring * SCALE_GROUP;
 #pragma unroll
-            for (int i = 0; i < S::MT; ++i) next_sa[i] = Scales::all(scales, t, wave / S::WN * (S::BM / S::WM) + 32 * i);
+            for (int i = 0; i < S::MT; ++i) next_sa[i] = *(const uint32_t*)(rows + i * 512 + slot * 4);
 #pragma unroll
-            for (int j = 0; j < S::NT; ++j) next_sb[j] = Scales::all(scales, t, S::BM + wave % S::WN * (S::BN / S::WN) + 32 * j);
+            for (int j = 0; j < S::NT; ++j) next_sb[j] = *(const uint32_t*)(cols + j * 512 + slot * 4);
         };
-        if constexpr (FOUR) next_scales(w.first);
-        int now = 0;
-        for (int t = w.first, end = w.first + per; t < end; ++t) {
-            const char* stage = lds + now * STAGE;
-            const int next = now == S::STAGES - 1 ? 0 : now + 1;
+        // of the last stage's four bytes only those of k's own blocks count
+        const int last_blocks = (int)(w.k - (int64_t)(w.stages - 1) * KE) / 8;
+        const uint32_t last_mask = last_blocks < 4 ? (1u << 8 * last_blocks) - 1 : ~0u;
+        uint32_t ring = 0, ring_next = 1, pair = 0;  // places of the scales, and of the pair of stages among the ring's
+        if constexpr (FOUR) next_scales(0, 0);
+        int t = w.first;
+        // One stage; `u`: its place in its pair.
+        auto stage_of = [&](int u) __attribute__((always_inline)) {
+            const char* here = lds + pair * 2 * STAGE;
+            const char* stage = here + u * STAGE;
+            const char* next = S::STAGES == 2 ? lds + (u ^ 1) * STAGE : (u == 0 ? here + STAGE : lds + (pair ^ 1) * 2 * STAGE);
             if constexpr (FOUR) {
-                const int blocks = (int)(w.k - (int64_t)t * KE) / 8;
+                const uint32_t mask = t < w.stages - 1 ? ~0u : (t == w.stages - 1 ? last_mask : 0u);
 #pragma unroll
-                for (int i = 0; i < S::MT; ++i) sa[i] = Scales::half(next_sa[i], blocks);
+                for (int i = 0; i < S::MT; ++i) sa[i] = Scales::half(next_sa[i] & mask);
 #pragma unroll
-                for (int j = 0; j < S::NT; ++j) sb[j] = Scales::half(next_sb[j], blocks);
-                if (t + 1 < end) next_scales(t + 1);
+                for (int j = 0; j < S::NT; ++j) sb[j] = Scales::half(next_sb[j] & mask);
             }
             // The order is kept as written: between two groups of matrix instructions go a few of the next
             // step's reads and a load. Of the last step, one group stands before the barrier.
@@ -424,21 +436,35 @@ struct TileProduct {
                     }
                     if (last && i == 0) {
                         ready(std::integral_constant<int, LATER>{});
-                        prepare(lds + now * STAGE);
+                        prepare(stage);
+                        if constexpr (FOUR) {
+                            scale_part = (pair * 2 + u) % SCALE_LOADS;
+                            if (u == 0 && pair == 0) ++scale_group, scale_ring = scale_ring == 2 ? 0 : scale_ring + 1;
+                        }
                     }
                     // the reads before the last group, of which the last step has one fewer
                     constexpr int G = S::MT > 2 ? S::MT - 1 : S::MT;
                     const int parts = S::MT > 1 && last && G > 1 ? G - 1 : G, p = S::MT > 1 && last && G > 1 ? i - 1 : i;
 #pragma unroll
                     for (int r = 0; r < READS; ++r)
-                        if (p >= 0 && p < parts && r * parts / READS == p)
-                            read(last ? lds + next * STAGE : stage, last ? 0 : s + 1, (s + 1) & 1, r);
+                        if (p >= 0 && p < parts && r * parts / READS == p) read(last ? next : stage, last ? 0 : s + 1, (s + 1) & 1, r);
                     load(last ? i : (s + 1) * S::MT + i);
+                    if (FOUR && s == 0 && i == S::MT - 1) {
+                        if (u == 1 && pair == 1) ring = ring_next, ring_next = ring_next == 2 ? 0 : ring_next + 1;
+                        next_scales(ring, u == 0 ? pair * 2 + 1 : (pair ^ 1) * 2);
+                    }
                     if (S::MT > 1) __builtin_amdgcn_sched_barrier(0);
                     else multiply(s, i);
                 }
             }
-            now = next;
+        };
+        // two at a time, so that a stage's place is a constant; one past the end adds zeros
+        for (int n = 0; n < per; n += 2) {
+            stage_of(0);
+            ++t;
+            stage_of(1);
+            ++t;
+            if (S::STAGES > 2) pair ^= 1;
         }
         // what was loaded past the end has landed and all reads are done: LDS is free
         ready(std::integral_constant<int, 0>{});

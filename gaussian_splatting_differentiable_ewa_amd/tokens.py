@@ -206,7 +206,7 @@ def _on16(t):
     """t itself, or a copy, so that every row starts on 16 bytes."""
     if t.data_ptr() % 16 == 0:
         sr, sc = t.stride()
-        if sc == 1 and (sr % 8 == 0 and 0 <= sr < 1 << 21 or t.shape[0] <= 1):
+        if sc == 1 and (sr % 8 == 0 and (sr >= t.shape[1] or sr == 0) and sr < 1 << 21 or t.shape[0] <= 1):
             return t
     return t.clone(memory_format=torch.contiguous_format)
 
@@ -276,7 +276,7 @@ def _on16_rows(t):
     """t itself, or a copy, so that every row starts on 16 bytes, whatever its type."""
     if t.data_ptr() % 16 == 0:
         sr, sc = t.stride()
-        if sc == 1 and (sr * t.element_size() % 16 == 0 and 0 <= sr < 1 << 21 or t.shape[0] <= 1):
+        if sc == 1 and (sr * t.element_size() % 16 == 0 and (sr >= t.shape[1] or sr == 0) and sr < 1 << 21 or t.shape[0] <= 1):
             return t
     return t.clone(memory_format=torch.contiguous_format)
 
@@ -286,7 +286,8 @@ def _four(four, channels, like):
     device, (rows, half), (sr, sc), (cr, cc) = like.get_device(), codes.shape, scales.stride(), codes.stride()
     if (codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or half * 2 != channels
             or scales.shape != (rows, (channels + 127) // 128 * 4) or codes.get_device() != device
-            or scales.get_device() != device or cc != 1 or sc != 1 or sr % 4 or scales.data_ptr() % 4):
+            or scales.get_device() != device or cc != 1 or sc != 1 or sr % 4 or 0 < sr < scales.shape[1]
+            or scales.data_ptr() % 4):
         raise ValueError(f"the weights must be quantise4's: uint8 [rows, {channels // 2}] and [rows, "
                          f"{(channels + 127) // 128 * 4}] on {like.device}, scales on 4 bytes")
     return _on16_rows(codes), scales

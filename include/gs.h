@@ -962,8 +962,8 @@ size_t gs_gated_ff_fwd_workspace_bytes(int64_t rows, int32_t channels, int32_t h
  *   ws       workspace of gs_gated_ff_fwd_workspace_bytes(...), or NULL if that is 0
  * Errors: null pointers, sizes that are not multiples of 8 or outside 8..2^17,
  * rows outside 0..2^24, a bad act or dtype, a small workspace; GS_ERR_UNSUPPORTED
- * for GS_F32, data or rows off 16 bytes, a row stride outside 0 .. 2^21 - 1, or
- * past 2^23 tiles of a product (256 rows by 128 columns).
+ * for GS_F32, data or rows off 16 bytes, a row stride of 2^21 or more or below the
+ * row's length but for 0 (one row for all), or past 2^22 tiles of a product.
  */
 gs_status gs_gated_ff_fwd(const gs_matrix* x, const gs_matrix* w_gate, const gs_matrix* w_up, const gs_matrix* w_down,
                           int64_t rows, int32_t channels, int32_t hidden, int32_t channels_out, int32_t act, int32_t dtype,
@@ -1005,7 +1005,7 @@ gs_status gs_gated_ff_bwd(const gs_matrix* gy, const gs_matrix* x, const gs_matr
  *           bytes a row is filled up with zero
  * Errors: null pointers, channels not a multiple of 32 or outside 32..2^17, rows
  * outside 0..2^24, a bad dtype; GS_ERR_UNSUPPORTED for data or rows off 16 bytes
- * (scales: 4), a row stride outside 0 .. 2^21 - 1.
+ * (scales: 4), a row stride of 2^21 or more or below the row's length but for 0.
  */
 gs_status gs_quantise_fp4(const gs_matrix* x, int64_t rows, int32_t channels, int32_t dtype, void* codes, void* scales,
                           void* stream);

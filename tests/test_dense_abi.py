@@ -62,7 +62,7 @@ def test_gated_ff_refusals(lib):
     both = (dict(x=None), dict(wg=None), dict(wu=None), dict(wd=None), dict(x=mat(0)), dict(wd=mat(0)), dict(h=None),
             dict(rows=-1), dict(rows=(1 << 24) + 1), dict(c=0), dict(c=60), dict(hid=4), dict(hid=-8), dict(co=12),
             dict(c=(1 << 17) + 8), dict(hid=1 << 18), dict(act=2), dict(act=-1), dict(t=3))
-    odd = (dict(t=L.GS_F32), dict(x=mat(4104)), dict(wg=mat(stride=1028)), dict(wu=mat(stride=-8)), dict(wd=mat(stride=1 << 21)),
+    odd = (dict(t=L.GS_F32), dict(x=mat(4104)), dict(wg=mat(stride=1028)), dict(wu=mat(stride=-8)), dict(wd=mat(stride=1 << 21)), dict(x=mat(stride=56)),
            dict(h=ctypes.c_void_p(4104)), dict(kept=ctypes.c_void_p(4104)), dict(rows=1 << 24, hid=1 << 17))
     for f, ok in ((lib.gs_gated_ff_fwd, fwd), (lib.gs_gated_ff_bwd, bwd)):
         big = {"wsb": 1 << 60} if ok is bwd else {}
@@ -111,7 +111,7 @@ def test_fp4_refusals(lib):
                 dict(wsb=need - 1)):
         assert call(lib.gs_linear_fp4, linear, **bad) == INV, bad
     for bad in (dict(x=mat(4104)), dict(x=mat(stride=1028)), dict(codes=mat(4104)), dict(codes=mat(stride=1032)),
-                dict(scales=mat(4098)), dict(scales=mat(stride=1026)), dict(scales=mat(stride=1 << 21)),
+                dict(scales=mat(4098)), dict(scales=mat(stride=1026)), dict(scales=mat(stride=1 << 21)), dict(codes=mat(stride=16)),
                 dict(y=ctypes.c_void_p(4097)), dict(rows=1 << 24, n=1 << 17)):
         assert call(lib.gs_linear_fp4, linear, **bad, **({"wsb": 1 << 60} if "rows" in bad else {})) == UNS, bad
 
