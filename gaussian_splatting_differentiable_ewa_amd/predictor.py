@@ -17,6 +17,10 @@ and computes what the causal form does: its keys, values and block summaries
 are kept, and only the blocks it touches are summarised again. ``train`` fits
 the causal form unless told otherwise.
 
+``gated`` makes the perceptron a gated one (``GatedFF``), ``layer_norm`` norms a
+tile's pixels before the embedding (``LayerNorm``), and ``pack4`` holds the
+layers' weights in 4 bits for ``extend`` (``linear4``), at a quarter of the bytes.
+
     python -m gaussian_splatting_differentiable_ewa_amd.predictor --steps 60
 """
 
@@ -79,12 +83,17 @@ class TileNet(torch.nn.Module):
     """Views [V, 3, H, W] -> Gaussian parameters [14][V x tiles x per_tile]."""
 
     def __init__(self, channels: int = 256, heads: int = 4, kv_heads: int = 2, layers: int = 2, per_tile: int = 4,
-                 top: int = 16, views: int = L.GS_MAX_VIEWS, depth: float = 8.0, dtype=torch.bfloat16, seed: int = 0):
+                 top: int = 16, views: int = L.GS_MAX_VIEWS, depth: float = 8.0, dtype=torch.bfloat16, seed: int = 0,
+                 hidden: Optional[int] = None, gated: Optional[str] = None, layer_norm: bool = False):
         super().__init__()
-        if channels % 8 or heads % kv_heads:
-            raise ValueError("channels must be a multiple of 8 and heads of kv_heads")
+        hidden = 4 * channels if hidden is None else hidden
+        if channels % 8 or hidden % 8 or heads % kv_heads:
+            raise ValueError("channels and hidden must be multiples of 8 and heads of kv_heads")
+        if gated is not None and gated not in T.ACTS:
+            raise ValueError(f"gated must be None or one of {sorted(T.ACTS)}, got {gated!r}")
         self.channels, self.heads, self.kv_heads, self.layers = channels, heads, kv_heads, layers
         self.per_tile, self.top, self.depth, self.dtype, self.views = per_tile, top, depth, dtype, views
+        self.gated = gated
         g = torch.Generator().manual_seed(seed)
 
         def weight(*shape, scale=1.0):
@@ -95,13 +104,16 @@ class TileNet(torch.nn.Module):
         self.first = torch.nn.Parameter(torch.ones(c))
         self.qkv = torch.nn.ParameterList([weight((heads + 2 * kv_heads) * DIM, c) for _ in range(layers)])
         self.out = torch.nn.ParameterList([weight(c, heads * DIM) for _ in range(layers)])
-        self.up = torch.nn.ParameterList([weight(4 * c, c) for _ in range(layers)])
-        self.down = torch.nn.ParameterList([weight(c, 4 * c) for _ in range(layers)])
+        self.up = torch.nn.ParameterList([weight(hidden, c) for _ in range(layers)])
+        self.down = torch.nn.ParameterList([weight(c, hidden) for _ in range(layers)])
         # norms after and before, and the gate of each view, of 2 blocks a layer
         self.post = torch.nn.ParameterList([torch.nn.Parameter(torch.ones(c)) for _ in range(2 * layers)])
         self.pre = torch.nn.ParameterList([torch.nn.Parameter(torch.ones(c)) for _ in range(2 * layers)])
         self.gate = torch.nn.ParameterList([torch.nn.Parameter(torch.ones(views, c)) for _ in range(2 * layers)])
         self.head = weight(per_tile * PARAMS, c, scale=0.1)
+        if gated is not None:  # the projection that opens and closes `up`'s
+            self.open = torch.nn.ParameterList([weight(hidden, c) for _ in range(layers)])
+        self.pixels = torch.nn.ParameterList([torch.nn.Parameter(f(tile)) for f in (torch.ones, torch.zeros)] if layer_norm else [])
         self.pairs = (8, 12, 12)  # of the 32 pairs of a head: view, row, column
         self.register_buffer("freq", torch.cat([100.0 ** (-torch.arange(p, dtype=torch.float32) / p) for p in self.pairs]))
 
@@ -117,21 +129,46 @@ class TileNet(torch.nn.Module):
         at = torch.arange(views * ty * tx, device=device)
         return torch.stack([at // (ty * tx) + first_view, at // tx % ty, at % tx], -1).int()[None]
 
-    def _linear(self, x, w):
-        return x @ w.to(self.dtype).t()
+    def _linear(self, x, w, four=None):
+        return x @ w.to(self.dtype).t() if four is None else T.linear4(x, four)
 
-    def _layers(self, tiles, pos, per_view, first_view, attend):
+    def _perceptron(self, i, h, four):
+        if self.gated is None:
+            return self._linear(F.gelu(self._linear(h, self.up[i], four.get("up"))), self.down[i], four.get("down"))
+        if not four:
+            return T.GatedFF.apply(h, *(w[i].to(self.dtype) for w in (self.open, self.up, self.down)), self.gated)
+        opened, up = T.linear4(h, four["open up"]).chunk(2, 1)
+        return T.linear4(getattr(F, self.gated)(opened) * up, four["down"])
+
+    def pack4(self) -> List[dict]:
+        """The layers' weights in 4 bits, for ``extend`` (channels, hidden and the
+        heads' width have to be multiples of 32); the embedding and the head stay
+        in 16."""
+        layers = []
+        for i in range(self.layers):
+            of = {"qkv": self.qkv[i], "out": self.out[i], "down": self.down[i]}
+            if self.gated is None:
+                of["up"] = self.up[i]
+            else:
+                of["open up"] = torch.cat([self.open[i], self.up[i]])
+            layers.append({name: T.quantise4(w.detach().to(self.dtype)) for name, w in of.items()})
+        return layers
+
+    def _layers(self, tiles, pos, per_view, first_view, attend, four=None):
         """Residual stream's norm after all layers; attend(layer, q, k, v)."""
         n, views = tiles.shape[0], tiles.shape[0] // per_view
+        four = [{}] * self.layers if four is None else four
+        if len(self.pixels):
+            tiles = T.LayerNorm.apply(tiles, *self.pixels)
         x, h = T.NormGate.apply(self._linear(tiles, self.embed), None, None, None, self.first)
         scale = 1.0 / math.sqrt(2 * self.layers)
         for i in range(self.layers):
-            q, k, v = self._linear(h, self.qkv[i]).view(1, n, -1, DIM).split([self.heads, self.kv_heads, self.kv_heads], 2)
+            q, k, v = self._linear(h, self.qkv[i], four[i].get("qkv")).view(1, n, -1, DIM).split([self.heads, self.kv_heads, self.kv_heads], 2)
             q, k = T.RopeAxes.apply(q, k, pos, self.freq, self.pairs)
-            f = self._linear(attend(i, q, k, v).reshape(n, -1), self.out[i])
+            f = self._linear(attend(i, q, k, v).reshape(n, -1), self.out[i], four[i].get("out"))
             gates = self.gate[2 * i][first_view: first_view + views].contiguous()
             x, h = T.NormGate.apply(x, f, gates, self.post[2 * i], self.pre[2 * i], scale, 1e-6, per_view)
-            f = self._linear(F.gelu(self._linear(h, self.up[i])), self.down[i])
+            f = self._perceptron(i, h, four[i])
             gates = self.gate[2 * i + 1][first_view: first_view + views].contiguous()
             x, h = T.NormGate.apply(x, f, gates, self.post[2 * i + 1], self.pre[2 * i + 1], scale, 1e-6, per_view)
         return h
@@ -193,10 +230,10 @@ class TileNet(torch.nn.Module):
         return self._gaussians(h, cams, ty, tx)
 
     @torch.no_grad()
-    def extend(self, image, cam, cache: TileCache):
+    def extend(self, image, cam, cache: TileCache, four: Optional[List[dict]] = None):
         """The Gaussians of the next view ([3, H, W]), its tokens attending to
         themselves and to all views before it. Views may differ in size: the cache
-        counts them."""
+        counts them. four: ``pack4``'s weights instead of the network's own."""
         _, h, w = image.shape
         ty, tx = (h + L.GS_TILE - 1) // L.GS_TILE, (w + L.GS_TILE - 1) // L.GS_TILE
         n, before, view = ty * tx, cache.tokens, cache.views
@@ -217,7 +254,7 @@ class TileNet(torch.nn.Module):
             lists = T.select_blocks(q, cache.sums[i], cache.capacity, self.top, cache.length)
             return T.block_attention(q, cache.k[i], cache.v[i], lists, None, cache.length)[0]
 
-        tokens = self._layers(self._tiles(image[None]), pos, n, view, attend)
+        tokens = self._layers(self._tiles(image[None]), pos, n, view, attend, four)
         cache.tokens, cache.views = before + n, view + 1
         return self._gaussians(tokens, [cam], ty, tx)
 
@@ -250,12 +287,14 @@ def main(argv=None):
     p = argparse.ArgumentParser(description="Fit a tile network to rendered views of a synthetic scene.")
     p.add_argument("--config", type=int, default=0, help="scene of scenes.CONFIGS (0: 256x256, 10k Gaussians)")
     p.add_argument("--steps", type=int, default=60)
+    p.add_argument("--gated", choices=sorted(T.ACTS), help="a gated perceptron with this activation")
+    p.add_argument("--layer-norm", action="store_true", help="norm the tiles' pixels before the embedding")
     a = p.parse_args(argv)
     cfg = scenes.CONFIGS[a.config]
     cams = cfg.cameras()
     params = torch.from_numpy(scenes.make_params(cfg)).cuda()
     images = render(params, cfg.sh_degree, cams).clone()
-    train(images, cams, a.steps, report=print)
+    train(images, cams, a.steps, net=TileNet(gated=a.gated, layer_norm=a.layer_norm), report=print)
 
 
 if __name__ == "__main__":
