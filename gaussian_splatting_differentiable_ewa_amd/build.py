@@ -1,4 +1,5 @@
-"""Builds the gfx950 HIP library ``libgs_hip.so`` in-tree with hipcc.
+"""Builds the gfx950 HIP library ``libgs_hip.so`` in-tree with hipcc: an object
+of each source, several at once, and a link.
 
 Flags:
   --offload-arch=gfx950            MI355X (CDNA4) code objects only
@@ -16,6 +17,8 @@ import glob
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,7 +28,7 @@ LIB = os.path.join(PKG, "libgs_hip.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     "-ffp-contract=fast-honor-pragmas", "-fhip-fp32-correctly-rounded-divide-sqrt",
     "-munsafe-fp-atomics", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-function", "-Wno-unused-command-line-argument",
@@ -36,10 +39,7 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.hip")))
 
 
-def build(verbose: bool = False, extra=()) -> str:
-    """Compile every source into one shared library (always recompiles)."""
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [HIPCC] + FLAGS + list(extra) + ["-I", INCLUDE, "-I", CSRC, "-o", tmp] + sources()
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -49,6 +49,22 @@ def build(verbose: bool = False, extra=()) -> str:
         raise RuntimeError("hipcc failed:\n" + out)
     if verbose and out:
         print(out, file=sys.stderr)
+
+
+def build(verbose: bool = False, extra=()) -> str:
+    """Compile every source and link one shared library (always recompiles)."""
+    tmp = LIB + ".tmp%d" % os.getpid()
+    jobs = min(8, int(os.environ.get("MAX_JOBS", 0)) or os.cpu_count() or 1)
+    with tempfile.TemporaryDirectory() as folder:
+        def compile_one(src):
+            obj = os.path.join(folder, os.path.basename(src) + ".o")
+            _run([HIPCC] + FLAGS + list(extra) + ["-c", "-I", INCLUDE, "-I", CSRC, "-o", obj, src], verbose)
+            return obj
+
+        # the longest first
+        with ThreadPoolExecutor(jobs) as pool:
+            objs = list(pool.map(compile_one, sorted(sources(), key=os.path.getsize, reverse=True)))
+        _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs, verbose)
     os.replace(tmp, LIB)
     return LIB
 
