@@ -193,7 +193,6 @@ __global__ __launch_bounds__(FEW_WAVES * 64) void k_fp4_few(const FourArgs p, co
     const uint8_t* scales = (const uint8_t*)p.b.data[1] + row * p.b.ld[1];
     const T* mine = x + (r < rows ? r : rows - 1) * stride_x;
     float4v acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
     for (int b = wave * 4 + q; b < (blocks + 3) / 4 * 4; b += FEW_WAVES * 4) {
         v8i w = {}, t = {};
         int sw = 0, st = 0;

@@ -48,27 +48,55 @@ __device__ __forceinline__ void activate(float g, float& a, float& da)
 template <typename T>
 struct Kept {
     static constexpr int MORE = std::is_same<T, bf16>::value ? 4 : 8;
-    typedef std::conditional_t<MORE == 4, uint8_t, uint16_t> Low;
-    static constexpr int BYTES = 4 + sizeof(Low);  // an element
+    static constexpr int LOW = 2 * MORE / 8, BYTES = 4 + LOW;  // of the third plane, and in all, an element
+    typedef std::conditional_t<LOW == 1, uint32_t, uint2> Low4;  // of four elements
     char* p;
     int64_t plane;  // elements
     __device__ __forceinline__ uint16_t* g(int64_t i) const { return (uint16_t*)p + i; }
     __device__ __forceinline__ uint16_t* u(int64_t i) const { return (uint16_t*)p + plane + i; }
-    __device__ __forceinline__ Low* low(int64_t i) const { return (Low*)(p + 4 * plane) + i; }
+    __device__ __forceinline__ char* low(int64_t i) const { return p + 4 * plane + i * LOW; }
     // Rounded to 16 + MORE bits, in the upper ones.
     static __device__ __forceinline__ uint32_t cut(float x)
     {
         const uint32_t b = __builtin_bit_cast(uint32_t, x) + (1u << (15 - MORE));
         return x != x ? 0x7fc00000u : b;
     }
-    static __device__ __forceinline__ Low lows(uint32_t g, uint32_t u)
+    // Four elements' bits by v_perm_b32, which takes any four of eight bytes: 3 to 5
+    // instructions an element less than with shifts and masks, where a tile's 65536
+    // elements pass the CU's 64 lanes with no product beside them.
+    static __device__ __forceinline__ uint32_t upper(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302); }
+    static __device__ __forceinline__ void pack(const float (&g)[4], const float (&u)[4], uint2& kg, uint2& ku, Low4& low)
     {
-        constexpr uint32_t M = (1u << MORE) - 1;
-        return (Low)((g >> (16 - MORE) & M) | (u >> (16 - MORE) & M) << MORE);
+        uint32_t a[4], b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] = cut(g[e]), b[e] = cut(u[e]);
+        kg = {upper(a[0], a[1]), upper(a[2], a[3])};
+        ku = {upper(b[0], b[1]), upper(b[2], b[3])};
+        const auto second = [](uint32_t x, uint32_t y, uint32_t to) { return __builtin_amdgcn_perm(y, x, to); };
+        constexpr uint32_t LOWER = 0x0c0c0501, HIGHER = 0x05010c0c;  // both second bytes, to either half
+        if constexpr (LOW == 1) {  // a byte an element: g's bits above u's
+            const uint32_t x = second(a[0], a[1], LOWER) | second(a[2], a[3], HIGHER);
+            const uint32_t y = second(b[0], b[1], LOWER) | second(b[2], b[3], HIGHER);
+            low = (x & 0xf0f0f0f0u) | (y >> 4 & 0x0f0f0f0fu);
+        } else {  // two: g's, u's
+            low = {second(a[0], b[0], LOWER) | second(a[1], b[1], HIGHER), second(a[2], b[2], LOWER) | second(a[3], b[3], HIGHER)};
+        }
     }
-    static __device__ __forceinline__ float whole(uint32_t high, uint32_t low)
+    static __device__ __forceinline__ void unpack(uint2 kg, uint2 ku, Low4 low, float (&g)[4], float (&u)[4])
     {
-        return __builtin_bit_cast(float, high << 16 | (low & ((1u << MORE) - 1)) << (16 - MORE));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t high = e % 2 ? 0x0706000cu : 0x0504000cu;  // 16 bits, a byte to come, and zeros
+            const uint32_t hg = e < 2 ? kg.x : kg.y, hu = e < 2 ? ku.x : ku.y;
+            if constexpr (LOW == 1) {
+                g[e] = __builtin_bit_cast(float, __builtin_amdgcn_perm(hg, low & 0xf0f0f0f0u, high | e << 8));
+                u[e] = __builtin_bit_cast(float, __builtin_amdgcn_perm(hu, low << 4 & 0xf0f0f0f0u, high | e << 8));
+            } else {
+                const uint32_t w = e < 2 ? low.x : low.y;
+                g[e] = __builtin_bit_cast(float, __builtin_amdgcn_perm(hg, w, high | 2 * (e % 2) << 8));
+                u[e] = __builtin_bit_cast(float, __builtin_amdgcn_perm(hu, w, high | (2 * (e % 2) + 1) << 8));
+            }
+        }
     }
 };
 
@@ -92,31 +120,28 @@ struct alignas(sizeof(T) * N) Vec {
 // Four columns from `col` on of one row.
 template <typename T, int ACT>
 struct Four {
+    using Low4 = typename Kept<T>::Low4;
     // h, and what is kept of g and u
-    static __device__ __forceinline__ void gate(const float (&g)[4], const float (&u)[4], Vec<T, 4>& h, Vec<uint16_t, 4>& kg,
-                                                Vec<uint16_t, 4>& ku, Vec<typename Kept<T>::Low, 4>& low)
+    static __device__ __forceinline__ void gate(const float (&g)[4], const float (&u)[4], Vec<T, 4>& h, uint2& kg, uint2& ku, Low4& low)
     {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float a, da;
             activate<ACT>(g[e], a, da);
             h.v[e] = (T)(a * u[e]);
-            const uint32_t cg = Kept<T>::cut(g[e]), cu = Kept<T>::cut(u[e]);
-            kg.v[e] = (uint16_t)(cg >> 16);
-            ku.v[e] = (uint16_t)(cu >> 16);
-            low.v[e] = Kept<T>::lows(cg, cu);
         }
+        Kept<T>::pack(g, u, kg, ku, low);
     }
     // gg and gu from gh
-    static __device__ __forceinline__ void grad(const float (&gh)[4], const Vec<uint16_t, 4>& kg, const Vec<uint16_t, 4>& ku,
-                                                const Vec<typename Kept<T>::Low, 4>& low, Vec<T, 4>& gg, Vec<T, 4>& gu)
+    static __device__ __forceinline__ void grad(const float (&gh)[4], uint2 kg, uint2 ku, Low4 low, Vec<T, 4>& gg, Vec<T, 4>& gu)
     {
+        float g[4], u[4];
+        Kept<T>::unpack(kg, ku, low, g, u);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float g = Kept<T>::whole(kg.v[e], low.v[e]), u = Kept<T>::whole(ku.v[e], low.v[e] >> Kept<T>::MORE);
             float a, da;
-            activate<ACT>(g, a, da);
-            gg.v[e] = (T)(gh[e] * u * da);
+            activate<ACT>(g[e], a, da);
+            gg.v[e] = (T)(gh[e] * u[e] * da);
             gu.v[e] = (T)(gh[e] * a);
         }
     }
@@ -129,6 +154,23 @@ struct ProductArgs {
     uint32_t mt, nt, per_split;  // tiles, and stages of a split
 };
 
+// Of 32 rows of COLS columns, what the forward pass kept, on its way from memory
+// to a scratch. It is read 32 rows ahead; with the packing above that took
+// 32640 x 2048 x 8192 from 1378 to 1300 us.
+template <typename T, int COLS>
+struct Held {
+    uint4 g[COLS / 16], u[COLS / 16];
+    uint2 low[COLS * Kept<T>::LOW / 16];
+    __device__ __forceinline__ void fetch(const Target& o, int64_t row0, int64_t n0, int64_t cols)
+    {
+        const Kept<T> kept{o.kept, o.m * o.n};
+        const int64_t first = row0 * o.n + n0, rows = o.m - row0;
+        Rows<COLS * 2>::fetch(g, (const char*)kept.g(first), o.n * 2, rows, cols * 2);
+        Rows<COLS * 2>::fetch(u, (const char*)kept.u(first), o.n * 2, rows, cols * 2);
+        Rows<COLS * Kept<T>::LOW>::fetch(low, kept.low(first), o.n * Kept<T>::LOW, rows, cols * Kept<T>::LOW);
+    }
+};
+
 // The wave's rows from m0 + 32 i on and columns from n0 on, for each i, out of
 // its accumulators through its scratch.
 template <typename T, typename S, int TO, int ACT, bool PART>
@@ -139,6 +181,8 @@ __device__ __forceinline__ void finish(char* scratch, const Target& o, const acc
     constexpr bool PAIR = TO == TO_GATED;
     constexpr int COLS = S::NT * 32 / (PAIR ? 2 : 1);
     const int64_t cols = o.n - n0 < COLS ? o.n - n0 : COLS;  // may be negative
+    Held<T, COLS> held;
+    if constexpr (TO == TO_GRAD && !PART) held.fetch(o, m0, n0, cols);
 #pragma unroll
     for (int i = 0; i < S::MT; ++i) {
         const int64_t row0 = m0 + 32 * i, rows = o.m - row0;
@@ -166,7 +210,7 @@ __device__ __forceinline__ void finish(char* scratch, const Target& o, const acc
         } else if constexpr (TO == TO_GATED) {
             constexpr int W = COLS * 2;
             const Rows<W> h{scratch}, g{scratch + 32 * W}, u{scratch + 64 * W};
-            const Rows<W * sizeof(typename Kept<T>::Low) / 2> low{scratch + 96 * W};
+            const Rows<COLS * Kept<T>::LOW> low{scratch + 96 * W};
             const Kept<T> kept{o.kept, o.m * o.n};
             wait_lds();
 #pragma unroll
@@ -177,15 +221,15 @@ __device__ __forceinline__ void finish(char* scratch, const Target& o, const acc
                     four(j, r, vg);
                     four(j + S::NT / 2, r, vu);
                     Vec<T, 4> vh;
-                    Vec<uint16_t, 4> kg, ku;
-                    Vec<typename Kept<T>::Low, 4> kl;
+                    uint2 kg, ku;
+                    typename Kept<T>::Low4 kl;
                     Four<T, ACT>::gate(vg, vu, vh, kg, ku, kl);
                     const int c = 32 * j + 8 * r + 4 * hi;
                     h.put(c * 2, vh);
                     if (o.kept) {
                         g.put(c * 2, kg);
                         u.put(c * 2, ku);
-                        low.put(c * (int)sizeof(typename Kept<T>::Low), kl);
+                        low.put(c * Kept<T>::LOW, kl);
                     }
                 }
             wait_lds();
@@ -194,21 +238,19 @@ __device__ __forceinline__ void finish(char* scratch, const Target& o, const acc
                 const int64_t first = row0 * o.n + n0;
                 g.store((char*)kept.g(first), o.n * 2, rows, cols * 2);
                 u.store((char*)kept.u(first), o.n * 2, rows, cols * 2);
-                low.store8((char*)kept.low(first), o.n * (int)sizeof(typename Kept<T>::Low), rows,
-                           cols * (int)sizeof(typename Kept<T>::Low));
+                low.store8((char*)kept.low(first), o.n * Kept<T>::LOW, rows,
+                           cols * Kept<T>::LOW);
             }
         } else if constexpr (TO == TO_GRAD) {
             constexpr int W = COLS * 2;
             const Rows<W> g{scratch}, u{scratch + 32 * W};
-            const Rows<W * sizeof(typename Kept<T>::Low) / 2> low{scratch + 64 * W};
-            const Kept<T> kept{o.kept, o.m * o.n};
-            const int64_t first = row0 * o.n + n0;
+            const Rows<COLS * Kept<T>::LOW> low{scratch + 64 * W};
             wait_lds();
-            g.load((const char*)kept.g(first), o.n * 2, rows, cols * 2);
-            u.load((const char*)kept.u(first), o.n * 2, rows, cols * 2);
-            low.load8((const char*)kept.low(first), o.n * (int)sizeof(typename Kept<T>::Low), rows,
-                      cols * (int)sizeof(typename Kept<T>::Low));
+            g.put_all(held.g);
+            u.put_all(held.u);
+            low.put_all(held.low);
             wait_lds();
+            if (i + 1 < S::MT) held.fetch(o, row0 + 32, n0, cols);  // while these are worked on
 #pragma unroll
             for (int j = 0; j < S::NT; ++j)
 #pragma unroll
@@ -217,8 +259,8 @@ __device__ __forceinline__ void finish(char* scratch, const Target& o, const acc
                     four(j, r, gh);
                     const int c = 32 * j + 8 * r + 4 * hi;
                     Vec<T, 4> gg, gu;
-                    Four<T, ACT>::grad(gh, g.template get<Vec<uint16_t, 4>>(c * 2), u.template get<Vec<uint16_t, 4>>(c * 2),
-                                       low.template get<Vec<typename Kept<T>::Low, 4>>(c * (int)sizeof(typename Kept<T>::Low)),
+                    Four<T, ACT>::grad(gh, g.template get<uint2>(c * 2), u.template get<uint2>(c * 2),
+                                       low.template get<typename Kept<T>::Low4>(c * Kept<T>::LOW),
                                        gg, gu);
                     g.put(c * 2, gg);  // where its own were read
                     u.put(c * 2, gu);
@@ -271,7 +313,8 @@ __device__ __forceinline__ void ff_product(char* lds, const ProductArgs& p, uint
     if (group > 0) return;
     char* scratch = lds + wave * Tiles::SCRATCH;
     const int64_t m = m0 + wave / S::WN * (S::BM / S::WM), n = n0 + wave % S::WN * (S::BN / S::WN / (PAIR ? 2 : 1));
-    static_assert(Tiles::SCRATCH >= 32 * 64 * 4 * 2, "a wave's scratch");
+    // h, g, u and what they keep beyond 16 bits, or a row of 32 sums at a time
+    static_assert(Tiles::SCRATCH >= std::max(S::BN / S::WN / (PAIR ? 2 : 1) * 2 * 32 * 4, 32 * 128), "a wave's scratch");
     if (p.o.part) finish<T, S, TO, ACT, true>(scratch, p.o, acc, m, n, split);
     else finish<T, S, TO, ACT, false>(scratch, p.o, acc, m, n, 0);
 }
@@ -323,23 +366,22 @@ __device__ __forceinline__ void ff_join(const Target& o, int32_t splits, uint32_
             for (int e = 0; e < 4; ++e) u[e] += y.v[e];
         }
     }
-    using Low4 = Vec<typename Kept<T>::Low, 4>;
-    using High4 = Vec<uint16_t, 4>;
+    using Low4 = typename Kept<T>::Low4;
     const Kept<T> kept{o.kept, o.m * o.n};
     if constexpr (TO == TO_GATED) {
         Vec<T, 4> h;
-        High4 kg, ku;
+        uint2 kg, ku;
         Low4 low;
         Four<T, ACT>::gate(v, u, h, kg, ku, low);
         *(Vec<T, 4>*)((T*)o.out[0] + row * o.ld[0] + col) = h;
         if (o.kept) {
-            *(High4*)kept.g(at) = kg;
-            *(High4*)kept.u(at) = ku;
+            *(uint2*)kept.g(at) = kg;
+            *(uint2*)kept.u(at) = ku;
             *(Low4*)kept.low(at) = low;
         }
     } else if constexpr (TO == TO_GRAD) {
         Vec<T, 4> gg, gu;
-        Four<T, ACT>::grad(v, *(const High4*)kept.g(at), *(const High4*)kept.u(at), *(const Low4*)kept.low(at), gg, gu);
+        Four<T, ACT>::grad(v, *(const uint2*)kept.g(at), *(const uint2*)kept.u(at), *(const Low4*)kept.low(at), gg, gu);
         T* to = (T*)o.out[0] + row * o.ld[0] + col;
         *(Vec<T, 4>*)to = gg;
         *(Vec<T, 4>*)(to + o.n) = gu;
@@ -457,16 +499,16 @@ __global__ __launch_bounds__(WAVES * 64) void k_ff_few(const FewArgs p)
     if (r >= rows || col >= p.o.n || part > 0 || 4 * q >= SIDE) return;
     if constexpr (TO == TO_GATED) {
         Vec<T, 4> h;
-        Vec<uint16_t, 4> kg, ku;
-        Vec<typename Kept<T>::Low, 4> low;
+        uint2 kg, ku;
+        typename Kept<T>::Low4 low;
         Four<T, ACT>::gate(v, u, h, kg, ku, low);
         *(Vec<T, 4>*)((T*)p.o.out[0] + r * p.o.ld[0] + col) = h;
         if (p.o.kept) {
             const Kept<T> kept{p.o.kept, p.o.m * p.o.n};
             const int64_t at = r * p.o.n + col;
-            *(Vec<uint16_t, 4>*)kept.g(at) = kg;
-            *(Vec<uint16_t, 4>*)kept.u(at) = ku;
-            *(Vec<typename Kept<T>::Low, 4>*)kept.low(at) = low;
+            *(uint2*)kept.g(at) = kg;
+            *(uint2*)kept.u(at) = ku;
+            *(typename Kept<T>::Low4*)kept.low(at) = low;
         }
     } else {
         Vec<T, 4> t;
@@ -501,27 +543,35 @@ static hipError_t few(const Operand& a, const Operand& b, const Target& o, int64
 }
 
 // The tiles. Smaller ones make more workgroups, and their groups of waves, which
-// share the sum over k, fill the CU that one workgroup has to itself.
+// share the sum over k, fill the CU. Two groups of Small leave room for a second
+// workgroup on the CU; four did not, and cost 1.2 us more a launch: 256 x 1024 x
+// 1024 took 7.4 us either way, 1024 x 1024 x 1024 8.0 against 8.2 us, 4096 x 1024
+// x 1024 29 against 21 us, 256 x 512 x 64 7.3 against 6.2 us.
 using Wide = TileShape<256, 256, 2, 4, 128, 2>;
 using Mid = TileShape<128, 128, 2, 2, 128, 2, 2>;
-using Small = TileShape<64, 64, 2, 2, 128, 2, 4>;
-using SmallPair = TileShape<64, 64, 2, 1, 128, 2, 4>;
+using Small = TileShape<64, 64, 2, 2, 128, 2, 2>;
+using SmallPair = TileShape<64, 64, 2, 1, 128, 2, 2>;
 enum { SMALL = 0, MID = 1, WIDE = 2 };
 constexpr int64_t CUS = 256;
 
 // How a product of m x n over k is cut into tiles of a shape and splits of the
-// sum, and the time one block takes: us a round of stages, as measured with
-// every CU at work, and a fixed part.
+// sum, and the time one block takes alone.
 struct Cut {
     int32_t stages, splits, per_split;
     int64_t mt, nt, blocks;
     double us;
 };
 
-static Cut cut_as(int shape, int64_t m, int64_t wide, int64_t k, int segments, int64_t splits)
+// Microseconds, by shape, as measured with 64 to 1024 blocks and k of 64 to 4096:
+// a launch of blocks that do nothing else, a round of stages (one by each group)
+// with few CUs at work and with all, and what an activation or its derivative
+// adds at the end where the sum is not split. SLOTS blocks run at once.
+static constexpr int64_t SIDE[3] = {64, 128, 256}, GROUPS[3] = {Small::KG, Mid::KG, Wide::KG}, SLOTS[3] = {2 * CUS, CUS, CUS};
+static constexpr double LAUNCH[3] = {2.9, 2.9, 4.1}, ROUND[3] = {0.58, 0.89, 1.03}, ROUND_ALL[3] = {0.68, 1.49, 1.75};
+static constexpr double ENDS[3][3] = {{0., 2.5, 3.}, {0., 4., 7.5}, {0., 7., 14.}};  // TO_STORE, TO_GATED, TO_GRAD
+
+static Cut cut_as(int shape, int64_t m, int64_t wide, int64_t k, int segments, int64_t splits, int to)
 {
-    static constexpr int64_t SIDE[3] = {64, 128, 256}, GROUPS[3] = {4, 2, 1};
-    static constexpr double ROUND[3] = {0.9, 1.2, 1.75};
     Cut c;
     c.mt = (m + SIDE[shape] - 1) / SIDE[shape];
     c.nt = (wide + SIDE[shape] - 1) / SIDE[shape];
@@ -530,12 +580,14 @@ static Cut cut_as(int shape, int64_t m, int64_t wide, int64_t k, int segments, i
     c.per_split = (int32_t)std::max<int64_t>(1, (total + splits - 1) / splits);
     c.splits = (int32_t)std::max<int64_t>(1, (total + c.per_split - 1) / c.per_split);
     c.blocks = c.mt * c.nt * c.splits;
-    c.us = 3.0 + ROUND[shape] * (double)((c.per_split + GROUPS[shape] - 1) / GROUPS[shape]);
+    const double at_work = std::min(1.0, (double)c.blocks / CUS), round = ROUND[shape] + (ROUND_ALL[shape] - ROUND[shape]) * at_work;
+    c.us = LAUNCH[shape] + round * (double)((c.per_split + GROUPS[shape] - 1) / GROUPS[shape]) + (c.splits > 1 ? 0. : ENDS[shape][to]);
     return c;
 }
 
-// Sums of splits are written, read and joined by another kernel: microseconds.
-static double join_us(const Cut& c, int64_t m, int64_t wide) { return c.splits > 1 ? 4.0 + (double)(c.splits * m * wide) * 3e-6 : 0.0; }
+// Sums of splits are written, read and joined by another kernel: microseconds,
+// with the gap before a launch.
+static double join_us(const Cut& c, int64_t m, int64_t wide) { return c.splits > 1 ? 5.0 + (double)(c.splits * m * wide) * 3e-6 : 0.0; }
 
 constexpr int64_t MOST_SPLITS = 32;
 
@@ -547,8 +599,8 @@ static Cut cut_of(int64_t m, int64_t n, int64_t k, int to, int* shape)
     double least = 1e30;
     for (int s = SMALL; s <= WIDE; ++s)
         for (int64_t splits = 1; splits <= MOST_SPLITS; splits *= 2) {
-            const Cut c = cut_as(s, m, wide, k, 1, splits);
-            const double us = (double)((c.blocks + CUS - 1) / CUS) * c.us + join_us(c, m, wide);
+            const Cut c = cut_as(s, m, wide, k, 1, splits, to);
+            const double us = (double)((c.blocks + SLOTS[s] - 1) / SLOTS[s]) * c.us + join_us(c, m, wide);
             if (us < least) least = us, best = c, *shape = s;
             if (c.per_split <= 4) break;
         }
@@ -617,7 +669,7 @@ static Back back_of(const Sizes& z)
     for (int s = SMALL; s <= WIDE; ++s) {
         Back b{};
         b.shape = s;
-        for (int i = 0; i < 3; ++i) b.m[i] = m[i], b.n[i] = n[i], b.c[i] = cut_as(s, m[i], n[i], k[i], i == 0 ? 2 : 1, 1);
+        for (int i = 0; i < 3; ++i) b.m[i] = m[i], b.n[i] = n[i], b.c[i] = cut_as(s, m[i], n[i], k[i], i == 0 ? 2 : 1, 1, TO_STORE);
         // the longest blocks in splits, as long as that makes it shorter
         for (;;) {
             double sum = 0, longest = 0, joins = 0;
@@ -629,11 +681,11 @@ static Back back_of(const Sizes& z)
                 joins += join_us(b.c[i], m[i], n[i]);
                 if (b.c[i].us > longest) longest = b.c[i].us, which = i;
             }
-            // whole rounds of the average block, or what the CUs do on average and half of the longest block
-            b.us = (blocks <= CUS ? longest : sum / CUS + longest / 2) + joins;
+            // whole rounds of the average block, or what a slot does on average and half of the longest block
+            b.us = (blocks <= SLOTS[s] ? longest : sum / SLOTS[s] + longest / 2) + joins;
             if (b.us < best.us) best = b;
             if (b.c[which].splits * 2 > MOST_SPLITS || b.c[which].per_split <= 4) break;
-            b.c[which] = cut_as(s, m[which], n[which], k[which], which == 0 ? 2 : 1, b.c[which].splits * 2);
+            b.c[which] = cut_as(s, m[which], n[which], k[which], which == 0 ? 2 : 1, b.c[which].splits * 2, TO_STORE);
         }
     }
     return best;

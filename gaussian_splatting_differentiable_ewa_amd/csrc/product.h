@@ -45,16 +45,12 @@ template <>
 struct Mma<fp4> {
     typedef int v8 __attribute__((ext_vector_type(4)));
     typedef int v8i __attribute__((ext_vector_type(8)));
-    // Scales: byte `s` of sa and sb, as exponents off 127.
+    // Scales: byte `s`, 0 or 1, of sa and sb, as exponents off 127.
     static __device__ __forceinline__ acc16 mma(v8 a, v8 b, acc16 c, int s, int sa, int sb)
     {
         const v8i x = {a[0], a[1], a[2], a[3], 0, 0, 0, 0}, y = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
-        switch (s) {
-            case 0: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 0, sa, 0, sb);
-            case 1: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 1, sa, 1, sb);
-            case 2: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 2, sa, 2, sb);
-            default: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 3, sa, 3, sb);
-        }
+        return s == 0 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 0, sa, 0, sb)
+                      : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 1, sa, 1, sb);
     }
 };
 
@@ -92,6 +88,8 @@ __device__ __forceinline__ Buffer buffer_of(const char* p, uint32_t bytes)
 // stages, waits for all of them at a read where it cannot (two products in one
 // kernel). They are waited for, and kept from reads, by `ready` below alone.
 // M0 and a buffer from vector instructions need the wait states in between.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // that M0, which no code keeps over these, is clobbered
 __device__ __forceinline__ void load_lds(Buffer src, uint32_t offset, uint32_t further, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(offset), "s"(src),
@@ -103,6 +101,7 @@ __device__ __forceinline__ void load_lds_4(Buffer src, uint32_t offset, uint32_t
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(src)
                  : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
 
@@ -534,36 +533,30 @@ struct Rows {
     {
         store_as<uint4>(to, ld, rows, bytes, first);
     }
-    // The same from memory, all reads before the first is used.
-    template <typename V>
-    __device__ __forceinline__ void load_as(const char* from, int64_t ld, int64_t rows, int64_t bytes) const
+    // The same from memory to registers, zeros past the end, and from those to the scratch.
+    template <typename V, int K>
+    static __device__ __forceinline__ void fetch(V (&v)[K], const char* from, int64_t ld, int64_t rows, int64_t bytes)
     {
         constexpr int N = W / sizeof(V);
-        V v[N / 2];
+        static_assert(K == N / 2, "a lane's part of 32 rows");
 #pragma unroll
-        for (int k = 0; k < N / 2; ++k) {
+        for (int k = 0; k < K; ++k) {
             const int row = (k * 64 + lane_id()) / N, byte = (lane_id() % N) * sizeof(V);
             v[k] = V{};
             if (row < rows && byte < bytes) v[k] = *(const V*)(from + row * ld + byte);
         }
-#pragma unroll
-        for (int k = 0; k < N / 2; ++k) {
-            const int row = (k * 64 + lane_id()) / N, byte = (lane_id() % N) * sizeof(V);
-            *(V*)(p + at(row, byte)) = v[k];
-        }
     }
-    __device__ __forceinline__ void load(const char* from, int64_t ld, int64_t rows, int64_t bytes) const
+    template <typename V, int K>
+    __device__ __forceinline__ void put_all(const V (&v)[K]) const
     {
-        load_as<uint4>(from, ld, rows, bytes);
+        constexpr int N = W / sizeof(V);
+#pragma unroll
+        for (int k = 0; k < K; ++k) *(V*)(p + at((k * 64 + lane_id()) / N, (lane_id() % N) * sizeof(V))) = v[k];
     }
     // Rows of a multiple of 8 bytes.
     __device__ __forceinline__ void store8(char* to, int64_t ld, int64_t rows, int64_t bytes) const
     {
         store_as<uint2>(to, ld, rows, bytes, 0);
-    }
-    __device__ __forceinline__ void load8(const char* from, int64_t ld, int64_t rows, int64_t bytes) const
-    {
-        load_as<uint2>(from, ld, rows, bytes);
     }
 };
 
