@@ -669,7 +669,7 @@ def gated_ff_bwd_workspace_bytes(rows: int, channels: int, hidden: int, channels
 
 
 def gs_gated_ff_bwd(gy, x, w_gate, w_up, w_down, h, kept, act, gx, gw_gate, gw_up, gw_down, ws, stream=None):
-    """gx, gw_gate with gw_up, and gw_down may be None."""
+    """gx, gw_gate with gw_up, and gw_down may be None; rows apart (no stride of 0)."""
     rows, c = x.shape
     _check(_at(x).gs_gated_ff_bwd(_mat(gy), _mat(x), _mat(w_gate), _mat(w_up), _mat(w_down), _ptr(h), _ptr(kept), rows, c,
                                   w_gate.shape[0], w_down.shape[0], act, dtype_of(x), _ptr(gx), _ptr(gw_gate), _ptr(gw_up),

@@ -691,7 +691,7 @@ static Back back_of(const Sizes& z)
     return best;
 }
 
-// Whether every product's workgroups, of 1024 threads at most, are below 2^32
+// Whether every product's workgroups, of 512 threads, are below 2^32
 // threads.
 static bool tiles_ok(const Sizes& z)
 {
@@ -798,6 +798,10 @@ static bool ff_rows_ok(const gs_matrix* m, int64_t columns)
     return ((uintptr_t)m->data & 15) == 0 && m->stride % 8 == 0 && (m->stride == 0 || m->stride >= columns) && m->stride < (1 << 21);
 }
 
+// The same where sums run over the rows: those of one row for all would not end,
+// and zeros of the other operand do not cancel an infinity.
+static bool ff_rows_apart(const gs_matrix* m, int64_t columns) { return ff_rows_ok(m, columns) && m->stride != 0; }
+
 __global__ __launch_bounds__(256) void k_ff_zero(uint4* p, int64_t n)
 {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -843,7 +847,8 @@ gs_status gs_gated_ff_fwd(const gs_matrix* x, const gs_matrix* w_gate, const gs_
     if (!given(x) || !given(w_gate) || !given(w_up) || !given(w_down) || !h || !y) return GS_ERR_INVALID_ARGUMENT;
     const size_t need = fwd_bytes(z);
     if (need && (!ws || ((uintptr_t)ws & 15) || ws_bytes < need)) return GS_ERR_INVALID_ARGUMENT;
-    if (!ff_rows_ok(x, channels) || !ff_rows_ok(w_gate, channels) || !ff_rows_ok(w_up, channels) || !ff_rows_ok(w_down, hidden) || (((uintptr_t)h | (uintptr_t)kept | (uintptr_t)y) & 15))
+    if (!ff_rows_ok(x, channels) || !ff_rows_ok(w_gate, channels) || !ff_rows_ok(w_up, channels) || !ff_rows_ok(w_down, hidden) ||
+        (((uintptr_t)h | (uintptr_t)kept | (uintptr_t)y) & 15))
         return GS_ERR_UNSUPPORTED;
     const hipStream_t s = (hipStream_t)stream;
     const auto f = dtype == GS_F16 ? (act == GS_SILU ? ff_fwd<f16, ACT_SILU> : ff_fwd<f16, ACT_GELU>)
@@ -878,7 +883,8 @@ gs_status gs_gated_ff_bwd(const gs_matrix* gy, const gs_matrix* x, const gs_matr
         return ff_zero(gw_down, (int64_t)channels_out * hidden, s) == hipSuccess ? GS_OK : GS_ERR_HIP;
     }
     if (!given(gy) || !given(x) || !given(w_gate) || !given(w_up) || !given(w_down) || !h || !kept) return GS_ERR_INVALID_ARGUMENT;
-    if (!ff_rows_ok(gy, channels_out) || !ff_rows_ok(x, channels) || !ff_rows_ok(w_gate, channels) || !ff_rows_ok(w_up, channels) || !ff_rows_ok(w_down, hidden) || (((uintptr_t)h | (uintptr_t)kept) & 15))
+    if (!ff_rows_apart(gy, channels_out) || !ff_rows_apart(x, channels) || !ff_rows_apart(w_gate, channels) ||
+        !ff_rows_apart(w_up, channels) || !ff_rows_apart(w_down, hidden) || (((uintptr_t)h | (uintptr_t)kept) & 15))
         return GS_ERR_UNSUPPORTED;
     const auto f = dtype == GS_F16 ? (act == GS_SILU ? ff_bwd<f16, ACT_SILU> : ff_bwd<f16, ACT_GELU>)
                                    : (act == GS_SILU ? ff_bwd<bf16, ACT_SILU> : ff_bwd<bf16, ACT_GELU>);

@@ -211,6 +211,11 @@ def _on16(t):
     return t.clone(memory_format=torch.contiguous_format)
 
 
+def _apart(t):
+    """The same, and rows that are one for all as a copy: sums run over them."""
+    return t.contiguous() if t.stride(0) == 0 and t.shape[0] > 1 else _on16(t)
+
+
 def _ff_args(x, w_gate, w_up, w_down, act):
     _rows("x", x)
     rows, c = x.shape
@@ -264,7 +269,7 @@ def gated_ff_backward(gy, x, w_gate, w_up, w_down, h, kept, act: str = "silu"):
         _lost("GatedFF")
     grads = x.new_empty(rows, c), x.new_empty(f, c), x.new_empty(f, c), x.new_empty(co, f)
     ws = x.new_empty(L.gated_ff_bwd_workspace_bytes(rows, c, f, co), dtype=torch.uint8)
-    L.gs_gated_ff_bwd(_on16(gy), _on16(x), _on16(w_gate), _on16(w_up), _on16(w_down), h, kept, ACTS[act], *grads, ws)
+    L.gs_gated_ff_bwd(_apart(gy), _apart(x), _apart(w_gate), _apart(w_up), _apart(w_down), h, kept, ACTS[act], *grads, ws)
     return grads
 
 

@@ -984,7 +984,8 @@ size_t gs_gated_ff_bwd_workspace_bytes(int64_t rows, int32_t channels, int32_t h
  * loss has to be scaled so that they fit it. Sums are fp32 and have a fixed
  * order: the same bits on every call.
  *   ws       workspace of gs_gated_ff_bwd_workspace_bytes(...)
- * Errors: as gs_gated_ff_fwd.
+ * What goes out may not lie over what comes in.
+ * Errors: as gs_gated_ff_fwd, and GS_ERR_UNSUPPORTED for a row stride of 0.
  */
 gs_status gs_gated_ff_bwd(const gs_matrix* gy, const gs_matrix* x, const gs_matrix* w_gate, const gs_matrix* w_up,
                           const gs_matrix* w_down, const void* h, const void* kept, int64_t rows, int32_t channels,

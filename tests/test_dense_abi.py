@@ -134,3 +134,12 @@ def test_tensor_functions_refuse(lib):
     for bad in (lambda: T.quantise4(cpu), lambda: T.linear4(cpu, (cpu, cpu)), lambda: T.dequantise4((cpu, cpu))):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_gated_ff_bwd_refuses_one_row_for_all(lib):
+    """Sums run over the rows of every operand."""
+    need = L.gated_ff_bwd_workspace_bytes(10, 64, 128, 64)
+    bwd = dict(gy=mat(), x=mat(), wg=mat(), wu=mat(), wd=mat(), h=FAKE, kept=FAKE, rows=10, c=64, hid=128, co=64, act=L.GS_SILU,
+               t=L.GS_BF16, gx=FAKE, gwg=FAKE, gwu=FAKE, gwd=FAKE, ws=FAKE, wsb=need, s=None)
+    for name in ("gy", "x", "wg", "wu", "wd"):
+        assert call(lib.gs_gated_ff_bwd, bwd, **{name: mat(stride=0)}) == UNS, name
