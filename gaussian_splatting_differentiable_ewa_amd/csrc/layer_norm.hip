@@ -159,7 +159,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_fwd(const LayerAr
             if (r + d < r1) one(r + d, next[d]);
 }
 
-template <typename T, int VEC, int NV, int NT, int AHEAD>
+template <typename T, int VEC, int NV, int NT, int AHEAD, bool FULL>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_bwd(const LayerArgs a)
 {
     constexpr int PER = NT < 256 ? 256 / NT : 1;
@@ -185,8 +185,8 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_layer_bwd(const LayerAr
     const auto one = [&](int64_t r, typename C::template Raw<T>& raw_x, typename C::template Raw<T>& raw_g) __attribute__((always_inline)) {
         const float mean = a.stats[r], rs = a.stats[a.rows + r];
         float xh[NV][VEC], d[NV][VEC], v[2] = {0.f, 0.f};
-        // past the channels gy is zero, and with it every term
-        GS_EACH(xh[i][e] = ((float)raw_x.v[i][e] - mean) * rs; const float g = (float)raw_g.v[i][e];
+        // past the channels gy is zero, and with it every term (of x there, mean times rs may pass fp32)
+        GS_EACH(xh[i][e] = FULL || col.has(i, e) ? ((float)raw_x.v[i][e] - mean) * rs : 0.f; const float g = (float)raw_g.v[i][e];
                 sum_w[i][e] = fmaf(g, xh[i][e], sum_w[i][e]); sum_b[i][e] += g; d[i][e] = g * w[i][e];
                 v[0] += d[i][e]; v[1] = fmaf(d[i][e], xh[i][e], v[1]))
         if (r + AHEAD < r1) {
@@ -229,9 +229,12 @@ static hipError_t layer_launch(const LayerArgs& a, bool backward, hipStream_t s)
     constexpr int PER = NT < 256 ? 256 / NT : 1, THREADS = NT < 256 ? 256 : NT;
     constexpr int AHEAD = 2, BACK = 1;
     const dim3 grid(grid_for((uint64_t)((a.rows + a.run - 1) / a.run), PER));
-    if (backward)
-        hipLaunchKernelGGL((k_layer_bwd<T, VEC, NV, NT, BACK>), grid, dim3(THREADS), 0, s, a);
-    else if (a.channels == VEC * NV * NT)
+    const bool full = a.channels == VEC * NV * NT;
+    if (backward && full)
+        hipLaunchKernelGGL((k_layer_bwd<T, VEC, NV, NT, BACK, true>), grid, dim3(THREADS), 0, s, a);
+    else if (backward)
+        hipLaunchKernelGGL((k_layer_bwd<T, VEC, NV, NT, BACK, false>), grid, dim3(THREADS), 0, s, a);
+    else if (full)
         hipLaunchKernelGGL((k_layer_fwd<T, VEC, NV, NT, AHEAD, true>), grid, dim3(THREADS), 0, s, a);
     else
         hipLaunchKernelGGL((k_layer_fwd<T, VEC, NV, NT, AHEAD, false>), grid, dim3(THREADS), 0, s, a);

@@ -136,7 +136,8 @@ class TileNet(torch.nn.Module):
         if self.gated is None:
             return self._linear(F.gelu(self._linear(h, self.up[i], four.get("up"))), self.down[i], four.get("down"))
         if not four:
-            return T.GatedFF.apply(h, *(w[i].to(self.dtype) for w in (self.open, self.up, self.down)), self.gated)
+            weights = (w[i].to(self.dtype) for w in (self.open, self.up, self.down))
+            return (T.GatedFF.apply if torch.is_grad_enabled() else T.gated_ff)(h, *weights, self.gated)
         opened, up = T.linear4(h, four["open up"]).chunk(2, 1)
         return T.linear4(getattr(F, self.gated)(opened) * up, four["down"])
 

@@ -111,6 +111,25 @@ def test_linear4_weights_of_one_row_for_all():
         assert torch.equal(y, T.linear4(x, w).expand(rows, 50))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("c", [1, 8, 32, 64])
+def test_layer_norm_far_from_zero(dtype, c):
+    """A constant row whose mean times 1 / sqrt(eps) passes fp32: x - mean is zero there, and the gradients are those
+    of a constant row of ones, also in threads that hold columns past the row's. (Powers of two, of which the sum,
+    2^127 at most, and the mean are exact; at other counts the mean's rounding squared passes fp32 in any form.)"""
+    x = torch.ones(3, c, device=DEV)
+    x[1] *= 2.0 ** 121
+    x = x.to(dtype)
+    gy = rand(gen(c), 1, c, dtype=dtype).expand(3, c).contiguous()
+    w = 1 + rand(gen(c + 1), c) / 8
+    y, stats = T.layer_norm(x, w)
+    assert not y.any() and stats[0, 1] == 2.0 ** 121 and stats[1, 1] == stats[1, 0]
+    gx, gw, gb = T.layer_norm_backward(gy, x, w, stats)
+    assert torch.isfinite(gx).all() and torch.equal(gx[0], gx[1]) and torch.equal(gx[0], gx[2])
+    assert not gw.any()
+    O.within(gb, gy.double().sum(0), 3 * O.E * gy.double().abs().sum(0), "gb")
+
+
 def block(x, ln, ff, four):
     """A layer as a model runs it: norm, feed-forward block and residual, and a head in 4 bits."""
     n, stats = T.layer_norm(x, *ln)
