@@ -415,7 +415,8 @@ __global__ __launch_bounds__(256) void k_ff_joins(const JoinArgs j)
     ff_join<T, TO_STORE, ACT_SILU>(j.o[which], j.splits[which], id);
 }
 
-// Few rows (16 at most): the weights are read once and bound it, so each wave
+// Few rows (16 at most): the weights are read once and bound it (one row, 2048 x
+// 8192: 67 MB in 13.0 us and 34 MB in 8.4, 5.2 and 4.0 TB/s), so each wave
 // takes them straight from memory to registers, 16 rows of them and the tokens
 // beside them to a 16 x 16 tile of the result, and the waves of a workgroup
 // share the sum over k, 64 elements in turn: a lane's two pieces of 16 bytes and
@@ -423,8 +424,13 @@ __global__ __launch_bounds__(256) void k_ff_joins(const JoinArgs j)
 // is free as long as both operands have the same). Their sums meet in LDS.
 // With PARTS = 2 a tile is 8 rows of the weights for 8 tokens, each twice, with
 // the first and the second half of k: of the 16 x 16 results the two 8 x 8 count
-// whose halves are the same. It makes twice the workgroups, for few columns.
-constexpr int FEW = 16;
+// whose halves are the same. It makes twice the workgroups, for up to 8 rows and
+// few columns: one row, 2048 columns, k 8192: 8.4 us against 12.2, k 2048: 4.5
+// against 5.4 (8 rows); 8192 columns, k 2048: 10.2 against 9.4.
+// The tiles below take as long at 16 rows of 2048 x 8192 (33 us with their
+// joins' launches, as here) and longer at fewer and smaller: 16 rows of 1024 x
+// 4096 19.2 against 16.7, 12 of 520 x 1368 15.8 against 8.2.
+constexpr int FEW = 16, FEW_WAVES = 8, NARROW = 4096;
 
 struct FewArgs {
     const char *x, *w[2];
@@ -433,10 +439,10 @@ struct FewArgs {
     int32_t k;
 };
 
-template <typename T, int TO, int ACT, int WAVES, int PARTS>
-__global__ __launch_bounds__(WAVES * 64) void k_ff_few(const FewArgs p)
+template <typename T, int TO, int ACT, int PARTS>
+__global__ __launch_bounds__(FEW_WAVES * 64) void k_ff_few(const FewArgs p)
 {
-    constexpr int M = TO == TO_GATED ? 2 : 1, AHEAD = (WAVES < 16 ? 8 : 4) / M, SIDE = 16 / PARTS;
+    constexpr int WAVES = FEW_WAVES, M = TO == TO_GATED ? 2 : 1, AHEAD = 8 / M, SIDE = 16 / PARTS;
     typedef typename Mma<T>::v8 V;
     __shared__ float4v s_sum[WAVES][M][64];
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane % SIDE, q = lane >> 4;
@@ -518,7 +524,6 @@ __global__ __launch_bounds__(WAVES * 64) void k_ff_few(const FewArgs p)
     }
 }
 
-// Waves to a workgroup: enough for the chip where there are few columns.
 template <typename T, int TO, int ACT>
 static hipError_t few(const Operand& a, const Operand& b, const Target& o, int64_t k, hipStream_t s)
 {
@@ -528,21 +533,20 @@ static hipError_t few(const Operand& a, const Operand& b, const Target& o, int64
     for (int i = 0; i < 2; ++i) p.w[i] = b.data[i], p.ld[i] = b.ld[i];
     p.o = o;
     p.k = (int32_t)k;
-    const auto launch = [&](auto waves, auto parts) {
-        constexpr int W = decltype(waves)::value, P = decltype(parts)::value;
-        hipLaunchKernelGGL((k_ff_few<T, TO, ACT, W, P>), dim3((unsigned)((o.n + 16 / P - 1) / (16 / P))), dim3(W * 64), 0, s, p);
-    };
-    const std::integral_constant<int, 1> one;
-    const std::integral_constant<int, 2> two;
-    const std::integral_constant<int, 4> four;
-    const std::integral_constant<int, 8> eight;
-    if (k <= 512) launch(four, one);
-    else if (o.m <= 8 && o.n <= 4096) launch(eight, two);
-    else launch(eight, one);
+    const auto blocks = [&](int64_t side) { return dim3((unsigned)((o.n + side - 1) / side)); };
+    if (o.m <= 8 && o.n <= NARROW) hipLaunchKernelGGL((k_ff_few<T, TO, ACT, 2>), blocks(8), dim3(FEW_WAVES * 64), 0, s, p);
+    else hipLaunchKernelGGL((k_ff_few<T, TO, ACT, 1>), blocks(16), dim3(FEW_WAVES * 64), 0, s, p);
     return hipGetLastError();
 }
 
-// The tiles. Smaller ones make more workgroups, and their groups of waves, which
+// The tiles. Wide is bound by the matrix unit at the clock its power leaves (1.5 to
+// 1.8 GHz; matrix instructions alone reach 1610 TFLOP/s): 32640 x 8192 x 2048 in 865 us
+// (1265 TFLOP/s; the library's own product 1526), the three products of the
+// backward pass in 4220 (1300, across k too; the library 1119 and 1243), and
+// both projections with h and what is kept, 1.9 GB, in 2010 (1090). Of more
+// stages or smaller ones, two workgroups of 256 x 128 on a CU, fetches to L2 ahead and wave
+// priorities none was faster (865 against 899 to 1031).
+// Smaller ones make more workgroups, and their groups of waves, which
 // share the sum over k, fill the CU. Two groups of Small leave room for a second
 // workgroup on the CU; four did not, and cost 1.2 us more a launch: 256 x 1024 x
 // 1024 took 7.4 us either way, 1024 x 1024 x 1024 8.0 against 8.2 us, 4096 x 1024

@@ -2,7 +2,8 @@
 // each row, and its gradients.
 //
 // Each element is read and written once in either direction, so both are bound
-// by HBM. NT threads hold a row in registers; a workgroup walks over a
+// by HBM: 32640 x 2048 bf16 forward 59 us (4.5 TB/s), back 84 (4.8 TB/s) and 6
+// for the sums. NT threads hold a row in registers; a workgroup walks over a
 // contiguous run of rows with the weights of its columns in registers, and the
 // next row is loaded (as it lies in memory, 4 registers for 16 bytes) before
 // the present one's reductions, so that its latency runs behind them.
@@ -227,7 +228,7 @@ template <typename T, int VEC, int NV, int NT>
 static hipError_t layer_launch(const LayerArgs& a, bool backward, hipStream_t s)
 {
     constexpr int PER = NT < 256 ? 256 / NT : 1, THREADS = NT < 256 ? 256 : NT;
-    constexpr int AHEAD = 2, BACK = 1;
+    constexpr int AHEAD = 2, BACK = 1;  // rows loaded ahead; 3 and 4 took no less
     const dim3 grid(grid_for((uint64_t)((a.rows + a.run - 1) / a.run), PER));
     const bool full = a.channels == VEC * NV * NT;
     if (backward && full)
@@ -242,7 +243,9 @@ static hipError_t layer_launch(const LayerArgs& a, bool backward, hipStream_t s)
 }
 
 // The fewest threads that hold a row in registers: one wave up to 16 values a
-// thread (no barrier per row), then 256 threads, then 1024.
+// thread (no barrier per row), then 256 threads, then 1024. For 2048 columns of
+// bf16 one wave, with 32 values a thread, took 104 us forward and 197 back, 256
+// threads 60 and 87.
 template <typename T, int VEC>
 static hipError_t layer_by_width(const LayerArgs& a, bool backward, hipStream_t s)
 {
