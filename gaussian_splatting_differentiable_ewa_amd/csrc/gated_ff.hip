@@ -589,9 +589,11 @@ static Cut cut_as(int shape, int64_t m, int64_t wide, int64_t k, int segments, i
     return c;
 }
 
-// Sums of splits are written, read and joined by another kernel: microseconds,
-// with the gap before a launch.
-static double join_us(const Cut& c, int64_t m, int64_t wide) { return c.splits > 1 ? 5.0 + (double)(c.splits * m * wide) * 3e-6 : 0.0; }
+// Sums of splits are written, read and joined by another kernel: microseconds of
+// its launch, with the gap before it (and half of what it takes on the host, which bounds
+// small calls that are not in a graph), and of the sums.
+constexpr double JOIN = 5.5;
+static double sums_us(const Cut& c, int64_t m, int64_t wide) { return c.splits > 1 ? (double)(c.splits * m * wide) * 3e-6 : 0.; }
 
 constexpr int64_t MOST_SPLITS = 32;
 
@@ -604,7 +606,7 @@ static Cut cut_of(int64_t m, int64_t n, int64_t k, int to, int* shape)
     for (int s = SMALL; s <= WIDE; ++s)
         for (int64_t splits = 1; splits <= MOST_SPLITS; splits *= 2) {
             const Cut c = cut_as(s, m, wide, k, 1, splits, to);
-            const double us = (double)((c.blocks + SLOTS[s] - 1) / SLOTS[s]) * c.us + join_us(c, m, wide);
+            const double us = (double)((c.blocks + SLOTS[s] - 1) / SLOTS[s]) * c.us + sums_us(c, m, wide) + (c.splits > 1 ? JOIN : 0.);
             if (us < least) least = us, best = c, *shape = s;
             if (c.per_split <= 4) break;
         }
@@ -676,17 +678,18 @@ static Back back_of(const Sizes& z)
         for (int i = 0; i < 3; ++i) b.m[i] = m[i], b.n[i] = n[i], b.c[i] = cut_as(s, m[i], n[i], k[i], i == 0 ? 2 : 1, 1, TO_STORE);
         // the longest blocks in splits, as long as that makes it shorter
         for (;;) {
-            double sum = 0, longest = 0, joins = 0;
+            double sum = 0, longest = 0, joins = 0, sums = 0;
             int64_t blocks = 0;
             int which = 0;
             for (int i = 0; i < 3; ++i) {
                 sum += b.c[i].us * (double)b.c[i].blocks;
                 blocks += b.c[i].blocks;
-                joins += join_us(b.c[i], m[i], n[i]);
+                joins = std::max(joins, b.c[i].splits > 1 ? JOIN : 0.);  // one launch for all
+                sums += sums_us(b.c[i], m[i], n[i]);
                 if (b.c[i].us > longest) longest = b.c[i].us, which = i;
             }
             // whole rounds of the average block, or what a slot does on average and half of the longest block
-            b.us = (blocks <= SLOTS[s] ? longest : sum / SLOTS[s] + longest / 2) + joins;
+            b.us = (blocks <= SLOTS[s] ? longest : sum / SLOTS[s] + longest / 2) + joins + sums;
             if (b.us < best.us) best = b;
             if (b.c[which].splits * 2 > MOST_SPLITS || b.c[which].per_split <= 4) break;
             b.c[which] = cut_as(s, m[which], n[which], k[which], which == 0 ? 2 : 1, b.c[which].splits * 2, TO_STORE);
