@@ -502,7 +502,9 @@ class LayerNorm(torch.autograd.Function):
 
 
 class GatedFF(torch.autograd.Function):
-    """apply(x, w_gate, w_up, w_down, act="silu") -> y."""
+    """apply(x, w_gate, w_up, w_down, act="silu") -> y. (Of any form here: a backward
+    pass that is captured into a graph needs leaves that no eager graph still
+    holds; torch ends the process otherwise.)"""
 
     @staticmethod
     def forward(ctx, x, w_gate, w_up, w_down, act="silu"):

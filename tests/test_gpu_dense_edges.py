@@ -208,3 +208,38 @@ def test_two_graphs_of_one_pool():
             torch.cuda.synchronize()
             for p, r in zip(got, block(*fresh)):
                 assert torch.equal(p, r), seed
+
+
+def test_autograd_in_a_graph():
+    """A training step through the autograd forms captured whole, gradients by autograd.grad; no eager graph of the
+    same leaves is alive then. Every replay gives the eager bits."""
+    def inputs(seed):
+        x, ln, ff, _ = block_inputs(seed, 150)
+        return [x, *ln, *ff, rand(gen(seed + 100), *x.shape, dtype=BF16)]
+
+    def run(x, w, b, wg, wu, wd, gy):
+        y = T.GatedFF.apply(T.LayerNorm.apply(x, w, b), wg, wu, wd, "silu")
+        return [y.detach(), *torch.autograd.grad(y, (x, w, b, wg, wu, wd), gy)]
+
+    held = inputs(0)
+    for t in held[:-1]:
+        t.requires_grad_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(*held)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        results = run(*held)
+    for seed in (1, 2, 3):
+        fresh = inputs(seed)
+        with torch.no_grad():
+            for t, u in zip(held, fresh):
+                t.copy_(u)
+        graph.replay()
+        got = [t.clone() for t in results]
+        torch.cuda.synchronize()
+        for t in fresh[:-1]:
+            t.requires_grad_()
+        assert all(torch.equal(p, r) for p, r in zip(got, run(*fresh))), seed
