@@ -246,20 +246,22 @@ def _gated_ff(x, w_gate, w_up, w_down, act, keep):
 
 def gated_ff(x, w_gate, w_up, w_down, act: str = "silu"):
     """(act(x w_gate^T) * (x w_up^T)) w_down^T for x [rows, channels], w_gate and
-    w_up [hidden, channels], w_down [out, hidden]; fp16 or bf16, sizes of 8. See
-    gs_gated_ff_fwd."""
+    w_up [hidden, channels], w_down [out, hidden]; fp16 or bf16, sizes of 8. In
+    fp16 the hidden layer, the product in brackets, has to fit the type (65504):
+    rows where it does not are not finite. See gs_gated_ff_fwd."""
     return _gated_ff(x, w_gate, w_up, w_down, act, False)[0]
 
 
 def gated_ff_train(x, w_gate, w_up, w_down, act: str = "silu"):
-    """(y, h, kept): gated_ff and what its backward pass takes, the hidden layer
-    and both projections (in gs_gated_ff_kept_bytes of the kernels' own layout)."""
+    """(y, h, kept): gated_ff, with its range in fp16, and what its backward pass
+    takes, the hidden layer and both projections (in gs_gated_ff_kept_bytes of
+    the kernels' own layout)."""
     return _gated_ff(x, w_gate, w_up, w_down, act, True)
 
 
 def gated_ff_backward(gy, x, w_gate, w_up, w_down, h, kept, act: str = "silu"):
-    """(gx, gw_gate, gw_up, gw_down); in fp16 the projections' gradients have to
-    fit the type. See gs_gated_ff_bwd."""
+    """(gx, gw_gate, gw_up, gw_down); in fp16 the hidden layer and the projections'
+    gradients have to fit the type. See gs_gated_ff_bwd."""
     rows, c, f, co = _ff_args(x, w_gate, w_up, w_down, act)
     _rows("gy", gy, co, x)
     _need(gy.shape[0] == rows, "gy must have x's rows")
@@ -502,7 +504,8 @@ class LayerNorm(torch.autograd.Function):
 
 
 class GatedFF(torch.autograd.Function):
-    """apply(x, w_gate, w_up, w_down, act="silu") -> y. (Of any form here: a backward
+    """apply(x, w_gate, w_up, w_down, act="silu") -> y; in fp16 with the range of
+    gated_ff and gated_ff_backward. (Of any form here: a backward
     pass that is captured into a graph needs leaves that no eager graph still
     holds; torch ends the process otherwise.)"""
 
