@@ -554,7 +554,7 @@ def gs_rope_axes(q, k, q_out, k_out, pos, freq, pairs, interleaved=False, invers
 
 
 def gs_norm_gate_fwd(x, f, gate, w_post, w_pre, y, h, stats, rows_per_gate, scale=1.0, eps=1e-6, stream=None):
-    """x, f, y, h [rows][channels] contiguous; f, gate, w_post, w_kept may be None."""
+    """x, f, y, h [rows][channels] contiguous; f, gate, w_post, w_pre may be None."""
     rows, c = x.shape
     _check(_at(x).gs_norm_gate_fwd(_ptr(x), _ptr(f), _ptr(gate), _ptr(w_post), _ptr(w_pre), _ptr(y), _ptr(h), _ptr(stats),
                                   rows, c, rows_per_gate, scale, eps, dtype_of(x), _current(x, stream)), "gs_norm_gate_fwd")
