@@ -54,7 +54,8 @@ def _run(cmd, verbose):
 def build(verbose: bool = False, extra=()) -> str:
     """Compile every source and link one shared library (always recompiles)."""
     tmp = LIB + ".tmp%d" % os.getpid()
-    jobs = min(8, int(os.environ.get("MAX_JOBS", 0)) or os.cpu_count() or 1)
+    jobs = os.environ.get("MAX_JOBS", "")
+    jobs = min(8, jobs.isdecimal() and int(jobs) or os.cpu_count() or 1)
     with tempfile.TemporaryDirectory() as folder:
         def compile_one(src):
             obj = os.path.join(folder, os.path.basename(src) + ".o")
@@ -64,7 +65,7 @@ def build(verbose: bool = False, extra=()) -> str:
         # the longest first
         with ThreadPoolExecutor(jobs) as pool:
             objs = list(pool.map(compile_one, sorted(sources(), key=os.path.getsize, reverse=True)))
-        _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs, verbose)
+        _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC"] + list(extra) + ["-o", tmp] + objs, verbose)
     os.replace(tmp, LIB)
     return LIB
 
