@@ -167,7 +167,8 @@ def _packed(t):
 
 def layer_norm(x, w=None, b=None, eps: float = 1e-5):
     """(y, stats): the layer norm of each row of x [rows, channels], times w plus
-    b (fp32 [channels], each may be None). See gs_layer_norm_fwd."""
+    b (fp32 [channels], each may be None), for rows whose sums and squares fit
+    fp32. See gs_layer_norm_fwd."""
     _rows("x", x)
     rows, c = x.shape
     _vector("w", w, (c,), x)

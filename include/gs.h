@@ -908,6 +908,8 @@ typedef struct gs_matrix {
 /*
  * gs_layer_norm_fwd -- layer norm of each row of [rows][channels]:
  *   m = mean x,  r = 1 / sqrt(mean (x - m)^2 + eps),  y = (x - m) r w + b
+ * Sums are fp32: a row whose squared deviations sum up past its range counts as
+ * infinitely wide (r = 0), one whose values do is NaN.
  *   x      any row stride >= 0 and alignment of its element
  *   w, b   fp32 [channels], or NULL (ones, zeros)
  *   y      out, the type of x, contiguous (may alias a contiguous x)
