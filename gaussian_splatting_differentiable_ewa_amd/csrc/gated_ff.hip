@@ -19,9 +19,14 @@ namespace gs {
 
 enum { ACT_SILU = 0, ACT_GELU = 1 };
 
-// act(g) and its derivative. gelu(g) = g F(g) with F the normal distribution,
-// whose error function is Abramowitz and Stegun's 7.1.26 (1.5e-7 off at most);
-// its exponential is that of the derivative too.
+// act(g) and its derivative. gelu(g) = g F(g) with F the normal distribution. For
+// g < 0, with x = |g| / sqrt 2 and t = 1 / (1 + 0.33 x), F = t P(t) exp(-x^2) / 2: P, of
+// degree 7, is fitted to erfc(x) exp(x^2) / t over x of 0 to 9.6 for the least largest
+// error relative to it, 8.2e-8, so a closing gate keeps its digits: 5e-7 off with the
+// roundings at g = -1, 2e-6 at -6 and 8e-6 at -12, where the exponent's argument
+// is 104. (Abramowitz and Stegun's 7.1.26, two terms shorter, is 5e-4 off at -4 and
+// 1e-2 at -8; the largest training step is 0.4 % faster with it.) The exponential is
+// that of the derivative too.
 template <int ACT>
 __device__ __forceinline__ void activate(float g, float& a, float& da)
 {
@@ -31,8 +36,10 @@ __device__ __forceinline__ void activate(float g, float& a, float& da)
         da = fmaf(a, 1.f - t, t);
     } else {
         const float e = exp2_fast(g * g * (-0.5f * LOG2E));
-        const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f * 0.70710678f, fabsf(g), 1.f));
-        const float p = fmaf(fmaf(fmaf(fmaf(1.061405429f, t, -1.453152027f), t, 1.421413741f), t, -0.284496736f), t, 0.254829592f);
+        const float t = __builtin_amdgcn_rcpf(fmaf(0.33f * 0.70710678f, fabsf(g), 1.f));
+        float p = fmaf(-0.135929227f, t, 0.462690145f);
+        p = fmaf(fmaf(fmaf(p, t, -0.355442464f), t, 0.412545085f), t, 0.0450086333f);
+        p = fmaf(fmaf(fmaf(p, t, 0.201924488f), t, 0.182837129f), t, 0.186366126f);
         const float q = 0.5f * p * t * e;  // F(-|g|)
         const float f = g < 0.f ? q : 1.f - q;
         a = g * f;
