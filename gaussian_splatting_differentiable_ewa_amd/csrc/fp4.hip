@@ -116,10 +116,11 @@ __global__ __launch_bounds__(256) void k_fp4_dequantise(const uint8_t* __restric
         }
 }
 
-// A product's tiles: 32640 x 2048 x 8192 in 389 us, 2.8 PFLOP/s, where the 16-bit
-// product takes 865: a step of the matrix unit lasts 32 cycles for 8 KB of
-// operands, so the reads from LDS bound it, at the clock that its power leaves.
-// 128 x 128 elements a workgroup, two to a CU, took 531; scales straight from memory to
+// A product's tiles: 32640 x 2048 x 8192 in 375 to 437 us, 2.5 to 2.9 PFLOP/s, where
+// the 16-bit product takes 865. A step of the matrix unit lasts 32 cycles for 8 KB
+// of operands; its instructions take 35 % of the cycles (at 1.97 GHz), the reads
+// from LDS 33 %, 38 % of those in conflicts of banks: neither fills the time, and
+// what keeps them from running beside each other is not found. 128 x 128 elements a workgroup, two to a CU, took 531; scales straight from memory to
 // registers 618 (they share the address path with the tiles' loads).
 struct FourArgs {
     Operand a, b;  // [0]: codes, [1]: scales

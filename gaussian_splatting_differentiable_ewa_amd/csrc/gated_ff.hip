@@ -24,7 +24,7 @@ enum { ACT_SILU = 0, ACT_GELU = 1 };
 // degree 7, is fitted to erfc(x) exp(x^2) / t over x of 0 to 9.6 for the least largest
 // error relative to it, 8.2e-8, so a closing gate keeps its digits: 5e-7 off with the
 // roundings at g = -1, 2e-6 at -6 and 8e-6 at -12, where the exponent's argument
-// is 104. (Abramowitz and Stegun's 7.1.26, two terms shorter, is 5e-4 off at -4 and
+// is 104. (Abramowitz and Stegun's 7.1.26, three terms shorter, is 5e-4 off at -4 and
 // 1e-2 at -8; the largest training step is 0.4 % faster with it.) The exponential is
 // that of the derivative too.
 template <int ACT>
@@ -544,11 +544,12 @@ static hipError_t few(const Operand& a, const Operand& b, const Target& o, int64
     return hipGetLastError();
 }
 
-// The tiles. Wide is bound by the matrix unit at the clock its power leaves (1.5 to
-// 1.8 GHz; matrix instructions alone reach 1610 TFLOP/s): 32640 x 8192 x 2048 in 865 us
-// (1265 TFLOP/s; the library's own product 1526), the three products of the
-// backward pass in 4220 (1300, across k too; the library 1119 and 1243), and
-// both projections with h and what is kept, 1.9 GB, in 2010 (1090). Of more
+// The tiles. Wide's matrix instructions take 72 to 79 % of the cycles of y and of
+// the backward's three products, 58 to 61 % with h's epilogue and 47 to 53 % with
+// that of gg and gu, at clocks that fall to 1.3 to 1.75 GHz: 32640 x 8192 x 2048 in
+// 857 to 865 us (1270 TFLOP/s; the library's own product 1526), the three products of
+// the backward pass in 4080 to 4220 (1300, across k too; the library 1119 and 1243), and
+// both projections with h and what is kept, 1.9 GB, in 2010 to 2090 (1050 to 1090). Of more
 // stages or smaller ones, two workgroups of 256 x 128 on a CU, fetches to L2 ahead and wave
 // priorities none was faster (865 against 899 to 1031).
 // Smaller ones make more workgroups, and their groups of waves, which
