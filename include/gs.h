@@ -954,8 +954,8 @@ size_t gs_gated_ff_fwd_workspace_bytes(int64_t rows, int32_t channels, int32_t h
  * with act(g) = g / (1 + exp(-g)) (GS_SILU) or g times the normal distribution
  * function (GS_GELU). Sums are fp32; h is rounded to the inputs' type for its
  * product. With GS_F16 it has to fit it: |h| up to 65504, where x of ten times
- * the size makes an h of up to a hundred times. A row that holds more is
- * not finite in y, and gw_down is not in the backward pass; GS_BF16 has no such limit.
+ * the size makes an h of up to a hundred times. A row that holds more is not
+ * finite in y, nor the columns of gw_down it reaches; GS_BF16 has no such limit.
  *   x        [rows][channels], GS_F16 or GS_BF16 as everything but kept
  *   w_gate, w_up  [hidden][channels];  w_down  [channels_out][hidden]
  *   h        out [rows][hidden] (for the backward pass, or scratch)
